@@ -143,7 +143,8 @@ enum {
     FW_ERR_UNSUPPORTED = -8, /* FW_ALGO_CHUNKED asked for a call it does not support */
     FW_ERR_ARG = -9,         /* eps negative or not finite, or o aliases an input */
     FW_ERR_DEVICE = -10,     /* the current device is not an sm_103 GPU */
-    FW_ERR_SCRATCH = -11     /* fw_prefill_noalloc: the call needs more than FW_SCRATCH_BYTES */
+    FW_ERR_SCRATCH = -11     /* fw_prefill_noalloc: the call needs more than FW_SCRATCH_BYTES;
+                                fw_decay_*, fw_layer_norm_backward: workspace_bytes too small */
 };
 
 /*
@@ -300,6 +301,111 @@ int fw_window_step(const void *q, const void *k_prev, const void *v, const float
                    const float *lambda, float *S, const fw_window *win_in, void *o,
                    const fw_window *win_out, const fw_shape *shape, int window, fw_dtype dtype,
                    fw_mode mode, fw_phi phi, float eps, unsigned flags, cudaStream_t stream);
+
+/* ---- linear attention with a decay for each head ---------------------------
+ *
+ * The decayed form of the linear-attention page ("Attention is also an FFN"
+ * blog, §3.2), with a fixed decay g_h = exp(log_decay[h]) for each head h:
+ *     S_t = g_h S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,
+ * forward over a prompt, its gradients, and one token.  The feature map is the
+ * caller's (q and k are used as given).  Beyond the shared conventions:
+ *   log_decay   float [H], <= 0 (0: no decay; -inf: g = 0).  Positive values
+ *               are computed literally.  The decays are constants of the
+ *               model: no gradient with respect to them is formed.
+ *   lens        int32 [B] or NULL.  Tokens of each batch row of a padded
+ *               batch, clamped to [0, T]; NULL: T for every row.  Rows of o
+ *               (dq, dk, dv) from lens[b] on are left as they were, and what q,
+ *               k, v and d_o hold there, NaN included, is never used.  With 0
+ *               tokens S_T = S0 (zero without S0).
+ *   workspace   device memory of at least fw_decay_workspace() bytes, owned by
+ *               the caller, or NULL where that is 0.  Its contents need not be
+ *               initialised and mean nothing after the call.  Calls that may
+ *               overlap (two streams, two captured graphs replayed at once)
+ *               need a workspace each.
+ *   No output may overlap an input, another output or the workspace, except
+ *   S_T = S0.
+ */
+
+/* Layer norm of every output row (one head's d_v values): y = (o - mean(o)) /
+ * sqrt(var(o) + eps) * weight + bias, var the mean of squares about the mean,
+ * taken from the fp32 row before it is rounded to `dtype`. */
+typedef struct {
+    const float *weight; /* float [d_v], device, or NULL (ones) */
+    const float *bias;   /* float [d_v], device, or NULL (zeros) */
+    float eps;           /* >= 0 */
+} fw_norm;
+
+/* Bytes of workspace of fw_decay_prefill (backward = 0) or fw_decay_backward
+ * (backward = 1) for this shape and type, or a negative FW_ERR_* code. */
+int64_t fw_decay_workspace(const fw_shape *shape, fw_dtype dtype, int backward);
+
+/*
+ * fw_decay_prefill -- T tokens for B*H independent chains.
+ *   q, k, v   in   [B][H][T][d] of `dtype`
+ *   S0        in   float [B][H][d][d] or NULL (zero)
+ *   norm      in   host pointer to the output norm, or NULL (o = scale S^T q)
+ *   o         out  [B][H][T][d] of `dtype`
+ *   S_T       out  float [B][H][d][d], the state after the last token; may equal S0
+ *   scale     finite
+ */
+int fw_decay_prefill(const void *q, const void *k, const void *v, const float *log_decay,
+                     const float *S0, const int32_t *lens, const fw_norm *norm, void *o,
+                     float *S_T, const fw_shape *shape, fw_dtype dtype, float scale,
+                     void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fw_decay_backward -- gradients of fw_decay_prefill without norm, given those
+ * of its outputs.  With D_t = scale q_t d_o_t^T + g D_{t+1} and g D_{T+1} := dS_T,
+ *     dq_t = scale S_t d_o_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t,  dS0 = g D_1.
+ * Nothing of the forward pass is needed but its inputs.
+ *   d_o       in   [B][H][T][d] of `dtype`
+ *   dS_T      in   float [B][H][d][d] or NULL (zero)
+ *   dq,dk,dv  out  [B][H][T][d] of `dtype`
+ *   dS0       out  float [B][H][d][d] or NULL (not wanted)
+ */
+int fw_decay_backward(const void *q, const void *k, const void *v, const float *log_decay,
+                      const float *S0, const int32_t *lens, const void *d_o, const float *dS_T,
+                      void *dq, void *dk, void *dv, float *dS0, const fw_shape *shape,
+                      fw_dtype dtype, float scale, void *workspace, int64_t workspace_bytes,
+                      cudaStream_t stream);
+
+/*
+ * fw_decay_step -- one token for B*H states, S updated in place.
+ *   q, k, v  in      [B][H][d] of `dtype`
+ *   S        in/out  float [B][H][d][d]
+ *   norm     in      as fw_decay_prefill
+ *   o        out     [B][H][d] of `dtype`
+ *   shape    T must be 1
+ */
+int fw_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *S,
+                  const fw_norm *norm, void *o, const fw_shape *shape, fw_dtype dtype,
+                  float scale, cudaStream_t stream);
+
+/* ---- layer norm --------------------------------------------------------------
+ *
+ * The norm after the mixer's output (blog, §5.1) over the last axis of
+ * x [rows][width], any width >= 1:
+ *     y = (x - m) r weight + bias,  m = mean(x),  r = 1 / sqrt(mean((x-m)^2) + eps),
+ *     dx = r (w dy - mean(w dy) - xh mean(w dy xh)),  xh = (x - m) r,
+ *     dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ * Statistics and sums in fp32, in an order that does not change between runs.
+ *   x, y, dy, dx  [rows][width] of `dtype`; y may equal x, dx may equal dy or x
+ *                 (other overlaps are refused)
+ *   weight, bias  float [width] or NULL (ones, zeros)
+ *   mean, rstd    float [rows]: out of the forward pass (NULL: not wanted), in
+ *                 to the backward pass
+ *   dweight, dbias  float [width] or NULL (not wanted)
+ *   workspace     of at least fw_layer_norm_workspace() bytes, the caller's; may
+ *                 be NULL when neither dweight nor dbias is wanted
+ */
+int fw_layer_norm(const void *x, const float *weight, const float *bias, void *y, float *mean,
+                  float *rstd, int64_t rows, int64_t width, fw_dtype dtype, float eps,
+                  cudaStream_t stream);
+int64_t fw_layer_norm_workspace(int64_t rows, int64_t width);
+int fw_layer_norm_backward(const void *dy, const void *x, const float *weight, const float *mean,
+                           const float *rstd, void *dx, float *dweight, float *dbias,
+                           int64_t rows, int64_t width, fw_dtype dtype, void *workspace,
+                           int64_t workspace_bytes, cudaStream_t stream);
 
 /* Synchronise `stream`, then read and clear the device error word.
  * Returns FW_OK, FW_ERR_TIMEOUT, or FW_ERR_CUDA. */

@@ -2,8 +2,10 @@
 // device error word.  See include/fw.h for the contract of every call.
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 
+#include "fw_decay.cuh"
 #include "fw_internal.cuh"
 
 namespace fw {
@@ -427,6 +429,249 @@ extern "C" int fw_window_step(const void *q, const void *k_prev, const void *v,
     return FW_OK;
 }
 
+namespace {
+
+// A buffer of a call: address and bytes (0 where it is not given).
+struct Span {
+    const void *p;
+    size_t n;
+};
+
+bool any_misaligned(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (misaligned(p)) return true;
+    return false;
+}
+
+// Does an output overlap an input or another output?
+bool outputs_clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span &i : ins)
+            if (overlaps(o->p, o->n, i.p, i.n)) return true;
+        for (const Span *q = o + 1; q != outs.end(); ++q)
+            if (overlaps(o->p, o->n, q->p, q->n)) return true;
+    }
+    return false;
+}
+
+// Shape and type of a decayed call.  The kernels index chunks of at least 64
+// tokens by a 32-bit grid.
+int check_decay(const fw_shape *shape, fw_dtype dtype) {
+    const int st = check_common(shape, dtype, FW_LINATTN, FW_PHI_IDENTITY, 0.f, 0u);
+    if (st != FW_OK) return st;
+    if (shape->T > (int64_t)INT32_MAX - 128) return FW_ERR_SHAPE;
+    if (shape->B * shape->H > (int64_t)INT32_MAX / ((shape->T + 63) / 64)) return FW_ERR_SHAPE;
+    return FW_OK;
+}
+
+int check_norm(const fw_norm *norm, NormArgs *out) {
+    *out = NormArgs{};
+    if (!norm) return FW_OK;
+    if (misaligned(norm->weight) || misaligned(norm->bias)) return FW_ERR_ALIGN;
+    if (!(std::isfinite(norm->eps) && norm->eps >= 0.f)) return FW_ERR_ARG;
+    out->on = 1;
+    out->weight = norm->weight;
+    out->bias = norm->bias;
+    out->eps = norm->eps;
+    return FW_OK;
+}
+
+ScanArgs scan_of(const fw_shape *shape, fw_dtype dtype, const float *log_decay,
+                 const int32_t *lens, int *err) {
+    ScanArgs s{};
+    s.log_decay = log_decay;
+    s.lens = lens;
+    s.n_chains = shape->B * shape->H;
+    s.T = shape->T;
+    s.H = (int)shape->H;
+    s.d = shape->d_k;
+    s.dtype = dtype;
+    s.in_scale = s.out_scale = 1.f;
+    s.err = err;
+    s.wait_ns = g_wait_us.load() * 1000LL;
+    return s;
+}
+
+}  // namespace
+
+extern "C" int64_t fw_decay_workspace(const fw_shape *shape, fw_dtype dtype, int backward) {
+    const int st = check_decay(shape, dtype);
+    if (st != FW_OK) return st;
+    const size_t one = scan_workspace(shape->B * shape->H, shape->T, shape->d_k, dtype);
+    return (int64_t)(backward ? 3 * one : one);
+}
+
+extern "C" int fw_decay_prefill(const void *q, const void *k, const void *v,
+                                const float *log_decay, const float *S0, const int32_t *lens,
+                                const fw_norm *norm, void *o, float *S_T, const fw_shape *shape,
+                                fw_dtype dtype, float scale, void *workspace,
+                                int64_t workspace_bytes, cudaStream_t stream) {
+    int st = check_decay(shape, dtype);
+    if (st != FW_OK) return st;
+    if (!q || !k || !v || !log_decay || !o || !S_T) return FW_ERR_NULL;
+    if (any_misaligned({q, k, v, log_decay, S0, lens, o, S_T, workspace})) return FW_ERR_ALIGN;
+    NormArgs na;
+    if ((st = check_norm(norm, &na)) != FW_OK) return st;
+    if (!std::isfinite(scale)) return FW_ERR_ARG;
+    const int64_t nc = shape->B * shape->H;
+    const int d = shape->d_k;
+    const size_t nx = (size_t)nc * shape->T * d * (dtype == FW_F32 ? 4 : 2);
+    const size_t ns = (size_t)nc * d * d * sizeof(float), nd = d * sizeof(float);
+    const int64_t need = fw_decay_workspace(shape, dtype, 0);
+    if (need > 0 && !workspace) return FW_ERR_NULL;
+    if (workspace_bytes < need) return FW_ERR_SCRATCH;
+    const Span ws{workspace, (size_t)need};
+    if (outputs_clash({{o, nx}, {S_T, ns}, ws},
+                      {{q, nx}, {k, nx}, {v, nx}, {log_decay, (size_t)shape->H * 4},
+                       {S0, S0 && S0 != S_T ? ns : 0}, {lens, lens ? (size_t)shape->B * 4 : 0},
+                       {na.weight, nd}, {na.bias, nd}}))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    ScanArgs s = scan_of(shape, dtype, log_decay, lens, err);
+    s.a = q; s.b = k; s.c = v; s.X0 = S0; s.X_out = S_T; s.out = o;
+    s.out_scale = scale;
+    s.norm = na;
+    s.ws = static_cast<float *>(workspace);
+    const cudaError_t e = launch_scans(&s, 1, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+extern "C" int fw_decay_backward(const void *q, const void *k, const void *v,
+                                 const float *log_decay, const float *S0, const int32_t *lens,
+                                 const void *d_o, const float *dS_T, void *dq, void *dk, void *dv,
+                                 float *dS0, const fw_shape *shape, fw_dtype dtype, float scale,
+                                 void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
+    int st = check_decay(shape, dtype);
+    if (st != FW_OK) return st;
+    if (!q || !k || !v || !log_decay || !d_o || !dq || !dk || !dv) return FW_ERR_NULL;
+    if (any_misaligned({q, k, v, log_decay, S0, lens, d_o, dS_T, dq, dk, dv, dS0, workspace}))
+        return FW_ERR_ALIGN;
+    if (!std::isfinite(scale)) return FW_ERR_ARG;
+    const int64_t nc = shape->B * shape->H;
+    const int d = shape->d_k;
+    const size_t nx = (size_t)nc * shape->T * d * (dtype == FW_F32 ? 4 : 2);
+    const size_t ns = (size_t)nc * d * d * sizeof(float);
+    const int64_t need = fw_decay_workspace(shape, dtype, 1);
+    if (need > 0 && !workspace) return FW_ERR_NULL;
+    if (workspace_bytes < need) return FW_ERR_SCRATCH;
+    const Span ws{workspace, (size_t)need};
+    if (outputs_clash({{dq, nx}, {dk, nx}, {dv, nx}, {dS0, dS0 ? ns : 0}, ws},
+                      {{q, nx}, {k, nx}, {v, nx}, {d_o, nx}, {log_decay, (size_t)shape->H * 4},
+                       {S0, S0 ? ns : 0}, {dS_T, dS_T ? ns : 0},
+                       {lens, lens ? (size_t)shape->B * 4 : 0}}))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    ScanArgs s[3];
+    for (int i = 0; i < 3; ++i) {
+        s[i] = scan_of(shape, dtype, log_decay, lens, err);
+        s[i].ws = static_cast<float *>(workspace) + i * (need / 3 / (int64_t)sizeof(float));
+        s[i].rev = i > 0;
+        s[i].x0_trans = i != 1;
+    }
+    s[0].a = d_o; s[0].b = v; s[0].c = k; s[0].X0 = S0; s[0].out = dq; s[0].out_scale = scale;
+    s[1].a = k; s[1].b = q; s[1].c = d_o; s[1].X0 = dS_T; s[1].out = dv; s[1].in_scale = scale;
+    s[1].X_out = dS0;
+    s[2].a = v; s[2].b = d_o; s[2].c = q; s[2].X0 = dS_T; s[2].out = dk; s[2].in_scale = scale;
+    const cudaError_t e = launch_scans(s, 3, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+extern "C" int fw_decay_step(const void *q, const void *k, const void *v, const float *log_decay,
+                             float *S, const fw_norm *norm, void *o, const fw_shape *shape,
+                             fw_dtype dtype, float scale, cudaStream_t stream) {
+    int st = check_decay(shape, dtype);
+    if (st != FW_OK) return st;
+    if (shape->T != 1) return FW_ERR_SHAPE;
+    if (!q || !k || !v || !log_decay || !S || !o) return FW_ERR_NULL;
+    if (any_misaligned({q, k, v, log_decay, S, o})) return FW_ERR_ALIGN;
+    DecayStepArgs a{};
+    if ((st = check_norm(norm, &a.norm)) != FW_OK) return st;
+    if (!std::isfinite(scale)) return FW_ERR_ARG;
+    const int64_t n = shape->B * shape->H;
+    const int d = shape->d_k;
+    const size_t nx = (size_t)n * d * (dtype == FW_F32 ? 4 : 2), nd = d * sizeof(float);
+    const size_t ns = (size_t)n * d * d * sizeof(float);
+    if (outputs_clash({{o, nx}, {S, ns}},
+                      {{q, nx}, {k, nx}, {v, nx}, {log_decay, (size_t)shape->H * 4},
+                       {a.norm.weight, nd}, {a.norm.bias, nd}}))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.S = S; a.o = o;
+    a.n_states = n; a.H = (int)shape->H; a.d = d; a.dtype = dtype; a.scale = scale;
+    const cudaError_t e = launch_decay_step(a, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+namespace {
+
+int check_rows(int64_t rows, int64_t width, fw_dtype dtype) {
+    if (rows < 1 || width < 1 || rows > (int64_t)INT32_MAX || width > (int64_t)1 << 24 ||
+        rows > INT64_MAX / 8 / width)
+        return FW_ERR_SHAPE;
+    if (dtype != FW_F32 && dtype != FW_BF16) return FW_ERR_DTYPE;
+    return FW_OK;
+}
+
+}  // namespace
+
+extern "C" int fw_layer_norm(const void *x, const float *weight, const float *bias, void *y,
+                             float *mean, float *rstd, int64_t rows, int64_t width,
+                             fw_dtype dtype, float eps, cudaStream_t stream) {
+    int st = check_rows(rows, width, dtype);
+    if (st != FW_OK) return st;
+    if (!x || !y) return FW_ERR_NULL;
+    if (any_misaligned({x, weight, bias, y, mean, rstd})) return FW_ERR_ALIGN;
+    if (!(std::isfinite(eps) && eps >= 0.f)) return FW_ERR_ARG;
+    const size_t nx = (size_t)rows * width * (dtype == FW_F32 ? 4 : 2);
+    const size_t nr = (size_t)rows * 4, nw = (size_t)width * 4;
+    if (outputs_clash({{y, nx}, {mean, nr}, {rstd, nr}}, {{weight, nw}, {bias, nw}}) ||
+        outputs_clash({{mean, nr}, {rstd, nr}}, {{x, nx}}) || (y != x && overlaps(y, nx, x, nx)))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    LayerNormArgs a{x, weight, bias, y, mean, rstd, rows, width, dtype, eps};
+    const cudaError_t e = launch_layer_norm(a, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+extern "C" int64_t fw_layer_norm_workspace(int64_t rows, int64_t width) {
+    const int st = check_rows(rows, width, FW_F32);
+    return st != FW_OK ? st : (int64_t)layer_norm_workspace(rows, width);
+}
+
+extern "C" int fw_layer_norm_backward(const void *dy, const void *x, const float *weight,
+                                      const float *mean, const float *rstd, void *dx,
+                                      float *dweight, float *dbias, int64_t rows, int64_t width,
+                                      fw_dtype dtype, void *workspace, int64_t workspace_bytes,
+                                      cudaStream_t stream) {
+    int st = check_rows(rows, width, dtype);
+    if (st != FW_OK) return st;
+    if (!dy || !x || !mean || !rstd || !dx) return FW_ERR_NULL;
+    if (any_misaligned({dy, x, weight, mean, rstd, dx, dweight, dbias, workspace}))
+        return FW_ERR_ALIGN;
+    const bool sums = dweight || dbias;
+    const size_t nx = (size_t)rows * width * (dtype == FW_F32 ? 4 : 2);
+    const size_t nr = (size_t)rows * 4, nw = (size_t)width * 4;
+    const int64_t need = sums ? (int64_t)layer_norm_workspace(rows, width) : 0;
+    if (sums && !workspace) return FW_ERR_NULL;
+    if (workspace_bytes < need) return FW_ERR_SCRATCH;
+    const Span ws{workspace, (size_t)need};
+    if (outputs_clash({{dx, nx}, {dweight, nw}, {dbias, nw}, ws},
+                      {{weight, nw}, {mean, nr}, {rstd, nr}, {dx != dy ? dy : nullptr, nx},
+                       {dx != x ? x : nullptr, nx}}) ||
+        outputs_clash({{dweight, nw}, {dbias, nw}, ws}, {{dy, nx}, {x, nx}}))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    LayerNormBwdArgs a{dy, x, weight, mean, rstd, dx, dweight, dbias, rows, width, dtype,
+                       sums ? static_cast<float *>(workspace) : nullptr};
+    const cudaError_t e = launch_layer_norm_backward(a, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
 extern "C" int fw_check(cudaStream_t stream) {
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -458,7 +703,7 @@ extern "C" const char *fw_status_string(int status) {
     case FW_ERR_UNSUPPORTED: return "FW_ERR_UNSUPPORTED: the chunked kernel does not take this call";
     case FW_ERR_ARG: return "FW_ERR_ARG: invalid eps or overlapping buffers";
     case FW_ERR_DEVICE: return "FW_ERR_DEVICE: the current device is not sm_103";
-    case FW_ERR_SCRATCH: return "FW_ERR_SCRATCH: the call needs more than FW_SCRATCH_BYTES of scratch";
+    case FW_ERR_SCRATCH: return "FW_ERR_SCRATCH: the call needs more workspace than it has";
     default: return "unknown status";
     }
 }

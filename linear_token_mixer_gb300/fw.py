@@ -7,6 +7,7 @@ every call raises.  torch supplies device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -47,8 +48,14 @@ class fw_window(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("n", ctypes.c_void_p)]
 
 
+class fw_norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
 EXPORTS = ("fw_prefill", "fw_prefill_ex", "fw_prefill_noalloc", "fw_step", "fw_step_ex", "fw_window_prefill",
-           "fw_window_step", "fw_check",
+           "fw_window_step", "fw_decay_workspace", "fw_decay_prefill", "fw_decay_backward",
+           "fw_decay_step", "fw_layer_norm", "fw_layer_norm_workspace", "fw_layer_norm_backward",
+           "fw_check",
            "fw_status_string", "fw_version", "fw_last_cuda_error", "fw_set_wait_limit_us",
            "fw_debug_force_timeout", "fw_debug_segment_split")
 
@@ -75,6 +82,15 @@ def lib():
         L.fw_window_prefill.argtypes = [P, P, P, P, P, P, P, WP, P, P, WP, SP, I, I, I, I, F, U,
                                         P]
         L.fw_window_step.argtypes = [P, P, P, P, P, P, WP, P, WP, SP, I, I, I, I, F, U, P]
+        N, I64 = ctypes.POINTER(fw_norm), ctypes.c_int64
+        L.fw_decay_workspace.argtypes = [SP, I, I]
+        L.fw_decay_prefill.argtypes = [P, P, P, P, P, P, N, P, P, SP, I, F, P, I64, P]
+        L.fw_decay_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, SP, I, F, P, I64, P]
+        L.fw_decay_step.argtypes = [P, P, P, P, P, N, P, SP, I, F, P]
+        L.fw_layer_norm.argtypes = [P, P, P, P, P, P, I64, I64, I, F, P]
+        L.fw_layer_norm_workspace.argtypes = [I64, I64]
+        L.fw_layer_norm_backward.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I, P, I64, P]
+        L.fw_decay_workspace.restype = L.fw_layer_norm_workspace.restype = I64
         L.fw_check.argtypes = [P]
         L.fw_status_string.argtypes = [I]
         L.fw_status_string.restype = ctypes.c_char_p
@@ -88,7 +104,8 @@ def lib():
         L.fw_debug_segment_split.restype = None
         for f in (L.fw_prefill, L.fw_prefill_ex, L.fw_prefill_noalloc, L.fw_step, L.fw_step_ex,
                   L.fw_window_prefill,
-                  L.fw_window_step, L.fw_check, L.fw_version, L.fw_last_cuda_error):
+                  L.fw_window_step, L.fw_decay_prefill, L.fw_decay_backward, L.fw_decay_step,
+                  L.fw_layer_norm, L.fw_layer_norm_backward, L.fw_check, L.fw_version, L.fw_last_cuda_error):
             f.restype = I
         _lib = L
     return _lib
@@ -115,7 +132,7 @@ def _flags(rbw, same_pair):
 
 def prefill(q, k, v, beta=None, lam=None, S0=None, *, mode="falcon1", phi="identity",
             eps=1e-6, k_init=None, algo="auto", o=None, S_T=None, stream=None, rbw=False,
-            same_pair=False, noalloc=False):
+            same_pair=False, noalloc=False, norm=None, norm_eps=1e-5):
     """Run the recurrence over q, k, v [B, H, T, d] (fp32 or bf16).
 
     mode: "falcon1", "falcon1a", "falcon2", "falcon2a" or "linattn"; rbw reads
@@ -124,36 +141,39 @@ def prefill(q, k, v, beta=None, lam=None, S0=None, *, mode="falcon1", phi="ident
     required in the falcon modes (beta [B,H,T,d] for falcon2 / falcon2a).  S0
     [B,H,d,d] fp32 or None.  noalloc: call fw_prefill_noalloc (the library's
     workspace from its static buffer; pass o and S_T to allocate nothing here
-    either)."""
+    either).  norm: (weight [d], bias [d]) fp32, either None: layer norm of every
+    row of o, in place."""
     B, H, T, d = q.shape
     if o is None:
         o = torch.empty_like(q)
     if S_T is None:
         S_T = torch.empty((B, H, d, d), device=q.device, dtype=torch.float32)
     shp = fw_shape(B, H, T, d, v.shape[-1])
+    _norm(norm, norm_eps, d, q)
     fn = lib().fw_prefill_noalloc if noalloc else lib().fw_prefill_ex
     st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(lam), _ptr(S0), _ptr(k_init), _ptr(o),
             _ptr(S_T), ctypes.byref(shp), DTYPES.get(q.dtype, -1), MODES[mode], PHIS[phi],
             float(eps), _flags(rbw, same_pair), ALGOS[algo], _stream(stream))
     if st != FW_OK:
         raise FwError(st, "fw_prefill_noalloc" if noalloc else "fw_prefill")
-    return o, S_T
+    return _with_norm(o, norm, norm_eps, stream), S_T
 
 
 def step(q, k_prev, v, beta, lam, S, *, mode="falcon1", phi="identity", eps=1e-6, o=None,
-         stream=None, rbw=False):
+         stream=None, rbw=False, norm=None, norm_eps=1e-5):
     """One decode step for q, k_prev, v [B, H, d]; S [B, H, d, d] fp32 is
-    updated in place (rbw: o = S_old^T q).  Returns o [B, H, d] in q's dtype."""
+    updated in place (rbw: o = S_old^T q); norm as in prefill.  Returns o [B, H, d] in q's dtype."""
     B, H, d = q.shape
     if o is None:
         o = torch.empty_like(q)
     shp = fw_shape(B, H, 1, d, v.shape[-1])
+    _norm(norm, norm_eps, d, q)
     st = lib().fw_step_ex(_ptr(q), _ptr(k_prev), _ptr(v), _ptr(beta), _ptr(lam), _ptr(S),
                           _ptr(o), ctypes.byref(shp), DTYPES.get(q.dtype, -1), MODES[mode],
                           PHIS[phi], float(eps), _flags(rbw, False), _stream(stream))
     if st != FW_OK:
         raise FwError(st, "fw_step")
-    return o
+    return _with_norm(o, norm, norm_eps, stream)
 
 
 def new_window(B, H, d, window, device="cuda"):
@@ -175,11 +195,12 @@ def _window(w):
 
 def window_prefill(q, k, v, beta, lam, window, S0=None, *, mode="falcon3", phi="identity",
                    eps=1e-6, k_init=None, win_in=None, win_out=None, o=None, S_T=None,
-                   stream=None, rbw=False, same_pair=False):
+                   stream=None, rbw=False, same_pair=False, norm=None, norm_eps=1e-5):
     """Falcon-3 ("falcon3") or 3A ("falcon3a") over q, k, v [B, H, T, d] with a
     window of `window` pairs.  win_in: the window carried from an earlier call
     (as returned here), or None; win_out: tensors to receive the window after
-    the last token (allocated when None).  Returns (o, S_T, win_out)."""
+    the last token (allocated when None); norm as in prefill.  Returns
+    (o, S_T, win_out)."""
     B, H, T, d = q.shape
     if o is None:
         o = torch.empty_like(q)
@@ -188,6 +209,7 @@ def window_prefill(q, k, v, beta, lam, window, S0=None, *, mode="falcon3", phi="
     if win_out is None:
         win_out = new_window(B, H, d, window, q.device)
     shp = fw_shape(B, H, T, d, v.shape[-1])
+    _norm(norm, norm_eps, d, q)
     st = lib().fw_window_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(lam), _ptr(S0),
                                  _ptr(k_init), _window(win_in), _ptr(o), _ptr(S_T),
                                  _window(win_out), ctypes.byref(shp), int(window),
@@ -195,27 +217,254 @@ def window_prefill(q, k, v, beta, lam, window, S0=None, *, mode="falcon3", phi="
                                  _flags(rbw, same_pair), _stream(stream))
     if st != FW_OK:
         raise FwError(st, "fw_window_prefill")
-    return o, S_T, win_out
+    return _with_norm(o, norm, norm_eps, stream), S_T, win_out
 
 
 def window_step(q, k_prev, v, beta, lam, S, window, win_in=None, win_out=None, *,
-                mode="falcon3", phi="identity", eps=1e-6, o=None, stream=None, rbw=False):
+                mode="falcon3", phi="identity", eps=1e-6, o=None, stream=None, rbw=False,
+                norm=None, norm_eps=1e-5):
     """One Falcon-3 / 3A decode step for q, k_prev, v [B, H, d]; S [B, H, d, d]
     fp32 is updated in place; the window moves from win_in (None: empty) to
-    win_out (allocated when None; must not be win_in).  Returns (o, win_out)."""
+    win_out (allocated when None; must not be win_in); norm as in prefill.  Returns
+    (o, win_out)."""
     B, H, d = q.shape
     if o is None:
         o = torch.empty_like(q)
     if win_out is None:
         win_out = new_window(B, H, d, window, q.device)
     shp = fw_shape(B, H, 1, d, v.shape[-1])
+    _norm(norm, norm_eps, d, q)
     st = lib().fw_window_step(_ptr(q), _ptr(k_prev), _ptr(v), _ptr(beta), _ptr(lam), _ptr(S),
                               _window(win_in), _ptr(o), _window(win_out), ctypes.byref(shp),
                               int(window), DTYPES.get(q.dtype, -1), MODES[mode], PHIS[phi],
                               float(eps), _flags(rbw, False), _stream(stream))
     if st != FW_OK:
         raise FwError(st, "fw_window_step")
-    return o, win_out
+    return _with_norm(o, norm, norm_eps, stream), win_out
+
+
+def _need(t, shape, dtype, name, like):
+    """Check a tensor argument (None passes) before its address is taken."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError("fw: %s must be %s of %s, not %s of %s" % (
+            name, tuple(shape), dtype, tuple(t.shape), t.dtype))
+    if t.device != like.device:
+        raise ValueError("fw: %s is on %s, the call's tensors are on %s" % (name, t.device,
+                                                                            like.device))
+
+
+class _On:
+    """The device and stream of a call.  New tensors come from that stream's
+    pool, so that a workspace freed at return is reused behind the kernels that
+    read it; outputs are also known to the caller's current stream."""
+
+    def __init__(self, t, stream):
+        if not t.is_cuda:
+            raise ValueError("fw: tensors must live on a CUDA device (no CPU path)")
+        self.device = t.device
+        self.current = torch.cuda.current_stream(t.device)
+        self.stream = stream if stream is not None else self.current
+        if self.stream.device != t.device:
+            raise ValueError("fw: the stream is on %s, the tensors are on %s" % (
+                self.stream.device, t.device))
+        self._ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self._dev = torch.cuda.device(self.device)
+        self._dev.__enter__()
+        self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        self._ctx.__exit__(*exc)
+        self._dev.__exit__(*exc)
+
+    def out(self, given, shape, dtype, name, like, zero=False):
+        if given is not None:
+            _need(given, shape, dtype, name, like)
+            return given
+        t = (torch.zeros if zero else torch.empty)(shape, device=self.device, dtype=dtype)
+        if self.stream != self.current:
+            t.record_stream(self.current)
+        return t
+
+    def workspace(self, given, need, where):
+        """(address, bytes) of a workspace, and what keeps it alive."""
+        if need < 0:
+            raise FwError(int(need), where)
+        if given is None:
+            given = torch.empty(need, device=self.device, dtype=torch.uint8) if need else None
+        elif given.device != self.device:
+            raise ValueError("fw: workspace is on %s, the tensors are on %s" % (given.device,
+                                                                              self.device))
+        return _ptr(given), given.numel() * given.element_size() if given is not None else 0, given
+
+    @property
+    def handle(self):
+        return self.stream.cuda_stream
+
+
+def _norm(norm, eps, width, like):
+    if norm is None:
+        return None
+    weight, bias = norm
+    _need(weight, (width,), torch.float32, "norm weight", like)
+    _need(bias, (width,), torch.float32, "norm bias", like)
+    if not 0.0 <= eps < float("inf"):
+        raise ValueError("fw: norm_eps must be finite and not negative")
+    return ctypes.byref(fw_norm(_ptr(weight), _ptr(bias), float(eps)))
+
+
+def _decay_args(q, k, v, log_decay, S, lens, lead):
+    shape, d = tuple(q.shape), q.shape[-1]
+    if len(shape) != lead + 1:
+        raise ValueError("fw: q must have %d axes, not %d" % (lead + 1, len(shape)))
+    B, H = shape[:2]
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, shape, q.dtype, name, q)
+    _need(log_decay, (H,), torch.float32, "log_decay", q)
+    _need(S, (B, H, d, d), torch.float32, "the state", q)
+    _need(lens, (B,), torch.int32, "lens", q)
+    return fw_shape(B, H, shape[2] if lead == 3 else 1, d, d)
+
+
+def decay_workspace(B, H, T, d, dtype=torch.bfloat16, *, backward=False):
+    """Bytes of workspace of decay_prefill (or decay_backward) for this shape."""
+    shp = fw_shape(B, H, T, d, d)
+    n = lib().fw_decay_workspace(ctypes.byref(shp), DTYPES.get(dtype, -1), int(backward))
+    if n < 0:
+        raise FwError(int(n), "fw_decay_workspace")
+    return n
+
+
+def decay_prefill(q, k, v, log_decay, S0=None, *, scale=1.0, lens=None, norm=None, norm_eps=1e-5,
+                  o=None, S_T=None, workspace=None, stream=None):
+    """Linear attention with a decay g_h = exp(log_decay[h]) for each head over
+    q, k, v [B, H, T, d] (fp32 or bf16): S_t = g_h S_{t-1} + k_t v_t^T,
+    o_t = scale S_t^T q_t.
+
+    log_decay [H] fp32; S0 [B, H, d, d] fp32 or None; lens [B] int32 or None
+    (tokens of each row of a padded batch; rows of o behind them are left as
+    they were, zero where o is allocated here); norm (weight [d], bias [d]) fp32,
+    either None: layer norm of every output row; workspace: a tensor of at least
+    decay_workspace() bytes (allocated when None).  Returns (o, S_T)."""
+    shp = _decay_args(q, k, v, log_decay, S0, lens, 3)
+    B, H, T, d = q.shape
+    with _On(q, stream) as on:
+        o = on.out(o, q.shape, q.dtype, "o", q, zero=lens is not None)
+        S_T = on.out(S_T, (B, H, d, d), torch.float32, "S_T", q)
+        dt = DTYPES.get(q.dtype, -1)
+        ws, nws, _keep = on.workspace(workspace, lib().fw_decay_workspace(ctypes.byref(shp), dt, 0),
+                                      "fw_decay_prefill")
+        st = lib().fw_decay_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0),
+                                    _ptr(lens), _norm(norm, norm_eps, d, q), _ptr(o), _ptr(S_T),
+                                    ctypes.byref(shp), dt, float(scale), ws, nws, on.handle)
+    if st != FW_OK:
+        raise FwError(st, "fw_decay_prefill")
+    return o, S_T
+
+
+def decay_backward(q, k, v, log_decay, do, S0=None, dS_T=None, *, scale=1.0, lens=None, dq=None,
+                   dk=None, dv=None, dS0=None, workspace=None, stream=None):
+    """Gradients of decay_prefill (without norm) given do [B, H, T, d], the
+    gradient of o, and dS_T [B, H, d, d] fp32 or None, that of S_T.  Returns
+    (dq, dk, dv, dS0) in q's dtype and fp32; dS0 is None unless S0 or dS0 is
+    given.  Rows behind lens are left as they were (zero where allocated here)."""
+    shp = _decay_args(q, k, v, log_decay, S0, lens, 3)
+    B, H, T, d = q.shape
+    _need(do, q.shape, q.dtype, "do", q)
+    _need(dS_T, (B, H, d, d), torch.float32, "dS_T", q)
+    with _On(q, stream) as on:
+        zero = lens is not None
+        dq = on.out(dq, q.shape, q.dtype, "dq", q, zero=zero)
+        dk = on.out(dk, q.shape, q.dtype, "dk", q, zero=zero)
+        dv = on.out(dv, q.shape, q.dtype, "dv", q, zero=zero)
+        if S0 is not None or dS0 is not None:
+            dS0 = on.out(dS0, (B, H, d, d), torch.float32, "dS0", q)
+        dt = DTYPES.get(q.dtype, -1)
+        ws, nws, _keep = on.workspace(workspace, lib().fw_decay_workspace(ctypes.byref(shp), dt, 1),
+                                      "fw_decay_backward")
+        st = lib().fw_decay_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0),
+                                     _ptr(lens), _ptr(do), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv),
+                                     _ptr(dS0), ctypes.byref(shp), dt, float(scale), ws, nws,
+                                     on.handle)
+    if st != FW_OK:
+        raise FwError(st, "fw_decay_backward")
+    return dq, dk, dv, dS0
+
+
+def decay_step(q, k, v, log_decay, S, *, scale=1.0, norm=None, norm_eps=1e-5, o=None, stream=None):
+    """One token of decay_prefill's recurrence for q, k, v [B, H, d]; S
+    [B, H, d, d] fp32 is updated in place.  Returns o [B, H, d] in q's dtype."""
+    if S is None:
+        raise ValueError("fw: decay_step needs the state S")
+    shp = _decay_args(q, k, v, log_decay, S, None, 2)
+    with _On(q, stream) as on:
+        o = on.out(o, q.shape, q.dtype, "o", q)
+        st = lib().fw_decay_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S),
+                                 _norm(norm, norm_eps, q.shape[-1], q), _ptr(o), ctypes.byref(shp),
+                                 DTYPES.get(q.dtype, -1), float(scale), on.handle)
+    if st != FW_OK:
+        raise FwError(st, "fw_decay_step")
+    return o
+
+
+def layer_norm(x, weight=None, bias=None, *, eps=1e-5, y=None, mean=None, rstd=None, stats=True,
+               stream=None):
+    """Layer norm over the last axis of x (fp32 or bf16, contiguous); weight,
+    bias [width] fp32 or None; y may be x.  Returns (y, mean, rstd), the
+    statistics fp32 of x's leading shape (None with stats=False)."""
+    if x.dim() < 1:
+        raise ValueError("fw: layer_norm needs at least one axis")
+    lead, width = tuple(x.shape[:-1]), x.shape[-1]
+    _need(weight, (width,), torch.float32, "weight", x)
+    _need(bias, (width,), torch.float32, "bias", x)
+    with _On(x, stream) as on:
+        y = on.out(y, x.shape, x.dtype, "y", x)
+        if stats:
+            mean = on.out(mean, lead, torch.float32, "mean", x)
+            rstd = on.out(rstd, lead, torch.float32, "rstd", x)
+        st = lib().fw_layer_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                 _ptr(mean) if stats else None, _ptr(rstd) if stats else None,
+                                 math.prod(lead), width, DTYPES.get(x.dtype, -1), float(eps),
+                                 on.handle)
+    if st != FW_OK:
+        raise FwError(st, "fw_layer_norm")
+    return (y, mean, rstd) if stats else (y, None, None)
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbias=None,
+                        workspace=None, stream=None):
+    """Gradients of layer_norm given dy (x's shape and dtype) and the forward
+    pass's mean and rstd; weight None: ones.  dx may be dy or x.  Returns
+    (dx, dweight, dbias), the last two fp32 [width]."""
+    lead, width = tuple(x.shape[:-1]), x.shape[-1]
+    _need(dy, x.shape, x.dtype, "dy", x)
+    _need(weight, (width,), torch.float32, "weight", x)
+    _need(mean, lead, torch.float32, "mean", x)
+    _need(rstd, lead, torch.float32, "rstd", x)
+    with _On(x, stream) as on:
+        dx = on.out(dx, x.shape, x.dtype, "dx", x)
+        dweight = on.out(dweight, (width,), torch.float32, "dweight", x)
+        dbias = on.out(dbias, (width,), torch.float32, "dbias", x)
+        ws, nws, _keep = on.workspace(workspace, lib().fw_layer_norm_workspace(mean.numel(), width),
+                                      "fw_layer_norm_backward")
+        st = lib().fw_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
+                                          _ptr(dx), _ptr(dweight), _ptr(dbias), mean.numel(), width,
+                                          DTYPES.get(x.dtype, -1), ws, nws, on.handle)
+    if st != FW_OK:
+        raise FwError(st, "fw_layer_norm_backward")
+    return dx, dweight, dbias
+
+
+def _with_norm(o, norm, norm_eps, stream):
+    """The output norm of the other paths: in place over the rows of o."""
+    if norm is not None:
+        weight, bias = norm
+        layer_norm(o, weight, bias, eps=norm_eps, y=o, stats=False, stream=stream)
+    return o
 
 
 def check(stream=None):
