@@ -489,6 +489,7 @@ ScanArgs scan_of(const fw_shape *shape, fw_dtype dtype, const float *log_decay,
     s.in_scale = s.out_scale = 1.f;
     s.err = err;
     s.wait_ns = g_wait_us.load() * 1000LL;
+    s.force_timeout = g_force_timeout.load();
     return s;
 }
 

@@ -43,6 +43,7 @@ struct ScanArgs {
     float *ws;                // workspace of this scan
     int *err;
     long long wait_ns;
+    int force_timeout;
 };
 
 struct DecayStepArgs {

@@ -8,7 +8,7 @@
 //
 // All sums in fp32.  A chunk of 64 keeps the 64 x 64 part a little cheaper than the d x d part
 // and gives B*H*T/64 blocks, which fills the GPU from a few thousand tokens on.
-#include "fw_decay.cuh"
+#include "fw_decay_tc.cuh"
 
 namespace fw {
 namespace {
@@ -297,17 +297,22 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
 }  // namespace
 
 size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype) {
-    (void)dtype;
+    if (dtype == FW_BF16) return scan_tc_workspace(n_chains, T, d);
     return (size_t)n_chains * (size_t)((T + C - 1) / C) * d * d * sizeof(float);
 }
 
+// bf16 rows run on the tensor cores, fp32 rows here.
 cudaError_t launch_scans(const ScanArgs *s, int n, cudaStream_t stream) {
+    if (s[0].dtype == FW_BF16) {
+        for (int i = 0; i < n; ++i) {
+            const cudaError_t e = launch_scan_tc(s[i], stream);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
     Scans all{};
     for (int i = 0; i < n; ++i) all.s[i] = s[i];
-    if (s[0].dtype == FW_F32)
-        return s[0].d == 64 ? launch<64, float>(all, n, stream) : launch<128, float>(all, n, stream);
-    return s[0].d == 64 ? launch<64, __nv_bfloat16>(all, n, stream)
-                        : launch<128, __nv_bfloat16>(all, n, stream);
+    return s[0].d == 64 ? launch<64, float>(all, n, stream) : launch<128, float>(all, n, stream);
 }
 
 }  // namespace fw
