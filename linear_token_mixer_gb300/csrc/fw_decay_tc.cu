@@ -15,15 +15,19 @@
 //   warp 0       TMA producer: tiles of B, A, C (128 x d, 128-byte swizzle), each released on
 //                its own
 //   warp 1       MMA issuer of G and P C
-//   warp 2       MMA issuer of A X and the state update
-//   warp 3       tensor-memory allocation
+//   warp 2       MMA issuer of the state update
+//   warp 3       MMA issuer of A X; tensor-memory allocation
 //   warps 4-7    P: tensor memory -> mask, decay, bf16 -> tensor memory (A operand of P C)
 //   warps 8-11   O: scales A X by its row's decay in place before P C accumulates on it, then
 //                [output norm,] rounds and stores the rows (one thread a row)
-//   warps 12-15  the three terms of (diag(w) B)^T, 32 tokens at a time, into tensor memory
-//                (thread = lane = row of X), double-buffered
-//   warps 16-19  X: tensor memory -> bf16 shared-memory copy for A X, and X * g^n back
-// Tensor memory: G (P over it) 128 columns, O 128, X 128, the split operand 2 x 48.
+//   warps 12-15  the three terms of (diag(w) B)^T, 32 tokens at a time, into tensor memory,
+//                double-buffered
+//   warps 16-23  X, in registers (fp32, half a row a thread): X <- g^n X + the chunk's update,
+//                and its bf16 shared-memory copy for A X
+// The update of a chunk is summed from zero in tensor memory and added to X by an fp32 FMA: the
+// MMAs round towards zero, and X would carry that bias from chunk to chunk.  It also takes the
+// MMAs of the update off the state's serial chain (update read -> copy -> A X).
+// Tensor memory: G (P over it) 128 columns, O 128, the update 128, the split operand 2 x 48.
 // Every wait is bounded; on expiry the kernel records an error, the other roles stop at their
 // next wait, copies and MMAs in flight are drained, tensor memory is freed and the kernel exits.
 #include <cudaTypedefs.h>
@@ -38,13 +42,17 @@ namespace {
 using namespace sm100;
 
 constexpr int C = 128;
-constexpr int NTHREADS = 640;
+constexpr int NTHREADS = 768;
 constexpr uint32_t KB = 1024;
 constexpr uint32_t HALF = 16 * KB;           // 128 rows x 128 bytes: 64 columns of a tile
 constexpr int kSMs = 152;                    // the grid's target (a workspace size needs no device)
 constexpr int kMinSegChunks = 4;
 
-constexpr uint32_t COL_G = 0, COL_O = 128, COL_X = 256, COL_K = 384, KBUF = 48;
+// Registers a thread: 80 for each of the six warpgroups at launch; P and O keep them, warps 0-3 and
+// the split-operand group hand theirs on to the two groups that hold X.
+constexpr int REGS = 80, REGS_W0 = 40, REGS_K = 72, REGS_X = 104;
+static_assert(REGS_W0 + 2 * REGS + REGS_K + 2 * REGS_X <= 6 * REGS, "registers of the launch");
+constexpr uint32_t COL_G = 0, COL_O = 128, COL_U = 256, COL_K = 384, KBUF = 48;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t kDrainNs = 2000000000ull;
 
@@ -54,14 +62,14 @@ template <int D, bool PRE> struct Lay {
     static constexpr int NST = (int)(192 * KB / (TILE * NT));    // 2 (3), d = 64: 4 (6)
     static constexpr uint32_t XB = NST * NT * TILE;              // bf16 copy of X
     static constexpr uint32_t TAB = XB + (uint32_t)D * D * 2;
-    static constexpr uint32_t T_PW = TAB, T_PR = T_PW + 132 * 4, T_KW = T_PR + 16 * 4,
+    static constexpr uint32_t T_PW = TAB, T_KW = T_PW + 132 * 4,
                               T_KT = T_KW + 128 * 4, BAR = T_KT + 128 * 4;
     // barriers
     static constexpr int FULL = 0, EMPTY = FULL + NST * NT, GDONE = EMPTY + NST * NT,
                          PRDY = GDONE + 1, QSDONE = PRDY + 1, OSC = QSDONE + 1, PVDONE = OSC + 1,
-                         OFREE = PVDONE + 1, XDONE = OFREE + 1, XBRDY = XDONE + 1,
-                         XSC = XBRDY + 1, KRDY = XSC + 1, KFREE = KRDY + 2, VZ = KFREE + 2,
-                         DRAIN0 = VZ + 1, DRAIN1 = DRAIN0 + 1, NEVER = DRAIN1 + 1,
+                         OFREE = PVDONE + 1, UDONE = OFREE + 1, XBRDY = UDONE + 1,
+                         UFREE = XBRDY + 1, KRDY = UFREE + 1, KFREE = KRDY + 2, VZ = KFREE + 2,
+                         DRAIN = VZ + 1, NEVER = DRAIN + 3,
                          NBAR = NEVER + 1;
     static constexpr uint32_t MISC = BAR + NBAR * 8;
     static constexpr uint32_t BYTES = MISC + 16;
@@ -69,7 +77,7 @@ template <int D, bool PRE> struct Lay {
     static_assert(ALLOC <= 227 * KB, "shared memory budget");
 };
 
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t limit,
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t limit,
                                        volatile int *abort_flag) {
     const uint64_t t0 = globaltimer();
     for (;;) {
@@ -83,6 +91,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t
                                          volatile int *abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
     return wait_slow(bar, parity, limit, abort_flag);
+}
+
+template <int N> __device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Segment `seg` of a chain: its chunks in processing order [first, last) of `total`.
@@ -117,10 +132,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 
 // 16 lanes x 16 columns: register 2c + h holds lane 8h + t / 4, column 4c + t % 4 of thread t.
@@ -130,28 +148,39 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  : "memory");
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(b0), "f"(b1));
+// Two fp32 operations in one instruction, on pairs.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-__device__ __forceinline__ void sub2(float &a0, float &a1, float b0, float b1) {   // a - b
-    asm("{\n\t.reg .b64 x, y, m;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-        "mov.b64 m, {%4, %4};\n\tfma.rn.f32x2 x, y, m, x;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(b0), "f"(b1), "f"(-1.f));
+__device__ __forceinline__ float2 halves(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void scale2(float &a0, float &a1, uint64_t b) {
+    const float2 f = halves(mul2(pair(a0, a1), b));
+    a0 = f.x;
+    a1 = f.y;
 }
 
-// The upper halves of two fp32 words (bf16, truncated), x0 in the low half.
-__device__ __forceinline__ uint32_t top_halves(float x0, float x1) {
-    return __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+// bf16 (truncated) of a pair, the first in the low half, and what the truncation drops (exact).
+__device__ __forceinline__ uint32_t top_halves(uint64_t x) {
+    return __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
 }
-// What that truncation drops of each (exact).
-__device__ __forceinline__ void below(float &x0, float &x1) {
-    sub2(x0, x1, __uint_as_float(__float_as_uint(x0) & 0xffff0000u),
-         __uint_as_float(__float_as_uint(x1) & 0xffff0000u));
+__device__ __forceinline__ uint64_t below(uint64_t x) {
+    return fma2(x & 0xffff0000ffff0000ull, pair(-1.f, -1.f), x);
 }
 
 // PRE: only the state of a segment, from zero (segment 0: from X0), into the workspace.
@@ -181,7 +210,6 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + L::MISC);
     volatile uint32_t *s_tmem = reinterpret_cast<volatile uint32_t *>(sm + L::MISC + 4);
     float *const pw = reinterpret_cast<float *>(sm + L::T_PW);   // g^n, n = 0..128
-    float *const pr = reinterpret_cast<float *>(sm + L::T_PR);   // g^(15-j) (reverse: g^j), j < 16
     float *const kw = reinterpret_cast<float *>(sm + L::T_KW);   // w_j of a full chunk
     float *const kt = reinterpret_cast<float *>(sm + L::T_KT);   // w_j of the tail chunk
     auto bar = [&](int i) -> uint32_t { return sb + L::BAR + 8u * (uint32_t)i; };
@@ -203,16 +231,16 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             if (e >= 0 && e < L::NST * L::NT)       // B: its readers' four warps (and G); C: the
                 c = e % L::NT == XB_ ? (PRE ? 4 : 5)   // update (and P C); A: the O group's warps
                   : e % L::NT == XC ? (PRE ? 1 : 2) : 4;
-            if (i == L::PRDY || i == L::OSC || i == L::OFREE || i == L::XBRDY || i == L::XSC ||
-                i == L::KRDY || i == L::KRDY + 1 || i == L::VZ)
+            if (i == L::PRDY || i == L::OSC || i == L::OFREE || i == L::KRDY || i == L::KRDY + 1 ||
+                i == L::VZ)
                 c = 4;
+            if (i == L::XBRDY || i == L::UFREE) c = 8;
             mbar_init(bar(i), c);
         }
         fence_mbar_init();
         *s_abort = 0;
     }
     for (int i = tid; i <= C; i += NTHREADS) pw[i] = decay_pow(lg, (float)i);
-    if (tid < 16) pr[tid] = decay_pow(lg, (float)(REV ? tid : 15 - tid));
     if (tid < C) kw[tid] = a.in_scale * decay_pow(lg, (float)(REV ? tid + 1 : C - 1 - tid));
     if (warp == 3) tmem_alloc(sb + L::MISC + 4, TMEM_COLS);
     tc_fence_before();
@@ -220,7 +248,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    if (warp == 0) {
+    if (warp < 4) {
+      reg_dec<REGS_W0>();
+      if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
         if (lane == 0) {
             bool ok = true;
@@ -229,7 +259,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             for (int i = 0; i < nch && ok; ++i) {
                 const int st = i % L::NST;
                 const int y = chunk_id(i) * C;
-#pragma unroll
+#pragma unroll 1
                 for (int x0 = 0; x0 < L::NT && ok; ++x0) {
                     const int x = PRE ? x0 : x0 == 0 ? XB_ : x0 == 1 ? XA : XC;
                     if (i >= L::NST) ok = wait_bar(empty(st, x), (uint32_t)(i / L::NST - 1) & 1u, limit, s_abort);
@@ -267,7 +297,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     constexpr uint32_t id = idesc_bf16(128, 128, false, false);
                     const uint64_t da = sdesc_sw128(tile(st, XA), 16, 1024);
                     const uint64_t db = sdesc_sw128(tile(st, XB_), 16, 1024);
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t off = ((kk >> 2) * HALF + (kk & 3) * 32u) >> 4;
                         mma_bf16(tmem + COL_G, da + off, db + off, id, kk > 0);
@@ -283,7 +313,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 {
                     constexpr uint32_t id = idesc_bf16(128, D, false, true);
                     const uint64_t dc = sdesc_sw128(tile(st, XC), HALF, 1024);
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < C / 16; ++kk)
                         mma_bf16_ta(tmem + COL_O, tmem + COL_G + 8 * kk, dc + kk * 128, id, 1);
                     mma_commit(bar(L::PVDONE));
@@ -292,35 +322,20 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
             if (!ok) fail_now();
             if (nch > 0) {
-                mma_commit(bar(L::DRAIN0));
-                mbar_wait(bar(L::DRAIN0), 0, kDrainNs);
+                mma_commit(bar(L::DRAIN));
+                mbar_wait(bar(L::DRAIN), 0, kDrainNs);
             }
         }
         __syncwarp();
     } else if (warp == 2) {
-        // ---------------------------------------------------------------- A X, state update
+        // ---------------------------------------------------------------- state update
         if (lane == 0) {
             bool ok = true;
-            for (int i = 0; i < nch; ++i) {
+            for (int i = 0; i < nch && ok; ++i) {
                 const int st = i % L::NST;
-                const uint32_t ph = (uint32_t)(i / L::NST) & 1u, pi = (uint32_t)i & 1u;
-                if (!PRE) {
-                    ok = wait_bar(full(st, XA), ph, limit, s_abort) &&
-                         wait_bar(bar(L::XBRDY), pi, limit, s_abort) &&
-                         (i == 0 || wait_bar(bar(L::OFREE), pi ^ 1u, limit, s_abort));
-                    if (!ok) break;
-                    tc_fence_after();
-                    constexpr uint32_t id = idesc_bf16(128, D, false, true);
-                    const uint64_t da = sdesc_sw128(tile(st, XA), 16, 1024);
-                    const uint64_t dx = sdesc_sw128(sb + L::XB, HALF, 1024);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        mma_bf16(tmem + COL_O, da + (((kk >> 2) * HALF + (kk & 3) * 32u) >> 4),
-                                 dx + kk * 128, id, kk > 0);
-                    mma_commit(bar(L::QSDONE));
-                }
-                ok = wait_bar(full(st, XC), ph, limit, s_abort) &&
-                     wait_bar(bar(L::XSC), pi, limit, s_abort);
+                ok = wait_bar(full(st, XC), (uint32_t)(i / L::NST) & 1u, limit, s_abort) &&
+                     (i == 0 || wait_bar(bar(L::UFREE), (uint32_t)(i - 1) & 1u, limit, s_abort));
+#pragma unroll 1
                 for (int u = 0; u < 4 && ok; ++u) {
                     const int b = u & 1;
                     ok = wait_bar(bar(L::KRDY + b), (uint32_t)(2 * i + (u >> 1)) & 1u, limit, s_abort);
@@ -328,68 +343,123 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     tc_fence_after();
                     constexpr uint32_t id = idesc_bf16(128, D, false, true);
                     const uint64_t dc = sdesc_sw128(tile(st, XC), HALF, 1024);
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                        for (int term = 0; term < 3; ++term)
-                            mma_bf16_ta(tmem + COL_X, tmem + COL_K + KBUF * b + 16 * term + 8 * kk,
-                                        dc + (2 * u + kk) * 128, id, 1);
+                        for (int term = 2; term >= 0; --term)   // the small terms first
+                            mma_bf16_ta(tmem + COL_U, tmem + COL_K + KBUF * b + 16 * term + 8 * kk,
+                                        dc + (2 * u + kk) * 128, id, u > 0 || kk > 0 || term < 2);
                     mma_commit(bar(L::KFREE + b));
                 }
                 if (!ok) break;
-                mma_commit(bar(L::XDONE));
+                mma_commit(bar(L::UDONE));
                 mma_commit(empty(st, XC));
             }
             if (!ok) fail_now();
             if (nch > 0) {
-                mma_commit(bar(L::DRAIN1));
-                mbar_wait(bar(L::DRAIN1), 0, kDrainNs);
+                mma_commit(bar(L::DRAIN + 1));
+                mbar_wait(bar(L::DRAIN + 1), 0, kDrainNs);
             }
         }
         __syncwarp();
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- A X
+        if (!PRE && lane == 0) {
+            bool ok = true;
+            for (int i = 0; i < nch; ++i) {
+                const int st = i % L::NST;
+                const uint32_t pi = (uint32_t)i & 1u;
+                ok = wait_bar(full(st, XA), (uint32_t)(i / L::NST) & 1u, limit, s_abort) &&
+                     wait_bar(bar(L::XBRDY), pi, limit, s_abort) &&
+                     (i == 0 || wait_bar(bar(L::OFREE), pi ^ 1u, limit, s_abort));
+                if (!ok) break;
+                tc_fence_after();
+                constexpr uint32_t id = idesc_bf16(128, D, false, true);
+                const uint64_t da = sdesc_sw128(tile(st, XA), 16, 1024);
+                const uint64_t dx = sdesc_sw128(sb + L::XB, HALF, 1024);
+#pragma unroll 1
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_bf16(tmem + COL_O, da + (((kk >> 2) * HALF + (kk & 3) * 32u) >> 4),
+                             dx + kk * 128, id, kk > 0);
+                mma_commit(bar(L::QSDONE));
+            }
+            if (!ok) fail_now();
+            if (nch > 0) {
+                mma_commit(bar(L::DRAIN + 2));
+                mbar_wait(bar(L::DRAIN + 2), 0, kDrainNs);
+            }
+        }
+        __syncwarp();
+      }
     } else if (warp >= 4 && warp < 8) {
         // ---------------------------------------------------------------- P
         if (!PRE) {
             const int w = warp & 3, row = w * 32 + lane;
             const uint32_t lb = (uint32_t)(w * 32) << 16;
+            // On the diagonal block, rows short of the far edge need g^-m, m <= 31: fine in fp32 (at
+            // most e^78, and g^lag itself far from underflow) unless the head forgets at once.
+            const bool mild = fabsf(lg) <= 2.5f;
+            const float f_diag = a.in_scale * (mild ? pw[REV ? 0 : lane] / pw[REV ? lane : 31] : 0.f);
+            // the blocks farthest from the diagonal first: distance of the row to their near edge
+            auto edge = [&](int b) -> float {        // b-th block from the sequence's far side
+                const int m = REV ? 32 * (3 - b) - row : row - 32 * b - 31;
+                return m >= 0 ? a.in_scale * pw[m] : 0.f;
+            };
+            const float f0 = edge(0), f1 = edge(1), f2 = edge(2);
+            const float gp[4] = {pw[1], pw[2], pw[3], pw[4]};
             bool ok = true;
             for (int i = 0; i < nch; ++i) {
-                const int nv = tokens(i);
                 ok = __all_sync(~0u, wait_bar(bar(L::GDONE), (uint32_t)i & 1u, limit, s_abort));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int jb = 0; jb < 8; ++jb) {     // 16 columns j
-                    float v[16];
-                    uint32_t pk[8];
-                    const int blk = jb >> 1;         // against this warp's 32 rows
-                    if (REV ? blk < w : blk > w) {
+                for (int jb = 0; jb < 4; ++jb) {     // 32 columns j against this warp's 32 rows
+                    float v[32];
+                    uint32_t pk[16];
+                    if (REV ? jb < w : jb > w) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) pk[e] = 0u;
+                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
                     } else {
-                        tmem_ld16(tmem + lb + COL_G + 16 * jb, v);
-                        if (blk == w) {              // the diagonal block: one power an element
-                            const int lag0 = REV ? 16 * jb - row : row - 16 * jb;
+                        tmem_ld32(tmem + lb + COL_G + 32 * jb, v);
+                        if (jb == w && !mild) {      // powers of the lag, one by one
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int lag = REV ? lag0 + e : lag0 - e;
-                                v[e] = lag >= 0 ? v[e] * (a.in_scale * pw[lag < 0 ? 0 : lag]) : 0.f;
+                            for (int e = 0; e < 32; ++e) {
+                                const int lag = REV ? e - lane : lane - e;
+                                v[e] *= a.in_scale * pw[lag < 0 ? 0 : lag];
                             }
-                        } else {                     // g^|i-j| = g^(to the block's edge) g^(in it)
-                            const float f = a.in_scale * pw[REV ? 16 * jb - row : row - 16 * jb - 15];
+                        } else {
+                            // g^|i-j| = g^(distance to the block's far edge) g^(distance in it): the
+                            // latter four columns at a time, from the edge.  On the diagonal the
+                            // former is a quotient, see `mild`.
+                            const float f = jb == w ? f_diag : jb == (REV ? 3 : 0) ? f0 : jb == (REV ? 2 : 1) ? f1 : f2;
+                            const uint64_t g4 = pair(gp[3], gp[3]);
+                            uint64_t ta = REV ? pair(f, f * gp[0]) : pair(f * gp[0], f);
+                            uint64_t tb = REV ? pair(f * gp[1], f * gp[2]) : pair(f * gp[2], f * gp[1]);
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                const float4 u = *reinterpret_cast<const float4 *>(pr + e);
-                                mul2(v[e], v[e + 1], f, f);
-                                mul2(v[e + 2], v[e + 3], f, f);
-                                mul2(v[e], v[e + 1], u.x, u.y);
-                                mul2(v[e + 2], v[e + 3], u.z, u.w);
+                            for (int z = 0; z < 32; z += 4) {
+                                const int e = REV ? z : 31 - z;       // g^z at column e
+                                if (REV) {
+                                    scale2(v[e], v[e + 1], ta);
+                                    scale2(v[e + 2], v[e + 3], tb);
+                                } else {
+                                    scale2(v[e - 1], v[e], ta);
+                                    scale2(v[e - 3], v[e - 2], tb);
+                                }
+                                ta = mul2(ta, g4);
+                                tb = mul2(tb, g4);
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                        if (jb == w) {               // the mask, on the packed pairs
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                if (REV) pk[e] = lane <= 2 * e ? pk[e] : lane == 2 * e + 1 ? pk[e] & 0xffff0000u : 0u;
+                                else pk[e] = lane > 2 * e ? pk[e] : lane == 2 * e ? pk[e] & 0xffffu : 0u;
+                            }
+                        }
                     }
-                    tmem_st8(tmem + lb + COL_G + 8 * jb, pk);   // over columns already read
+                    tmem_st16u(tmem + lb + COL_G + 16 * jb, pk);   // over columns already read
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -412,12 +482,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 tc_fence_after();
                 const float rd = pw[REV ? (row < nv ? nv - 1 - row : 0) : row + 1];
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float v[16];
-                    tmem_ld16(tmem + lb + COL_O + c, v);
+                for (int c = 0; c < D; c += 32) {
+                    float v[32];
+                    tmem_ld32(tmem + lb + COL_O + c, v);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) mul2(v[e], v[e + 1], rd, rd);
+                    for (int e = 0; e < 32; e += 2) scale2(v[e], v[e + 1], pair(rd, rd));
                     tmem_st16(tmem + lb + COL_O + c, v);
+                    tmem_st16(tmem + lb + COL_O + c + 16, v + 16);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -456,32 +527,36 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
                                      (chain * a.T + row0 + row) * D;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float v[16];
-                    tmem_ld16(tmem + lb + COL_O + c, v);
+                for (int c = 0; c < D; c += 32) {
+                    float v[32];
+                    tmem_ld32(tmem + lb + COL_O + c, v);
                     if (NORM) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = (v[e] - mean) * rstd;
+                        for (int e = 0; e < 32; ++e) v[e] = (v[e] - mean) * rstd;
                         if (a.norm.weight)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] *= __ldg(a.norm.weight + c + e);
+                            for (int e = 0; e < 32; ++e) v[e] *= __ldg(a.norm.weight + c + e);
                         if (a.norm.bias)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] += __ldg(a.norm.bias + c + e);
+                            for (int e = 0; e < 32; ++e) v[e] += __ldg(a.norm.bias + c + e);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) mul2(v[e], v[e + 1], rstd, rstd);
+                        for (int e = 0; e < 32; e += 2) scale2(v[e], v[e + 1], pair(rstd, rstd));
                     }
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 8) {
-                        const uint4 o4 = make_uint4(pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),
-                                                    pack_bf16(v[e + 4], v[e + 5]), pack_bf16(v[e + 6], v[e + 7]));
-                        if (whole)
-                            st_shared_v4(tile(st, XA) + (uint32_t)(c >> 6) * HALF +
-                                             sw128(row, ((uint32_t)(c + e) & 63u) >> 3),
-                                         o4.x, o4.y, o4.z, o4.w);
-                        else if (row < nv)
-                            *reinterpret_cast<uint4 *>(out + c + e) = o4;
+                    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                    if (whole) {
+                        const uint32_t to = tile(st, XA) + (uint32_t)(c >> 6) * HALF + (row >> 3) * 1024u + (row & 7) * 128u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            st_shared_v4(to + ((((uint32_t)(c & 32) >> 3) + e ^ (row & 7u)) << 4), pk[4 * e],
+                                         pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+                    } else if (row < nv) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4 *>(out + c + 8 * e) =
+                                make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                     }
                 }
                 tc_fence_before();
@@ -504,6 +579,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         }
     } else if (warp >= 12 && warp < 16) {
         // ---------------------------------------------------------------- (diag(w) B)^T
+        reg_dec<REGS_K>();
         const int w = warp & 3;
         const uint32_t lb = (uint32_t)(w * 32) << 16;
         const bool mine = w * 32 < D;
@@ -547,10 +623,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 tc_fence_after();
                 if (mine) {
                     // thread t: tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3
-                    float2 wv[4];
+                    uint64_t wv[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        wv[c] = *reinterpret_cast<const float2 *>(wt + 32 * u + 8 * c + 2 * (lane & 3));
+                        wv[c] = *reinterpret_cast<const uint64_t *>(wt + 32 * u + 8 * c + 2 * (lane & 3));
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {    // rows w * 32 + 16 h .. +15 of X
                         uint32_t hi[8], mid[8], lo[8];
@@ -563,14 +639,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
 #pragma unroll
                             for (int z = 0; z < 4; ++z) {
                                 const int c = 2 * t2 + (z >> 1), o = 2 * c + (z & 1);
-                                float x0 = __uint_as_float(k2[z] << 16);
-                                float x1 = __uint_as_float(k2[z] & 0xffff0000u);
-                                mul2(x0, x1, wv[c].x, wv[c].y);
-                                hi[o] = top_halves(x0, x1);
-                                below(x0, x1);
-                                mid[o] = top_halves(x0, x1);
-                                below(x0, x1);
-                                lo[o] = top_halves(x0, x1);
+                                uint64_t x = mul2(pair(__uint_as_float(k2[z] << 16),
+                                                       __uint_as_float(k2[z] & 0xffff0000u)), wv[c]);
+                                hi[o] = top_halves(x);
+                                x = below(x);
+                                mid[o] = top_halves(x);
+                                lo[o] = top_halves(below(x));
                             }
                         }
                         const uint32_t at = tmem + lb + ((uint32_t)(16 * h) << 16) + COL_K + KBUF * b;
@@ -592,111 +666,102 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         if (!ok && lane == 0) fail_now();
     } else if (warp >= 16) {
         // ---------------------------------------------------------------- X
-        const int w = warp & 3, d = w * 32 + lane;
+        reg_inc<REGS_X>();
+        constexpr int XC_ = D / 2;                   // columns of a thread
+        const int w = warp & 3, d = w * 32 + lane, c0 = ((warp >> 2) & 1) * XC_;
         const uint32_t lb = (uint32_t)(w * 32) << 16;
         const bool mine = w * 32 < D;
-        const float *X0 = a.X0 ? a.X0 + chain * D * D : nullptr;
-        // with S_T = S0 the last segment may finish before another starts: they read a copy
-        const bool copy = nseg > 1 && a.X0 && a.X_out == a.X0;
-        const float *src0 = !PRE && copy ? ws + (int64_t)(nseg - 1) * D * D : X0;
         bool ok = true;
-        // the state on entry, 16 columns at a time
-        auto entry = [&](int c, float *v) {
+        float x[XC_];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0.f;
-            if (seg == 0) {
-                if (src0) {
+        for (int e = 0; e < XC_; ++e) x[e] = 0.f;
+        if (mine) {                                  // the state on entry
+            // with S_T = S0 the last segment may finish before another starts: they read a copy
+            const bool copy = nseg > 1 && a.X0 && a.X_out == a.X0;
+            float *const x0_copy = ws + (int64_t)(nseg - 1) * D * D;
+            if (seg == 0 && a.X0) {
+                const float *src = !PRE && copy ? x0_copy : a.X0 + chain * D * D;
+                src += a.x0_trans ? c0 * D + d : d * D + c0;
+                const int step = a.x0_trans ? D : 1;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        v[e] = a.x0_trans ? src0[(int64_t)(c + e) * D + d] : src0[(int64_t)d * D + c + e];
+                for (int e = 0; e < XC_; ++e) {
+                    x[e] = src[e * step];
+                    if (e % 8 == 7) asm volatile("" ::: "memory");   // eight loads in flight
                 }
-            } else if (!PRE) {
-                for (int r = 0; r < seg; ++r) {
+                if (PRE && copy)
+#pragma unroll
+                    for (int e = 0; e < XC_; ++e) x0_copy[d * D + c0 + e] = x[e];
+            }
+            if (!PRE)
+                for (int r = 0; r < seg; ++r) {      // X <- g^n X + the state of segment r
                     const Seg q = seg_of(n, r, nseg);
                     if (q.first >= q.last && r > 0) continue;
-                    const float g = r == 0 ? 0.f : decay_pow(lg, (float)seg_tokens<REV>(n, q));
-                    const float *M = ws + (int64_t)r * D * D + d * D + c;
+                    const float g = decay_pow(lg, (float)seg_tokens<REV>(n, q));
+                    const float4 *M = reinterpret_cast<const float4 *>(ws + (int64_t)r * D * D + d * D + c0);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 m = *reinterpret_cast<const float4 *>(M + e);
-                        v[e] = r == 0 ? m.x : fmaf(g, v[e], m.x);
-                        v[e + 1] = r == 0 ? m.y : fmaf(g, v[e + 1], m.y);
-                        v[e + 2] = r == 0 ? m.z : fmaf(g, v[e + 2], m.z);
-                        v[e + 3] = r == 0 ? m.w : fmaf(g, v[e + 3], m.w);
+                    for (int e = 0; e < XC_; e += 4) {
+                        const float4 m = M[e / 4];
+                        x[e] = fmaf(g, x[e], m.x);
+                        x[e + 1] = fmaf(g, x[e + 1], m.y);
+                        x[e + 2] = fmaf(g, x[e + 2], m.z);
+                        x[e + 3] = fmaf(g, x[e + 3], m.w);
+                        if (e % 16 == 12) asm volatile("" ::: "memory");
                     }
                 }
+        }
+        auto put_copy = [&](int e0) {                // 16 columns in bf16, rows of X: B operand of A X
+#pragma unroll
+            for (int e = e0; e < e0 + 16; e += 8)
+                st_shared_v4(sb + L::XB + (uint32_t)((c0 + e) >> 6) * ((uint32_t)D * 128u) +
+                                 sw128(d, ((uint32_t)(c0 + e) & 63u) >> 3),
+                             pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]),
+                             pack_bf16(x[e + 4], x[e + 5]), pack_bf16(x[e + 6], x[e + 7]));
+        };
+        if (!PRE && nch > 0) {
+            if (mine) {
+#pragma unroll
+                for (int e = 0; e < XC_; e += 16) put_copy(e);
+                fence_proxy_async();
             }
-        };
-        float *dst = PRE ? ws + (int64_t)seg * D * D : final_seg ? a.X_out ? a.X_out + chain * D * D : nullptr : nullptr;
-        auto put_row = [&](float *base, int c, const float *v) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4 *>(base + (int64_t)d * D + c + e) =
-                    make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        };
-        auto put_copy = [&](int c, const float *v) {   // bf16, rows of X: B operand of A X
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-                st_shared_v4(sb + L::XB + (uint32_t)((c + e) >> 6) * ((uint32_t)D * 128u) +
-                                 sw128(d, ((uint32_t)(c + e) & 63u) >> 3),
-                             pack_bf16(v[e], v[e + 1]), pack_bf16(v[e + 2], v[e + 3]),
-                             pack_bf16(v[e + 4], v[e + 5]), pack_bf16(v[e + 6], v[e + 7]));
-        };
-        if (nch == 0) {                              // no tokens: the state passes through
-            if (mine)
-                for (int c = 0; c < D; c += 16) {
-                    float v[16];
-                    entry(c, v);
-                    if (dst) put_row(dst, c, v);
-                    if (PRE && copy) put_row(ws + (int64_t)(nseg - 1) * D * D, c, v);
-                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::XBRDY));
         }
         for (int i = 0; i < nch; ++i) {
             const float g = pw[tokens(i)];
-            if (i > 0) {
-                ok = __all_sync(~0u, wait_bar(bar(L::XDONE), (uint32_t)(i - 1) & 1u, limit, s_abort) &&
-                                         (PRE || wait_bar(bar(L::QSDONE), (uint32_t)(i - 1) & 1u, limit, s_abort)));
-                if (!ok) break;
-                tc_fence_after();
-            }
+            const bool more = !PRE && i + 1 < nch;
+            ok = __all_sync(~0u, wait_bar(bar(L::UDONE), (uint32_t)i & 1u, limit, s_abort) &&
+                                     (!more || wait_bar(bar(L::QSDONE), (uint32_t)i & 1u, limit, s_abort)));
+            if (!ok) break;
+            tc_fence_after();
             if (mine) {
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float v[16];
-                    if (i > 0) {
-                        tmem_ld16(tmem + lb + COL_X + c, v);
-                    } else {
-                        entry(c, v);
-                        if (PRE && copy) put_row(ws + (int64_t)(nseg - 1) * D * D, c, v);
-                    }
-                    if (!PRE) put_copy(c, v);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) mul2(v[e], v[e + 1], g, g);
-                    tmem_st16(tmem + lb + COL_X + c, v);
+                for (int e = 0; e < XC_; e += 16) {
+                    float u[16];
+                    tmem_ld16(tmem + lb + COL_U + c0 + e, u);
+#pragma unroll
+                    for (int z = 0; z < 16; z += 2) {
+                        const float2 r = halves(fma2(pair(g, g), pair(x[e + z], x[e + z + 1]), pair(u[z], u[z + 1])));
+                        x[e + z] = r.x;
+                        x[e + z + 1] = r.y;
+                    }
+                    if (more) put_copy(e);
                 }
-                tmem_st_wait();
                 tc_fence_before();
-                if (!PRE) fence_proxy_async();
+                if (more) fence_proxy_async();
             }
             __syncwarp();
             if (lane == 0) {
-                if (!PRE) mbar_arrive(bar(L::XBRDY));
-                mbar_arrive(bar(L::XSC));
+                mbar_arrive(bar(L::UFREE));
+                if (more) mbar_arrive(bar(L::XBRDY));
             }
         }
-        if (ok && nch > 0 && dst) {
-            ok = __all_sync(~0u, wait_bar(bar(L::XDONE), (uint32_t)(nch - 1) & 1u, limit, s_abort));
-            if (ok && mine) {
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float v[16];
-                    tmem_ld16(tmem + lb + COL_X + c, v);
-                    put_row(dst, c, v);
-                }
-                tc_fence_before();
-            }
-        }
+        float *dst = PRE ? ws + (int64_t)seg * D * D
+                         : final_seg && a.X_out ? a.X_out + chain * D * D : nullptr;
+        if (ok && mine && dst)
+#pragma unroll
+            for (int e = 0; e < XC_; e += 4)
+                *reinterpret_cast<float4 *>(dst + d * D + c0 + e) =
+                    make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         if (!ok && lane == 0) fail_now();
     }
 
