@@ -42,16 +42,16 @@ namespace {
 using namespace sm100;
 
 constexpr int C = 128;
-constexpr int NTHREADS = 768;
+constexpr int NTHREADS = 896;
 constexpr uint32_t KB = 1024;
 constexpr uint32_t HALF = 16 * KB;           // 128 rows x 128 bytes: 64 columns of a tile
 constexpr int kSMs = 152;                    // the grid's target (a workspace size needs no device)
 constexpr int kMinSegChunks = 4;
 
-// Registers a thread: 80 for each of the six warpgroups at launch; P and O keep them, warps 0-3 and
-// the split-operand group hand theirs on to the two groups that hold X.
-constexpr int REGS = 80, REGS_W0 = 40, REGS_K = 72, REGS_X = 104;
-static_assert(REGS_W0 + 2 * REGS + REGS_K + 2 * REGS_X <= 6 * REGS, "registers of the launch");
+// Registers a thread: 72 for each of the seven warpgroups at launch; O keeps them, the others hand
+// theirs on to the two groups that hold X.
+constexpr int REGS = 72, REGS_W0 = 40, REGS_P = 64, REGS_K = 64, REGS_X = 96;
+static_assert(REGS_W0 + 2 * REGS_P + REGS + REGS_K + 2 * REGS_X <= 7 * REGS, "registers of the launch");
 constexpr uint32_t COL_G = 0, COL_O = 128, COL_U = 256, COL_K = 384, KBUF = 48;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t kDrainNs = 2000000000ull;
@@ -231,10 +231,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             if (e >= 0 && e < L::NST * L::NT)       // B: its readers' four warps (and G); C: the
                 c = e % L::NT == XB_ ? (PRE ? 4 : 5)   // update (and P C); A: the O group's warps
                   : e % L::NT == XC ? (PRE ? 1 : 2) : 4;
-            if (i == L::PRDY || i == L::OSC || i == L::OFREE || i == L::KRDY || i == L::KRDY + 1 ||
+            if (i == L::OSC || i == L::OFREE || i == L::KRDY || i == L::KRDY + 1 ||
                 i == L::VZ)
                 c = 4;
-            if (i == L::XBRDY || i == L::UFREE) c = 8;
+            if (i == L::XBRDY || i == L::UFREE || i == L::PRDY) c = 8;
             mbar_init(bar(i), c);
         }
         fence_mbar_init();
@@ -315,7 +315,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     const uint64_t dc = sdesc_sw128(tile(st, XC), HALF, 1024);
 #pragma unroll 1
                     for (int kk = 0; kk < C / 16; ++kk)
-                        mma_bf16_ta(tmem + COL_O, tmem + COL_G + 8 * kk, dc + kk * 128, id, 1);
+                        mma_bf16_ta(tmem + COL_O, tmem + COL_G + 8 * kk + 32 * (kk >> 2), dc + kk * 128, id, 1);
                     mma_commit(bar(L::PVDONE));
                     mma_commit(empty(st, XC));
                 }
@@ -391,13 +391,15 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         }
         __syncwarp();
       }
-    } else if (warp >= 4 && warp < 8) {
+    } else if ((warp >= 4 && warp < 8) || warp >= 24) {
         // ---------------------------------------------------------------- P
+        reg_dec<REGS_P>();
         if (!PRE) {
             const int w = warp & 3, row = w * 32 + lane;
             const uint32_t lb = (uint32_t)(w * 32) << 16;
             // On the diagonal block, rows short of the far edge need g^-m, m <= 31: fine in fp32 (at
             // most e^78, and g^lag itself far from underflow) unless the head forgets at once.
+            const int jb0 = warp >= 24 ? 2 : 0;
             const bool mild = fabsf(lg) <= 2.5f;
             const float f_diag = a.in_scale * (mild ? pw[REV ? 0 : lane] / pw[REV ? lane : 31] : 0.f);
             // the blocks farthest from the diagonal first: distance of the row to their near edge
@@ -413,7 +415,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int jb = 0; jb < 4; ++jb) {     // 32 columns j against this warp's 32 rows
+                for (int jb = jb0; jb < jb0 + 2; ++jb) {   // 32 columns j against this warp's 32 rows
                     float v[32];
                     uint32_t pk[16];
                     if (REV ? jb < w : jb > w) {
@@ -459,7 +461,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                             }
                         }
                     }
-                    tmem_st16u(tmem + lb + COL_G + 16 * jb, pk);   // over columns already read
+                    tmem_st16u(tmem + lb + COL_G + 16 * (jb + jb0), pk);   // over columns this warp has read
                 }
                 tmem_st_wait();
                 tc_fence_before();
