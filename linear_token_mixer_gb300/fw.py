@@ -7,7 +7,7 @@ every call raises.  torch supplies device memory and streams.
 from __future__ import annotations
 
 import ctypes
-import math
+import functools
 import os
 
 import torch
@@ -243,97 +243,111 @@ def window_step(q, k_prev, v, beta, lam, S, window, win_in=None, win_out=None, *
     return _with_norm(o, norm, norm_eps, stream), win_out
 
 
-def _need(t, shape, dtype, name, like):
-    """Check a tensor argument (None passes) before its address is taken."""
-    if t is None:
-        return
+def _bad(t, shape, dtype, name, like):
     if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError("fw: %s must be %s of %s, not %s of %s" % (
+        return ValueError("fw: %s must be %s of %s, not %s of %s" % (
             name, tuple(shape), dtype, tuple(t.shape), t.dtype))
-    if t.device != like.device:
-        raise ValueError("fw: %s is on %s, the call's tensors are on %s" % (name, t.device,
+    if t.get_device() != like.get_device():
+        return ValueError("fw: %s is on %s, the call's tensors are on %s" % (name, t.device,
                                                                             like.device))
+    return ValueError("fw: tensors must be contiguous (%s is not)" % name)
+
+
+def _arg(t, shape, dtype, name, like):
+    """The address of a tensor argument (None: NULL) of the given shape and dtype on like's
+    device (_On refuses one that is not a GPU).  These calls serve single tokens, so the checks
+    cost as little as they can."""
+    if t is None:
+        return None
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != like.get_device()
+            or not t.is_contiguous()):
+        raise _bad(t, shape, dtype, name, like)
+    return t.data_ptr()
 
 
 class _On:
-    """The device and stream of a call.  New tensors come from that stream's
-    pool, so that a workspace freed at return is reused behind the kernels that
-    read it; outputs are also known to the caller's current stream."""
+    """The stream of a call and where its new tensors come from: that stream's pool, so that a
+    workspace freed at return is reused behind the kernels that read it; outputs are also known
+    to the caller's current stream.  A call on the current stream (stream None) allocates as
+    torch does."""
+    __slots__ = ("like", "index", "handle", "stream", "current")
 
-    def __init__(self, t, stream):
-        if not t.is_cuda:
+    def __init__(self, like, stream):
+        if not like.is_cuda:
             raise ValueError("fw: tensors must live on a CUDA device (no CPU path)")
-        self.device = t.device
-        self.current = torch.cuda.current_stream(t.device)
-        self.stream = stream if stream is not None else self.current
-        if self.stream.device != t.device:
-            raise ValueError("fw: the stream is on %s, the tensors are on %s" % (
-                self.stream.device, t.device))
-        self._ctx = torch.cuda.stream(self.stream)
+        self.like, self.index, self.stream = like, like.get_device(), None
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(self.index)
+            return
+        if stream.device != like.device:
+            raise ValueError("fw: the stream is on %s, the tensors are on %s" % (stream.device,
+                                                                              like.device))
+        self.handle = stream.cuda_stream
+        self.current = torch.cuda.current_stream(like.device)
+        if stream != self.current:
+            self.stream = stream
 
-    def __enter__(self):
-        self._dev = torch.cuda.device(self.device)
-        self._dev.__enter__()
-        self._ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        self._ctx.__exit__(*exc)
-        self._dev.__exit__(*exc)
-
-    def out(self, given, shape, dtype, name, like, zero=False):
-        if given is not None:
-            _need(given, shape, dtype, name, like)
-            return given
-        t = (torch.zeros if zero else torch.empty)(shape, device=self.device, dtype=dtype)
-        if self.stream != self.current:
-            t.record_stream(self.current)
+    def new(self, shape, dtype, zero=False):
+        make = torch.zeros if zero else torch.empty
+        if self.stream is None:
+            return make(shape, dtype=dtype, device=self.like.device)
+        with torch.cuda.stream(self.stream):
+            t = make(shape, dtype=dtype, device=self.like.device)
+        t.record_stream(self.current)
         return t
 
     def workspace(self, given, need, where):
-        """(address, bytes) of a workspace, and what keeps it alive."""
+        """(tensor to keep alive, address, bytes) of a workspace of `need` bytes."""
         if need < 0:
             raise FwError(int(need), where)
         if given is None:
-            given = torch.empty(need, device=self.device, dtype=torch.uint8) if need else None
-        elif given.device != self.device:
-            raise ValueError("fw: workspace is on %s, the tensors are on %s" % (given.device,
-                                                                              self.device))
-        return _ptr(given), given.numel() * given.element_size() if given is not None else 0, given
+            if need == 0:
+                return None, None, 0
+            given = self.new((need,), torch.uint8)
+        elif not given.is_cuda or given.get_device() != self.index or not given.is_contiguous():
+            raise ValueError("fw: the workspace must be contiguous and on %s" % self.like.device)
+        return given, given.data_ptr(), given.numel() * given.element_size()
 
-    @property
-    def handle(self):
-        return self.stream.cuda_stream
+    def call(self, fn, where, *args):
+        """fn(*args, stream) on the tensors' device."""
+        if torch._C._cuda_getDevice() == self.index:
+            st = fn(*args, self.handle)
+        else:
+            with torch.cuda.device(self.index):
+                st = fn(*args, self.handle)
+        if st != FW_OK:
+            raise FwError(st, where)
 
 
 def _norm(norm, eps, width, like):
     if norm is None:
         return None
     weight, bias = norm
-    _need(weight, (width,), torch.float32, "norm weight", like)
-    _need(bias, (width,), torch.float32, "norm bias", like)
     if not 0.0 <= eps < float("inf"):
         raise ValueError("fw: norm_eps must be finite and not negative")
-    return ctypes.byref(fw_norm(_ptr(weight), _ptr(bias), float(eps)))
+    return ctypes.byref(fw_norm(_arg(weight, (width,), torch.float32, "norm weight", like),
+                                _arg(bias, (width,), torch.float32, "norm bias", like), eps))
 
 
-def _decay_args(q, k, v, log_decay, S, lens, lead):
-    shape, d = tuple(q.shape), q.shape[-1]
-    if len(shape) != lead + 1:
-        raise ValueError("fw: q must have %d axes, not %d" % (lead + 1, len(shape)))
-    B, H = shape[:2]
-    for t, name in ((k, "k"), (v, "v")):
-        _need(t, shape, q.dtype, name, q)
-    _need(log_decay, (H,), torch.float32, "log_decay", q)
-    _need(S, (B, H, d, d), torch.float32, "the state", q)
-    _need(lens, (B,), torch.int32, "lens", q)
-    return fw_shape(B, H, shape[2] if lead == 3 else 1, d, d)
+@functools.lru_cache(maxsize=4096)
+def _decay_need(B, H, T, d, dtype, backward):
+    return lib().fw_decay_workspace(ctypes.byref(fw_shape(B, H, T, d, d)), dtype, backward)
+
+
+@functools.lru_cache(maxsize=4096)
+def _layer_norm_need(rows, width):
+    return lib().fw_layer_norm_workspace(rows, width)
+
+
+def _axes(q, n):
+    if q.dim() != n:
+        raise ValueError("fw: q must have %d axes, not %d" % (n, q.dim()))
+    return q.shape
 
 
 def decay_workspace(B, H, T, d, dtype=torch.bfloat16, *, backward=False):
     """Bytes of workspace of decay_prefill (or decay_backward) for this shape."""
-    shp = fw_shape(B, H, T, d, d)
-    n = lib().fw_decay_workspace(ctypes.byref(shp), DTYPES.get(dtype, -1), int(backward))
+    n = _decay_need(B, H, T, d, DTYPES.get(dtype, -1), int(backward))
     if n < 0:
         raise FwError(int(n), "fw_decay_workspace")
     return n
@@ -350,19 +364,21 @@ def decay_prefill(q, k, v, log_decay, S0=None, *, scale=1.0, lens=None, norm=Non
     they were, zero where o is allocated here); norm (weight [d], bias [d]) fp32,
     either None: layer norm of every output row; workspace: a tensor of at least
     decay_workspace() bytes (allocated when None).  Returns (o, S_T)."""
-    shp = _decay_args(q, k, v, log_decay, S0, lens, 3)
-    B, H, T, d = q.shape
-    with _On(q, stream) as on:
-        o = on.out(o, q.shape, q.dtype, "o", q, zero=lens is not None)
-        S_T = on.out(S_T, (B, H, d, d), torch.float32, "S_T", q)
-        dt = DTYPES.get(q.dtype, -1)
-        ws, nws, _keep = on.workspace(workspace, lib().fw_decay_workspace(ctypes.byref(shp), dt, 0),
-                                      "fw_decay_prefill")
-        st = lib().fw_decay_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0),
-                                    _ptr(lens), _norm(norm, norm_eps, d, q), _ptr(o), _ptr(S_T),
-                                    ctypes.byref(shp), dt, float(scale), ws, nws, on.handle)
-    if st != FW_OK:
-        raise FwError(st, "fw_decay_prefill")
+    shape = B, H, T, d = _axes(q, 4)
+    state, dt, f32 = (B, H, d, d), q.dtype, torch.float32
+    args = (_arg(q, shape, dt, "q", q), _arg(k, shape, dt, "k", q), _arg(v, shape, dt, "v", q),
+            _arg(log_decay, (H,), f32, "log_decay", q), _arg(S0, state, f32, "S0", q),
+            _arg(lens, (B,), torch.int32, "lens", q), _norm(norm, norm_eps, d, q))
+    on = _On(q, stream)
+    if o is None:
+        o = on.new(shape, dt, lens is not None)
+    if S_T is None:
+        S_T = on.new(state, f32)
+    code = DTYPES.get(dt, -1)
+    _keep, ws, nws = on.workspace(workspace, _decay_need(B, H, T, d, code, 0), "fw_decay_prefill")
+    on.call(lib().fw_decay_prefill, "fw_decay_prefill", *args, _arg(o, shape, dt, "o", q),
+            _arg(S_T, state, f32, "S_T", q), ctypes.byref(fw_shape(B, H, T, d, d)), code, scale, ws,
+            nws)
     return o, S_T
 
 
@@ -372,42 +388,43 @@ def decay_backward(q, k, v, log_decay, do, S0=None, dS_T=None, *, scale=1.0, len
     gradient of o, and dS_T [B, H, d, d] fp32 or None, that of S_T.  Returns
     (dq, dk, dv, dS0) in q's dtype and fp32; dS0 is None unless S0 or dS0 is
     given.  Rows behind lens are left as they were (zero where allocated here)."""
-    shp = _decay_args(q, k, v, log_decay, S0, lens, 3)
-    B, H, T, d = q.shape
-    _need(do, q.shape, q.dtype, "do", q)
-    _need(dS_T, (B, H, d, d), torch.float32, "dS_T", q)
-    with _On(q, stream) as on:
-        zero = lens is not None
-        dq = on.out(dq, q.shape, q.dtype, "dq", q, zero=zero)
-        dk = on.out(dk, q.shape, q.dtype, "dk", q, zero=zero)
-        dv = on.out(dv, q.shape, q.dtype, "dv", q, zero=zero)
-        if S0 is not None or dS0 is not None:
-            dS0 = on.out(dS0, (B, H, d, d), torch.float32, "dS0", q)
-        dt = DTYPES.get(q.dtype, -1)
-        ws, nws, _keep = on.workspace(workspace, lib().fw_decay_workspace(ctypes.byref(shp), dt, 1),
-                                      "fw_decay_backward")
-        st = lib().fw_decay_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S0),
-                                     _ptr(lens), _ptr(do), _ptr(dS_T), _ptr(dq), _ptr(dk), _ptr(dv),
-                                     _ptr(dS0), ctypes.byref(shp), dt, float(scale), ws, nws,
-                                     on.handle)
-    if st != FW_OK:
-        raise FwError(st, "fw_decay_backward")
+    shape = B, H, T, d = _axes(q, 4)
+    state, dt, f32 = (B, H, d, d), q.dtype, torch.float32
+    args = (_arg(q, shape, dt, "q", q), _arg(k, shape, dt, "k", q), _arg(v, shape, dt, "v", q),
+            _arg(log_decay, (H,), f32, "log_decay", q), _arg(S0, state, f32, "S0", q),
+            _arg(lens, (B,), torch.int32, "lens", q), _arg(do, shape, dt, "do", q),
+            _arg(dS_T, state, f32, "dS_T", q))
+    on, zero = _On(q, stream), lens is not None
+    if dq is None:
+        dq = on.new(shape, dt, zero)
+    if dk is None:
+        dk = on.new(shape, dt, zero)
+    if dv is None:
+        dv = on.new(shape, dt, zero)
+    if dS0 is None and S0 is not None:
+        dS0 = on.new(state, f32)
+    code = DTYPES.get(dt, -1)
+    _keep, ws, nws = on.workspace(workspace, _decay_need(B, H, T, d, code, 1), "fw_decay_backward")
+    on.call(lib().fw_decay_backward, "fw_decay_backward", *args, _arg(dq, shape, dt, "dq", q),
+            _arg(dk, shape, dt, "dk", q), _arg(dv, shape, dt, "dv", q),
+            _arg(dS0, state, f32, "dS0", q), ctypes.byref(fw_shape(B, H, T, d, d)), code, scale, ws,
+            nws)
     return dq, dk, dv, dS0
 
 
 def decay_step(q, k, v, log_decay, S, *, scale=1.0, norm=None, norm_eps=1e-5, o=None, stream=None):
     """One token of decay_prefill's recurrence for q, k, v [B, H, d]; S
     [B, H, d, d] fp32 is updated in place.  Returns o [B, H, d] in q's dtype."""
-    if S is None:
-        raise ValueError("fw: decay_step needs the state S")
-    shp = _decay_args(q, k, v, log_decay, S, None, 2)
-    with _On(q, stream) as on:
-        o = on.out(o, q.shape, q.dtype, "o", q)
-        st = lib().fw_decay_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(S),
-                                 _norm(norm, norm_eps, q.shape[-1], q), _ptr(o), ctypes.byref(shp),
-                                 DTYPES.get(q.dtype, -1), float(scale), on.handle)
-    if st != FW_OK:
-        raise FwError(st, "fw_decay_step")
+    shape = B, H, d = _axes(q, 3)
+    dt, f32 = q.dtype, torch.float32
+    args = (_arg(q, shape, dt, "q", q), _arg(k, shape, dt, "k", q), _arg(v, shape, dt, "v", q),
+            _arg(log_decay, (H,), f32, "log_decay", q), _arg(S, (B, H, d, d), f32, "S", q),
+            _norm(norm, norm_eps, d, q))
+    on = _On(q, stream)
+    if o is None:
+        o = on.new(shape, dt)
+    on.call(lib().fw_decay_step, "fw_decay_step", *args, _arg(o, shape, dt, "o", q),
+            ctypes.byref(fw_shape(B, H, 1, d, d)), DTYPES.get(dt, -1), scale)
     return o
 
 
@@ -418,21 +435,24 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, y=None, mean=None, rstd=N
     statistics fp32 of x's leading shape (None with stats=False)."""
     if x.dim() < 1:
         raise ValueError("fw: layer_norm needs at least one axis")
-    lead, width = tuple(x.shape[:-1]), x.shape[-1]
-    _need(weight, (width,), torch.float32, "weight", x)
-    _need(bias, (width,), torch.float32, "bias", x)
-    with _On(x, stream) as on:
-        y = on.out(y, x.shape, x.dtype, "y", x)
-        if stats:
-            mean = on.out(mean, lead, torch.float32, "mean", x)
-            rstd = on.out(rstd, lead, torch.float32, "rstd", x)
-        st = lib().fw_layer_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-                                 _ptr(mean) if stats else None, _ptr(rstd) if stats else None,
-                                 math.prod(lead), width, DTYPES.get(x.dtype, -1), float(eps),
-                                 on.handle)
-    if st != FW_OK:
-        raise FwError(st, "fw_layer_norm")
-    return (y, mean, rstd) if stats else (y, None, None)
+    shape, dt, f32 = x.shape, x.dtype, torch.float32
+    lead, width = shape[:-1], shape[-1]
+    args = (_arg(x, shape, dt, "x", x), _arg(weight, (width,), f32, "weight", x),
+            _arg(bias, (width,), f32, "bias", x))
+    on = _On(x, stream)
+    if y is None:
+        y = on.new(shape, dt)
+    if not stats:
+        mean = rstd = None
+    else:
+        if mean is None:
+            mean = on.new(lead, f32)
+        if rstd is None:
+            rstd = on.new(lead, f32)
+    on.call(lib().fw_layer_norm, "fw_layer_norm", *args, _arg(y, shape, dt, "y", x),
+            _arg(mean, lead, f32, "mean", x), _arg(rstd, lead, f32, "rstd", x), lead.numel(), width,
+            DTYPES.get(dt, -1), eps)
+    return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbias=None,
@@ -440,22 +460,25 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbi
     """Gradients of layer_norm given dy (x's shape and dtype) and the forward
     pass's mean and rstd; weight None: ones.  dx may be dy or x.  Returns
     (dx, dweight, dbias), the last two fp32 [width]."""
-    lead, width = tuple(x.shape[:-1]), x.shape[-1]
-    _need(dy, x.shape, x.dtype, "dy", x)
-    _need(weight, (width,), torch.float32, "weight", x)
-    _need(mean, lead, torch.float32, "mean", x)
-    _need(rstd, lead, torch.float32, "rstd", x)
-    with _On(x, stream) as on:
-        dx = on.out(dx, x.shape, x.dtype, "dx", x)
-        dweight = on.out(dweight, (width,), torch.float32, "dweight", x)
-        dbias = on.out(dbias, (width,), torch.float32, "dbias", x)
-        ws, nws, _keep = on.workspace(workspace, lib().fw_layer_norm_workspace(mean.numel(), width),
-                                      "fw_layer_norm_backward")
-        st = lib().fw_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
-                                          _ptr(dx), _ptr(dweight), _ptr(dbias), mean.numel(), width,
-                                          DTYPES.get(x.dtype, -1), ws, nws, on.handle)
-    if st != FW_OK:
-        raise FwError(st, "fw_layer_norm_backward")
+    if x.dim() < 1:
+        raise ValueError("fw: layer_norm needs at least one axis")
+    shape, dt, f32 = x.shape, x.dtype, torch.float32
+    lead, width = shape[:-1], shape[-1]
+    rows = lead.numel()
+    args = (_arg(dy, shape, dt, "dy", x), _arg(x, shape, dt, "x", x),
+            _arg(weight, (width,), f32, "weight", x), _arg(mean, lead, f32, "mean", x),
+            _arg(rstd, lead, f32, "rstd", x))
+    on = _On(x, stream)
+    if dx is None:
+        dx = on.new(shape, dt)
+    if dweight is None:
+        dweight = on.new((width,), f32)
+    if dbias is None:
+        dbias = on.new((width,), f32)
+    _keep, ws, nws = on.workspace(workspace, _layer_norm_need(rows, width), "fw_layer_norm_backward")
+    on.call(lib().fw_layer_norm_backward, "fw_layer_norm_backward", *args,
+            _arg(dx, shape, dt, "dx", x), _arg(dweight, (width,), f32, "dweight", x),
+            _arg(dbias, (width,), f32, "dbias", x), rows, width, DTYPES.get(dt, -1), ws, nws)
     return dx, dweight, dbias
 
 
