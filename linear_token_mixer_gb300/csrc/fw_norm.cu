@@ -4,15 +4,18 @@
 //     dw = sum_rows dy xh,   db = sum_rows dy
 //
 // Both passes are bound by their rows' bytes: each row is read once into registers (as loaded:
-// 16 bytes a thread and vector), the statistics are taken from there (the variance from centred
-// values, never as E[x^2] - E[x]^2) and the result is written.  A row is held by ROWT threads:
-// a part of a warp for short rows, a warp, or a block.  Widths that are no multiple of 16 bytes
-// take the same kernels with one element a load; rows that do not fit the registers of 1024
-// threads take the looping kernels, which read the row again for each pass.
+// 16 bytes a thread and vector, the next row's loads in flight while this one is worked on), the
+// statistics are taken from there and the result is written.  A row is held by ROWT threads: a
+// part of a warp for short rows, a warp, or a block; blocks stride over the rows and keep the
+// weights of their columns in registers.  Mean and variance come from one reduction: each thread
+// takes the mean and the centred sum of squares of its own values, and pairs are merged by the
+// parallel update of Chan, Golub and LeVeque (never E[x^2] - E[x]^2).  Widths that are no multiple
+// of 16 bytes take the same kernels with one element a load; rows that do not fit the registers of
+// 1024 threads take the looping kernels, which read the row again for each pass.
 //
-// The backward kernel's blocks stride over the rows and keep their columns' dw and db in
-// registers; every block writes one partial row and a second kernel adds the partial rows in a
-// fixed order, so the sums do not depend on the order in which blocks run.
+// The backward kernel keeps its columns' dw and db in registers too; every block writes one
+// partial row and a second kernel adds the partial rows in a fixed order, so the sums do not
+// depend on the order in which blocks run.
 #include "fw_decay.cuh"
 
 namespace fw {
@@ -26,23 +29,81 @@ template <typename T> struct Vec<T, 1> { T e[1]; };
 template <> struct alignas(16) Vec<float, 4> { float e[4]; };
 template <> struct alignas(16) Vec<__nv_bfloat16, 8> { __nv_bfloat16 e[8]; };
 
-// Sum over the ROWT threads of a row; `red` is used by the block form only.
-template <int ROWT>
-__device__ __forceinline__ float row_sum(float v, float *red) {
-    constexpr int W = ROWT < 32 ? ROWT : 32;
+// fp32 arithmetic on the VW elements of a vector, two in one instruction where there are two.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a0, a1)), "l"(pack2(b0, b1)), "l"(pack2(c0, c1)));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(r));
+}
+template <int N> struct Row {   // N values
+    float e[N];
+};
+// a b + c; a scalar stands for N equal values
+template <int N> __device__ __forceinline__ Row<N> fma_n(const Row<N> &a, const Row<N> &b, const Row<N> &c) {
+    Row<N> d;
+    if constexpr (N % 2 == 0) {
 #pragma unroll
-    for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    if constexpr (ROWT > 32) {
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = 0.f;
+        for (int i = 0; i < N; i += 2)
+            fma2(d.e[i], d.e[i + 1], a.e[i], a.e[i + 1], b.e[i], b.e[i + 1], c.e[i], c.e[i + 1]);
+    } else {
 #pragma unroll
-        for (int i = 0; i < ROWT / 32; ++i) v += red[i];
-        __syncthreads();
+        for (int i = 0; i < N; ++i) d.e[i] = fmaf(a.e[i], b.e[i], c.e[i]);
     }
+    return d;
+}
+template <int N> __device__ __forceinline__ Row<N> all(float x) {
+    Row<N> r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.e[i] = x;
+    return r;
+}
+template <int N> __device__ __forceinline__ float total(const Row<N> &a) {
+    float t = a.e[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) t += a.e[i];
+    return t;
+}
+template <typename T, int N> __device__ __forceinline__ Row<N> widen(const Vec<T, N> &v) {
+    Row<N> r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.e[i] = to_f32(v.e[i]);
+    return r;
+}
+template <typename T, int N> __device__ __forceinline__ Vec<T, N> narrow(const Row<N> &a) {
+    Vec<T, N> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.e[i] = from_f32<T>(a.e[i]);
+    return v;
+}
+template <> __device__ __forceinline__ Vec<__nv_bfloat16, 8> narrow(const Row<8> &a) {
+    Vec<__nv_bfloat16, 8> v;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+        reinterpret_cast<__nv_bfloat162 *>(v.e)[i / 2] = __floats2bfloat162_rn(a.e[i], a.e[i + 1]);
     return v;
 }
 
+// Sum over a block of 1024 threads (looping kernels).
+__device__ __forceinline__ float block_sum(float v, float *red) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += red[i];
+    __syncthreads();
+    return v;
+}
+
+// Sums of two values over the ROWT threads of a row.  The block form takes one barrier: `red`
+// (2 x 32 floats for each parity of the turn) is not written again before the next but one.
 template <int ROWT>
 __device__ __forceinline__ void row_sum2(float &u, float &v, float *red) {
     constexpr int W = ROWT < 32 ? ROWT : 32;
@@ -63,65 +124,126 @@ __device__ __forceinline__ void row_sum2(float &u, float &v, float *red) {
             u += red[i];
             v += red[32 + i];
         }
-        __syncthreads();
     }
+}
+
+// Count, mean and centred sum of squares of a set of values.
+struct Moments {
+    float n, m, s;
+};
+__device__ __forceinline__ Moments merge(const Moments &a, const Moments &b) {
+    const float n = a.n + b.n, r = n > 0.f ? __fdividef(b.n, n) : 0.f, d = b.m - a.m;
+    return {n, fmaf(d, r, a.m), fmaf(d * d, a.n * r, a.s + b.s)};
+}
+template <int ROWT> __device__ __forceinline__ Moments row_merge(Moments x, Moments *red) {
+    constexpr int W = ROWT < 32 ? ROWT : 32;
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) {
+        const Moments y{__shfl_xor_sync(~0u, x.n, o), __shfl_xor_sync(~0u, x.m, o),
+                        __shfl_xor_sync(~0u, x.s, o)};
+        // the same order on both sides, so that every thread has the same bits
+        x = threadIdx.x & o ? merge(y, x) : merge(x, y);
+    }
+    if constexpr (ROWT > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+        __syncthreads();
+        x = red[0];
+#pragma unroll
+        for (int i = 1; i < ROWT / 32; ++i) x = merge(x, red[i]);
+    }
+    return x;
 }
 
 template <int ROWT> constexpr int block_of() { return ROWT <= 32 ? kBlock : ROWT; }
 
-template <typename T, int VW, int ROWT, int VPT>
-__global__ void __launch_bounds__(block_of<ROWT>())
-ln_fwd(LayerNormArgs a) {
-    __shared__ float red[32];
-    constexpr int RPB = block_of<ROWT>() / ROWT;
-    using V = Vec<T, VW>;
-    const int lane = threadIdx.x % ROWT;
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / ROWT;
-    const bool on = row < a.rows;
-    const int W = (int)a.width, nv = W / VW;
-    const V *x = reinterpret_cast<const V *>(static_cast<const T *>(a.x) + row * a.width);
-    V xv[VPT];
-    float sum = 0.f;
+// VW floats of weight or bias from column c on (c a multiple of VW).
+template <int VW, bool GIVEN> __device__ __forceinline__ Row<VW> load_w(const float *p, int c, float none) {
+    Row<VW> w;
+    if constexpr (VW >= 4) {
 #pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-        const int i = p * ROWT + lane;
-        if (on && i < nv) xv[p] = x[i];
-        else
-#pragma unroll
-            for (int e = 0; e < VW; ++e) xv[p].e[e] = from_f32<T>(0.f);
-#pragma unroll
-        for (int e = 0; e < VW; ++e) sum += to_f32(xv[p].e[e]);
-    }
-    const float mean = row_sum<ROWT>(sum, red) / W;
-    float var = 0.f;
-#pragma unroll
-    for (int p = 0; p < VPT; ++p)
-        if (p * ROWT + lane < nv)
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const float d = to_f32(xv[p].e[e]) - mean;
-                var = fmaf(d, d, var);
-            }
-    const float rstd = rsqrtf(row_sum<ROWT>(var, red) / W + a.eps);
-    if (!on) return;
-    V *y = reinterpret_cast<V *>(static_cast<T *>(a.y) + row * a.width);
-#pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-        const int i = p * ROWT + lane;
-        if (i >= nv) continue;
-        V yv;
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-            float f = (to_f32(xv[p].e[e]) - mean) * rstd;
-            if (a.weight) f *= a.weight[i * VW + e];
-            if (a.bias) f += a.bias[i * VW + e];
-            yv.e[e] = from_f32<T>(f);
+        for (int e = 0; e < VW; e += 4) {
+            const float4 f = GIVEN || p ? *reinterpret_cast<const float4 *>(p + c + e) : make_float4(none, none, none, none);
+            w.e[e] = f.x; w.e[e + 1] = f.y; w.e[e + 2] = f.z; w.e[e + 3] = f.w;
         }
-        y[i] = yv;
+    } else {
+        w.e[0] = GIVEN || p ? p[c] : none;
     }
-    if (lane == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
+    return w;
+}
+
+// FAST: every thread holds VPT whole vectors, and weight and bias are given (the checks for the
+// other cases are as many instructions as the work).
+template <typename T, int VW, int ROWT, int VPT, bool FAST>
+__global__ void __launch_bounds__(block_of<ROWT>(), FAST && ROWT <= 512 ? 512 / block_of<ROWT>() : 1)
+ln_fwd(LayerNormArgs a) {
+    __shared__ Moments red[2][32];
+    constexpr int RPB = block_of<ROWT>() / ROWT;
+    constexpr bool KEEP = VPT * VW <= 16;  // weights in registers, or from L1 for every row
+    using V = Vec<T, VW>;
+    const int lane = threadIdx.x % ROWT, sub = threadIdx.x / ROWT;
+    const int nv = (int)a.width / VW;
+    Row<VW> w[KEEP ? VPT : 1], b[KEEP ? VPT : 1];
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int p = 0; p < VPT; ++p)
+            if ((FAST || p * ROWT + lane < nv)) {
+                w[p] = load_w<VW, FAST>(a.weight, (p * ROWT + lane) * VW, 1.f);
+                b[p] = load_w<VW, FAST>(a.bias, (p * ROWT + lane) * VW, 0.f);
+            }
+    }
+    V xv[VPT], nx[VPT];
+    auto load = [&](V (&to)[VPT], int64_t row) {
+        const V *x = reinterpret_cast<const V *>(static_cast<const T *>(a.x) + row * a.width);
+#pragma unroll
+        for (int p = 0; p < VPT; ++p)
+            if (row < a.rows && (FAST || p * ROWT + lane < nv)) to[p] = x[p * ROWT + lane];
+    };
+    const int64_t stride = (int64_t)gridDim.x * RPB;
+    int turn = 0;
+    load(nx, (int64_t)blockIdx.x * RPB + sub);
+    // every thread of the block makes the same number of turns (the merge synchronises)
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += stride, turn ^= 1) {
+        const int64_t row = r0 + sub;
+        const bool on = row < a.rows;
+#pragma unroll
+        for (int p = 0; p < VPT; ++p) xv[p] = nx[p];
+        load(nx, row + stride);
+        Moments mo{0.f, 0.f, 0.f};
+        Row<VW> acc = all<VW>(0.f);
+#pragma unroll
+        for (int p = 0; p < VPT; ++p)
+            if (on && (FAST || p * ROWT + lane < nv)) {
+                mo.n += (float)VW;
+                acc = fma_n(widen(xv[p]), all<VW>(1.f), acc);
+            }
+        mo.m = mo.n > 0.f ? total(acc) / mo.n : 0.f;
+        acc = all<VW>(0.f);
+#pragma unroll
+        for (int p = 0; p < VPT; ++p)
+            if (on && (FAST || p * ROWT + lane < nv)) {
+                const Row<VW> d = fma_n(widen(xv[p]), all<VW>(1.f), all<VW>(-mo.m));
+                acc = fma_n(d, d, acc);
+            }
+        mo.s = total(acc);
+        mo = row_merge<ROWT>(mo, red[turn]);
+        if (!on) continue;
+        const float mean = mo.m, rstd = rsqrtf(mo.s / (float)a.width + a.eps);
+        V *y = reinterpret_cast<V *>(static_cast<T *>(a.y) + row * a.width);
+#pragma unroll
+        for (int p = 0; p < VPT; ++p) {
+            const int i = p * ROWT + lane;
+            if (!FAST && i >= nv) continue;
+            if constexpr (!KEEP) {
+                w[0] = load_w<VW, FAST>(a.weight, i * VW, 1.f);
+                b[0] = load_w<VW, FAST>(a.bias, i * VW, 0.f);
+            }
+            const Row<VW> d = fma_n(widen(xv[p]), all<VW>(1.f), all<VW>(-mean));
+            y[i] = narrow<T>(fma_n(fma_n(d, all<VW>(rstd), all<VW>(0.f)), w[KEEP ? p : 0], b[KEEP ? p : 0]));
+        }
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
     }
 }
 
@@ -135,13 +257,13 @@ ln_fwd_long(LayerNormArgs a) {
     T *y = static_cast<T *>(a.y) + row * a.width;
     float sum = 0.f;
     for (int64_t i = threadIdx.x; i < a.width; i += 1024) sum += to_f32(x[i]);
-    const float mean = row_sum<1024>(sum, red) / (float)a.width;
+    const float mean = block_sum(sum, red) / (float)a.width;
     float var = 0.f;
     for (int64_t i = threadIdx.x; i < a.width; i += 1024) {
         const float d = to_f32(x[i]) - mean;
         var = fmaf(d, d, var);
     }
-    const float rstd = rsqrtf(row_sum<1024>(var, red) / (float)a.width + a.eps);
+    const float rstd = rsqrtf(block_sum(var, red) / (float)a.width + a.eps);
     for (int64_t i = threadIdx.x; i < a.width; i += 1024) {
         float f = (to_f32(x[i]) - mean) * rstd;
         if (a.weight) f *= a.weight[i];
@@ -154,70 +276,72 @@ ln_fwd_long(LayerNormArgs a) {
     }
 }
 
-template <typename T, int VW, int ROWT, int VPT>
-__global__ void __launch_bounds__(block_of<ROWT>())
+template <typename T, int VW, int ROWT, int VPT, bool FAST>
+__global__ void __launch_bounds__(block_of<ROWT>(), FAST && ROWT <= 512 ? 512 / block_of<ROWT>() : 1)
 ln_bwd(LayerNormBwdArgs a) {
-    __shared__ float red[64];
+    __shared__ float red[2][64];
     extern __shared__ float sacc[];        // part-of-a-warp forms: [RPB][2][width]
     constexpr int RPB = block_of<ROWT>() / ROWT;
     using V = Vec<T, VW>;
     const int lane = threadIdx.x % ROWT, sub = threadIdx.x / ROWT;
     const int W = (int)a.width, nv = W / VW;
     const bool sums = a.ws != nullptr;
-    float w[VPT][VW], dw[VPT][VW], db[VPT][VW];
+    Row<VW> w[VPT], dw[VPT], db[VPT];
 #pragma unroll
-    for (int p = 0; p < VPT; ++p)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-            const int c = (p * ROWT + lane) * VW + e;
-            w[p][e] = a.weight && c < W ? a.weight[c] : 1.f;
-            dw[p][e] = db[p][e] = 0.f;
-        }
-    const int64_t stride = (int64_t)gridDim.x * RPB;
-    // every thread of the block makes the same number of turns (the row sums synchronise)
-    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += stride) {
-        const int64_t row = r0 + sub;
-        const bool on = row < a.rows;
+    for (int p = 0; p < VPT; ++p) {
+        w[p] = dw[p] = db[p] = all<VW>(0.f);
+        if ((FAST || p * ROWT + lane < nv)) w[p] = load_w<VW, FAST>(a.weight, (p * ROWT + lane) * VW, 1.f);
+    }
+    V nx[VPT], ng[VPT];
+    float nmean = 0.f, nrstd = 0.f;
+    auto load = [&](int64_t row) {
+        if (row >= a.rows) return;
         const V *x = reinterpret_cast<const V *>(static_cast<const T *>(a.x) + row * a.width);
         const V *dy = reinterpret_cast<const V *>(static_cast<const T *>(a.dy) + row * a.width);
-        V xv[VPT], gv[VPT];
-#pragma unroll
-        for (int p = 0; p < VPT; ++p) {
-            const int i = p * ROWT + lane;
-            if (on && i < nv) {
-                xv[p] = x[i];
-                gv[p] = dy[i];
-            }
-        }
-        const float mean = on ? a.mean[row] : 0.f, rstd = on ? a.rstd[row] : 0.f;
-        float c1 = 0.f, c2 = 0.f;
 #pragma unroll
         for (int p = 0; p < VPT; ++p)
-            if (on && p * ROWT + lane < nv)
+            if ((FAST || p * ROWT + lane < nv)) {
+                nx[p] = x[p * ROWT + lane];
+                ng[p] = dy[p * ROWT + lane];
+            }
+        nmean = a.mean[row];
+        nrstd = a.rstd[row];
+    };
+    const int64_t stride = (int64_t)gridDim.x * RPB;
+    int turn = 0;
+    load((int64_t)blockIdx.x * RPB + sub);
+    // every thread of the block makes the same number of turns (the row sums synchronise)
+    for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += stride, turn ^= 1) {
+        const int64_t row = r0 + sub;
+        const bool on = row < a.rows;
+        const float mean = nmean, rstd = nrstd;
+        Row<VW> xh[VPT], gw[VPT];
+        Row<VW> s1 = all<VW>(0.f), s2 = all<VW>(0.f);
 #pragma unroll
-                for (int e = 0; e < VW; ++e) {
-                    const float g = to_f32(gv[p].e[e]);
-                    const float xh = (to_f32(xv[p].e[e]) - mean) * rstd;
-                    dw[p][e] = fmaf(g, xh, dw[p][e]);
-                    db[p][e] += g;
-                    c1 = fmaf(g, w[p][e], c1);
-                    c2 = fmaf(g * w[p][e], xh, c2);
-                }
-        row_sum2<ROWT>(c1, c2, red);
+        for (int p = 0; p < VPT; ++p)
+            if (on && (FAST || p * ROWT + lane < nv)) {
+                const Row<VW> g = widen(ng[p]);
+                const Row<VW> d = fma_n(widen(nx[p]), all<VW>(1.f), all<VW>(-mean));
+                xh[p] = fma_n(d, all<VW>(rstd), all<VW>(0.f));
+                gw[p] = fma_n(g, w[p], all<VW>(0.f));
+                dw[p] = fma_n(g, xh[p], dw[p]);
+                db[p] = fma_n(g, all<VW>(1.f), db[p]);
+                s1 = fma_n(gw[p], all<VW>(1.f), s1);
+                s2 = fma_n(gw[p], xh[p], s2);
+            }
+        load(row + stride);
+        float c1 = total(s1), c2 = total(s2);
+        row_sum2<ROWT>(c1, c2, red[turn]);
         c1 /= W;
         c2 /= W;
+        if (!on) continue;
         V *dx = reinterpret_cast<V *>(static_cast<T *>(a.dx) + row * a.width);
 #pragma unroll
         for (int p = 0; p < VPT; ++p) {
             const int i = p * ROWT + lane;
-            if (!on || i >= nv) continue;
-            V o;
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const float xh = (to_f32(xv[p].e[e]) - mean) * rstd;
-                o.e[e] = from_f32<T>(rstd * (to_f32(gv[p].e[e]) * w[p][e] - c1 - xh * c2));
-            }
-            dx[i] = o;
+            if (!FAST && i >= nv) continue;
+            const Row<VW> t = fma_n(xh[p], all<VW>(-c2), fma_n(gw[p], all<VW>(1.f), all<VW>(-c1)));
+            dx[i] = narrow<T>(fma_n(t, all<VW>(rstd), all<VW>(0.f)));
         }
     }
     if (!sums) return;
@@ -228,9 +352,9 @@ ln_bwd(LayerNormBwdArgs a) {
 #pragma unroll
             for (int e = 0; e < VW; ++e) {
                 const int c = (p * ROWT + lane) * VW + e;
-                if (c < W) {
-                    part[c] = dw[p][e];
-                    part[W + c] = db[p][e];
+                if (FAST || c < W) {
+                    part[c] = dw[p].e[e];
+                    part[W + c] = db[p].e[e];
                 }
             }
     } else {
@@ -239,9 +363,9 @@ ln_bwd(LayerNormBwdArgs a) {
 #pragma unroll
             for (int e = 0; e < VW; ++e) {
                 const int c = (p * ROWT + lane) * VW + e;
-                if (c < W) {
-                    sacc[sub * 2 * W + c] = dw[p][e];
-                    sacc[sub * 2 * W + W + c] = db[p][e];
+                if (FAST || c < W) {
+                    sacc[sub * 2 * W + c] = dw[p].e[e];
+                    sacc[sub * 2 * W + W + c] = db[p].e[e];
                 }
             }
         __syncthreads();
@@ -270,7 +394,8 @@ ln_bwd_long(LayerNormBwdArgs a) {
         c1 += g;
         c2 = fmaf(g, (to_f32(x[i]) - mean) * rstd, c2);
     }
-    row_sum2<1024>(c1, c2, red);
+    c1 = block_sum(c1, red);
+    c2 = block_sum(c2, red);
     c1 /= (float)a.width;
     c2 /= (float)a.width;
     for (int64_t i = threadIdx.x; i < a.width; i += 1024) {
@@ -318,10 +443,29 @@ ln_sum_partials(const float *ws, int n, int64_t W, float *dw, float *db) {
 
 template <typename T> constexpr int vec_of() { return 16 / (int)sizeof(T); }
 
+// Blocks of a grid whose blocks stride over the rows: all of them, or what fits the GPU at once.
+template <typename K> cudaError_t resident(K k, int threads, size_t smem, int64_t blocks, int64_t *n) {
+    int dev = 0, sms = 0, per = 0;
+    cudaError_t e;
+    *n = blocks;
+    if (blocks <= 148) return cudaSuccess;   // at most one an SM in any case
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, threads, smem)) != cudaSuccess) return e;
+    const int64_t most = (int64_t)sms * (per < 1 ? 1 : per);
+    if (*n > most) *n = most;
+    return cudaSuccess;
+}
+
 template <typename T, int VW, int ROWT, int VPT>
 cudaError_t fwd(const LayerNormArgs &a, cudaStream_t s) {
     constexpr int RPB = block_of<ROWT>() / ROWT;
-    ln_fwd<T, VW, ROWT, VPT><<<(unsigned)((a.rows + RPB - 1) / RPB), block_of<ROWT>(), 0, s>>>(a);
+    int64_t n;
+    const bool fast = VW > 1 && a.width == (int64_t)VW * ROWT * VPT && a.weight && a.bias;
+    auto k = fast ? ln_fwd<T, VW, ROWT, VPT, (VW > 1)> : ln_fwd<T, VW, ROWT, VPT, false>;
+    const cudaError_t e = resident(k, block_of<ROWT>(), 0, (a.rows + RPB - 1) / RPB, &n);
+    if (e != cudaSuccess) return e;
+    k<<<(unsigned)n, block_of<ROWT>(), 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -329,18 +473,26 @@ template <typename T>
 cudaError_t forward(const LayerNormArgs &a, cudaStream_t s) {
     constexpr int VW = vec_of<T>();
     const int64_t w = a.width;
+    // few rows: one vector a thread, for the latency; many: eight, for the reductions' share of
+    // the instructions
+    const bool few = a.rows < 1024;
     if (w % VW == 0) {
         const int64_t nv = w / VW;
+        if (few) {
+            if (nv <= 32) return fwd<T, VW, 32, 1>(a, s);
+            if (nv <= 256) return fwd<T, VW, 256, 1>(a, s);
+            if (nv <= 1024) return fwd<T, VW, 1024, 1>(a, s);
+        }
         if (nv <= 4) return fwd<T, VW, 4, 1>(a, s);
-        if (nv <= 8) return fwd<T, VW, 8, 1>(a, s);
-        if (nv <= 16) return fwd<T, VW, 16, 1>(a, s);
-        if (nv <= 32) return fwd<T, VW, 32, 1>(a, s);
-        if (nv <= 64) return fwd<T, VW, 32, 2>(a, s);
+        if (nv <= 8) return fwd<T, VW, 4, 2>(a, s);
+        if (nv <= 16) return fwd<T, VW, 4, 4>(a, s);
+        if (nv <= 32) return fwd<T, VW, 8, 4>(a, s);
+        if (nv <= 64) return fwd<T, VW, 16, 4>(a, s);
         if (nv <= 128) return fwd<T, VW, 32, 4>(a, s);
-        if (nv <= 256) return fwd<T, VW, 128, 2>(a, s);
-        if (nv <= 512) return fwd<T, VW, 256, 2>(a, s);
-        if (nv <= 1024) return fwd<T, VW, 256, 4>(a, s);
-        if (nv <= 4096) return fwd<T, VW, 1024, 4>(a, s);
+        if (nv <= 256) return fwd<T, VW, 32, 8>(a, s);
+        if (nv <= 512) return fwd<T, VW, 64, 8>(a, s);
+        if (nv <= 1024) return fwd<T, VW, 128, 8>(a, s);
+        if (nv <= 4096) return fwd<T, VW, 512, 8>(a, s);
     } else {
         if (w <= 32) return fwd<T, 1, 32, 1>(a, s);
         if (w <= 128) return fwd<T, 1, 32, 4>(a, s);
@@ -366,14 +518,14 @@ template <typename T, int VW, int ROWT, int VPT>
 cudaError_t bwd(const LayerNormBwdArgs &a, cudaStream_t s) {
     constexpr int RPB = block_of<ROWT>() / ROWT;
     const int64_t blocks = (a.rows + RPB - 1) / RPB;
-    const int64_t n = blocks < partials(a.rows) ? blocks : partials(a.rows);
-    const size_t smem = RPB > 1 ? (size_t)RPB * 2 * a.width * sizeof(float) : 0;
-    cudaError_t e;
-    if (smem > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(ln_bwd<T, VW, ROWT, VPT>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-        return e;
-    ln_bwd<T, VW, ROWT, VPT><<<(unsigned)n, block_of<ROWT>(), smem, s>>>(a);
+    const size_t smem = RPB > 1 ? (size_t)RPB * 2 * a.width * sizeof(float) : 0;   // <= 32 KB
+    int64_t n;
+    const bool fast = VW > 1 && a.width == (int64_t)VW * ROWT * VPT && a.weight;
+    auto k = fast ? ln_bwd<T, VW, ROWT, VPT, (VW > 1)> : ln_bwd<T, VW, ROWT, VPT, false>;
+    cudaError_t e = resident(k, block_of<ROWT>(), smem, blocks, &n);
+    if (e != cudaSuccess) return e;
+    if (n > partials(a.rows)) n = partials(a.rows);
+    k<<<(unsigned)n, block_of<ROWT>(), smem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return add_partials(a, n, s);
 }
@@ -385,12 +537,12 @@ cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t s) {
     if (w % VW == 0) {
         const int64_t nv = w / VW;
         if (nv <= 4) return bwd<T, VW, 4, 1>(a, s);
-        if (nv <= 8) return bwd<T, VW, 8, 1>(a, s);
-        if (nv <= 16) return bwd<T, VW, 16, 1>(a, s);
-        if (nv <= 32) return bwd<T, VW, 32, 1>(a, s);
+        if (nv <= 8) return bwd<T, VW, 4, 2>(a, s);
+        if (nv <= 16) return bwd<T, VW, 8, 2>(a, s);
+        if (nv <= 32) return bwd<T, VW, 16, 2>(a, s);
         if (nv <= 64) return bwd<T, VW, 32, 2>(a, s);
-        if (nv <= 128) return bwd<T, VW, 128, 1>(a, s);
-        if (nv <= 256) return bwd<T, VW, 256, 1>(a, s);
+        if (nv <= 128) return bwd<T, VW, 64, 2>(a, s);
+        if (nv <= 256) return bwd<T, VW, 128, 2>(a, s);
         if (nv <= 512) return bwd<T, VW, 256, 2>(a, s);
         if (nv <= 1024) return bwd<T, VW, 512, 2>(a, s);
         if (nv <= 2048) return bwd<T, VW, 1024, 2>(a, s);
