@@ -455,12 +455,14 @@ bool outputs_clash(std::initializer_list<Span> outs, std::initializer_list<Span>
 }
 
 // Shape and type of a decayed call.  The kernels index chunks of at least 64
-// tokens by a 32-bit grid.
+// tokens, and 256 elements of a state, by a 32-bit grid.
 int check_decay(const fw_shape *shape, fw_dtype dtype) {
     const int st = check_common(shape, dtype, FW_LINATTN, FW_PHI_IDENTITY, 0.f, 0u);
     if (st != FW_OK) return st;
     if (shape->T > (int64_t)INT32_MAX - 128) return FW_ERR_SHAPE;
-    if (shape->B * shape->H > (int64_t)INT32_MAX / ((shape->T + 63) / 64)) return FW_ERR_SHAPE;
+    if (shape->B * shape->H > (int64_t)INT32_MAX / ((shape->T + 63) / 64) ||
+        shape->B * shape->H > (int64_t)1 << 24)
+        return FW_ERR_SHAPE;
     return FW_OK;
 }
 

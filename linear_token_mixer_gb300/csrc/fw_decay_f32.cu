@@ -1,0 +1,376 @@
+// fw_decay_f32.cu -- decayed linear attention scans (see fw_decay.cuh) for fp32 rows, d = 64 and
+// 128, parallel over chunks of 64 tokens:
+//
+//   scan_local    M_c = in_scale sum_j w_j b_j c_j^T of every chunk (one block each)
+//   scan_prefix   the short recurrence X' = g^n X + M_c over a chain's chunks, one thread a state
+//                 element; M_c is replaced by the state on entry to chunk c
+//   scan_out      out = rd (A X_c) + (mask . decay . A B^T) C of every chunk (one block each)
+//
+// The products run on warp-level tf32 MMAs with every operand split in two (11 + 11 bits):
+// a b = a1 b1 + a1 b2 + a2 b1 leaves out 2^-22 relative, so the rows keep fp32's accuracy; sums
+// are fp32.  A chunk of 64 keeps the 64 x 64 part no larger than the d x d part and gives
+// B*H*T/64 blocks, which is what short batches need to fill the GPU.  The three launches overlap
+// their starts (programmatic dependent launch): scan_out loads its rows and forms the masked
+// scores before it waits for the states.
+#include "fw_decay_tc.cuh"
+#include "fw_sm100.cuh"
+
+namespace fw {
+namespace {
+
+constexpr int C = 64;          // tokens per chunk
+
+struct Scans {
+    ScanArgs s[3];
+};
+
+// 2 x (D / 32) warps, a 32 x 32 tile of the 64 x D rows each.
+template <int D> constexpr int threads() { return 2 * (D / 32) * 32; }
+// Row strides that make the MMA fragments' reads free of bank conflicts: 4 (mod 32) where a
+// fragment's rows are tile rows, 8 where its k runs along tile rows.
+template <int D> constexpr int ld_row() { return D + 4; }
+template <int D> constexpr int ld_col() { return D + 8; }
+
+__device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_grid_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// x = hi + lo + (at most 2^-22 |x|); infinities and NaN stay in hi.
+__device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
+    hi = sm100::f2tf32(x);
+    const float r = x - __uint_as_float(hi);
+    lo = isfinite(r) ? sm100::f2tf32(r) : 0u;
+}
+
+// acc += A B for a warp's 16 MT x 8 NT tile; element (m, k) of A at a[m * am + k * ak], element
+// (k, n) of B at b[k * bk + n * bn].
+template <int MT, int NT>
+__device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, int am, int ak,
+                                     const float *b, int bk, int bn, int K) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    a += g * am + t * ak;
+    b += t * bk + g * bn;
+#pragma unroll 1
+    for (int k = 0; k < K; k += 8) {
+        uint32_t ah[MT][4], al[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                split(a[(16 * m + 8 * (e & 1)) * am + (k + 4 * (e >> 1)) * ak], ah[m][e], al[m][e]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) split(b[(k + 4 * e) * bk + 8 * n * bn], bh[e], bl[e]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                sm100::mma_tf32_16x8x8(acc[m][n], al[m], bh);
+                sm100::mma_tf32_16x8x8(acc[m][n], ah[m], bl);
+                sm100::mma_tf32_16x8x8(acc[m][n], ah[m], bh);
+            }
+        }
+    }
+}
+
+// Rows [0, nv) of a chunk's 64 x D tile (rows behind them zero), each times row_w[r].
+template <int D, int LD>
+__device__ __forceinline__ void load_tile(float *dst, const float *src, int nv, const float *row_w) {
+    constexpr int PR = D / 4;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < C * PR; i += threads<D>()) {
+        const int r = i / PR, c = (i % PR) * 4;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < nv) {
+            f = *reinterpret_cast<const float4 *>(src + (int64_t)r * D + c);
+            if (row_w) {
+                const float w = row_w[r];
+                f.x *= w; f.y *= w; f.z *= w; f.w *= w;
+            }
+        }
+        *reinterpret_cast<float4 *>(dst + r * LD + c) = f;
+    }
+}
+
+struct ChunkOf {
+    int64_t chain, chunk;
+    int nv;            // valid rows
+    bool last;         // last chunk in processing order
+};
+
+__device__ __forceinline__ ChunkOf chunk_of(const ScanArgs &s, int64_t nch) {
+    ChunkOf r;
+    r.chain = (int64_t)blockIdx.x / nch;
+    r.chunk = (int64_t)blockIdx.x % nch;
+    const int64_t n = chain_len(s.lens, r.chain, s.H, s.T);
+    const int64_t left = n - r.chunk * C;
+    r.nv = left < 0 ? 0 : left > C ? C : (int)left;
+    r.last = s.rev ? r.chunk == 0 : (r.chunk + 1) * C >= n;
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(threads<D>())
+scan_local(const __grid_constant__ Scans all, int64_t nch) {
+    extern __shared__ float4 smem4[];
+    let_next_grid_start();
+    const ScanArgs &s = all.s[blockIdx.y];
+    const ChunkOf k = chunk_of(s, nch);
+    if (k.nv == 0 || (k.last && !s.X_out)) return;   // no later chunk and nobody reads the end
+    constexpr int LD = ld_col<D>();
+    float *sB = reinterpret_cast<float *>(smem4), *sC = sB + C * LD, *w = sC + C * LD;
+    const float lg = s.log_decay[k.chain % s.H];
+    if (threadIdx.x < C) {
+        const int j = threadIdx.x;
+        w[j] = s.in_scale * decay_pow(lg, (float)(s.rev ? j + 1 : max(k.nv - 1 - j, 0)));
+    }
+    __syncthreads();
+    const int64_t base = (k.chain * s.T + k.chunk * C) * D;
+    load_tile<D, LD>(sB, static_cast<const float *>(s.b) + base, k.nv, w);
+    load_tile<D, LD>(sC, static_cast<const float *>(s.c) + base, k.nv, nullptr);
+    __syncthreads();
+    // D x D over 2 x (D / 32) warps: D / 2 rows of X by 32 columns each
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m0 = (warp & 1) * (D / 2), n0 = (warp >> 1) * 32;
+    constexpr int MT = D / 32;
+    float acc[MT][4][4] = {};
+    gemm<MT, 4>(acc, sB + m0, 1, LD, sC + n0, LD, 1, C);
+    float *M = s.ws + (int64_t)blockIdx.x * D * D;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2 *>(M + (m0 + 16 * m + (lane >> 2) + 8 * h) * D + n0 + 8 * n + 2 * (lane & 3)) =
+                    make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(256)
+scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
+    const ScanArgs &s = all.s[blockIdx.y];
+    constexpr int PER = D * D / 256;       // blocks of a chain
+    const int64_t chain = blockIdx.x / PER;
+    const int el = (int)(blockIdx.x % PER) * 256 + threadIdx.x;
+    let_next_grid_start();
+    float x = 0.f;
+    if (s.X0) x = s.X0[chain * D * D + (s.x0_trans ? (el % D) * D + el / D : el)];
+    const int64_t n = chain_len(s.lens, chain, s.H, s.T);
+    const int64_t used = (n + C - 1) / C;
+    const float lg = s.log_decay[chain % s.H];
+    const float gC = decay_pow(lg, (float)C), gT = decay_pow(lg, (float)(n - (used - 1) * C));
+    float *M = s.ws + chain * nch * D * D + el;
+    wait_previous_grid();
+    constexpr int U = 8;                   // chunks read ahead of the recurrence
+    for (int64_t i0 = 0; i0 < used; i0 += U) {
+        float m[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u, c = s.rev ? used - 1 - i : i;
+            m[u] = i < used && (i + 1 < used || s.X_out) ? M[c * D * D] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u, c = s.rev ? used - 1 - i : i;
+            if (i < used) {
+                M[c * D * D] = x;
+                x = fmaf(c == used - 1 ? gT : gC, x, m[u]);
+            }
+        }
+    }
+    if (s.X_out) s.X_out[chain * D * D + el] = x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(threads<D>())
+scan_out(const __grid_constant__ Scans all, int64_t nch) {
+    extern __shared__ float4 smem4[];
+    const ScanArgs &s = all.s[blockIdx.y];
+    const ChunkOf k = chunk_of(s, nch);
+    if (k.nv == 0) {                       // (no block ends before the grids it follows)
+        wait_previous_grid();
+        return;
+    }
+    constexpr int LR = ld_row<D>(), LC = ld_col<D>(), WN = D / 32, LP = C + 4;
+    float *sA = reinterpret_cast<float *>(smem4), *sB = sA + C * LR, *sC = sB + C * LR,
+          *sX = sC + C * LC, *pw = sX + D * LC, *red = pw + C + 4;
+    const float lg = s.log_decay[k.chain % s.H];
+    for (int i = threadIdx.x; i <= C; i += threads<D>()) pw[i] = decay_pow(lg, (float)i);
+    const int64_t base = (k.chain * s.T + k.chunk * C) * D;
+    load_tile<D, LR>(sA, static_cast<const float *>(s.a) + base, k.nv, nullptr);
+    load_tile<D, LR>(sB, static_cast<const float *>(s.b) + base, k.nv, nullptr);
+    load_tile<D, LC>(sC, static_cast<const float *>(s.c) + base, k.nv, nullptr);
+    __syncthreads();
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int m0 = (warp & 1) * 32, wn = warp >> 1;
+    {   // P = mask . decay . A B^T over B's rows: 32 rows by 64 / WN columns a warp
+        constexpr int NT = C / WN / 8;
+        const int n0 = wn * (C / WN);
+        float p[2][NT][4] = {};
+        gemm<2, NT>(p, sA + m0 * LR, LR, 1, sB + n0 * LR, 1, LR, D);
+        __syncthreads();                   // B is read
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = m0 + 16 * m + g + 8 * (e >> 1), j = n0 + 8 * n + 2 * t + (e & 1);
+                    const int lag = s.rev ? j - r : r - j;
+                    sB[r * LP + j] = lag >= 0 && j < k.nv ? p[m][n][e] * (pw[lag] * s.in_scale) : 0.f;
+                }
+    }
+    wait_previous_grid();                  // the states
+    const float4 *X = reinterpret_cast<const float4 *>(s.ws + (int64_t)blockIdx.x * D * D);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < D * D / 4; i += threads<D>())
+        *reinterpret_cast<float4 *>(sX + i / (D / 4) * LC + i % (D / 4) * 4) = X[i];
+    __syncthreads();
+
+    const int n0 = wn * 32;
+    float acc[2][4][4] = {};
+    gemm<2, 4>(acc, sA + m0 * LR, LR, 1, sX + n0, LC, 1, D);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = m0 + 16 * m + g + 8 * h;
+            const float rd = pw[s.rev ? max(k.nv - 1 - r, 0) : r + 1];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                acc[m][n][2 * h] *= rd;
+                acc[m][n][2 * h + 1] *= rd;
+            }
+        }
+    gemm<2, 4>(acc, sB + m0 * LP, LP, 1, sC + n0, LC, 1, C);
+
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][n][e] *= s.out_scale;
+    if (s.norm.on) {                       // a row is held by four lanes of each of WN warps
+        auto row_sums = [&](float (&z)[2][2]) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    z[m][h] += __shfl_xor_sync(~0u, z[m][h], 1);
+                    z[m][h] += __shfl_xor_sync(~0u, z[m][h], 2);
+                    if (t == 0) red[(m0 + 16 * m + g + 8 * h) * WN + wn] = z[m][h];
+                }
+            __syncthreads();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    z[m][h] = 0.f;
+#pragma unroll
+                    for (int w = 0; w < WN; ++w) z[m][h] += red[(m0 + 16 * m + g + 8 * h) * WN + w];
+                }
+            __syncthreads();
+        };
+        float z[2][2] = {};
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[m][e >> 1] += acc[m][n][e];
+        row_sums(z);
+        float v[2][2] = {};
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[m][n][e] -= z[m][e >> 1] / D;
+                    v[m][e >> 1] = fmaf(acc[m][n][e], acc[m][n][e], v[m][e >> 1]);
+                }
+        row_sums(v);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int col = n0 + 8 * n + 2 * t + (e & 1);
+                    acc[m][n][e] *= rsqrtf(v[m][e >> 1] / D + s.norm.eps);
+                    if (s.norm.weight) acc[m][n][e] *= s.norm.weight[col];
+                    if (s.norm.bias) acc[m][n][e] += s.norm.bias[col];
+                }
+    }
+    float *out = static_cast<float *>(s.out) + base;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = m0 + 16 * m + g + 8 * h;
+            if (r >= k.nv) continue;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                *reinterpret_cast<float2 *>(out + (int64_t)r * D + n0 + 8 * n + 2 * t) =
+                    make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+        }
+}
+
+template <typename K, typename... A>
+cudaError_t launch_after(K k, dim3 grid, int threads, size_t smem, cudaStream_t stream, bool overlap, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+template <int D>
+cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
+    const ScanArgs &s = all.s[0];
+    const int64_t nch = (s.T + C - 1) / C;
+    const dim3 grid((unsigned)(s.n_chains * nch), n);
+    constexpr int smem_l = (2 * C * ld_col<D>() + C) * 4;
+    constexpr int smem_o = (2 * C * ld_row<D>() + (C + D) * ld_col<D>() + C + 4 + C * (D / 32)) * 4;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(scan_local<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_l)) != cudaSuccess)
+        return e;
+    if ((e = cudaFuncSetAttribute(scan_out<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_o)) != cudaSuccess)
+        return e;
+    if ((e = launch_after(scan_local<D>, grid, threads<D>(), smem_l, stream, false, all, nch)) != cudaSuccess) return e;
+    const dim3 gp((unsigned)(s.n_chains * (D * D / 256)), n);
+    if ((e = launch_after(scan_prefix<D>, gp, 256, 0, stream, true, all, nch)) != cudaSuccess) return e;
+    return launch_after(scan_out<D>, grid, threads<D>(), smem_o, stream, true, all, nch);
+}
+
+}  // namespace
+
+size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype) {
+    if (dtype == FW_BF16) return scan_tc_workspace(n_chains, T, d);
+    return (size_t)n_chains * (size_t)((T + C - 1) / C) * d * d * sizeof(float);
+}
+
+// bf16 rows run on the fifth-generation tensor cores, fp32 rows here.
+cudaError_t launch_scans(const ScanArgs *s, int n, cudaStream_t stream) {
+    if (s[0].dtype == FW_BF16) {
+        for (int i = 0; i < n; ++i) {
+            const cudaError_t e = launch_scan_tc(s[i], stream);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
+    Scans all{};
+    for (int i = 0; i < n; ++i) all.s[i] = s[i];
+    return s[0].d == 64 ? launch<64>(all, n, stream) : launch<128>(all, n, stream);
+}
+
+}  // namespace fw
