@@ -36,11 +36,11 @@ __device__ __forceinline__ void let_next_grid_start() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// x = hi + lo + (at most 2^-22 |x|); infinities and NaN stay in hi.
+// x = hi + lo: hi rounded to 11 bits, lo what that leaves (exact in fp32; the MMA reads its top 11
+// bits, so 2^-22 |x| at most is lost).  An infinity leaves NaN.
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
     hi = sm100::f2tf32(x);
-    const float r = x - __uint_as_float(hi);
-    lo = isfinite(r) ? sm100::f2tf32(r) : 0u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
 // acc += A B for a warp's 16 MT x 8 NT tile; element (m, k) of A at a[m * am + k * ak], element
@@ -59,18 +59,19 @@ __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, in
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 split(a[(16 * m + 8 * (e & 1)) * am + (k + 4 * (e >> 1)) * ak], ah[m][e], al[m][e]);
+        uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            uint32_t bh[2], bl[2];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) split(b[(k + 4 * e) * bk + 8 * n * bn], bh[e], bl[e]);
+            for (int e = 0; e < 2; ++e) split(b[(k + 4 * e) * bk + 8 * n * bn], bh[n][e], bl[n][e]);
+        // the three terms one after the other over all tiles: no MMA waits for the one before it
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                sm100::mma_tf32_16x8x8(acc[m][n], al[m], bh);
-                sm100::mma_tf32_16x8x8(acc[m][n], ah[m], bl);
-                sm100::mma_tf32_16x8x8(acc[m][n], ah[m], bh);
-            }
-        }
+        for (int term = 0; term < 3; ++term)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    sm100::mma_tf32_16x8x8(acc[m][n], term == 0 ? al[m] : ah[m], term == 1 ? bl[n] : bh[n]);
     }
 }
 
