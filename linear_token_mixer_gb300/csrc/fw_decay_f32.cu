@@ -51,7 +51,7 @@ __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, in
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     a += g * am + t * ak;
     b += t * bk + g * bn;
-#pragma unroll 1
+#pragma unroll 2
     for (int k = 0; k < K; k += 8) {
         uint32_t ah[MT][4], al[MT][4];
 #pragma unroll
@@ -111,14 +111,9 @@ __device__ __forceinline__ ChunkOf chunk_of(const ScanArgs &s, int64_t nch) {
     return r;
 }
 
-template <int D>
-__global__ void __launch_bounds__(threads<D>())
-scan_local(const __grid_constant__ Scans all, int64_t nch) {
-    extern __shared__ float4 smem4[];
-    let_next_grid_start();
-    const ScanArgs &s = all.s[blockIdx.y];
-    const ChunkOf k = chunk_of(s, nch);
-    if (k.nv == 0 || (k.last && !s.X_out)) return;   // no later chunk and nobody reads the end
+// M_c into the workspace; ONE (chains of one chunk): the final state into X_out.
+template <int D, bool ONE>
+__device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, float4 *smem4) {
     constexpr int LD = ld_col<D>();
     float *sB = reinterpret_cast<float *>(smem4), *sC = sB + C * LD, *w = sC + C * LD;
     const float lg = s.log_decay[k.chain % s.H];
@@ -137,15 +132,34 @@ scan_local(const __grid_constant__ Scans all, int64_t nch) {
     constexpr int MT = D / 32;
     float acc[MT][4][4] = {};
     gemm<MT, 4>(acc, sB + m0, 1, LD, sC + n0, LD, 1, C);
-    float *M = s.ws + (int64_t)blockIdx.x * D * D;
+    float *M = ONE ? s.X_out + k.chain * D * D : s.ws + (int64_t)blockIdx.x * D * D;
+    const float *X0 = ONE && s.X0 ? s.X0 + k.chain * D * D : nullptr;
+    const float gn = decay_pow(lg, (float)k.nv);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float2 *>(M + (m0 + 16 * m + (lane >> 2) + 8 * h) * D + n0 + 8 * n + 2 * (lane & 3)) =
-                    make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+            for (int h = 0; h < 2; ++h) {
+                const int r = m0 + 16 * m + (lane >> 2) + 8 * h, c = n0 + 8 * n + 2 * (lane & 3);
+                float2 v = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+                if (X0) {
+                    v.x = fmaf(gn, s.x0_trans ? X0[c * D + r] : X0[r * D + c], v.x);
+                    v.y = fmaf(gn, s.x0_trans ? X0[(c + 1) * D + r] : X0[r * D + c + 1], v.y);
+                }
+                *reinterpret_cast<float2 *>(M + r * D + c) = v;
+            }
+}
+
+template <int D>
+__global__ void __launch_bounds__(threads<D>())
+scan_local(const __grid_constant__ Scans all, int64_t nch) {
+    extern __shared__ float4 smem4[];
+    let_next_grid_start();
+    const ScanArgs &s = all.s[blockIdx.y];
+    const ChunkOf k = chunk_of(s, nch);
+    if (k.nv == 0 || (k.last && !s.X_out)) return;   // no later chunk and nobody reads the end
+    local_part<D, false>(s, k, smem4);
 }
 
 template <int D>
@@ -184,19 +198,12 @@ scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
     if (s.X_out) s.X_out[chain * D * D + el] = x;
 }
 
-template <int D>
-__global__ void __launch_bounds__(threads<D>())
-scan_out(const __grid_constant__ Scans all, int64_t nch) {
-    extern __shared__ float4 smem4[];
-    const ScanArgs &s = all.s[blockIdx.y];
-    const ChunkOf k = chunk_of(s, nch);
-    if (k.nv == 0) {                       // (no block ends before the grids it follows)
-        wait_previous_grid();
-        return;
-    }
+// The output rows of a chunk, from the state in the workspace; ONE: from X0.
+template <int D, bool ONE>
+__device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, float4 *smem4) {
     constexpr int LR = ld_row<D>(), LC = ld_col<D>(), WN = D / 32, LP = C + 4;
     float *sA = reinterpret_cast<float *>(smem4), *sB = sA + C * LR, *sC = sB + C * LR,
-          *sX = sC + C * LC, *pw = sX + D * LC, *red = pw + C + 4;
+          *pw = sC + C * LC, *red = pw + C + 4;
     const float lg = s.log_decay[k.chain % s.H];
     for (int i = threadIdx.x; i <= C; i += threads<D>()) pw[i] = decay_pow(lg, (float)i);
     const int64_t base = (k.chain * s.T + k.chunk * C) * D;
@@ -224,16 +231,17 @@ scan_out(const __grid_constant__ Scans all, int64_t nch) {
                     sB[r * LP + j] = lag >= 0 && j < k.nv ? p[m][n][e] * (pw[lag] * s.in_scale) : 0.f;
                 }
     }
-    wait_previous_grid();                  // the states
-    const float4 *X = reinterpret_cast<const float4 *>(s.ws + (int64_t)blockIdx.x * D * D);
-#pragma unroll 8
-    for (int i = threadIdx.x; i < D * D / 4; i += threads<D>())
-        *reinterpret_cast<float4 *>(sX + i / (D / 4) * LC + i % (D / 4) * 4) = X[i];
-    __syncthreads();
+    if (!ONE) wait_previous_grid();        // the states
+    __syncthreads();                       // P is written
+    const float *X = ONE ? s.X0 ? s.X0 + k.chain * D * D : nullptr : s.ws + (int64_t)blockIdx.x * D * D;
+    const bool trans = ONE && s.x0_trans;
+    const bool zero = !s.X0 && (ONE || (s.rev ? k.nv < C || (k.chunk + 1) * C >= chain_len(s.lens, k.chain, s.H, s.T)
+                                              : k.chunk == 0));   // nothing carried in
 
     const int n0 = wn * 32;
     float acc[2][4][4] = {};
-    gemm<2, 4>(acc, sA + m0 * LR, LR, 1, sX + n0, LC, 1, D);
+    if (!zero)
+        gemm<2, 4>(acc, sA + m0 * LR, LR, 1, X + n0 * (trans ? D : 1), trans ? 1 : D, trans ? D : 1, D);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -320,6 +328,33 @@ scan_out(const __grid_constant__ Scans all, int64_t nch) {
         }
 }
 
+template <int D>
+__global__ void __launch_bounds__(threads<D>())
+scan_out(const __grid_constant__ Scans all, int64_t nch) {
+    extern __shared__ float4 smem4[];
+    const ScanArgs &s = all.s[blockIdx.y];
+    const ChunkOf k = chunk_of(s, nch);
+    if (k.nv == 0) {                       // (no block ends before the grids it follows)
+        wait_previous_grid();
+        return;
+    }
+    out_part<D, false>(s, k, smem4);
+}
+
+// Chains of one chunk (X_out apart from X0): final states (z = 0) and rows (z = 1) at once.
+template <int D>
+__global__ void __launch_bounds__(threads<D>())
+scan_one(const __grid_constant__ Scans all) {
+    extern __shared__ float4 smem4[];
+    const ScanArgs &s = all.s[blockIdx.y];
+    const ChunkOf k = chunk_of(s, 1);
+    if (blockIdx.z == 0) {
+        if (s.X_out) local_part<D, true>(s, k, smem4);
+    } else if (k.nv > 0) {
+        out_part<D, true>(s, k, smem4);
+    }
+}
+
 template <typename K, typename... A>
 cudaError_t launch_after(K k, dim3 grid, int threads, size_t smem, cudaStream_t stream, bool overlap, A... args) {
     cudaLaunchConfig_t cfg = {};
@@ -341,8 +376,17 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     const int64_t nch = (s.T + C - 1) / C;
     const dim3 grid((unsigned)(s.n_chains * nch), n);
     constexpr int smem_l = (2 * C * ld_col<D>() + C) * 4;
-    constexpr int smem_o = (2 * C * ld_row<D>() + (C + D) * ld_col<D>() + C + 4 + C * (D / 32)) * 4;
+    constexpr int smem_o = (2 * C * ld_row<D>() + C * ld_col<D>() + C + 4 + C * (D / 32)) * 4;
     cudaError_t e;
+    bool one = nch == 1;
+    for (int i = 0; i < n; ++i) one = one && !(all.s[i].X_out && all.s[i].X_out == all.s[i].X0);
+    if (one) {
+        constexpr int smem = smem_l > smem_o ? smem_l : smem_o;
+        if ((e = cudaFuncSetAttribute(scan_one<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return e;
+        scan_one<D><<<dim3((unsigned)s.n_chains, n, 2), threads<D>(), smem, stream>>>(all);
+        return cudaGetLastError();
+    }
     if ((e = cudaFuncSetAttribute(scan_local<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_l)) != cudaSuccess)
         return e;
     if ((e = cudaFuncSetAttribute(scan_out<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_o)) != cudaSuccess)
