@@ -86,7 +86,7 @@ cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const LayerNormBwdArgs &a, cudaStream_t s);
 size_t layer_norm_workspace(int64_t rows, int64_t width);
 
-// g^n = exp(n log g) for n >= 0.  The product n log g is rounded to fp32; what the rounding
+// g^n = exp(n log g).  The product n log g is rounded to fp32; what the rounding
 // dropped is recovered by an FMA and multiplied back in, so a large exponent costs no relative
 // accuracy.  g^0 = 1 for every g, g = 0 (log g = -inf) included.
 __device__ __forceinline__ float decay_pow(float log_g, float n) {

@@ -18,10 +18,10 @@
 //   warp 2       MMA issuer of the state update
 //   warp 3       MMA issuer of A X; tensor-memory allocation
 //   warps 4-7    P: tensor memory -> mask, decay, bf16 -> tensor memory (A operand of P C)
-//   warps 8-11   O: scales A X by its row's decay in place before P C accumulates on it, then
-//                [output norm,] rounds and stores the rows (one thread a row)
-//   warps 12-15  the three terms of (diag(w) B)^T, 32 tokens at a time, into tensor memory,
-//                double-buffered
+//   warps 8-11   O: its rows' decay [, output norm], rounded and stored (one thread a row); of a
+//                steep head A X is scaled in place before P C accumulates on it
+//   warps 12-15, 24-27  the three terms of (diag(w) B)^T, 32 tokens at a time, into tensor
+//                memory, a buffer for each four warps (a segment's state alone: 4-11 too)
 //   warps 16-23  X, in registers (fp32, half a row a thread): X <- g^n X + the chunk's update,
 //                and its bf16 shared-memory copy for A X
 // The update of a chunk is summed from zero in tensor memory and added to X by an fp32 FMA: the
@@ -48,17 +48,20 @@ constexpr uint32_t HALF = 16 * KB;           // 128 rows x 128 bytes: 64 columns
 constexpr int kSMs = 152;                    // the grid's target (a workspace size needs no device)
 constexpr int kMinSegChunks = 4;
 
-// Registers a thread: 72 for each of the seven warpgroups at launch; O keeps them, the others hand
-// theirs on to the two groups that hold X.
-constexpr int REGS = 72, REGS_W0 = 40, REGS_P = 64, REGS_K = 64, REGS_X = 96;
-static_assert(REGS_W0 + 2 * REGS_P + REGS + REGS_K + 2 * REGS_X <= 7 * REGS, "registers of the launch");
-constexpr uint32_t COL_G = 0, COL_O = 128, COL_U = 256, COL_K = 384, KBUF = 48;
+// Registers a thread: 72 for each of the seven warpgroups at launch; P and O keep them, warps 0-3
+// and the split-operand groups hand theirs on to the two groups that hold X.
+constexpr int REGS = 72, REGS_W0 = 40, REGS_K = 64, REGS_X = 96;
+static_assert(REGS_W0 + 2 * REGS + 2 * REGS_K + 2 * REGS_X <= 7 * REGS, "registers of the launch");
+constexpr uint32_t COL_G = 0, COL_O = 128, COL_U = 256, KBUF = 48;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t kDrainNs = 2000000000ull;
 
 template <int D, bool PRE> struct Lay {
     static constexpr uint32_t TILE = (uint32_t)C * D * 2;
     static constexpr int NT = PRE ? 2 : 3;                       // tiles per stage
+    // split-operand groups, a tensor-memory buffer each (a state alone leaves room for four)
+    static constexpr int KG = PRE ? 4 : 2;
+    static constexpr uint32_t COL_K = PRE ? 0 : 384;
     static constexpr int NST = (int)(192 * KB / (TILE * NT));    // 2 (3), d = 64: 4 (6)
     static constexpr uint32_t XB = NST * NT * TILE;              // bf16 copy of X
     static constexpr uint32_t TAB = XB + (uint32_t)D * D * 2;
@@ -68,7 +71,7 @@ template <int D, bool PRE> struct Lay {
     static constexpr int FULL = 0, EMPTY = FULL + NST * NT, GDONE = EMPTY + NST * NT,
                          PRDY = GDONE + 1, QSDONE = PRDY + 1, OSC = QSDONE + 1, PVDONE = OSC + 1,
                          OFREE = PVDONE + 1, UDONE = OFREE + 1, XBRDY = UDONE + 1,
-                         UFREE = XBRDY + 1, KRDY = UFREE + 1, KFREE = KRDY + 2, VZ = KFREE + 2,
+                         UFREE = XBRDY + 1, KRDY = UFREE + 1, KFREE = KRDY + KG, VZ = KFREE + KG,
                          DRAIN = VZ + 1, NEVER = DRAIN + 3,
                          NBAR = NEVER + 1;
     static constexpr uint32_t MISC = BAR + NBAR * 8;
@@ -132,13 +135,43 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+// Sixteen columns of tensor memory into registers that may be read only after tmem_landed().
+__device__ __forceinline__ void tmem_fetch16(uint32_t taddr, float (&v)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void tmem_landed(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15])::"memory");
+}
+// do_(v, c) for the columns c = c0, c0 + 16, .. < c1 (an even number of pieces) of this warp's lanes,
+// each piece's load in flight while the one before it is worked on.
+template <typename F> __device__ __forceinline__ void tmem_stream(uint32_t taddr, int c0, int c1, F do_) {
+    float v[16], u[16];
+    if (c0 >= c1) return;
+    tmem_fetch16(taddr + c0, v);
+#pragma unroll 1
+    for (int c = c0; c < c1; c += 32) {
+        tmem_landed(v);
+        tmem_fetch16(taddr + c + 16, u);
+        do_(v, c);
+        tmem_landed(u);
+        if (c + 32 < c1) tmem_fetch16(taddr + c + 32, v);
+        do_(u, c + 16);
+    }
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 // 16 lanes x 16 columns: register 2c + h holds lane 8h + t / 4, column 4c + t % 4 of thread t.
@@ -204,6 +237,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     if (nch == 0 && !(final_seg && a.X_out) && !(PRE && seg == 0)) return;
     const uint64_t limit = (uint64_t)a.wait_ns;
     const float lg = a.log_decay[chain % a.H];
+    // Within a chunk of a mild head every quotient of powers of g is safe in fp32 and bf16
+    // (e^60 at most): the rows' decay of a chunk, g^(i+1) (A X + (mask . g^-(j+1) . G) C), is then
+    // one factor in the epilogue.  Otherwise A X is scaled by its rows' decay on its own and the
+    // scores by g^(i-j), and nothing is divided by a power of g.
+    const bool mild = fabsf(lg) * C <= 60.f;
     const int x_slots = nseg;                       // workspace: nseg - 1 segment states, X0's copy
     float *const ws = a.ws + chain * x_slots * D * D;
 
@@ -228,13 +266,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         for (int i = 0; i < L::NBAR; ++i) {
             uint32_t c = 1;
             const int e = i - L::EMPTY;
-            if (e >= 0 && e < L::NST * L::NT)       // B: its readers' four warps (and G); C: the
-                c = e % L::NT == XB_ ? (PRE ? 4 : 5)   // update (and P C); A: the O group's warps
+            if (e >= 0 && e < L::NST * L::NT)       // B: its readers' warps (and G); C: the
+                c = e % L::NT == XB_ ? 4 * L::KG + (PRE ? 0 : 1)   // update (and P C); A: the O group's warps
                   : e % L::NT == XC ? (PRE ? 1 : 2) : 4;
-            if (i == L::OSC || i == L::OFREE || i == L::KRDY || i == L::KRDY + 1 ||
-                i == L::VZ)
-                c = 4;
-            if (i == L::XBRDY || i == L::UFREE || i == L::PRDY) c = 8;
+            if (i == L::PRDY || i == L::OSC || i == L::OFREE || (i >= L::KRDY && i < L::KFREE)) c = 4;
+            if (i == L::VZ) c = 4 * L::KG;
+            if (i == L::XBRDY || i == L::UFREE) c = 8;
             mbar_init(bar(i), c);
         }
         fence_mbar_init();
@@ -307,7 +344,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 }
                 ok = wait_bar(bar(L::PRDY), pi, limit, s_abort) &&
                      wait_bar(full(st, XC), ph, limit, s_abort) &&
-                     wait_bar(bar(L::OSC), pi, limit, s_abort);
+                     wait_bar(bar(mild ? L::QSDONE : L::OSC), pi, limit, s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 {
@@ -315,7 +352,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     const uint64_t dc = sdesc_sw128(tile(st, XC), HALF, 1024);
 #pragma unroll 1
                     for (int kk = 0; kk < C / 16; ++kk)
-                        mma_bf16_ta(tmem + COL_O, tmem + COL_G + 8 * kk + 32 * (kk >> 2), dc + kk * 128, id, 1);
+                        mma_bf16_ta(tmem + COL_O, tmem + COL_G + 8 * kk, dc + kk * 128, id, 1);
                     mma_commit(bar(L::PVDONE));
                     mma_commit(empty(st, XC));
                 }
@@ -337,8 +374,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                      (i == 0 || wait_bar(bar(L::UFREE), (uint32_t)(i - 1) & 1u, limit, s_abort));
 #pragma unroll 1
                 for (int u = 0; u < 4 && ok; ++u) {
-                    const int b = u & 1;
-                    ok = wait_bar(bar(L::KRDY + b), (uint32_t)(2 * i + (u >> 1)) & 1u, limit, s_abort);
+                    const int b = u % L::KG;
+                    ok = wait_bar(bar(L::KRDY + b), (uint32_t)((4 * i + u) / L::KG) & 1u, limit, s_abort);
                     if (!ok) break;
                     tc_fence_after();
                     constexpr uint32_t id = idesc_bf16(128, D, false, true);
@@ -347,7 +384,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                         for (int term = 2; term >= 0; --term)   // the small terms first
-                            mma_bf16_ta(tmem + COL_U, tmem + COL_K + KBUF * b + 16 * term + 8 * kk,
+                            mma_bf16_ta(tmem + COL_U, tmem + L::COL_K + KBUF * b + 16 * term + 8 * kk,
                                         dc + (2 * u + kk) * 128, id, u > 0 || kk > 0 || term < 2);
                     mma_commit(bar(L::KFREE + b));
                 }
@@ -391,78 +428,65 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         }
         __syncwarp();
       }
-    } else if ((warp >= 4 && warp < 8) || warp >= 24) {
+    } else if (!PRE && warp >= 4 && warp < 8) {
         // ---------------------------------------------------------------- P
-        reg_dec<REGS_P>();
-        if (!PRE) {
+        {
             const int w = warp & 3, row = w * 32 + lane;
             const uint32_t lb = (uint32_t)(w * 32) << 16;
-            // On the diagonal block, rows short of the far edge need g^-m, m <= 31: fine in fp32 (at
-            // most e^78, and g^lag itself far from underflow) unless the head forgets at once.
-            const int jb0 = warp >= 24 ? 2 : 0;
-            const bool mild = fabsf(lg) <= 2.5f;
-            const float f_diag = a.in_scale * (mild ? pw[REV ? 0 : lane] / pw[REV ? lane : 31] : 0.f);
-            // the blocks farthest from the diagonal first: distance of the row to their near edge
-            auto edge = [&](int b) -> float {        // b-th block from the sequence's far side
-                const int m = REV ? 32 * (3 - b) - row : row - 32 * b - 31;
-                return m >= 0 ? a.in_scale * pw[m] : 0.f;
-            };
-            const float f0 = edge(0), f1 = edge(1), f2 = edge(2);
-            const float gp[4] = {pw[1], pw[2], pw[3], pw[4]};
+            const float sg = REV ? lg : -lg;         // powers from one column to the next
+            const float h1 = decay_pow(sg, 1.f), h2 = decay_pow(sg, 2.f), h3 = decay_pow(sg, 3.f),
+                        h4 = decay_pow(sg, 4.f), h16 = decay_pow(sg, 16.f);
             bool ok = true;
             for (int i = 0; i < nch; ++i) {
                 ok = __all_sync(~0u, wait_bar(bar(L::GDONE), (uint32_t)i & 1u, limit, s_abort));
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int jb = jb0; jb < jb0 + 2; ++jb) {   // 32 columns j against this warp's 32 rows
-                    float v[32];
-                    uint32_t pk[16];
-                    if (REV ? jb < w : jb > w) {
+                // bf16, and on the diagonal blocks of 16 and 32 the mask, over columns already read
+                auto put = [&](float (&v)[16], int c) {
+                    uint32_t pk[8];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = 0u;
-                    } else {
-                        tmem_ld32(tmem + lb + COL_G + 32 * jb, v);
-                        if (jb == w && !mild) {      // powers of the lag, one by one
+                    for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                    if (c >> 5 == w) {
+                        const int d = row - c;       // columns up to (reverse: from) d of this piece
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int lag = REV ? e - lane : lane - e;
-                                v[e] *= a.in_scale * pw[lag < 0 ? 0 : lag];
-                            }
-                        } else {
-                            // g^|i-j| = g^(distance to the block's far edge) g^(distance in it): the
-                            // latter four columns at a time, from the edge.  On the diagonal the
-                            // former is a quotient, see `mild`.
-                            const float f = jb == w ? f_diag : jb == (REV ? 3 : 0) ? f0 : jb == (REV ? 2 : 1) ? f1 : f2;
-                            const uint64_t g4 = pair(gp[3], gp[3]);
-                            uint64_t ta = REV ? pair(f, f * gp[0]) : pair(f * gp[0], f);
-                            uint64_t tb = REV ? pair(f * gp[1], f * gp[2]) : pair(f * gp[2], f * gp[1]);
-#pragma unroll
-                            for (int z = 0; z < 32; z += 4) {
-                                const int e = REV ? z : 31 - z;       // g^z at column e
-                                if (REV) {
-                                    scale2(v[e], v[e + 1], ta);
-                                    scale2(v[e + 2], v[e + 3], tb);
-                                } else {
-                                    scale2(v[e - 1], v[e], ta);
-                                    scale2(v[e - 3], v[e - 2], tb);
-                                }
-                                ta = mul2(ta, g4);
-                                tb = mul2(tb, g4);
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-                        if (jb == w) {               // the mask, on the packed pairs
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                if (REV) pk[e] = lane <= 2 * e ? pk[e] : lane == 2 * e + 1 ? pk[e] & 0xffff0000u : 0u;
-                                else pk[e] = lane > 2 * e ? pk[e] : lane == 2 * e ? pk[e] & 0xffffu : 0u;
-                            }
+                        for (int e = 0; e < 8; ++e) {
+                            if (REV) pk[e] = d <= 2 * e ? pk[e] : d == 2 * e + 1 ? pk[e] & 0xffff0000u : 0u;
+                            else pk[e] = d > 2 * e ? pk[e] : d == 2 * e ? pk[e] & 0xffffu : 0u;
                         }
                     }
-                    tmem_st16u(tmem + lb + COL_G + 16 * (jb + jb0), pk);   // over columns this warp has read
+                    tmem_st8(tmem + lb + COL_G + (c >> 1), pk);
+                };
+                // the blocks of 32 columns that this warp's 32 rows see, 16 columns a turn
+                const int c0 = REV ? 32 * w : 0, c1 = REV ? C : 32 * w + 32;
+                if (mild) {
+                    // column j times g^-(j+1), reverse g^-(n-1-j)
+                    float f = a.in_scale * decay_pow(lg, (float)(REV ? c0 + 1 - tokens(i) : -1));
+                    tmem_stream(tmem + lb + COL_G, c0, c1, [&](float (&v)[16], int c) {
+                        uint64_t ta = pair(f, f * h1), tb = pair(f * h2, f * h3);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            scale2(v[e], v[e + 1], ta);
+                            scale2(v[e + 2], v[e + 3], tb);
+                            ta = mul2(ta, pair(h4, h4));
+                            tb = mul2(tb, pair(h4, h4));
+                        }
+                        f *= h16;
+                        put(v, c);
+                    });
+                } else {
+                    tmem_stream(tmem + lb + COL_G, c0, c1, [&](float (&v)[16], int c) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int lag = REV ? c + e - row : row - c - e;
+                            v[e] *= a.in_scale * pw[lag < 0 ? 0 : lag];
+                        }
+                        put(v, c);
+                    });
                 }
+                const uint32_t none[8] = {};
+#pragma unroll 1
+                for (int c = REV ? 0 : 32 * w + 32; c < (REV ? 32 * w : C); c += 16)
+                    tmem_st8(tmem + lb + COL_G + (c >> 1), none);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -470,56 +494,56 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
             if (!ok && lane == 0) fail_now();
         }
-    } else if (warp >= 8 && warp < 12) {
+    } else if (!PRE && warp >= 8 && warp < 12) {
         // ---------------------------------------------------------------- O
-        if (!PRE) {
+        {
             const int w = warp & 3, row = w * 32 + lane;
             const uint32_t lb = (uint32_t)(w * 32) << 16;
             bool ok = true;
             for (int i = 0; i < nch; ++i) {
                 const uint32_t pi = (uint32_t)i & 1u;
                 const int nv = tokens(i);
-                ok = __all_sync(~0u, wait_bar(bar(L::QSDONE), pi, limit, s_abort));
-                if (!ok) break;
-                tc_fence_after();
-                const float rd = pw[REV ? (row < nv ? nv - 1 - row : 0) : row + 1];
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float v[32];
-                    tmem_ld32(tmem + lb + COL_O + c, v);
+                float rd = pw[REV ? (row < nv ? nv - 1 - row : 0) : row + 1];
+                if (!mild) {
+                    ok = __all_sync(~0u, wait_bar(bar(L::QSDONE), pi, limit, s_abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                    tmem_stream(tmem + lb + COL_O, 0, D, [&](float (&v)[16], int c) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) scale2(v[e], v[e + 1], pair(rd, rd));
-                    tmem_st16(tmem + lb + COL_O + c, v);
-                    tmem_st16(tmem + lb + COL_O + c + 16, v + 16);
+                        for (int e = 0; e < 16; e += 2) scale2(v[e], v[e + 1], pair(rd, rd));
+                        tmem_st16(tmem + lb + COL_O + c, v);
+                    });
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::OSC));
+                    rd = 1.f;
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::OSC));
+                rd *= a.out_scale;
 
                 ok = __all_sync(~0u, wait_bar(bar(L::PVDONE), pi, limit, s_abort));
                 if (!ok) break;
                 tc_fence_after();
-                float mean = 0.f, rstd = a.out_scale;
+                float mean = 0.f, rstd = 1.f;
                 if (NORM) {                          // a thread holds its whole row
-                    float s = 0.f;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float v[32];
-                        tmem_ld32(tmem + lb + COL_O + c, v);
+                    // mean and centred sum of squares of 16 values at a time, merged
+                    float cnt = 0.f, m2 = 0.f;
+                    tmem_stream(tmem + lb + COL_O, 0, D, [&](float (&v)[16], int) {
+                        float t = 0.f, q = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s += v[e];
-                    }
-                    mean = s / D;                    // of the unscaled row
-                    s = 0.f;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float v[32];
-                        tmem_ld32(tmem + lb + COL_O + c, v);
+                        for (int e = 0; e < 16; ++e) {
+                            v[e] *= rd;
+                            t += v[e];
+                        }
+                        t *= 1.f / 16.f;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s = fmaf(v[e] - mean, v[e] - mean, s);
-                    }
-                    rstd = a.out_scale * rsqrtf(a.out_scale * a.out_scale * (s / D) + a.norm.eps);
+                        for (int e = 0; e < 16; ++e) q = fmaf(v[e] - t, v[e] - t, q);
+                        const float r = __fdividef(16.f, cnt + 16.f), dm = t - mean;
+                        mean = fmaf(dm, r, mean);
+                        m2 += fmaf(dm * dm, cnt * r, q);
+                        cnt += 16.f;
+                    });
+                    rstd = rsqrtf(m2 / D + a.norm.eps);
                 }
                 // G and A X have read this chunk's A tile: the rows are staged over it and leave
                 // by a tensor store a warp (whole rows), or one by one at a sequence's end
@@ -528,39 +552,40 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 const int64_t row0 = (int64_t)chunk_id(i) * C;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
                                      (chain * a.T + row0 + row) * D;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float v[32];
-                    tmem_ld32(tmem + lb + COL_O + c, v);
+                const uint32_t to = tile(st, XA) + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
+                tmem_stream(tmem + lb + COL_O, 0, D, [&](float (&v)[16], int c) {
                     if (NORM) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = (v[e] - mean) * rstd;
-                        if (a.norm.weight)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] *= __ldg(a.norm.weight + c + e);
-                        if (a.norm.bias)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] += __ldg(a.norm.bias + c + e);
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 wt = a.norm.weight ? __ldg(reinterpret_cast<const float4 *>(a.norm.weight + c + e))
+                                                            : make_float4(1.f, 1.f, 1.f, 1.f);
+                            const float4 bs = a.norm.bias ? __ldg(reinterpret_cast<const float4 *>(a.norm.bias + c + e))
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                            v[e] = fmaf(fmaf(v[e], rd, -mean) * rstd, wt.x, bs.x);
+                            v[e + 1] = fmaf(fmaf(v[e + 1], rd, -mean) * rstd, wt.y, bs.y);
+                            v[e + 2] = fmaf(fmaf(v[e + 2], rd, -mean) * rstd, wt.z, bs.z);
+                            v[e + 3] = fmaf(fmaf(v[e + 3], rd, -mean) * rstd, wt.w, bs.w);
+                        }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) scale2(v[e], v[e + 1], pair(rstd, rstd));
+                        for (int e = 0; e < 16; e += 2) scale2(v[e], v[e + 1], pair(rd, rd));
                     }
-                    uint32_t pk[16];
+                    uint32_t pk[8];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                    for (int e = 0; e < 8; ++e) pk[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
                     if (whole) {
-                        const uint32_t to = tile(st, XA) + (uint32_t)(c >> 6) * HALF + (row >> 3) * 1024u + (row & 7) * 128u;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            st_shared_v4(to + ((((uint32_t)(c & 32) >> 3) + e ^ (row & 7u)) << 4), pk[4 * e],
-                                         pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+                        for (int e = 0; e < 2; ++e)
+                            st_shared_v4(to + (uint32_t)(c >> 6) * HALF +
+                                             (((((uint32_t)c & 63u) >> 3) + e ^ ((uint32_t)row & 7u)) << 4),
+                                         pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                     } else if (row < nv) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 2; ++e)
                             *reinterpret_cast<uint4 *>(out + c + 8 * e) =
                                 make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                     }
-                }
+                });
                 tc_fence_before();
                 if (whole) fence_proxy_async();
                 __syncwarp();
@@ -579,10 +604,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             if (lane == 0) bulk_wait0();
             if (!ok && lane == 0) fail_now();
         }
-    } else if (warp >= 12 && warp < 16) {
+    } else if (warp < 16 || warp >= 24) {
         // ---------------------------------------------------------------- (diag(w) B)^T
         reg_dec<REGS_K>();
-        const int w = warp & 3;
+        // the group: warps 12-15 and 24-27, and in a PRE launch 4-11 too
+        const int w = warp & 3, b = warp >= 24 ? 1 : warp >= 12 ? 0 : warp >= 8 ? 3 : 2;
         const uint32_t lb = (uint32_t)(w * 32) << 16;
         const bool mine = w * 32 < D;
         bool ok = true;
@@ -601,7 +627,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     kt[j] = j < nv ? a.in_scale * pw[REV ? j + 1 : nv - 1 - j] : 0.f;
                 ok = __all_sync(~0u, wait_bar(full(st, XC), ph, limit, s_abort));
                 if (!ok) break;
-                for (int j = nv + w; j < C; j += 4)
+                for (int j = nv + 4 * b + w; j < C; j += 4 * L::KG)
                     for (int x = lane; x < D / 4; x += 32) {   // D / 8 pieces of B, as many of C
                         const uint32_t y = (uint32_t)x % (D / 8);
                         st_shared_v4(tile(st, x < D / 8 ? XB_ : XC) + (y >> 3) * HALF + sw128(j, y & 7),
@@ -617,9 +643,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
             // ldmatrix x4: matrices (tokens +0, +8) x (rows +0, +8) of X, 16 rows a half-warp
             const uint32_t r8 = (uint32_t)lane & 7u, m = (uint32_t)lane >> 3;
-            for (int u = 0; u < 4; ++u) {
-                const int b = u & 1;
-                const int use = 2 * i + (u >> 1);    // of this buffer
+            for (int u = b; u < 4; u += L::KG) {
+                const int use = (4 * i + u) / L::KG;   // of this buffer
                 if (use > 0) ok = __all_sync(~0u, wait_bar(bar(L::KFREE + b), (uint32_t)(use - 1) & 1u, limit, s_abort));
                 if (!ok) break;
                 tc_fence_after();
@@ -649,7 +674,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                                 lo[o] = top_halves(below(x));
                             }
                         }
-                        const uint32_t at = tmem + lb + ((uint32_t)(16 * h) << 16) + COL_K + KBUF * b;
+                        const uint32_t at = tmem + lb + ((uint32_t)(16 * h) << 16) + L::COL_K + KBUF * b;
                         tmem_st_16x128b_x4(at, hi);
                         tmem_st_16x128b_x4(at + 16, mid);
                         tmem_st_16x128b_x4(at + 32, lo);
@@ -660,13 +685,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar(L::KRDY + b));
-                    if (u == 3) mbar_arrive(empty(st, XB_));
+                    if (u + L::KG >= 4) mbar_arrive(empty(st, XB_));
                 }
             }
             if (!ok) break;
         }
         if (!ok && lane == 0) fail_now();
-    } else if (warp >= 16) {
+    } else {
         // ---------------------------------------------------------------- X
         reg_inc<REGS_X>();
         constexpr int XC_ = D / 2;                   // columns of a thread
