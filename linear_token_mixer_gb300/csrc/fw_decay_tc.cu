@@ -7,9 +7,10 @@
 //     P = mask . g^|i-j| . G          (bf16)
 //     O = diag(g^(i+1)) (A X) + P C                 128 x d x d, 128 x d x 128
 //     X <- g^n X + (diag(w) B)^T C                  d x d x 128, three times
-// The last product's left operand is split into three bf16 terms (24 bits of w_j b_j), so the
-// fp32 state loses nothing to its operands; P and the copy of X that A reads are rounded to bf16
-// once, like the output rows.
+// The last product's left operand is split into bf16 terms, so that the fp32 state loses nothing to
+// its operands: three (24 bits of w_j b_j) where the chunk still weighs in the state that is
+// returned, two (16 bits) where e^-3.5 of it or less is left by then, or none is returned.  P and
+// the copy of X that A reads are rounded to bf16 once, like the output rows.
 //
 // One CTA per chain, or per segment of a chain where chains are few, warp-specialised:
 //   warp 0       TMA producer: tiles of B, A, C (128 x d, 128-byte swizzle), each released on
@@ -260,6 +261,13 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         atomicExch(a.err, kDevErrTimeout);
     };
     auto chunk_id = [&](int i) -> int { return REV ? sg.total - 1 - (sg.first + i) : sg.first + i; };
+    // Does chunk i's update need the third term?  Two leave 2^-17 of it, and 2^-17 e^-3.5 = 2.3e-7 of
+    // the returned state.
+    auto third = [&](int i) -> bool {
+        if (!a.X_out) return false;
+        const int64_t done = (int64_t)(sg.first + i + 1) * C;   // tokens up to the end of chunk i, at most
+        return !((float)(n - done) * lg <= -3.5f);
+    };
     auto tokens = [&](int i) -> int { return step_tokens<REV>(n, sg.total, sg.first + i); };
 
     if (tid == 0) {
@@ -370,6 +378,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             bool ok = true;
             for (int i = 0; i < nch && ok; ++i) {
                 const int st = i % L::NST;
+                const int terms = third(i) ? 3 : 2;
                 ok = wait_bar(full(st, XC), (uint32_t)(i / L::NST) & 1u, limit, s_abort) &&
                      (i == 0 || wait_bar(bar(L::UFREE), (uint32_t)(i - 1) & 1u, limit, s_abort));
 #pragma unroll 1
@@ -384,8 +393,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                         for (int term = 2; term >= 0; --term)   // the small terms first
-                            mma_bf16_ta(tmem + COL_U, tmem + L::COL_K + KBUF * b + 16 * term + 8 * kk,
-                                        dc + (2 * u + kk) * 128, id, u > 0 || kk > 0 || term < 2);
+                            if (term < terms)
+                                mma_bf16_ta(tmem + COL_U, tmem + L::COL_K + KBUF * b + 16 * term + 8 * kk,
+                                            dc + (2 * u + kk) * 128, id, u > 0 || kk > 0 || term < terms - 1);
                     mma_commit(bar(L::KFREE + b));
                 }
                 if (!ok) break;
@@ -643,42 +653,48 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
             // ldmatrix x4: matrices (tokens +0, +8) x (rows +0, +8) of X, 16 rows a half-warp
             const uint32_t r8 = (uint32_t)lane & 7u, m = (uint32_t)lane >> 3;
+            const bool lo3 = third(i);
             for (int u = b; u < 4; u += L::KG) {
                 const int use = (4 * i + u) / L::KG;   // of this buffer
+                // thread t: tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3
+                uint64_t wv[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    wv[c] = *reinterpret_cast<const uint64_t *>(wt + 32 * u + 8 * c + 2 * (lane & 3));
+                uint32_t hi[8], mid[8], lo[8];
+                auto form = [&](int h) {             // rows w * 32 + 16 h .. +15 of X
+#pragma unroll
+                    for (int t2 = 0; t2 < 2; ++t2) { // tokens 32 u + 16 t2 .. +15
+                        const uint32_t row = 32u * u + 16u * t2 + 8u * (m >> 1) + r8;
+                        const uint32_t dd = (uint32_t)w * 32u + 16u * h + 8u * (m & 1u);
+                        uint32_t k2[4];              // (tokens 0-7, rows 0-7), (0-7, 8-15), (8-15, 0-7), ..
+                        ldmatrix_x4_trans(tile(st, XB_) + (dd >> 6) * HALF + sw128(row, (dd & 63u) >> 3), k2);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int c = 2 * t2 + (z >> 1), o = 2 * c + (z & 1);
+                            uint64_t x = mul2(pair(__uint_as_float(k2[z] << 16),
+                                                   __uint_as_float(k2[z] & 0xffff0000u)), wv[c]);
+                            hi[o] = top_halves(x);
+                            x = below(x);
+                            mid[o] = top_halves(x);
+                            if (lo3) lo[o] = top_halves(below(x));
+                        }
+                    }
+                };
+                auto store = [&](int h) {
+                    const uint32_t at = tmem + lb + ((uint32_t)(16 * h) << 16) + L::COL_K + KBUF * b;
+                    tmem_st_16x128b_x4(at, hi);
+                    tmem_st_16x128b_x4(at + 16, mid);
+                    if (lo3) tmem_st_16x128b_x4(at + 32, lo);
+                };
+                if (mine) form(0);                   // before the buffer is free
                 if (use > 0) ok = __all_sync(~0u, wait_bar(bar(L::KFREE + b), (uint32_t)(use - 1) & 1u, limit, s_abort));
                 if (!ok) break;
                 tc_fence_after();
                 if (mine) {
-                    // thread t: tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3
-                    uint64_t wv[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        wv[c] = *reinterpret_cast<const uint64_t *>(wt + 32 * u + 8 * c + 2 * (lane & 3));
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {    // rows w * 32 + 16 h .. +15 of X
-                        uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-                        for (int t2 = 0; t2 < 2; ++t2) {   // tokens 32 u + 16 t2 .. +15
-                            const uint32_t row = 32u * u + 16u * t2 + 8u * (m >> 1) + r8;
-                            const uint32_t dd = (uint32_t)w * 32u + 16u * h + 8u * (m & 1u);
-                            uint32_t k2[4];          // (tokens 0-7, rows 0-7), (0-7, 8-15), (8-15, 0-7), ..
-                            ldmatrix_x4_trans(tile(st, XB_) + (dd >> 6) * HALF + sw128(row, (dd & 63u) >> 3), k2);
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                const int c = 2 * t2 + (z >> 1), o = 2 * c + (z & 1);
-                                uint64_t x = mul2(pair(__uint_as_float(k2[z] << 16),
-                                                       __uint_as_float(k2[z] & 0xffff0000u)), wv[c]);
-                                hi[o] = top_halves(x);
-                                x = below(x);
-                                mid[o] = top_halves(x);
-                                lo[o] = top_halves(below(x));
-                            }
-                        }
-                        const uint32_t at = tmem + lb + ((uint32_t)(16 * h) << 16) + L::COL_K + KBUF * b;
-                        tmem_st_16x128b_x4(at, hi);
-                        tmem_st_16x128b_x4(at + 16, mid);
-                        tmem_st_16x128b_x4(at + 32, lo);
-                    }
+                    store(0);
+                    form(1);
+                    store(1);
                     tmem_st_wait();
                 }
                 tc_fence_before();
