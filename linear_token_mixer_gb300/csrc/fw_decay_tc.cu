@@ -48,6 +48,7 @@ constexpr uint32_t KB = 1024;
 constexpr uint32_t HALF = 16 * KB;           // 128 rows x 128 bytes: 64 columns of a tile
 constexpr int kSMs = 152;                    // the grid's target (a workspace size needs no device)
 constexpr int kMinSegChunks = 4;
+constexpr int kMaxRanked = 64;               // batch rows ranked by length (every CTA reads them all)
 
 // Registers a thread: 72 for each of the seven warpgroups at launch; P and O keep them, warps 0-3
 // and the split-operand groups hand theirs on to the two groups that hold X.
@@ -63,6 +64,7 @@ template <int D, bool PRE> struct Lay {
     // split-operand groups, a tensor-memory buffer each (a state alone leaves room for four)
     static constexpr int KG = PRE ? 4 : 2;
     static constexpr uint32_t COL_K = PRE ? 0 : 384;
+    static constexpr int UB = PRE ? 2 : 1;                       // buffers of the update
     static constexpr int NST = (int)(192 * KB / (TILE * NT));    // 2 (3), d = 64: 4 (6)
     static constexpr uint32_t XB = NST * NT * TILE;              // bf16 copy of X
     static constexpr uint32_t TAB = XB + (uint32_t)D * D * 2;
@@ -71,8 +73,8 @@ template <int D, bool PRE> struct Lay {
     // barriers
     static constexpr int FULL = 0, EMPTY = FULL + NST * NT, GDONE = EMPTY + NST * NT,
                          PRDY = GDONE + 1, QSDONE = PRDY + 1, OSC = QSDONE + 1, PVDONE = OSC + 1,
-                         OFREE = PVDONE + 1, UDONE = OFREE + 1, XBRDY = UDONE + 1,
-                         UFREE = XBRDY + 1, KRDY = UFREE + 1, KFREE = KRDY + KG, VZ = KFREE + KG,
+                         OFREE = PVDONE + 1, UDONE = OFREE + 1, XBRDY = UDONE + UB,
+                         UFREE = XBRDY + 1, KRDY = UFREE + UB, KFREE = KRDY + KG, VZ = KFREE + KG,
                          DRAIN = VZ + 1, NEVER = DRAIN + 3,
                          NBAR = NEVER + 1;
     static constexpr uint32_t MISC = BAR + NBAR * 8;
@@ -222,15 +224,27 @@ template <int D, bool REV, bool PRE, bool NORM>
 __global__ void __launch_bounds__(NTHREADS, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                const __grid_constant__ CUtensorMap tmc, const __grid_constant__ CUtensorMap tmo,
-               const ScanArgs a, const int nseg) {
+               const ScanArgs a, const int nseg, const int by_length) {
     using L = Lay<D, PRE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grid_seg = PRE ? nseg - 1 : nseg;
-    const int64_t chain = blockIdx.x / grid_seg;
+    int64_t chain = blockIdx.x / grid_seg;
     const int seg = blockIdx.x % grid_seg;
+    if (!PRE && by_length) {                        // the longest batch rows' chains start first
+        int *row = reinterpret_cast<int *>(sm + L::MISC + 8);
+        const int B = (int)(a.n_chains / a.H);
+        if (tid < B) {
+            const int mine = a.lens[tid];
+            int rank = 0;
+            for (int b = 0; b < B; ++b) rank += a.lens[b] > mine || (a.lens[b] == mine && b < tid);
+            if (rank == (int)(chain / a.H)) *row = tid;
+        }
+        __syncthreads();
+        chain = (int64_t)*row * a.H + chain % a.H;
+    }
     const int64_t n = chain_len(a.lens, chain, a.H, a.T);
     const Seg sg = seg_of(n, seg, nseg);
     const int nch = sg.last - sg.first;
@@ -279,7 +293,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                   : e % L::NT == XC ? (PRE ? 1 : 2) : 4;
             if (i == L::PRDY || i == L::OSC || i == L::OFREE || (i >= L::KRDY && i < L::KFREE)) c = 4;
             if (i == L::VZ) c = 4 * L::KG;
-            if (i == L::XBRDY || i == L::UFREE) c = 8;
+            if (i >= L::XBRDY && i < L::KRDY) c = 8;   // XBRDY, UFREE
             mbar_init(bar(i), c);
         }
         fence_mbar_init();
@@ -378,9 +392,9 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             bool ok = true;
             for (int i = 0; i < nch && ok; ++i) {
                 const int st = i % L::NST;
-                const int terms = third(i) ? 3 : 2;
+                const int terms = third(i) ? 3 : 2, ub = i % L::UB;
                 ok = wait_bar(full(st, XC), (uint32_t)(i / L::NST) & 1u, limit, s_abort) &&
-                     (i == 0 || wait_bar(bar(L::UFREE), (uint32_t)(i - 1) & 1u, limit, s_abort));
+                     (i < L::UB || wait_bar(bar(L::UFREE + ub), (uint32_t)(i / L::UB - 1) & 1u, limit, s_abort));
 #pragma unroll 1
                 for (int u = 0; u < 4 && ok; ++u) {
                     const int b = u % L::KG;
@@ -394,12 +408,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
 #pragma unroll
                         for (int term = 2; term >= 0; --term)   // the small terms first
                             if (term < terms)
-                                mma_bf16_ta(tmem + COL_U, tmem + L::COL_K + KBUF * b + 16 * term + 8 * kk,
+                                mma_bf16_ta(tmem + COL_U + 128 * ub, tmem + L::COL_K + KBUF * b + 16 * term + 8 * kk,
                                             dc + (2 * u + kk) * 128, id, u > 0 || kk > 0 || term < terms - 1);
                     mma_commit(bar(L::KFREE + b));
                 }
                 if (!ok) break;
-                mma_commit(bar(L::UDONE));
+                mma_commit(bar(L::UDONE + ub));
                 mma_commit(empty(st, XC));
             }
             if (!ok) fail_now();
@@ -772,7 +786,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         for (int i = 0; i < nch; ++i) {
             const float g = pw[tokens(i)];
             const bool more = !PRE && i + 1 < nch;
-            ok = __all_sync(~0u, wait_bar(bar(L::UDONE), (uint32_t)i & 1u, limit, s_abort) &&
+            const int ub = i % L::UB;
+            ok = __all_sync(~0u, wait_bar(bar(L::UDONE + ub), (uint32_t)(i / L::UB) & 1u, limit, s_abort) &&
                                      (!more || wait_bar(bar(L::QSDONE), (uint32_t)i & 1u, limit, s_abort)));
             if (!ok) break;
             tc_fence_after();
@@ -780,7 +795,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
 #pragma unroll
                 for (int e = 0; e < XC_; e += 16) {
                     float u[16];
-                    tmem_ld16(tmem + lb + COL_U + c0 + e, u);
+                    tmem_ld16(tmem + lb + COL_U + 128 * ub + c0 + e, u);
 #pragma unroll
                     for (int z = 0; z < 16; z += 2) {
                         const float2 r = halves(fma2(pair(g, g), pair(x[e + z], x[e + z + 1]), pair(u[z], u[z + 1])));
@@ -794,7 +809,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(bar(L::UFREE));
+                mbar_arrive(bar(L::UFREE + ub));
                 if (more) mbar_arrive(bar(L::XBRDY));
             }
         }
@@ -863,14 +878,17 @@ cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
         constexpr int smem = (int)Lay<D, true>::ALLOC;
         if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
             return e;
-        k<<<(unsigned)(a.n_chains * (nseg - 1)), NTHREADS, smem, s>>>(ta, tb, tc, to, a, nseg);
+        k<<<(unsigned)(a.n_chains * (nseg - 1)), NTHREADS, smem, s>>>(ta, tb, tc, to, a, nseg, 0);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     auto k = a.norm.on ? scan_tc_kernel<D, REV, false, true> : scan_tc_kernel<D, REV, false, false>;
     constexpr int smem = (int)Lay<D, false>::ALLOC;
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
         return e;
-    k<<<(unsigned)(a.n_chains * nseg), NTHREADS, smem, s>>>(ta, tb, tc, to, a, nseg);
+    // Padded batches of more chains than SMs: the CTAs of the longest rows start first, so that none
+    // of them runs alone in the end.
+    const int by_length = a.lens && a.n_chains > kSMs && a.n_chains / a.H <= kMaxRanked;
+    k<<<(unsigned)(a.n_chains * nseg), NTHREADS, smem, s>>>(ta, tb, tc, to, a, nseg, by_length);
     return cudaGetLastError();
 }
 
