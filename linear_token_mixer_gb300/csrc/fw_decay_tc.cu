@@ -33,6 +33,7 @@
 // next wait, copies and MMAs in flight are drained, tensor memory is freed and the kernel exits.
 #include <cudaTypedefs.h>
 
+#include <climits>
 #include <mutex>
 
 #include "fw_decay_tc.cuh"
@@ -116,11 +117,6 @@ __device__ __forceinline__ Seg seg_of(int64_t n, int seg, int nseg) {
     s.first = (int)((int64_t)seg * s.total / nseg);
     s.last = (int)((int64_t)(seg + 1) * s.total / nseg);
     return s;
-}
-// Tokens of processing step i of a chain of n tokens in `total` chunks.
-template <bool REV> __device__ __forceinline__ int step_tokens(int64_t n, int total, int i) {
-    const int c = REV ? total - 1 - i : i;
-    return c == total - 1 ? (int)(n - (int64_t)c * C) : C;
 }
 template <bool REV>
 __device__ __forceinline__ int64_t seg_tokens(int64_t n, const Seg &s) {
@@ -270,19 +266,34 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     auto empty = [&](int st, int x) -> uint32_t { return bar(L::EMPTY + st * L::NT + x); };
     auto tile = [&](int st, int x) -> uint32_t { return sb + (uint32_t)(st * L::NT + x) * L::TILE; };
     constexpr int XB_ = 0, XC = 1, XA = 2;          // tiles of a stage: B, C and (not PRE) A
+    struct Ring {                                   // stage of a chunk and the phase of its barriers
+        int st = 0;
+        uint32_t ph = 0;
+        __device__ __forceinline__ void next() {
+            if (++st == L::NST) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+    };
     auto fail_now = [&]() {
         *s_abort = 1;
         atomicExch(a.err, kDevErrTimeout);
     };
     auto chunk_id = [&](int i) -> int { return REV ? sg.total - 1 - (sg.first + i) : sg.first + i; };
-    // Does chunk i's update need the third term?  Two leave 2^-17 of it, and 2^-17 e^-3.5 = 2.3e-7 of
-    // the returned state.
-    auto third = [&](int i) -> bool {
-        if (!a.X_out) return false;
-        const int64_t done = (int64_t)(sg.first + i + 1) * C;   // tokens up to the end of chunk i, at most
-        return !((float)(n - done) * lg <= -3.5f);
-    };
-    auto tokens = [&](int i) -> int { return step_tokens<REV>(n, sg.total, sg.first + i); };
+    // The chunk of this segment that a sequence's end cuts short (-1: none), and its tokens.
+    const int tail_tokens = (int)(n - (int64_t)(sg.total - 1) * C);
+    const int tail_i = tail_tokens == C ? -1 : (REV ? 0 : sg.total - 1) - sg.first;
+    auto tokens = [&](int i) -> int { return i == tail_i ? tail_tokens : C; };
+    // From chunk `third_from` on the update takes the third term: two leave 2^-17 of it, and
+    // 2^-17 e^-3.5 = 2.3e-7 of the returned state.  (A chunk early rather than late; all of them
+    // without decay.)
+    int third_from = 0;
+    if (!a.X_out) third_from = INT_MAX;
+    else if (lg < 0.f) {
+        const float left = (float)n - 3.5f / -lg;    // tokens processed when e^-3.5 begins to matter
+        third_from = max((int)(fmaxf(left, 0.f) / C) - 2 - sg.first, 0);
+    }
 
     if (tid == 0) {
         for (int i = 0; i < L::NBAR; ++i) {
@@ -305,8 +316,19 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = __shfl_sync(~0u, *s_tmem, 0);
 
+    // Every MMA of this warp has finished before it leaves.
+    auto drain = [&](bool ok, int which) {
+        if (lane == 0) {
+            if (!ok) fail_now();
+            if (nch > 0) {
+                mma_commit(bar(L::DRAIN + which));
+                mbar_wait(bar(L::DRAIN + which), 0, kDrainNs);
+            }
+        }
+        __syncwarp();
+    };
     if (warp < 4) {
       reg_dec<REGS_W0>();
       if (warp == 0) {
@@ -339,118 +361,114 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+      } else if (warp == 1) {
         // ---------------------------------------------------------------- G, P C
-        if (!PRE && lane == 0) {
-            bool ok = true;
-            for (int i = 0; i < nch; ++i) {
-                const int st = i % L::NST;
-                const uint32_t ph = (uint32_t)(i / L::NST) & 1u, pi = (uint32_t)i & 1u;
-                ok = wait_bar(full(st, XB_), ph, limit, s_abort) &&
-                     wait_bar(full(st, XA), ph, limit, s_abort) &&
-                     (tokens(i) == C || wait_bar(bar(L::VZ), 0, limit, s_abort)) &&
-                     (i == 0 || wait_bar(bar(L::PVDONE), pi ^ 1u, limit, s_abort));
-                if (!ok) break;
-                tc_fence_after();
-                {
-                    constexpr uint32_t id = idesc_bf16(128, 128, false, false);
-                    const uint64_t da = sdesc_sw128(tile(st, XA), 16, 1024);
-                    const uint64_t db = sdesc_sw128(tile(st, XB_), 16, 1024);
-#pragma unroll 1
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = ((kk >> 2) * HALF + (kk & 3) * 32u) >> 4;
-                        mma_bf16(tmem + COL_G, da + off, db + off, id, kk > 0);
-                    }
-                    mma_commit(bar(L::GDONE));
-                    mma_commit(empty(st, XB_));
-                }
-                ok = wait_bar(bar(L::PRDY), pi, limit, s_abort) &&
-                     wait_bar(full(st, XC), ph, limit, s_abort) &&
-                     wait_bar(bar(mild ? L::QSDONE : L::OSC), pi, limit, s_abort);
-                if (!ok) break;
-                tc_fence_after();
-                {
-                    constexpr uint32_t id = idesc_bf16(128, D, false, true);
-                    const uint64_t dc = sdesc_sw128(tile(st, XC), HALF, 1024);
-#pragma unroll 1
-                    for (int kk = 0; kk < C / 16; ++kk)
-                        mma_bf16_ta(tmem + COL_O, tmem + COL_G + 8 * kk, dc + kk * 128, id, 1);
-                    mma_commit(bar(L::PVDONE));
-                    mma_commit(empty(st, XC));
-                }
-            }
-            if (!ok) fail_now();
-            if (nch > 0) {
-                mma_commit(bar(L::DRAIN));
-                mbar_wait(bar(L::DRAIN), 0, kDrainNs);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ---------------------------------------------------------------- state update
-        if (lane == 0) {
-            bool ok = true;
-            for (int i = 0; i < nch && ok; ++i) {
-                const int st = i % L::NST;
-                const int terms = third(i) ? 3 : 2, ub = i % L::UB;
-                ok = wait_bar(full(st, XC), (uint32_t)(i / L::NST) & 1u, limit, s_abort) &&
-                     (i < L::UB || wait_bar(bar(L::UFREE + ub), (uint32_t)(i / L::UB - 1) & 1u, limit, s_abort));
-#pragma unroll 1
-                for (int u = 0; u < 4 && ok; ++u) {
-                    const int b = u % L::KG;
-                    ok = wait_bar(bar(L::KRDY + b), (uint32_t)((4 * i + u) / L::KG) & 1u, limit, s_abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    constexpr uint32_t id = idesc_bf16(128, D, false, true);
-                    const uint64_t dc = sdesc_sw128(tile(st, XC), HALF, 1024);
-#pragma unroll 1
-                    for (int kk = 0; kk < 2; ++kk)
+        // (the issuers' loops run warp-uniform, so that addresses stay in uniform registers, and
+        // unrolled: an MMA issued from a rolled loop of one lane took about 200 cycles)
+        bool ok = true;
+        Ring r;
+        const uint64_t da0 = sdesc_sw128(tile(0, XA), 16, 1024), db0 = sdesc_sw128(tile(0, XB_), 16, 1024);
+        const uint64_t dc0 = sdesc_sw128(tile(0, XC), HALF, 1024);
+        for (int i = 0; !PRE && i < nch; ++i, r.next()) {
+            const uint32_t pi = (uint32_t)i & 1u, off_st = r.st * ((L::NT * L::TILE) >> 4);
+            const int st = r.st;
+            ok = __all_sync(~0u, wait_bar(full(st, XB_), r.ph, limit, s_abort) &&
+                                     wait_bar(full(st, XA), r.ph, limit, s_abort) &&
+                                     (i != tail_i || wait_bar(bar(L::VZ), 0, limit, s_abort)) &&
+                                     (i == 0 || wait_bar(bar(L::PVDONE), pi ^ 1u, limit, s_abort)));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+                const uint64_t da = da0 + off_st, db = db0 + off_st;
 #pragma unroll
-                        for (int term = 2; term >= 0; --term)   // the small terms first
-                            if (term < terms)
-                                mma_bf16_ta(tmem + COL_U + 128 * ub, tmem + L::COL_K + KBUF * b + 16 * term + 8 * kk,
-                                            dc + (2 * u + kk) * 128, id, u > 0 || kk > 0 || term < terms - 1);
-                    mma_commit(bar(L::KFREE + b));
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = ((kk >> 2) * HALF + (kk & 3) * 32u) >> 4;
+                    mma_bf16(tmem + COL_G, da + off, db + off, id, kk > 0);
                 }
-                if (!ok) break;
-                mma_commit(bar(L::UDONE + ub));
+                mma_commit(bar(L::GDONE));
+                mma_commit(empty(st, XB_));
+            }
+            __syncwarp();
+            ok = __all_sync(~0u, wait_bar(bar(L::PRDY), pi, limit, s_abort) &&
+                                     wait_bar(full(st, XC), r.ph, limit, s_abort) &&
+                                     wait_bar(bar(mild ? L::QSDONE : L::OSC), pi, limit, s_abort));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+                constexpr uint32_t id = idesc_bf16(128, D, false, true);
+                const uint64_t dc = dc0 + off_st;
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    mma_bf16_ta(tmem + COL_O, tmem + COL_G + 8 * kk, dc + kk * 128, id, 1);
+                mma_commit(bar(L::PVDONE));
                 mma_commit(empty(st, XC));
             }
-            if (!ok) fail_now();
-            if (nch > 0) {
-                mma_commit(bar(L::DRAIN + 1));
-                mbar_wait(bar(L::DRAIN + 1), 0, kDrainNs);
-            }
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp == 3) {
-        // ---------------------------------------------------------------- A X
-        if (!PRE && lane == 0) {
-            bool ok = true;
-            for (int i = 0; i < nch; ++i) {
-                const int st = i % L::NST;
-                const uint32_t pi = (uint32_t)i & 1u;
-                ok = wait_bar(full(st, XA), (uint32_t)(i / L::NST) & 1u, limit, s_abort) &&
-                     wait_bar(bar(L::XBRDY), pi, limit, s_abort) &&
-                     (i == 0 || wait_bar(bar(L::OFREE), pi ^ 1u, limit, s_abort));
+        if (!PRE) drain(ok, 0);
+      } else if (warp == 2) {
+        // ---------------------------------------------------------------- state update
+        bool ok = true;
+        Ring r;
+        const uint64_t dc0 = sdesc_sw128(tile(0, XC), HALF, 1024);
+        for (int i = 0; i < nch && ok; ++i, r.next()) {
+            const int st = r.st, ub = i % L::UB;
+            const bool lo3 = i >= third_from;
+            ok = __all_sync(~0u, wait_bar(full(st, XC), r.ph, limit, s_abort) &&
+                                     (i < L::UB || wait_bar(bar(L::UFREE + ub), (uint32_t)(i / L::UB - 1) & 1u, limit, s_abort)));
+            const uint64_t dc = dc0 + r.st * ((L::NT * L::TILE) >> 4);
+            const uint32_t du = tmem + COL_U + 128 * ub;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int b = u % L::KG;
+                ok = ok && __all_sync(~0u, wait_bar(bar(L::KRDY + b), (uint32_t)((4 * i + u) / L::KG) & 1u, limit, s_abort));
                 if (!ok) break;
                 tc_fence_after();
+                if (lane == 0) {
+                    constexpr uint32_t id = idesc_bf16(128, D, false, true);
+                    const uint32_t ka = tmem + L::COL_K + KBUF * b;
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {         // the small terms first
+                        const uint64_t dk = dc + (2 * u + kk) * 128;
+                        if (lo3) mma_bf16_ta(du, ka + 32 + 8 * kk, dk, id, u > 0 || kk > 0);
+                        mma_bf16_ta(du, ka + 16 + 8 * kk, dk, id, u > 0 || kk > 0 || lo3);
+                        mma_bf16_ta(du, ka + 8 * kk, dk, id, 1);
+                    }
+                    mma_commit(bar(L::KFREE + b));
+                    if (u == 3) {
+                        mma_commit(bar(L::UDONE + ub));
+                        mma_commit(empty(st, XC));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        drain(ok, 1);
+      } else {
+        // ---------------------------------------------------------------- A X
+        bool ok = true;
+        Ring r;
+        const uint64_t da0 = sdesc_sw128(tile(0, XA), 16, 1024), dx = sdesc_sw128(sb + L::XB, HALF, 1024);
+        for (int i = 0; !PRE && i < nch; ++i, r.next()) {
+            const uint32_t pi = (uint32_t)i & 1u;
+            ok = __all_sync(~0u, wait_bar(full(r.st, XA), r.ph, limit, s_abort) &&
+                                     wait_bar(bar(L::XBRDY), pi, limit, s_abort) &&
+                                     (i == 0 || wait_bar(bar(L::OFREE), pi ^ 1u, limit, s_abort)));
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
                 constexpr uint32_t id = idesc_bf16(128, D, false, true);
-                const uint64_t da = sdesc_sw128(tile(st, XA), 16, 1024);
-                const uint64_t dx = sdesc_sw128(sb + L::XB, HALF, 1024);
-#pragma unroll 1
+                const uint64_t da = da0 + r.st * ((L::NT * L::TILE) >> 4);
+#pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     mma_bf16(tmem + COL_O, da + (((kk >> 2) * HALF + (kk & 3) * 32u) >> 4),
                              dx + kk * 128, id, kk > 0);
                 mma_commit(bar(L::QSDONE));
             }
-            if (!ok) fail_now();
-            if (nch > 0) {
-                mma_commit(bar(L::DRAIN + 2));
-                mbar_wait(bar(L::DRAIN + 2), 0, kDrainNs);
-            }
+            __syncwarp();
         }
-        __syncwarp();
+        if (!PRE) drain(ok, 2);
       }
     } else if (!PRE && warp >= 4 && warp < 8) {
         // ---------------------------------------------------------------- P
@@ -636,11 +654,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         const uint32_t lb = (uint32_t)(w * 32) << 16;
         const bool mine = w * 32 < D;
         bool ok = true;
-        for (int i = 0; i < nch; ++i) {
-            const int st = i % L::NST;
-            const uint32_t ph = (uint32_t)(i / L::NST) & 1u;
+        Ring r;
+        for (int i = 0; i < nch; ++i, r.next()) {
+            const int st = r.st;
+            const uint32_t ph = r.ph;
+            const bool tail = i == tail_i;
             const int nv = tokens(i);
-            const bool tail = nv < C;
             ok = __all_sync(~0u, wait_bar(full(st, XB_), ph, limit, s_abort));
             if (!ok) break;
             const float *wt = kw;
@@ -667,7 +686,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
             // ldmatrix x4: matrices (tokens +0, +8) x (rows +0, +8) of X, 16 rows a half-warp
             const uint32_t r8 = (uint32_t)lane & 7u, m = (uint32_t)lane >> 3;
-            const bool lo3 = third(i);
+            const bool lo3 = i >= third_from;
             for (int u = b; u < 4; u += L::KG) {
                 const int use = (4 * i + u) / L::KG;   // of this buffer
                 // thread t: tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3
