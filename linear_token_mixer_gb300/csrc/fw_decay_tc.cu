@@ -153,17 +153,12 @@ __device__ __forceinline__ void tmem_landed(float (&v)[16]) {
 // do_(v, c) for the columns c = c0, c0 + 16, .. < c1 (an even number of pieces) of this warp's lanes,
 // each piece's load in flight while the one before it is worked on.
 template <typename F> __device__ __forceinline__ void tmem_stream(uint32_t taddr, int c0, int c1, F do_) {
-    float v[16], u[16];
-    if (c0 >= c1) return;
-    tmem_fetch16(taddr + c0, v);
+    float v[16];
 #pragma unroll 1
-    for (int c = c0; c < c1; c += 32) {
+    for (int c = c0; c < c1; c += 16) {
+        tmem_fetch16(taddr + c, v);
         tmem_landed(v);
-        tmem_fetch16(taddr + c + 16, u);
         do_(v, c);
-        tmem_landed(u);
-        if (c + 32 < c1) tmem_fetch16(taddr + c + 32, v);
-        do_(u, c + 16);
     }
 }
 
@@ -720,16 +715,18 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     tmem_st_16x128b_x4(at + 16, mid);
                     if (lo3) tmem_st_16x128b_x4(at + 32, lo);
                 };
-                if (mine) form(0);                   // before the buffer is free
-                if (use > 0) ok = __all_sync(~0u, wait_bar(bar(L::KFREE + b), (uint32_t)(use - 1) & 1u, limit, s_abort));
-                if (!ok) break;
-                tc_fence_after();
-                if (mine) {
-                    store(0);
-                    form(1);
-                    store(1);
-                    tmem_st_wait();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (mine) form(h);               // the first before the buffer is free
+                    if (h == 0) {
+                        if (use > 0) ok = __all_sync(~0u, wait_bar(bar(L::KFREE + b), (uint32_t)(use - 1) & 1u, limit, s_abort));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (mine) store(h);
                 }
+                if (!ok) break;
+                if (mine) tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
