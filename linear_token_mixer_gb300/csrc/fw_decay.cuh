@@ -15,9 +15,46 @@
 //     dk = reverse scan(v, do, q; X0 = dS_T^T)         in_scale  = scale
 #pragma once
 
+#include <atomic>
+
 #include "fw_internal.cuh"
 
 namespace fw {
+
+// Let kernel k use `bytes` of dynamic shared memory: one driver call a device, not one a launch.
+// `done` is the kernel's own (a bit for each device).
+template <typename K> cudaError_t allow_smem(K k, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+__device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_grid_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launch k; `overlap`: its blocks may start as soon as the blocks of the grid before it have called
+// let_next_grid_start(), and call wait_previous_grid() themselves.
+template <typename K, typename... A>
+cudaError_t launch_after(K k, dim3 grid, int threads, size_t smem, cudaStream_t stream, bool overlap, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
 
 // Output norm fused into a scan's or a step's epilogue.
 struct NormArgs {

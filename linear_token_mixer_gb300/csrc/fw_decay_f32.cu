@@ -31,11 +31,6 @@ template <int D> constexpr int threads() { return 2 * (D / 32) * 32; }
 template <int D> constexpr int ld_row() { return D + 4; }
 template <int D> constexpr int ld_col() { return D + 8; }
 
-__device__ __forceinline__ void wait_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_grid_start() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // x = hi + lo: hi rounded to 11 bits, lo what that leaves (exact in fp32; the MMA reads its top 11
 // bits, so 2^-22 |x| at most is lost).  An infinity leaves NaN.
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
@@ -355,21 +350,6 @@ scan_one(const __grid_constant__ Scans all) {
     }
 }
 
-template <typename K, typename... A>
-cudaError_t launch_after(K k, dim3 grid, int threads, size_t smem, cudaStream_t stream, bool overlap, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k, args...);
-}
-
 template <int D>
 cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     const ScanArgs &s = all.s[0];
@@ -382,15 +362,14 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     for (int i = 0; i < n; ++i) one = one && !(all.s[i].X_out && all.s[i].X_out == all.s[i].X0);
     if (one) {
         constexpr int smem = smem_l > smem_o ? smem_l : smem_o;
-        if ((e = cudaFuncSetAttribute(scan_one<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-            return e;
+        static std::atomic<uint64_t> done{0};
+        if ((e = allow_smem(scan_one<D>, smem, done)) != cudaSuccess) return e;
         scan_one<D><<<dim3((unsigned)s.n_chains, n, 2), threads<D>(), smem, stream>>>(all);
         return cudaGetLastError();
     }
-    if ((e = cudaFuncSetAttribute(scan_local<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_l)) != cudaSuccess)
-        return e;
-    if ((e = cudaFuncSetAttribute(scan_out<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_o)) != cudaSuccess)
-        return e;
+    static std::atomic<uint64_t> local_done{0}, out_done{0};
+    if ((e = allow_smem(scan_local<D>, smem_l, local_done)) != cudaSuccess) return e;
+    if ((e = allow_smem(scan_out<D>, smem_o, out_done)) != cudaSuccess) return e;
     if ((e = launch_after(scan_local<D>, grid, threads<D>(), smem_l, stream, false, all, nch)) != cudaSuccess) return e;
     const dim3 gp((unsigned)(s.n_chains * (D * D / 256)), n);
     if ((e = launch_after(scan_prefix<D>, gp, 256, 0, stream, true, all, nch)) != cudaSuccess) return e;
@@ -408,7 +387,7 @@ size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype) {
 cudaError_t launch_scans(const ScanArgs *s, int n, cudaStream_t stream) {
     if (s[0].dtype == FW_BF16) {
         for (int i = 0; i < n; ++i) {
-            const cudaError_t e = launch_scan_tc(s[i], stream);
+            const cudaError_t e = launch_scan_tc(s[i], i > 0, stream);
             if (e != cudaSuccess) return e;
         }
         return cudaSuccess;

@@ -49,6 +49,10 @@ constexpr uint32_t KB = 1024;
 constexpr uint32_t HALF = 16 * KB;           // 128 rows x 128 bytes: 64 columns of a tile
 constexpr int kSMs = 152;                    // the grid's target (a workspace size needs no device)
 constexpr int kMinSegChunks = 4;
+// The launches of a call overlap (programmatic dependent launch).  A segment kernel's successor
+// waits for it before it begins; a scan that follows an independent one takes the SMs as they come
+// free and waits for it only before it ends, so that the last grid to end is the last of all.
+constexpr int kWaitFirst = 1, kWaitLast = 2;
 constexpr int kMaxRanked = 64;               // batch rows ranked by length (every CTA reads them all)
 
 // Registers a thread: 72 for each of the seven warpgroups at launch; P and O keep them, warps 0-3
@@ -215,8 +219,10 @@ template <int D, bool REV, bool PRE, bool NORM>
 __global__ void __launch_bounds__(NTHREADS, 1)
 scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                const __grid_constant__ CUtensorMap tmc, const __grid_constant__ CUtensorMap tmo,
-               const ScanArgs a, const int nseg, const int by_length) {
+               const ScanArgs a, const int nseg, const int by_length, const int order) {
     using L = Lay<D, PRE>;
+    let_next_grid_start();
+    if (order & kWaitFirst) wait_previous_grid();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(sm);
@@ -240,7 +246,10 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     const Seg sg = seg_of(n, seg, nseg);
     const int nch = sg.last - sg.first;
     const bool final_seg = !PRE && seg == nseg - 1;
-    if (nch == 0 && !(final_seg && a.X_out) && !(PRE && seg == 0)) return;
+    if (nch == 0 && !(final_seg && a.X_out) && !(PRE && seg == 0)) {
+        if (order & kWaitLast) wait_previous_grid();
+        return;
+    }
     const uint64_t limit = (uint64_t)a.wait_ns;
     const float lg = a.log_decay[chain % a.H];
     // Within a chunk of a mild head every quotient of powers of g is safe in fp32 and bf16
@@ -842,6 +851,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     if (warp == 3) tmem_dealloc(tmem, TMEM_COLS);
+    if (order & kWaitLast) wait_previous_grid();
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -881,8 +891,9 @@ int segments(int64_t n_chains, int64_t T) {
     return s < 1 ? 1 : (int)s;
 }
 
+// `follows`: behind another scan of the same call.
 template <int D, bool REV>
-cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
+cudaError_t launch(const ScanArgs &a, bool follows, cudaStream_t s) {
     CUtensorMap ta, tb, tc, to;
     if (!make_map(&ta, a.a, a.T, a.n_chains, D) || !make_map(&tb, a.b, a.T, a.n_chains, D) ||
         !make_map(&tc, a.c, a.T, a.n_chains, D) || !make_map(&to, a.out, a.T, a.n_chains, D, 32))
@@ -892,20 +903,21 @@ cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
     if (nseg > 1) {
         auto k = scan_tc_kernel<D, REV, true, false>;
         constexpr int smem = (int)Lay<D, true>::ALLOC;
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+        static std::atomic<uint64_t> pre_done{0};
+        if ((e = allow_smem(k, smem, pre_done)) != cudaSuccess) return e;
+        if ((e = launch_after(k, dim3((unsigned)(a.n_chains * (nseg - 1))), NTHREADS, smem, s, follows, ta, tb,
+                              tc, to, a, nseg, 0, follows ? kWaitLast : 0)) != cudaSuccess)
             return e;
-        k<<<(unsigned)(a.n_chains * (nseg - 1)), NTHREADS, smem, s>>>(ta, tb, tc, to, a, nseg, 0);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     auto k = a.norm.on ? scan_tc_kernel<D, REV, false, true> : scan_tc_kernel<D, REV, false, false>;
     constexpr int smem = (int)Lay<D, false>::ALLOC;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-        return e;
+    static std::atomic<uint64_t> done[2];
+    if ((e = allow_smem(k, smem, done[a.norm.on ? 1 : 0])) != cudaSuccess) return e;
     // Padded batches of more chains than SMs: the CTAs of the longest rows start first, so that none
     // of them runs alone in the end.
     const int by_length = a.lens && a.n_chains > kSMs && a.n_chains / a.H <= kMaxRanked;
-    k<<<(unsigned)(a.n_chains * nseg), NTHREADS, smem, s>>>(ta, tb, tc, to, a, nseg, by_length);
-    return cudaGetLastError();
+    return launch_after(k, dim3((unsigned)(a.n_chains * nseg)), NTHREADS, smem, s, nseg > 1 || follows, ta, tb, tc,
+                        to, a, nseg, by_length, nseg > 1 ? kWaitFirst : follows ? kWaitLast : 0);
 }
 
 }  // namespace
@@ -915,9 +927,9 @@ size_t scan_tc_workspace(int64_t n_chains, int64_t T, int d) {
     return nseg > 1 ? (size_t)n_chains * nseg * d * d * sizeof(float) : 0;
 }
 
-cudaError_t launch_scan_tc(const ScanArgs &a, cudaStream_t s) {
-    if (a.d == 64) return a.rev ? launch<64, true>(a, s) : launch<64, false>(a, s);
-    return a.rev ? launch<128, true>(a, s) : launch<128, false>(a, s);
+cudaError_t launch_scan_tc(const ScanArgs &a, bool follows, cudaStream_t s) {
+    if (a.d == 64) return a.rev ? launch<64, true>(a, follows, s) : launch<64, false>(a, follows, s);
+    return a.rev ? launch<128, true>(a, follows, s) : launch<128, false>(a, follows, s);
 }
 
 }  // namespace fw

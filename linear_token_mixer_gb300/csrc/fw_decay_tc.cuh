@@ -6,6 +6,7 @@
 namespace fw {
 
 size_t scan_tc_workspace(int64_t n_chains, int64_t T, int d);
-cudaError_t launch_scan_tc(const ScanArgs &a, cudaStream_t s);
+// `follows`: behind another scan of the same call, of which it is independent.
+cudaError_t launch_scan_tc(const ScanArgs &a, bool follows, cudaStream_t s);
 
 }  // namespace fw

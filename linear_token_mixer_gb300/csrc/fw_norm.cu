@@ -496,9 +496,11 @@ cudaError_t forward(const LayerNormArgs &a, cudaStream_t s) {
     } else {
         if (w <= 32) return fwd<T, 1, 32, 1>(a, s);
         if (w <= 128) return fwd<T, 1, 32, 4>(a, s);
-        if (w <= 512) return fwd<T, 1, 32, 16>(a, s);
-        if (w <= 2048) return fwd<T, 1, 128, 16>(a, s);
-        if (w <= 4096) return fwd<T, 1, 256, 16>(a, s);
+        if (w <= 256) return fwd<T, 1, 32, 8>(a, s);
+        if (w <= 512) return fwd<T, 1, 64, 8>(a, s);
+        if (w <= 1024) return fwd<T, 1, 128, 8>(a, s);
+        if (w <= 2048) return fwd<T, 1, 256, 8>(a, s);
+        if (w <= 4096) return fwd<T, 1, 512, 8>(a, s);
         if (w <= 16384) return fwd<T, 1, 1024, 16>(a, s);
     }
     ln_fwd_long<T><<<(unsigned)a.rows, 1024, 0, s>>>(a);
