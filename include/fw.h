@@ -322,6 +322,9 @@ int fw_window_step(const void *q, const void *k_prev, const void *v, const float
  *               initialised and mean nothing after the call.  Calls that may
  *               overlap (two streams, two captured graphs replayed at once)
  *               need a workspace each.
+ *   A NaN or infinity in a row of v (in the backward pass of q, k or d_o) can
+ *   reach, besides the rows that depend on it, other rows of the 128 tokens of
+ *   its chain that are worked on together.
  *   No output may overlap an input, another output or the workspace, except
  *   S_T = S0.
  */

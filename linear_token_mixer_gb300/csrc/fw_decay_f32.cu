@@ -11,7 +11,8 @@
 // are fp32.  A chunk of 64 keeps the 64 x 64 part no larger than the d x d part and gives
 // B*H*T/64 blocks, which is what short batches need to fill the GPU.  The three launches overlap
 // their starts (programmatic dependent launch): scan_out loads its rows and forms the masked
-// scores before it waits for the states.
+// scores before it waits for the states, which it reads straight into the MMAs' operands.  Chains
+// of one chunk need no workspace and no order between the parts: one launch does both (scan_one).
 #include "fw_decay_tc.cuh"
 #include "fw_sm100.cuh"
 

@@ -503,10 +503,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                     tmem_st8(tmem + lb + COL_G + (c >> 1), pk);
                 };
                 // the blocks of 32 columns that this warp's 32 rows see, 16 columns a turn
+                const int nv = tokens(i);
                 const int c0 = REV ? 32 * w : 0, c1 = REV ? C : 32 * w + 32;
                 if (mild) {
                     // column j times g^-(j+1), reverse g^-(n-1-j)
-                    float f = a.in_scale * decay_pow(lg, (float)(REV ? c0 + 1 - tokens(i) : -1));
+                    float f = a.in_scale * decay_pow(lg, (float)(REV ? c0 + 1 - nv : -1));
                     tmem_stream(tmem + lb + COL_G, c0, c1, [&](float (&v)[16], int c) {
                         uint64_t ta = pair(f, f * h1), tb = pair(f * h2, f * h3);
 #pragma unroll
@@ -524,7 +525,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int lag = REV ? c + e - row : row - c - e;
-                            v[e] *= a.in_scale * pw[lag < 0 ? 0 : lag];
+                            // (behind a sequence's end the power may have overflowed)
+                            v[e] *= REV && c + e >= nv ? 0.f : a.in_scale * pw[lag < 0 ? 0 : lag];
                         }
                         put(v, c);
                     });
@@ -883,11 +885,14 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t T, int64_t nc, int d, int
 }
 
 // Segments of each chain: as many as fill the GPU with one CTA an SM, none shorter than
-// kMinSegChunks chunks (a segment's state is read back from memory by the ones behind it).
+// kMinSegChunks chunks.  The last segment adds up the states of all before it, about 0.6 us each,
+// against about 4.6 us a chunk for the two passes over a segment: past sqrt(5 chunks) segments the
+// sum costs more than the split saves.
 int segments(int64_t n_chains, int64_t T) {
     const int64_t chunks = (T + C - 1) / C;
     int64_t s = kSMs / n_chains;
     if (s > chunks / kMinSegChunks) s = chunks / kMinSegChunks;
+    while (s > 1 && s * s > 5 * chunks) --s;
     return s < 1 ? 1 : (int)s;
 }
 

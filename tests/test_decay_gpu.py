@@ -381,3 +381,113 @@ def test_binding_refusals_on_the_gpu():
     with pytest.raises(fw.FwError, match="SCRATCH"):
         f = [g[n].float().repeat(1, 1, 20, 1) for n in "qkv"]
         fw.decay_prefill(*f, g["ld"], workspace=torch.empty(16, device="cuda", dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", ["slow", "mixed"])
+def test_padded_batch_of_more_chains_than_fit_at_once(kind, dtype):
+    """13 x 13 chains of very different lengths (the longest start first)."""
+    B, H, T, d = 13, 13, 420, 64
+    x, g = inputs(B, H, T, d, dtype, seed=77, kind=kind)
+    ln = torch.tensor([0, 420, 1, 300, 300, 128, 127, 5, 420, 64, 256, 17, 399], dtype=torch.int32)
+    o, S = fw.decay_prefill(g["q"], g["k"], g["v"], g["ld"], g["S0"], lens=ln.cuda())
+    got = fw.decay_backward(g["q"], g["k"], g["v"], g["ld"], g["do"], g["S0"], g["dS"],
+                            lens=ln.cuda())
+    fw.check()
+    ro, rS, ref = _reference_on_gpu(g, ln, 1.0)
+    check_rows(o, ro, dtype)
+    check_state(S, rS)
+    for a, r in zip(got[:3], ref[:3]):
+        check_rows(a, r, dtype)
+    check_state(got[3], ref[3])
+
+
+@pytest.mark.parametrize("ld", [-0.46, -0.48, -3.0, -20.0, 0.46, 2.0])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_decays_on_both_sides_of_what_may_be_divided_by(ld, dtype):
+    """Heads whose decay over 128 tokens is e^-60 and around it, forward and backward, where a
+    chunk's end and a sequence's end fall together or not.  (Growing ones only for a few tokens:
+    e^0.46 a token passes fp32 after 190.)"""
+    T = 300 if ld < 0 else (100 if ld < 1 else 20)
+    x, g = inputs(1, 1, T, 64, dtype, seed=31)
+    l = torch.tensor([ld])
+    o, S = fw.decay_prefill(g["q"], g["k"], g["v"], l.cuda())
+    got = fw.decay_backward(g["q"], g["k"], g["v"], l.cuda(), g["do"])
+    ro, rS, _ = R.forward(x["q"], x["k"], x["v"], l)
+    ref = R.backward(x["q"], x["k"], x["v"], l, x["do"])
+    check_rows(o, ro, dtype)
+    check_state(S, rS)
+    for a, r in zip(got[:3], ref[:3]):
+        check_rows(a, r, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_non_finite_values_stay_behind_their_chunk(dtype):
+    x, g = inputs(1, 2, 300, 64, dtype, seed=2)
+    v = g["v"].clone()
+    v[0, 1, 200, 3] = float("inf")
+    o, S = fw.decay_prefill(g["q"], g["k"], v, g["ld"])
+    ro, rS, _ = R.forward(x["q"], x["k"], x["v"], x["ld"])
+    check_rows(o[:, :1], ro[:, :1], dtype)
+    check_rows(o[:, 1:, :128], ro[:, 1:, :128], dtype)
+    assert not torch.isfinite(o[0, 1, 200:, 3]).any() and not torch.isfinite(S[0, 1, :, 3]).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_bounded_wait_reports_and_recovers(d):
+    """A wait that nothing ends runs out: fw_check reports it, and the next call is right."""
+    L = fw.lib()
+    x, g = inputs(1, 2, 700, d, BF16, seed=1)
+    L.fw_set_wait_limit_us(2000)
+    L.fw_debug_force_timeout(1)
+    try:
+        fw.decay_prefill(g["q"], g["k"], g["v"], g["ld"])
+        with pytest.raises(fw.FwError) as ei:
+            fw.check()
+        assert ei.value.status == -7
+    finally:
+        L.fw_debug_force_timeout(0)
+        L.fw_set_wait_limit_us(0)
+    fw.check()
+    o, S = fw.decay_prefill(g["q"], g["k"], g["v"], g["ld"])
+    ro, rS, _ = R.forward(x["q"], x["k"], x["v"], x["ld"])
+    check_rows(o, ro, BF16)
+    check_state(S, rS)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_beyond_32_bits(dtype):
+    """One chain of 2^24 + 300 tokens: 2^31 + 38400 elements.  With g = e^-0.5 a row depends on the
+    500 tokens before it alone (e^-250 of the rest is left)."""
+    T, d, n = 2 ** 24 + 300, 128, 700
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    t = [torch.randn(1, 1, T, d, device="cuda", dtype=dtype, generator=gen) for _ in range(3)]
+    ld = torch.tensor([-0.5])
+    o, S = fw.decay_prefill(*t, ld.cuda())
+    fw.check()
+    cut = [z[:, :, -n:].clone() for z in t]
+    ro, rS, _ = R.forward(*cut, ld)
+    check_rows(o[:, :, -200:], ro[:, :, -200:], dtype)
+    check_state(S, rS)
+    first = R.forward(*[z[:, :, :200].clone() for z in t], ld)[0]
+    check_rows(o[:, :, :200], first, dtype)
+    if dtype == BF16:
+        do = torch.randn(1, 1, T, d, device="cuda", dtype=dtype, generator=gen)
+        got = fw.decay_backward(*t, ld.cuda(), do)
+        fw.check()
+        ref = R.backward(*cut, ld, do[:, :, -n:].clone())
+        for a, r in zip(got[:3], ref[:3]):
+            check_rows(a[:, :, -200:], r[:, :, -200:], dtype)
+
+
+def test_step_offsets_beyond_32_bits():
+    B, H, d = 2 ** 13 + 1, 16, 128            # 2^31 + 2^18 state elements
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    S = torch.randn(B, H, d, d, device="cuda", generator=gen)
+    q, k, v = (torch.randn(B, H, d, device="cuda", generator=gen) for _ in range(3))
+    ld = decays(H).cuda()
+    before = S[-1:].clone()
+    o = fw.decay_step(q, k, v, ld, S)
+    ro, rS, _ = R.forward(*(z[-1:, :, None] for z in (q, k, v)), ld, before)
+    check_rows(o[-1:, :, None], ro, F32)
+    check_state(S[-1:], rS)

@@ -160,3 +160,20 @@ def test_norm_of_the_other_paths(dtype):
                                             x["S0"].clone(), 3, **k)[0]):
         o, y = call(), call(norm=(nw, nb), norm_eps=1e-4)
         assert R.rel(y, R.layer_norm(o, nw, nb, 1e-4)[0]) <= TOL[dtype]
+
+
+def test_offsets_beyond_32_bits():
+    rows, width = 2 ** 24 + 9, 128
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(rows, width, device="cuda", dtype=BF16, generator=gen)
+    dy = torch.randn(rows, width, device="cuda", dtype=BF16, generator=gen)
+    w = torch.randn(width, device="cuda", generator=gen)
+    y, mean, rstd = fw.layer_norm(x, w)
+    dx, dw, db = fw.layer_norm_backward(dy, x, w, mean, rstd)
+    tail = slice(rows - 300, rows)
+    assert R.rel(y[tail], R.layer_norm(x[tail], w)[0]) <= TOL[BF16]
+    assert R.rel(dx[tail], R.layer_norm_backward(dy[tail], x[tail], w)[0]) <= TOL[BF16]
+    assert R.rel(mean[tail], R.layer_norm(x[tail])[1]) <= 10 * TOL[F32]   # means near zero
+    # fp32 sums of 2^24 terms over 608 x 2 or more partial sums of at most 14000 terms each
+    rdb = dy.double().sum(0).cpu()
+    assert R.rel(db, rdb) <= 14000 ** 0.5 * 2.0 ** -24 * 4
