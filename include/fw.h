@@ -97,14 +97,15 @@ typedef struct {
                     written as zeros */
 } fw_window;
 
-/* Flags (bitwise OR) of fw_prefill_ex and fw_step_ex.
+/* Flags (bitwise OR) of fw_prefill_ex and fw_step_ex, and (FW_FLAG_ZERO_REST
+ * alone) of fw_decay_prefill and fw_decay_backward.
  * FW_FLAG_RBW: read before the write, o_t = S_{t-1}^T q_t (every mode).
  * FW_FLAG_SAME_PAIR: FW_FALCON1 / FW_FALCON1A pair (phi(k_t), v_t) for every
  *   token, so the first token writes too and k_init is not used (prefill
  *   only; FW_LINATTN always pairs this way, and a step pairs whatever key it
  *   is given).  The pages name these arms without printing formulas; the
  *   readings above are the plainest ones. */
-typedef enum { FW_FLAG_RBW = 1, FW_FLAG_SAME_PAIR = 2 } fw_flag;
+typedef enum { FW_FLAG_RBW = 1, FW_FLAG_SAME_PAIR = 2, FW_FLAG_ZERO_REST = 4 } fw_flag;
 
 /* Feature map phi.  FW_FALCON1 applies it to the key only (the read uses q as
  * given); FW_LINATTN applies it to both q and k, never to v.
@@ -314,8 +315,9 @@ int fw_window_step(const void *q, const void *k_prev, const void *v, const float
  *               model: no gradient with respect to them is formed.
  *   lens        int32 [B] or NULL.  Tokens of each batch row of a padded
  *               batch, clamped to [0, T]; NULL: T for every row.  Rows of o
- *               (dq, dk, dv) from lens[b] on are left as they were, and what q,
- *               k, v and d_o hold there, NaN included, is never used.  With 0
+ *               (dq, dk, dv) from lens[b] on are left as they were (zeros with
+ *               FW_FLAG_ZERO_REST), and what q, k, v and d_o hold there, NaN
+ *               included, is never used.  With 0
  *               tokens S_T = S0 (zero without S0).
  *   workspace   device memory of at least fw_decay_workspace() bytes, owned by
  *               the caller, or NULL where that is 0.  Its contents need not be
@@ -350,11 +352,13 @@ int64_t fw_decay_workspace(const fw_shape *shape, fw_dtype dtype, int backward);
  *   o         out  [B][H][T][d] of `dtype`
  *   S_T       out  float [B][H][d][d], the state after the last token; may equal S0
  *   scale     finite
+ *   flags     0 or FW_FLAG_ZERO_REST (FW_ERR_MODE otherwise)
  */
 int fw_decay_prefill(const void *q, const void *k, const void *v, const float *log_decay,
                      const float *S0, const int32_t *lens, const fw_norm *norm, void *o,
                      float *S_T, const fw_shape *shape, fw_dtype dtype, float scale,
-                     void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+                     unsigned flags, void *workspace, int64_t workspace_bytes,
+                     cudaStream_t stream);
 
 /*
  * fw_decay_backward -- gradients of fw_decay_prefill without norm, given those
@@ -369,8 +373,8 @@ int fw_decay_prefill(const void *q, const void *k, const void *v, const float *l
 int fw_decay_backward(const void *q, const void *k, const void *v, const float *log_decay,
                       const float *S0, const int32_t *lens, const void *d_o, const float *dS_T,
                       void *dq, void *dk, void *dv, float *dS0, const fw_shape *shape,
-                      fw_dtype dtype, float scale, void *workspace, int64_t workspace_bytes,
-                      cudaStream_t stream);
+                      fw_dtype dtype, float scale, unsigned flags, void *workspace,
+                      int64_t workspace_bytes, cudaStream_t stream);
 
 /*
  * fw_decay_step -- one token for B*H states, S updated in place.

@@ -507,10 +507,11 @@ extern "C" int64_t fw_decay_workspace(const fw_shape *shape, fw_dtype dtype, int
 extern "C" int fw_decay_prefill(const void *q, const void *k, const void *v,
                                 const float *log_decay, const float *S0, const int32_t *lens,
                                 const fw_norm *norm, void *o, float *S_T, const fw_shape *shape,
-                                fw_dtype dtype, float scale, void *workspace,
+                                fw_dtype dtype, float scale, unsigned flags, void *workspace,
                                 int64_t workspace_bytes, cudaStream_t stream) {
     int st = check_decay(shape, dtype);
     if (st != FW_OK) return st;
+    if (flags & ~(unsigned)FW_FLAG_ZERO_REST) return FW_ERR_MODE;
     if (!q || !k || !v || !log_decay || !o || !S_T) return FW_ERR_NULL;
     if (any_misaligned({q, k, v, log_decay, S0, lens, o, S_T, workspace})) return FW_ERR_ALIGN;
     NormArgs na;
@@ -535,6 +536,7 @@ extern "C" int fw_decay_prefill(const void *q, const void *k, const void *v,
     s.a = q; s.b = k; s.c = v; s.X0 = S0; s.X_out = S_T; s.out = o;
     s.out_scale = scale;
     s.norm = na;
+    s.zero_rest = lens && (flags & FW_FLAG_ZERO_REST);
     s.ws = static_cast<float *>(workspace);
     const cudaError_t e = launch_scans(&s, 1, stream);
     return e == cudaSuccess ? FW_OK : cuda_fail(e);
@@ -544,9 +546,11 @@ extern "C" int fw_decay_backward(const void *q, const void *k, const void *v,
                                  const float *log_decay, const float *S0, const int32_t *lens,
                                  const void *d_o, const float *dS_T, void *dq, void *dk, void *dv,
                                  float *dS0, const fw_shape *shape, fw_dtype dtype, float scale,
-                                 void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
+                                 unsigned flags, void *workspace, int64_t workspace_bytes,
+                                 cudaStream_t stream) {
     int st = check_decay(shape, dtype);
     if (st != FW_OK) return st;
+    if (flags & ~(unsigned)FW_FLAG_ZERO_REST) return FW_ERR_MODE;
     if (!q || !k || !v || !log_decay || !d_o || !dq || !dk || !dv) return FW_ERR_NULL;
     if (any_misaligned({q, k, v, log_decay, S0, lens, d_o, dS_T, dq, dk, dv, dS0, workspace}))
         return FW_ERR_ALIGN;
@@ -572,6 +576,7 @@ extern "C" int fw_decay_backward(const void *q, const void *k, const void *v,
         s[i].ws = static_cast<float *>(workspace) + i * (need / 3 / (int64_t)sizeof(float));
         s[i].rev = i > 0;
         s[i].x0_trans = i != 1;
+        s[i].zero_rest = lens && (flags & FW_FLAG_ZERO_REST);
     }
     s[0].a = d_o; s[0].b = v; s[0].c = k; s[0].X0 = S0; s[0].out = dq; s[0].out_scale = scale;
     s[1].a = k; s[1].b = q; s[1].c = d_o; s[1].X0 = dS_T; s[1].out = dv; s[1].in_scale = scale;

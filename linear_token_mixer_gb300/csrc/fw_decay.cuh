@@ -75,6 +75,7 @@ struct ScanArgs {
     fw_dtype dtype;
     int rev;                  // reverse scan
     int x0_trans;             // X0 is stored transposed
+    int zero_rest;            // write zeros to the rows of out from lens[b] on
     float in_scale, out_scale;
     NormArgs norm;
     float *ws;                // workspace of this scan

@@ -40,13 +40,15 @@ __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
 }
 
 // acc += A B for a warp's 16 MT x 8 NT tile; element (m, k) of A at a[m * am + k * ak], element
-// (k, n) of B at b[k * bk + n * bn].
-template <int MT, int NT>
+// (k, n) of B at b[k * bk + n * bn].  The MMAs round towards zero: APART sums the two small terms on
+// their own, so that the large sum is cut a third as often.
+template <int MT, int NT, bool APART>
 __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, int am, int ak,
                                      const float *b, int bk, int bn, int K) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     a += g * am + t * ak;
     b += t * bk + g * bn;
+    float low[APART ? MT : 1][APART ? NT : 1][4] = {};
 #pragma unroll 2
     for (int k = 0; k < K; k += 8) {
         uint32_t ah[MT][4], al[MT][4];
@@ -67,8 +69,16 @@ __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, in
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    sm100::mma_tf32_16x8x8(acc[m][n], term == 0 ? al[m] : ah[m], term == 1 ? bl[n] : bh[n]);
+                    sm100::mma_tf32_16x8x8(APART && term < 2 ? low[APART ? m : 0][APART ? n : 0] : acc[m][n],
+                                           term == 0 ? al[m] : ah[m], term == 1 ? bl[n] : bh[n]);
     }
+    if constexpr (APART)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][n][e] += low[m][n][e];
 }
 
 // Rows [0, nv) of a chunk's 64 x D tile (rows behind them zero), each times row_w[r].
@@ -88,6 +98,15 @@ __device__ __forceinline__ void load_tile(float *dst, const float *src, int nv, 
         }
         *reinterpret_cast<float4 *>(dst + r * LD + c) = f;
     }
+}
+
+// Zeros to the rows of a chunk behind the sequence's end.
+template <int D> __device__ __forceinline__ void zero_rest(const ScanArgs &s, int64_t chain, int64_t chunk, int nv) {
+    const int64_t left = s.T - chunk * C;
+    const int rows = left < C ? (int)left : C;
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(s.out) + (chain * s.T + chunk * C) * D);
+    for (int i = nv * (D / 4) + threadIdx.x; i < rows * (D / 4); i += threads<D>())
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 struct ChunkOf {
@@ -127,7 +146,7 @@ __device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, 
     const int m0 = (warp & 1) * (D / 2), n0 = (warp >> 1) * 32;
     constexpr int MT = D / 32;
     float acc[MT][4][4] = {};
-    gemm<MT, 4>(acc, sB + m0, 1, LD, sC + n0, LD, 1, C);
+    gemm<MT, 4, (MT == 2)>(acc, sB + m0, 1, LD, sC + n0, LD, 1, C);
     float *M = ONE ? s.X_out + k.chain * D * D : s.ws + (int64_t)blockIdx.x * D * D;
     const float *X0 = ONE && s.X0 ? s.X0 + k.chain * D * D : nullptr;
     const float gn = decay_pow(lg, (float)k.nv);
@@ -214,7 +233,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, fl
         constexpr int NT = C / WN / 8;
         const int n0 = wn * (C / WN);
         float p[2][NT][4] = {};
-        gemm<2, NT>(p, sA + m0 * LR, LR, 1, sB + n0 * LR, 1, LR, D);
+        gemm<2, NT, true>(p, sA + m0 * LR, LR, 1, sB + n0 * LR, 1, LR, D);
         __syncthreads();                   // B is read
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -237,7 +256,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, fl
     const int n0 = wn * 32;
     float acc[2][4][4] = {};
     if (!zero)
-        gemm<2, 4>(acc, sA + m0 * LR, LR, 1, X + n0 * (trans ? D : 1), trans ? 1 : D, trans ? D : 1, D);
+        gemm<2, 4, true>(acc, sA + m0 * LR, LR, 1, X + n0 * (trans ? D : 1), trans ? 1 : D, trans ? D : 1, D);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -250,7 +269,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, fl
                 acc[m][n][2 * h + 1] *= rd;
             }
         }
-    gemm<2, 4>(acc, sB + m0 * LP, LP, 1, sC + n0, LC, 1, C);
+    gemm<2, 4, true>(acc, sB + m0 * LP, LP, 1, sC + n0, LC, 1, C);
 
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -325,11 +344,12 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, fl
 }
 
 template <int D>
-__global__ void __launch_bounds__(threads<D>())
+__global__ void __launch_bounds__(threads<D>(), 2)
 scan_out(const __grid_constant__ Scans all, int64_t nch) {
     extern __shared__ float4 smem4[];
     const ScanArgs &s = all.s[blockIdx.y];
     const ChunkOf k = chunk_of(s, nch);
+    if (s.zero_rest) zero_rest<D>(s, k.chain, k.chunk, k.nv);
     if (k.nv == 0) {                       // (no block ends before the grids it follows)
         wait_previous_grid();
         return;
@@ -346,8 +366,9 @@ scan_one(const __grid_constant__ Scans all) {
     const ChunkOf k = chunk_of(s, 1);
     if (blockIdx.z == 0) {
         if (s.X_out) local_part<D, true>(s, k, smem4);
-    } else if (k.nv > 0) {
-        out_part<D, true>(s, k, smem4);
+    } else {
+        if (s.zero_rest) zero_rest<D>(s, k.chain, 0, k.nv);
+        if (k.nv > 0) out_part<D, true>(s, k, smem4);
     }
 }
 

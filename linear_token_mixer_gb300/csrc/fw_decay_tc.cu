@@ -48,7 +48,6 @@ constexpr int NTHREADS = 896;
 constexpr uint32_t KB = 1024;
 constexpr uint32_t HALF = 16 * KB;           // 128 rows x 128 bytes: 64 columns of a tile
 constexpr int kSMs = 152;                    // the grid's target (a workspace size needs no device)
-constexpr int kMinSegChunks = 4;
 // The launches of a call overlap (programmatic dependent launch).  A segment kernel's successor
 // waits for it before it begins; a scan that follows an independent one takes the SMs as they come
 // free and waits for it only before it ends, so that the last grid to end is the last of all.
@@ -246,7 +245,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     const Seg sg = seg_of(n, seg, nseg);
     const int nch = sg.last - sg.first;
     const bool final_seg = !PRE && seg == nseg - 1;
-    if (nch == 0 && !(final_seg && a.X_out) && !(PRE && seg == 0)) {
+    if (nch == 0 && !(final_seg && (a.X_out || a.zero_rest)) && !(PRE && seg == 0)) {
         if (order & kWaitLast) wait_previous_grid();
         return;
     }
@@ -651,6 +650,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
             if (lane == 0) bulk_wait0();
             if (!ok && lane == 0) fail_now();
+            if (a.zero_rest && final_seg && ok) {    // rows behind the sequence's end
+                uint4 *rest = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (chain * a.T + n) * D);
+                const int64_t pieces = (a.T - n) * (D / 8);
+                for (int64_t z = tid - 8 * 32; z < pieces; z += 128) rest[z] = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
     } else if (warp < 16 || warp >= 24) {
         // ---------------------------------------------------------------- (diag(w) B)^T
@@ -765,33 +769,40 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             float *const x0_copy = ws + (int64_t)(nseg - 1) * D * D;
             if (seg == 0 && a.X0) {
                 const float *src = !PRE && copy ? x0_copy : a.X0 + chain * D * D;
-                src += a.x0_trans ? c0 * D + d : d * D + c0;
-                const int step = a.x0_trans ? D : 1;
+                if (a.x0_trans) {
 #pragma unroll
-                for (int e = 0; e < XC_; ++e) {
-                    x[e] = src[e * step];
-                    if (e % 8 == 7) asm volatile("" ::: "memory");   // eight loads in flight
+                    for (int e = 0; e < XC_; ++e) x[e] = src[(c0 + e) * D + d];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < XC_; e += 4) {
+                        const float4 m = *reinterpret_cast<const float4 *>(src + d * D + c0 + e);
+                        x[e] = m.x; x[e + 1] = m.y; x[e + 2] = m.z; x[e + 3] = m.w;
+                    }
                 }
                 if (PRE && copy)
 #pragma unroll
                     for (int e = 0; e < XC_; ++e) x0_copy[d * D + c0 + e] = x[e];
             }
-            if (!PRE)
-                for (int r = 0; r < seg; ++r) {      // X <- g^n X + the state of segment r
-                    const Seg q = seg_of(n, r, nseg);
-                    if (q.first >= q.last && r > 0) continue;
-                    const float g = decay_pow(lg, (float)seg_tokens<REV>(n, q));
-                    const float4 *M = reinterpret_cast<const float4 *>(ws + (int64_t)r * D * D + d * D + c0);
+            if (!PRE && seg > 0) {                   // X <- g^n X + the state of each segment before
 #pragma unroll
-                    for (int e = 0; e < XC_; e += 4) {
-                        const float4 m = M[e / 4];
-                        x[e] = fmaf(g, x[e], m.x);
-                        x[e + 1] = fmaf(g, x[e + 1], m.y);
-                        x[e + 2] = fmaf(g, x[e + 2], m.z);
-                        x[e + 3] = fmaf(g, x[e + 3], m.w);
-                        if (e % 16 == 12) asm volatile("" ::: "memory");
+                for (int e0 = 0; e0 < XC_; e0 += 16) {
+#pragma unroll 2
+                    for (int r = 0; r < seg; ++r) {
+                        const Seg q = seg_of(n, r, nseg);
+                        if (q.first >= q.last && r > 0) continue;
+                        const float g = decay_pow(lg, (float)seg_tokens<REV>(n, q));
+                        const float4 *M = reinterpret_cast<const float4 *>(ws + (int64_t)r * D * D + d * D + c0 + e0);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 m = M[e / 4];
+                            x[e0 + e] = fmaf(g, x[e0 + e], m.x);
+                            x[e0 + e + 1] = fmaf(g, x[e0 + e + 1], m.y);
+                            x[e0 + e + 2] = fmaf(g, x[e0 + e + 2], m.z);
+                            x[e0 + e + 3] = fmaf(g, x[e0 + e + 3], m.w);
+                        }
                     }
                 }
+            }
         }
         auto put_copy = [&](int e0) {                // 16 columns in bf16, rows of X: B operand of A X
 #pragma unroll
@@ -884,16 +895,21 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t T, int64_t nc, int d, int
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Segments of each chain: as many as fill the GPU with one CTA an SM, none shorter than
-// kMinSegChunks chunks.  The last segment adds up the states of all before it, about 0.6 us each,
-// against about 4.6 us a chunk for the two passes over a segment: past sqrt(5 chunks) segments the
-// sum costs more than the split saves.
+// Segments of each chain, at most what fills the GPU with one CTA an SM: those of the least
+// estimated time, from what was measured at d = 128: 2.8 us a chunk, and where there are segments a
+// launch of 11 us and 2 us a chunk for their states, and 0.7 us to add up each state before the last.
 int segments(int64_t n_chains, int64_t T) {
     const int64_t chunks = (T + C - 1) / C;
-    int64_t s = kSMs / n_chains;
-    if (s > chunks / kMinSegChunks) s = chunks / kMinSegChunks;
-    while (s > 1 && s * s > 5 * chunks) --s;
-    return s < 1 ? 1 : (int)s;
+    int best = 1;
+    double least = 2.8 * (double)chunks;
+    for (int s = 2; s <= kSMs / n_chains && s <= chunks; ++s) {
+        const double t = 11.0 + 4.8 * (double)((chunks + s - 1) / s) + 0.7 * s;
+        if (t < least) {
+            least = t;
+            best = s;
+        }
+    }
+    return best;
 }
 
 // `follows`: behind another scan of the same call.

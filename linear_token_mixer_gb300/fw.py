@@ -19,7 +19,7 @@ FW_F32, FW_BF16 = 0, 1
 MODES = {"falcon1": 0, "linattn": 1, "falcon1a": 2, "falcon2": 3, "falcon2a": 4,
          "falcon3": 5, "falcon3a": 6}
 WINDOW_MAX = 8
-FLAG_RBW, FLAG_SAME_PAIR = 1, 2
+FLAG_RBW, FLAG_SAME_PAIR, FLAG_ZERO_REST = 1, 2, 4
 PHIS = {"identity": 0, "elu1": 1}
 ALGOS = {"auto": 0, "recurrent": 1, "chunked": 2}
 DTYPES = {torch.float32: FW_F32, torch.bfloat16: FW_BF16}
@@ -84,8 +84,8 @@ def lib():
         L.fw_window_step.argtypes = [P, P, P, P, P, P, WP, P, WP, SP, I, I, I, I, F, U, P]
         N, I64 = ctypes.POINTER(fw_norm), ctypes.c_int64
         L.fw_decay_workspace.argtypes = [SP, I, I]
-        L.fw_decay_prefill.argtypes = [P, P, P, P, P, P, N, P, P, SP, I, F, P, I64, P]
-        L.fw_decay_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, SP, I, F, P, I64, P]
+        L.fw_decay_prefill.argtypes = [P, P, P, P, P, P, N, P, P, SP, I, F, U, P, I64, P]
+        L.fw_decay_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, SP, I, F, U, P, I64, P]
         L.fw_decay_step.argtypes = [P, P, P, P, P, N, P, SP, I, F, P]
         L.fw_layer_norm.argtypes = [P, P, P, P, P, P, I64, I64, I, F, P]
         L.fw_layer_norm_workspace.argtypes = [I64, I64]
@@ -287,12 +287,11 @@ class _On:
         if stream != self.current:
             self.stream = stream
 
-    def new(self, shape, dtype, zero=False):
-        make = torch.zeros if zero else torch.empty
+    def new(self, shape, dtype):
         if self.stream is None:
-            return make(shape, dtype=dtype, device=self.like.device)
+            return torch.empty(shape, dtype=dtype, device=self.like.device)
         with torch.cuda.stream(self.stream):
-            t = make(shape, dtype=dtype, device=self.like.device)
+            t = torch.empty(shape, dtype=dtype, device=self.like.device)
         t.record_stream(self.current)
         return t
 
@@ -345,6 +344,15 @@ def _axes(q, n):
     return q.shape
 
 
+def _fresh(on, t, shape, dtype, zero):
+    if t is None:
+        t = on.new(shape, dtype)
+        if zero:
+            with torch.cuda.stream(on.stream or torch.cuda.current_stream(t.device)):
+                t.zero_()
+    return t
+
+
 def decay_workspace(B, H, T, d, dtype=torch.bfloat16, *, backward=False):
     """Bytes of workspace of decay_prefill (or decay_backward) for this shape."""
     n = _decay_need(B, H, T, d, DTYPES.get(dtype, -1), int(backward))
@@ -361,7 +369,7 @@ def decay_prefill(q, k, v, log_decay, S0=None, *, scale=1.0, lens=None, norm=Non
 
     log_decay [H] fp32; S0 [B, H, d, d] fp32 or None; lens [B] int32 or None
     (tokens of each row of a padded batch; rows of o behind them are left as
-    they were, zero where o is allocated here); norm (weight [d], bias [d]) fp32,
+    they were with o given, zero without); norm (weight [d], bias [d]) fp32,
     either None: layer norm of every output row; workspace: a tensor of at least
     decay_workspace() bytes (allocated when None).  Returns (o, S_T)."""
     shape = B, H, T, d = _axes(q, 4)
@@ -370,15 +378,16 @@ def decay_prefill(q, k, v, log_decay, S0=None, *, scale=1.0, lens=None, norm=Non
             _arg(log_decay, (H,), f32, "log_decay", q), _arg(S0, state, f32, "S0", q),
             _arg(lens, (B,), torch.int32, "lens", q), _norm(norm, norm_eps, d, q))
     on = _On(q, stream)
+    flags = FLAG_ZERO_REST if o is None and lens is not None else 0
     if o is None:
-        o = on.new(shape, dt, lens is not None)
+        o = on.new(shape, dt)
     if S_T is None:
         S_T = on.new(state, f32)
     code = DTYPES.get(dt, -1)
     _keep, ws, nws = on.workspace(workspace, _decay_need(B, H, T, d, code, 0), "fw_decay_prefill")
     on.call(lib().fw_decay_prefill, "fw_decay_prefill", *args, _arg(o, shape, dt, "o", q),
-            _arg(S_T, state, f32, "S_T", q), ctypes.byref(fw_shape(B, H, T, d, d)), code, scale, ws,
-            nws)
+            _arg(S_T, state, f32, "S_T", q), ctypes.byref(fw_shape(B, H, T, d, d)), code, scale,
+            flags, ws, nws)
     return o, S_T
 
 
@@ -387,28 +396,26 @@ def decay_backward(q, k, v, log_decay, do, S0=None, dS_T=None, *, scale=1.0, len
     """Gradients of decay_prefill (without norm) given do [B, H, T, d], the
     gradient of o, and dS_T [B, H, d, d] fp32 or None, that of S_T.  Returns
     (dq, dk, dv, dS0) in q's dtype and fp32; dS0 is None unless S0 or dS0 is
-    given.  Rows behind lens are left as they were (zero where allocated here)."""
+    given.  Rows behind lens are left as they were in a tensor that is given, and
+    zero in one that is allocated here."""
     shape = B, H, T, d = _axes(q, 4)
     state, dt, f32 = (B, H, d, d), q.dtype, torch.float32
     args = (_arg(q, shape, dt, "q", q), _arg(k, shape, dt, "k", q), _arg(v, shape, dt, "v", q),
             _arg(log_decay, (H,), f32, "log_decay", q), _arg(S0, state, f32, "S0", q),
             _arg(lens, (B,), torch.int32, "lens", q), _arg(do, shape, dt, "do", q),
             _arg(dS_T, state, f32, "dS_T", q))
-    on, zero = _On(q, stream), lens is not None
-    if dq is None:
-        dq = on.new(shape, dt, zero)
-    if dk is None:
-        dk = on.new(shape, dt, zero)
-    if dv is None:
-        dv = on.new(shape, dt, zero)
+    on = _On(q, stream)
+    fresh = dq is None and dk is None and dv is None
+    flags = FLAG_ZERO_REST if fresh and lens is not None else 0
+    dq, dk, dv = (_fresh(on, t, shape, dt, lens is not None and not fresh) for t in (dq, dk, dv))
     if dS0 is None and S0 is not None:
         dS0 = on.new(state, f32)
     code = DTYPES.get(dt, -1)
     _keep, ws, nws = on.workspace(workspace, _decay_need(B, H, T, d, code, 1), "fw_decay_backward")
     on.call(lib().fw_decay_backward, "fw_decay_backward", *args, _arg(dq, shape, dt, "dq", q),
             _arg(dk, shape, dt, "dk", q), _arg(dv, shape, dt, "dv", q),
-            _arg(dS0, state, f32, "dS0", q), ctypes.byref(fw_shape(B, H, T, d, d)), code, scale, ws,
-            nws)
+            _arg(dS0, state, f32, "dS0", q), ctypes.byref(fw_shape(B, H, T, d, d)), code, scale,
+            flags, ws, nws)
     return dq, dk, dv, dS0
 
 

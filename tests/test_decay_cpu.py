@@ -115,10 +115,10 @@ def _shape(s):
 
 
 def _prefill(L, q=P[0], k=P[1], v=P[2], ld=P[3], S0=None, lens=None, norm=None, o=P[4], S_T=P[5],
-             shape=(1, 2, 8, 64, 64), dtype=1, scale=1.0, ws=P[6], nws=WS):
+             shape=(1, 2, 8, 64, 64), dtype=1, scale=1.0, flags=0, ws=P[6], nws=WS):
     n = None if norm is None else ctypes.byref(fw.fw_norm(*norm))
-    return L.fw_decay_prefill(q, k, v, ld, S0, lens, n, o, S_T, _shape(shape), dtype, scale, ws,
-                              nws, None)
+    return L.fw_decay_prefill(q, k, v, ld, S0, lens, n, o, S_T, _shape(shape), dtype, scale,
+                              flags, ws, nws, None)
 
 
 COMMON = [
@@ -130,6 +130,7 @@ COMMON = [
     (dict(shape=(2**20, 2**10, 2**17, 64, 64)), -2),
     (dict(dtype=5), -3), (dict(scale=float("nan")), -9), (dict(scale=float("inf")), -9),
     (dict(q=P[0] + 8), -4), (dict(ld=P[3] + 4), -4), (dict(o=P[4] + 2), -4),
+    (dict(flags=1), -5), (dict(flags=8), -5),
 ]
 
 
@@ -146,10 +147,10 @@ def test_prefill_refusals(L, kw, code):
 
 
 def _backward(L, q=P[0], k=P[1], v=P[2], ld=P[3], S0=None, lens=None, do=P[4], dS_T=None, dq=P[5],
-              dk=P[6], dv=P[7], dS0=None, shape=(1, 2, 8, 64, 64), dtype=1, scale=1.0, ws=P[8],
-              nws=WS):
+              dk=P[6], dv=P[7], dS0=None, shape=(1, 2, 8, 64, 64), dtype=1, scale=1.0, flags=0,
+              ws=P[8], nws=WS):
     return L.fw_decay_backward(q, k, v, ld, S0, lens, do, dS_T, dq, dk, dv, dS0, _shape(shape),
-                               dtype, scale, ws, nws, None)
+                               dtype, scale, flags, ws, nws, None)
 
 
 @no_gpu

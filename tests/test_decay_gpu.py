@@ -161,9 +161,16 @@ def test_padded_batch(lens, d, dtype):
         check_rows(torch.where(behind, torch.zeros((), dtype=dtype), got), want, dtype)
     check_state(S, rS)
     check_state(dS0, ref[3])
-    # allocated here, they are zero
-    o2, _ = fw.decay_prefill(bad["q"], bad["k"], bad["v"], g["ld"], lens=ln.cuda())
-    assert (o2.cpu()[behind.expand_as(o2)] == 0).all()
+    # allocated there, they are zero
+    o2, _ = fw.decay_prefill(bad["q"], bad["k"], bad["v"], g["ld"], g["S0"], scale=0.5, lens=ln.cuda())
+    new = fw.decay_backward(bad["q"], bad["k"], bad["v"], g["ld"], bad["do"], g["S0"], g["dS"],
+                            scale=0.5, lens=ln.cuda())
+    mixed = fw.decay_backward(bad["q"], bad["k"], bad["v"], g["ld"], bad["do"], g["S0"], g["dS"],
+                              scale=0.5, lens=ln.cuda(), dk=torch.full_like(bad["k"], mark))
+    for z, was in zip((o2, *new[:3], *mixed[:3]), (o, dq, dk, dv, dq, dk, dv)):
+        want = mark if z is mixed[1] else 0.0
+        assert (z.cpu()[behind.expand_as(z)] == want).all()
+        assert torch.equal(z.cpu()[~behind.expand_as(z)], was.cpu()[~behind.expand_as(z)])
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
