@@ -21,9 +21,12 @@ namespace {
 
 constexpr int C = 64;          // tokens per chunk
 
+// The third scan's states (dk: sum v do^T) are the second's (dv: sum do v^T) transposed, so the
+// second's are formed once and read both ways.
 struct Scans {
     ScanArgs s[3];
 };
+constexpr int kSharing = 2;    // the scan that reads the one before it
 
 // 2 x (D / 32) warps, a 32 x 32 tile of the 64 x D rows each.
 template <int D> constexpr int threads() { return 2 * (D / 32) * 32; }
@@ -213,9 +216,11 @@ scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
     if (s.X_out) s.X_out[chain * D * D + el] = x;
 }
 
-// The output rows of a chunk, from the state in the workspace; ONE: from X0.
+// The output rows of a chunk, from the state at X (element (i, j) at X[i * D + j], or
+// X[j * D + i] with `trans`); ONE: known before the launch.
 template <int D, bool ONE>
-__device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, float4 *smem4) {
+__device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, const float *X, const bool trans,
+                                         float4 *smem4) {
     constexpr int LR = ld_row<D>(), LC = ld_col<D>(), WN = D / 32, LP = C + 4;
     float *sA = reinterpret_cast<float *>(smem4), *sB = sA + C * LR, *sC = sB + C * LR,
           *pw = sC + C * LC, *red = pw + C + 4;
@@ -248,8 +253,6 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, fl
     }
     if (!ONE) wait_previous_grid();        // the states
     __syncthreads();                       // P is written
-    const float *X = ONE ? s.X0 ? s.X0 + k.chain * D * D : nullptr : s.ws + (int64_t)blockIdx.x * D * D;
-    const bool trans = ONE && s.x0_trans;
     const bool zero = !s.X0 && (ONE || (s.rev ? k.nv < C || (k.chunk + 1) * C >= chain_len(s.lens, k.chain, s.H, s.T)
                                               : k.chunk == 0));   // nothing carried in
 
@@ -354,7 +357,9 @@ scan_out(const __grid_constant__ Scans all, int64_t nch) {
         wait_previous_grid();
         return;
     }
-    out_part<D, false>(s, k, smem4);
+    const bool trans = blockIdx.y == kSharing;
+    const float *ws = trans ? all.s[kSharing - 1].ws : s.ws;
+    out_part<D, false>(s, k, ws + (int64_t)blockIdx.x * D * D, trans, smem4);
 }
 
 // Chains of one chunk (X_out apart from X0): final states (z = 0) and rows (z = 1) at once.
@@ -368,7 +373,7 @@ scan_one(const __grid_constant__ Scans all) {
         if (s.X_out) local_part<D, true>(s, k, smem4);
     } else {
         if (s.zero_rest) zero_rest<D>(s, k.chain, 0, k.nv);
-        if (k.nv > 0) out_part<D, true>(s, k, smem4);
+        if (k.nv > 0) out_part<D, true>(s, k, s.X0 ? s.X0 + k.chain * D * D : nullptr, s.x0_trans, smem4);
     }
 }
 
@@ -392,8 +397,11 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     static std::atomic<uint64_t> local_done{0}, out_done{0};
     if ((e = allow_smem(scan_local<D>, smem_l, local_done)) != cudaSuccess) return e;
     if ((e = allow_smem(scan_out<D>, smem_o, out_done)) != cudaSuccess) return e;
-    if ((e = launch_after(scan_local<D>, grid, threads<D>(), smem_l, stream, false, all, nch)) != cudaSuccess) return e;
-    const dim3 gp((unsigned)(s.n_chains * (D * D / 256)), n);
+    const int states = n < kSharing ? n : kSharing;
+    if ((e = launch_after(scan_local<D>, dim3(grid.x, states), threads<D>(), smem_l, stream, false, all, nch)) !=
+        cudaSuccess)
+        return e;
+    const dim3 gp((unsigned)(s.n_chains * (D * D / 256)), states);
     if ((e = launch_after(scan_prefix<D>, gp, 256, 0, stream, true, all, nch)) != cudaSuccess) return e;
     return launch_after(scan_out<D>, grid, threads<D>(), smem_o, stream, true, all, nch);
 }

@@ -10,12 +10,14 @@
 // weights of their columns in registers.  Mean and variance come from one reduction: each thread
 // takes the mean and the centred sum of squares of its own values, and pairs are merged by the
 // parallel update of Chan, Golub and LeVeque (never E[x^2] - E[x]^2).  Widths that are no multiple
-// of 16 bytes take the same kernels with one element a load; rows that do not fit the registers of
+// of 16 bytes take the same kernels with two elements a load, or one; rows that do not fit the registers of
 // 1024 threads take the looping kernels, which read the row again for each pass.
 //
 // The backward kernel keeps its columns' dw and db in registers too; every block writes one
 // partial row and a second kernel adds the partial rows in a fixed order, so the sums do not
 // depend on the order in which blocks run.
+#include <type_traits>
+
 #include "fw_decay.cuh"
 
 namespace fw {
@@ -28,6 +30,8 @@ template <typename T, int VW> struct Vec;
 template <typename T> struct Vec<T, 1> { T e[1]; };
 template <> struct alignas(16) Vec<float, 4> { float e[4]; };
 template <> struct alignas(16) Vec<__nv_bfloat16, 8> { __nv_bfloat16 e[8]; };
+template <> struct alignas(8) Vec<float, 2> { float e[2]; };               // even widths
+template <> struct alignas(4) Vec<__nv_bfloat16, 2> { __nv_bfloat16 e[2]; };
 
 // fp32 arithmetic on the VW elements of a vector, two in one instruction where there are two.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -165,6 +169,10 @@ template <int VW, bool GIVEN> __device__ __forceinline__ Row<VW> load_w(const fl
             const float4 f = GIVEN || p ? *reinterpret_cast<const float4 *>(p + c + e) : make_float4(none, none, none, none);
             w.e[e] = f.x; w.e[e + 1] = f.y; w.e[e + 2] = f.z; w.e[e + 3] = f.w;
         }
+    } else if constexpr (VW == 2) {
+        const float2 f = GIVEN || p ? *reinterpret_cast<const float2 *>(p + c) : make_float2(none, none);
+        w.e[0] = f.x;
+        w.e[1] = f.y;
     } else {
         w.e[0] = GIVEN || p ? p[c] : none;
     }
@@ -494,14 +502,20 @@ cudaError_t forward(const LayerNormArgs &a, cudaStream_t s) {
         if (nv <= 1024) return fwd<T, VW, 128, 8>(a, s);
         if (nv <= 4096) return fwd<T, VW, 512, 8>(a, s);
     } else {
-        if (w <= 32) return fwd<T, 1, 32, 1>(a, s);
-        if (w <= 128) return fwd<T, 1, 32, 4>(a, s);
-        if (w <= 256) return fwd<T, 1, 32, 8>(a, s);
-        if (w <= 512) return fwd<T, 1, 64, 8>(a, s);
-        if (w <= 1024) return fwd<T, 1, 128, 8>(a, s);
-        if (w <= 2048) return fwd<T, 1, 256, 8>(a, s);
-        if (w <= 4096) return fwd<T, 1, 512, 8>(a, s);
-        if (w <= 16384) return fwd<T, 1, 1024, 16>(a, s);
+        const auto by = [&](auto vw) -> cudaError_t {
+            constexpr int V = decltype(vw)::value;
+            const int64_t nv = w / V;
+            if (nv <= 32) return fwd<T, V, 32, 1>(a, s);
+            if (nv <= 128) return fwd<T, V, 32, 4>(a, s);
+            if (nv <= 256) return fwd<T, V, 32, 8>(a, s);
+            if (nv <= 512) return fwd<T, V, 64, 8>(a, s);
+            if (nv <= 1024) return fwd<T, V, 128, 8>(a, s);
+            if (nv <= 2048) return fwd<T, V, 256, 8>(a, s);
+            if (nv <= 4096) return fwd<T, V, 512, 8>(a, s);
+            return fwd<T, V, 1024, 16>(a, s);
+        };
+        if (w % 2 == 0 && w <= 32768) return by(std::integral_constant<int, 2>{});
+        if (w <= 16384) return by(std::integral_constant<int, 1>{});
     }
     ln_fwd_long<T><<<(unsigned)a.rows, 1024, 0, s>>>(a);
     return cudaGetLastError();
@@ -549,12 +563,19 @@ cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t s) {
         if (nv <= 1024) return bwd<T, VW, 512, 2>(a, s);
         if (nv <= 2048) return bwd<T, VW, 1024, 2>(a, s);
     } else {
-        if (w <= 32) return bwd<T, 1, 32, 1>(a, s);
-        if (w <= 128) return bwd<T, 1, 32, 4>(a, s);
-        if (w <= 1024) return bwd<T, 1, 128, 8>(a, s);
-        if (w <= 2048) return bwd<T, 1, 256, 8>(a, s);
-        if (w <= 4096) return bwd<T, 1, 512, 8>(a, s);
-        if (w <= 8192) return bwd<T, 1, 1024, 8>(a, s);
+        const auto by = [&](auto vw) -> cudaError_t {
+            constexpr int V = decltype(vw)::value;
+            const int64_t nv = w / V;
+            if (nv <= 32) return bwd<T, V, 32, 1>(a, s);
+            if (nv <= 128) return bwd<T, V, 32, 4>(a, s);
+            if (nv <= 512) return bwd<T, V, 128, 4>(a, s);
+            if (nv <= 1024) return bwd<T, V, 256, 4>(a, s);
+            if (nv <= 2048) return bwd<T, V, 512, 4>(a, s);
+            if (nv <= 4096) return bwd<T, V, 1024, 4>(a, s);
+            return bwd<T, V, 1024, 8>(a, s);
+        };
+        if (w % 2 == 0 && w <= 8192) return by(std::integral_constant<int, 2>{});
+        if (w <= 8192) return by(std::integral_constant<int, 1>{});
     }
     cudaError_t e;
     if (a.ws) {
