@@ -28,6 +28,12 @@
 // The update of a chunk is summed from zero in tensor memory and added to X by an fp32 FMA: the
 // MMAs round towards zero, and X would carry that bias from chunk to chunk.  It also takes the
 // MMAs of the update off the state's serial chain (update read -> copy -> A X).
+// Measured (one GB300): B8 H16 T4096 d = 128, 128 chains, 545 MB of rows and states: 103.6 us, 5.3
+// TB/s, 77 % of the measured copy rate; B1 H32 T32768, four segments a chain: 312 us, of which the
+// states of the segments, read again, are a third.  What bounds it is the period of a chunk, 2.8 us,
+// in one CTA: the tensor pipe is busy for 32 % of it, the issue slots for 38 %, DRAM at 56 % (ncu,
+// T2048), and the rest is the roles' round trips through tensor memory and barriers.  A second CTA an
+// SM would fill it but finds no room: the tiles take 192 KB, G, O and the update 384 columns.
 // Tensor memory: G (P over it) 128 columns, O 128, the update 128, the split operand 2 x 48.
 // Every wait is bounded; on expiry the kernel records an error, the other roles stop at their
 // next wait, copies and MMAs in flight are drained, tensor memory is freed and the kernel exits.
@@ -153,8 +159,9 @@ __device__ __forceinline__ void tmem_landed(float (&v)[16]) {
                    "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
                    "+f"(v[15])::"memory");
 }
-// do_(v, c) for the columns c = c0, c0 + 16, .. < c1 (an even number of pieces) of this warp's lanes,
-// each piece's load in flight while the one before it is worked on.
+// do_(v, c) for the columns c = c0, c0 + 16, .. < c1 of this warp's lanes.  (One load at a time:
+// seven roles share the instruction cache, and with their loops twice as long, the next load in flight,
+// B8 H16 T4096 d = 128 took 107.6 us for 102.5.)
 template <typename F> __device__ __forceinline__ void tmem_stream(uint32_t taddr, int c0, int c1, F do_) {
     float v[16];
 #pragma unroll 1
@@ -251,11 +258,12 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     }
     const uint64_t limit = (uint64_t)a.wait_ns;
     const float lg = a.log_decay[chain % a.H];
-    // Within a chunk of a mild head every quotient of powers of g is safe in fp32 and bf16
-    // (e^60 at most): the rows' decay of a chunk, g^(i+1) (A X + (mask . g^-(j+1) . G) C), is then
-    // one factor in the epilogue.  Otherwise A X is scaled by its rows' decay on its own and the
-    // scores by g^(i-j), and nothing is divided by a power of g.
-    const bool mild = fabsf(lg) * C <= 60.f;
+    // Within a chunk of a mild head every quotient of powers of g is at most e^24 = 2.6e10, which
+    // leaves the scores and their sums 28 of fp32's and bf16's 38 decimal orders: the rows' decay
+    // of a chunk, g^(i+1) (A X + (mask . g^-(j+1) . G) C), is then one factor in the epilogue.
+    // Otherwise A X is scaled by its rows' decay on its own and the scores by g^(i-j), and nothing
+    // is divided by a power of g.
+    const bool mild = fabsf(lg) * C <= 24.f;
     const int x_slots = nseg;                       // workspace: nseg - 1 segment states, X0's copy
     float *const ws = a.ws + chain * x_slots * D * D;
 

@@ -428,6 +428,27 @@ def test_decays_on_both_sides_of_what_may_be_divided_by(ld, dtype):
         check_rows(a, r, dtype)
 
 
+@pytest.mark.parametrize("ld", [-0.46, -0.2, -0.185, 0.0])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_large_values_do_not_overflow_inside_a_chunk(ld, dtype):
+    """Rows of 1e4: scores of 1e9, outputs of 1e13 to 1e15, which no quotient of decays may carry
+    past the largest fp32.  Scaling every input scales the outputs and their errors alike."""
+    x, _ = inputs(1, 1, 300, 128, dtype, seed=57)
+    x = {n: (t if n == "ld" else (t.double() * 1e4).to(t.dtype)) for n, t in x.items()}
+    g = {n: t.cuda() for n, t in x.items()}
+    l = torch.tensor([ld])
+    o, S = fw.decay_prefill(g["q"], g["k"], g["v"], l.cuda(), g["S0"])
+    got = fw.decay_backward(g["q"], g["k"], g["v"], l.cuda(), g["do"], g["S0"], g["dS"])
+    fw.check()
+    ro, rS, _ = R.forward(x["q"], x["k"], x["v"], l, x["S0"])
+    ref = R.backward(x["q"], x["k"], x["v"], l, x["do"], x["S0"], x["dS"])
+    check_rows(o, ro, dtype)
+    check_state(S, rS)
+    for a, r in zip(got[:3], ref[:3]):
+        check_rows(a, r, dtype)
+    check_state(got[3], ref[3])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_non_finite_values_stay_behind_their_chunk(dtype):
     x, g = inputs(1, 2, 300, 64, dtype, seed=2)
