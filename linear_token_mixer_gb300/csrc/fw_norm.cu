@@ -3,15 +3,20 @@
 //     dx = r (w dy - mean(w dy) - xh mean(w dy xh)),   xh = (x - m) r
 //     dw = sum_rows dy xh,   db = sum_rows dy
 //
-// Both passes are bound by their rows' bytes: each row is read once into registers (as loaded:
-// 16 bytes a thread and vector, the next row's loads in flight while this one is worked on), the
-// statistics are taken from there and the result is written.  A row is held by ROWT threads: a
+// Both passes are bound by their rows' bytes: each row is read once (16 bytes a thread and vector, the
+// loads of the next row, or of the next two or three, in flight while this one is worked on) into
+// registers, the statistics are taken from there and the result is written.  A row is held by ROWT threads: a
 // part of a warp for short rows, a warp, or a block; blocks stride over the rows and keep the
 // weights of their columns in registers.  Mean and variance come from one reduction: each thread
 // takes the mean and the centred sum of squares of its own values, and pairs are merged by the
 // parallel update of Chan, Golub and LeVeque (never E[x^2] - E[x]^2).  Widths that are no multiple
 // of 16 bytes take the same kernels with two elements a load, or one; rows that do not fit the registers of
 // 1024 threads take the looping kernels, which read the row again for each pass.
+//
+// Measured (one GB300, 32768 x 2048 bf16): forward 56 us, 4.8 TB/s, 70 % of the measured copy rate;
+// backward with its sums 81 us, 5.0 TB/s, 73 %.  What is left is the turn of a row: its reduction is
+// a chain of shuffles and a barrier that the few rows of an SM cover only in part.  64 x 2048: 7.3 us and
+// 12.4 us, of which a launch is most.
 //
 // The backward kernel keeps its columns' dw and db in registers too; every block writes one
 // partial row and a second kernel adds the partial rows in a fixed order, so the sums do not
@@ -179,13 +184,47 @@ template <int VW, bool GIVEN> __device__ __forceinline__ Row<VW> load_w(const fl
     return w;
 }
 
+// Rows on their way through shared memory, DEPTH - 1 of them behind the one that is worked on: for
+// each thread its own PIECES of 16 bytes and two floats of its row.  (With one row ahead, in registers,
+// the backward pass had 32 KB an SM in flight, where the memory's latency needs twice that.)
+template <int THREADS, int PIECES> struct Ahead {
+    static constexpr int STAGE = THREADS * (PIECES * 16 + 8);
+    static constexpr int DEPTH = 4 * STAGE * (THREADS < 512 ? 512 / THREADS : 1) <= 160 * 1024 ? 4 : 3;
+    static constexpr int BYTES = DEPTH * STAGE;
+};
+template <int N> __device__ __forceinline__ void copy_async(void *to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(from), "n"(N)
+                 : "memory");
+}
+template <> __device__ __forceinline__ void copy_async<16>(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_begun() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups have landed (a thread reads its own copies alone).
+template <int N> __device__ __forceinline__ void copies_landed() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The forward pass takes its rows that way where a part of a warp holds one: 524288 x 128 bf16 61 us
+// in registers, 54 us ahead; rows held by blocks, of which more fit an SM without, 32768 x 2048 56 us
+// and 60 us.  (With one vector a thread there is one row, or next to nothing, to read ahead.)
+template <typename T, int VW, int ROWT, int VPT> constexpr bool fwd_ahead() {
+    return VW * sizeof(T) == 16 && VPT > 1 && ROWT <= 32;
+}
+
 // FAST: every thread holds VPT whole vectors, and weight and bias are given (the checks for the
 // other cases are as many instructions as the work).
 template <typename T, int VW, int ROWT, int VPT, bool FAST>
 __global__ void __launch_bounds__(block_of<ROWT>(), FAST && ROWT <= 512 ? 512 / block_of<ROWT>() : 1)
 ln_fwd(LayerNormArgs a) {
     __shared__ Moments red[2][32];
-    constexpr int RPB = block_of<ROWT>() / ROWT;
+    extern __shared__ float4 dyn[];        // the rows ahead
+    constexpr int RPB = block_of<ROWT>() / ROWT, THREADS = block_of<ROWT>();
+    constexpr bool ASYNC = fwd_ahead<T, VW, ROWT, VPT>();
+    using Q = Ahead<THREADS, VPT>;
     constexpr bool KEEP = VPT * VW <= 16;  // weights in registers, or from L1 for every row
     using V = Vec<T, VW>;
     const int lane = threadIdx.x % ROWT, sub = threadIdx.x / ROWT;
@@ -200,22 +239,40 @@ ln_fwd(LayerNormArgs a) {
             }
     }
     V xv[VPT], nx[VPT];
-    auto load = [&](V (&to)[VPT], int64_t row) {
+    auto load = [&](int64_t row, int slot) {
         const V *x = reinterpret_cast<const V *>(static_cast<const T *>(a.x) + row * a.width);
 #pragma unroll
         for (int p = 0; p < VPT; ++p)
-            if (row < a.rows && (FAST || p * ROWT + lane < nv)) to[p] = x[p * ROWT + lane];
+            if (row < a.rows && (FAST || p * ROWT + lane < nv)) {
+                if constexpr (ASYNC) copy_async<16>(dyn + (slot * VPT + p) * THREADS + threadIdx.x, x + p * ROWT + lane);
+                else nx[p] = x[p * ROWT + lane];
+            }
+        if constexpr (ASYNC) copies_begun();
     };
     const int64_t stride = (int64_t)gridDim.x * RPB;
-    int turn = 0;
-    load(nx, (int64_t)blockIdx.x * RPB + sub);
+    int turn = 0, slot = 0;
+    load((int64_t)blockIdx.x * RPB + sub, 0);
+    if constexpr (ASYNC)
+#pragma unroll
+        for (int i = 1; i < Q::DEPTH - 1; ++i) load((int64_t)blockIdx.x * RPB + sub + i * stride, i);
     // every thread of the block makes the same number of turns (the merge synchronises)
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += stride, turn ^= 1) {
         const int64_t row = r0 + sub;
         const bool on = row < a.rows;
+        if constexpr (ASYNC) {
+            copies_landed<Q::DEPTH - 2>();
+            const V *const at = reinterpret_cast<const V *>(dyn + slot * VPT * THREADS + threadIdx.x);
 #pragma unroll
-        for (int p = 0; p < VPT; ++p) xv[p] = nx[p];
-        load(nx, row + stride);
+            for (int p = 0; p < VPT; ++p)
+                if (on && (FAST || p * ROWT + lane < nv)) xv[p] = at[p * THREADS];
+            // over the row before this one
+            load(row + (Q::DEPTH - 1) * stride, slot == 0 ? Q::DEPTH - 1 : slot - 1);
+            slot = slot == Q::DEPTH - 1 ? 0 : slot + 1;
+        } else {
+#pragma unroll
+            for (int p = 0; p < VPT; ++p) xv[p] = nx[p];
+            load(row + stride, 0);
+        }
         Moments mo{0.f, 0.f, 0.f};
         Row<VW> acc = all<VW>(0.f);
 #pragma unroll
@@ -288,12 +345,17 @@ template <typename T, int VW, int ROWT, int VPT, bool FAST>
 __global__ void __launch_bounds__(block_of<ROWT>(), FAST && ROWT <= 512 ? 512 / block_of<ROWT>() : 1)
 ln_bwd(LayerNormBwdArgs a) {
     __shared__ float red[2][64];
-    extern __shared__ float sacc[];        // part-of-a-warp forms: [RPB][2][width]
-    constexpr int RPB = block_of<ROWT>() / ROWT;
+    // 16-byte vectors: the rows ahead; then, part-of-a-warp forms: sums [RPB][2][width]
+    extern __shared__ float4 dyn[];
+    float *const sacc = reinterpret_cast<float *>(dyn);
+    constexpr int RPB = block_of<ROWT>() / ROWT, THREADS = block_of<ROWT>();
+    constexpr bool ASYNC = VW * sizeof(T) == 16;
     using V = Vec<T, VW>;
+    using Q = Ahead<THREADS, 2 * VPT>;
     const int lane = threadIdx.x % ROWT, sub = threadIdx.x / ROWT;
     const int W = (int)a.width, nv = W / VW;
     const bool sums = a.ws != nullptr;
+    let_next_grid_start();
     Row<VW> w[VPT], dw[VPT], db[VPT];
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
@@ -302,26 +364,61 @@ ln_bwd(LayerNormBwdArgs a) {
     }
     V nx[VPT], ng[VPT];
     float nmean = 0.f, nrstd = 0.f;
-    auto load = [&](int64_t row) {
-        if (row >= a.rows) return;
-        const V *x = reinterpret_cast<const V *>(static_cast<const T *>(a.x) + row * a.width);
-        const V *dy = reinterpret_cast<const V *>(static_cast<const T *>(a.dy) + row * a.width);
+    float2 *const stats = reinterpret_cast<float2 *>(dyn + Q::DEPTH * 2 * VPT * THREADS);
+    auto load = [&](int64_t row, int slot) {
+        if (row < a.rows) {
+            const V *x = reinterpret_cast<const V *>(static_cast<const T *>(a.x) + row * a.width);
+            const V *dy = reinterpret_cast<const V *>(static_cast<const T *>(a.dy) + row * a.width);
+            float4 *const to = dyn + slot * 2 * VPT * THREADS + threadIdx.x;
 #pragma unroll
-        for (int p = 0; p < VPT; ++p)
-            if ((FAST || p * ROWT + lane < nv)) {
-                nx[p] = x[p * ROWT + lane];
-                ng[p] = dy[p * ROWT + lane];
+            for (int p = 0; p < VPT; ++p)
+                if ((FAST || p * ROWT + lane < nv)) {
+                    if constexpr (ASYNC) {
+                        copy_async<16>(to + p * THREADS, x + p * ROWT + lane);
+                        copy_async<16>(to + (VPT + p) * THREADS, dy + p * ROWT + lane);
+                    } else {
+                        nx[p] = x[p * ROWT + lane];
+                        ng[p] = dy[p * ROWT + lane];
+                    }
+                }
+            if constexpr (ASYNC) {
+                copy_async<4>(&stats[slot * THREADS + threadIdx.x].x, a.mean + row);
+                copy_async<4>(&stats[slot * THREADS + threadIdx.x].y, a.rstd + row);
+            } else {
+                nmean = a.mean[row];
+                nrstd = a.rstd[row];
             }
-        nmean = a.mean[row];
-        nrstd = a.rstd[row];
+        }
+        if constexpr (ASYNC) copies_begun();
     };
     const int64_t stride = (int64_t)gridDim.x * RPB;
-    int turn = 0;
-    load((int64_t)blockIdx.x * RPB + sub);
+    int turn = 0, slot = 0;
+    load((int64_t)blockIdx.x * RPB + sub, 0);
+    if constexpr (ASYNC)
+#pragma unroll
+        for (int i = 1; i < Q::DEPTH - 1; ++i) load((int64_t)blockIdx.x * RPB + sub + i * stride, i);
     // every thread of the block makes the same number of turns (the row sums synchronise)
     for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += stride, turn ^= 1) {
         const int64_t row = r0 + sub;
         const bool on = row < a.rows;
+        if constexpr (ASYNC) {
+            copies_landed<Q::DEPTH - 2>();
+            const V *const at = reinterpret_cast<const V *>(dyn + slot * 2 * VPT * THREADS + threadIdx.x);
+            if (on) {
+#pragma unroll
+                for (int p = 0; p < VPT; ++p)
+                    if (FAST || p * ROWT + lane < nv) {
+                        nx[p] = at[p * THREADS];
+                        ng[p] = at[(VPT + p) * THREADS];
+                    }
+                const float2 st = stats[slot * THREADS + threadIdx.x];
+                nmean = st.x;
+                nrstd = st.y;
+            }
+            // over the row before this one
+            load(row + (Q::DEPTH - 1) * stride, slot == 0 ? Q::DEPTH - 1 : slot - 1);
+            slot = slot == Q::DEPTH - 1 ? 0 : slot + 1;
+        }
         const float mean = nmean, rstd = nrstd;
         Row<VW> xh[VPT], gw[VPT];
         Row<VW> s1 = all<VW>(0.f), s2 = all<VW>(0.f);
@@ -337,7 +434,7 @@ ln_bwd(LayerNormBwdArgs a) {
                 s1 = fma_n(gw[p], all<VW>(1.f), s1);
                 s2 = fma_n(gw[p], xh[p], s2);
             }
-        load(row + stride);
+        if constexpr (!ASYNC) load(row + stride, 0);
         float c1 = total(s1), c2 = total(s2);
         row_sum2<ROWT>(c1, c2, red[turn]);
         c1 /= W;
@@ -366,6 +463,10 @@ ln_bwd(LayerNormBwdArgs a) {
                 }
             }
     } else {
+        if constexpr (ASYNC) {
+            copies_landed<0>();
+            __syncthreads();               // the sums take the place of the rows
+        }
 #pragma unroll
         for (int p = 0; p < VPT; ++p)
 #pragma unroll
@@ -432,6 +533,7 @@ ln_bwd_sums_long(LayerNormBwdArgs a) {
 __global__ void __launch_bounds__(1024)
 ln_sum_partials(const float *ws, int n, int64_t W, float *dw, float *db) {
     __shared__ float s[32][33];
+    wait_previous_grid();
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;   // column of [2][W]
     const int y = threadIdx.x / 32;
     float v = 0.f;
@@ -471,9 +573,12 @@ cudaError_t fwd(const LayerNormArgs &a, cudaStream_t s) {
     int64_t n;
     const bool fast = VW > 1 && a.width == (int64_t)VW * ROWT * VPT && a.weight && a.bias;
     auto k = fast ? ln_fwd<T, VW, ROWT, VPT, (VW > 1)> : ln_fwd<T, VW, ROWT, VPT, false>;
-    const cudaError_t e = resident(k, block_of<ROWT>(), 0, (a.rows + RPB - 1) / RPB, &n);
-    if (e != cudaSuccess) return e;
-    k<<<(unsigned)n, block_of<ROWT>(), 0, s>>>(a);
+    constexpr int smem = fwd_ahead<T, VW, ROWT, VPT>() ? Ahead<block_of<ROWT>(), VPT>::BYTES : 0;
+    static std::atomic<uint64_t> done[2];
+    cudaError_t e;
+    if (smem > 48 * 1024 && (e = allow_smem(k, smem, done[fast])) != cudaSuccess) return e;
+    if ((e = resident(k, block_of<ROWT>(), smem, (a.rows + RPB - 1) / RPB, &n)) != cudaSuccess) return e;
+    k<<<(unsigned)n, block_of<ROWT>(), smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -523,9 +628,8 @@ cudaError_t forward(const LayerNormArgs &a, cudaStream_t s) {
 
 cudaError_t add_partials(const LayerNormBwdArgs &a, int64_t n, cudaStream_t s) {
     if (!a.ws) return cudaSuccess;
-    ln_sum_partials<<<(unsigned)((2 * a.width + 31) / 32), 1024, 0, s>>>(a.ws, (int)n, a.width,
-                                                                       a.dweight, a.dbias);
-    return cudaGetLastError();
+    return launch_after(ln_sum_partials, dim3((unsigned)((2 * a.width + 31) / 32)), 1024, 0, s, true,
+                        (const float *)a.ws, (int)n, a.width, a.dweight, a.dbias);
 }
 
 int64_t partials(int64_t rows) { return rows < kPartials ? rows : kPartials; }
@@ -534,11 +638,16 @@ template <typename T, int VW, int ROWT, int VPT>
 cudaError_t bwd(const LayerNormBwdArgs &a, cudaStream_t s) {
     constexpr int RPB = block_of<ROWT>() / ROWT;
     const int64_t blocks = (a.rows + RPB - 1) / RPB;
-    const size_t smem = RPB > 1 ? (size_t)RPB * 2 * a.width * sizeof(float) : 0;   // <= 32 KB
+    constexpr int ahead = VW * sizeof(T) == 16 ? Ahead<block_of<ROWT>(), 2 * VPT>::BYTES : 0;
+    const int sums = RPB > 1 ? RPB * 2 * (int)a.width * (int)sizeof(float) : 0;   // <= 32 KB
+    const int smem = ahead > sums ? ahead : sums;
     int64_t n;
     const bool fast = VW > 1 && a.width == (int64_t)VW * ROWT * VPT && a.weight;
     auto k = fast ? ln_bwd<T, VW, ROWT, VPT, (VW > 1)> : ln_bwd<T, VW, ROWT, VPT, false>;
-    cudaError_t e = resident(k, block_of<ROWT>(), smem, blocks, &n);
+    static std::atomic<uint64_t> done[2];
+    cudaError_t e;
+    if (ahead > 48 * 1024 && (e = allow_smem(k, ahead, done[fast])) != cudaSuccess) return e;
+    e = resident(k, block_of<ROWT>(), smem, blocks, &n);
     if (e != cudaSuccess) return e;
     if (n > partials(a.rows)) n = partials(a.rows);
     k<<<(unsigned)n, block_of<ROWT>(), smem, s>>>(a);
@@ -560,7 +669,7 @@ cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t s) {
         if (nv <= 128) return bwd<T, VW, 64, 2>(a, s);
         if (nv <= 256) return bwd<T, VW, 128, 2>(a, s);
         // sixteen columns a thread: as many as leave its sums in registers (16384 x 2048 fp32: eight 73 us,
-        // sixteen 65 us; 16384 x 4096 bf16: eight 110 us, sixteen 104 us, 32, for want of registers, 233 us)
+        // sixteen 67 us; 32768 x 2048 bf16: sixteen 81 us, 32, for want of registers, 181 us)
         constexpr int V = VW == 4 ? 4 : 2;
         if (nv <= 512) return bwd<T, VW, 512 / V, V>(a, s);
         if (nv <= 1024) return bwd<T, VW, 1024 / V, V>(a, s);
