@@ -13,6 +13,11 @@
 // their starts (programmatic dependent launch): scan_out loads its rows and forms the masked
 // scores before it waits for the states, which it reads straight into the MMAs' operands.  Chains
 // of one chunk need no workspace and no order between the parts: one launch does both (scan_one).
+//
+// Measured (one GB300): B4 H8 T1000 d = 64 ragged 33 us, B4 H8 T2048 d = 128 196 us, the three scans of
+// a backward pass of B2 H8 T1023 d = 64 47 us.  The short ones are bound by the three launches that
+// follow each other (10.7, 10.3 and 17.4 us alone from cold caches), the long
+// ones by the issue of the split MMAs, three for each product, and of what splits their operands.
 #include "fw_decay_tc.cuh"
 #include "fw_sm100.cuh"
 
