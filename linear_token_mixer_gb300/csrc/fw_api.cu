@@ -455,7 +455,7 @@ bool outputs_clash(std::initializer_list<Span> outs, std::initializer_list<Span>
 }
 
 // Shape and type of a decayed call.  The kernels index chunks of at least 64
-// tokens, and 256 elements of a state, by a 32-bit grid.
+// tokens, and parts of a state, by a 32-bit grid.
 int check_decay(const fw_shape *shape, fw_dtype dtype) {
     const int st = check_common(shape, dtype, FW_LINATTN, FW_PHI_IDENTITY, 0.f, 0u);
     if (st != FW_OK) return st;

@@ -2,8 +2,8 @@
 // 128, parallel over chunks of 64 tokens:
 //
 //   scan_local    M_c = in_scale sum_j w_j b_j c_j^T of every chunk (one block each)
-//   scan_prefix   the short recurrence X' = g^n X + M_c over a chain's chunks, one thread a state
-//                 element; M_c is replaced by the state on entry to chunk c
+//   scan_prefix   the short recurrence X' = g^n X + M_c over a chain's chunks, a thread for
+//                 four elements; M_c is replaced by the state on entry to chunk c
 //   scan_out      out = rd (A X_c) + (mask . decay . A B^T) C of every chunk (one block each)
 //
 // The products run on warp-level tf32 MMAs with every operand split in two (11 + 11 bits):
@@ -14,10 +14,11 @@
 // scores before it waits for the states, which it reads straight into the MMAs' operands.  Chains
 // of one chunk need no workspace and no order between the parts: one launch does both (scan_one).
 //
-// Measured (one GB300): B4 H8 T1000 d = 64 ragged 33 us, B4 H8 T2048 d = 128 196 us, the three scans of
-// a backward pass of B2 H8 T1023 d = 64 47 us.  The short ones are bound by the three launches that
-// follow each other (10.7, 10.3 and 17.4 us alone from cold caches), the long
-// ones by the issue of the split MMAs, three for each product, and of what splits their operands.
+// Measured (one GB300): B4 H8 T1000 d = 64 ragged 34 us, B4 H8 T2048 d = 128 171 us, the three scans of
+// a backward pass of B2 H8 T1023 d = 64 44 us.  The short ones are bound by three launches that follow
+// each other, the long ones by the split products: scan_out (107 us of d = 128) issues in 36 % of its
+// cycles, its tensor pipe is busy for 39 %, and its sixteen warps an SM wait for the states' loads and
+// for each other's MMAs.
 #include "fw_decay_tc.cuh"
 #include "fw_sm100.cuh"
 
@@ -185,40 +186,51 @@ scan_local(const __grid_constant__ Scans all, int64_t nch) {
     local_part<D, false>(s, k, smem4);
 }
 
+constexpr int kPrefix = 128;   // threads of a block
+
+// Four elements of a chain's state a thread, eight chunks read ahead of the recurrence (one element a
+// thread: B4 H8 T2048 d = 128 196 us in all for 171 us, B2 H8 T1023 d = 64 backward 46 us for 44 us).
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kPrefix)
 scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
     const ScanArgs &s = all.s[blockIdx.y];
-    constexpr int PER = D * D / 256;       // blocks of a chain
+    constexpr int PER = D * D / 4 / kPrefix;   // blocks of a chain
     const int64_t chain = blockIdx.x / PER;
-    const int el = (int)(blockIdx.x % PER) * 256 + threadIdx.x;
+    const int el = 4 * ((int)(blockIdx.x % PER) * kPrefix + (int)threadIdx.x);
     let_next_grid_start();
-    float x = 0.f;
-    if (s.X0) x = s.X0[chain * D * D + (s.x0_trans ? (el % D) * D + el / D : el)];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s.X0) {
+        const float *X0 = s.X0 + chain * D * D;
+        const int r = el / D, c = el % D;
+        x = s.x0_trans ? make_float4(X0[c * D + r], X0[(c + 1) * D + r], X0[(c + 2) * D + r], X0[(c + 3) * D + r])
+                       : *reinterpret_cast<const float4 *>(X0 + el);
+    }
     const int64_t n = chain_len(s.lens, chain, s.H, s.T);
-    const int64_t used = (n + C - 1) / C;
+    const int used = (int)((n + C - 1) / C);
     const float lg = s.log_decay[chain % s.H];
-    const float gC = decay_pow(lg, (float)C), gT = decay_pow(lg, (float)(n - (used - 1) * C));
-    float *M = s.ws + chain * nch * D * D + el;
+    const float gC = decay_pow(lg, (float)C), gT = decay_pow(lg, (float)(n - (int64_t)(used - 1) * C));
+    // in processing order; the end is nobody's entry, and is left out where it is not asked for
+    const int read = s.X_out ? used : used - 1;
+    const int64_t step = s.rev ? -(D * D / 4) : D * D / 4;
+    float4 *M = reinterpret_cast<float4 *>(s.ws + chain * nch * D * D + el) + (s.rev ? (int64_t)(used - 1) * (D * D / 4) : 0);
     wait_previous_grid();
-    constexpr int U = 8;                   // chunks read ahead of the recurrence
-    for (int64_t i0 = 0; i0 < used; i0 += U) {
-        float m[U];
+    constexpr int U = 8;
+    for (int i0 = 0; i0 < used; i0 += U, M += U * step) {
+        float4 m[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) m[u] = i0 + u < read ? M[u * step] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u, c = s.rev ? used - 1 - i : i;
-            m[u] = i < used && (i + 1 < used || s.X_out) ? M[c * D * D] : 0.f;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u, c = s.rev ? used - 1 - i : i;
-            if (i < used) {
-                M[c * D * D] = x;
-                x = fmaf(c == used - 1 ? gT : gC, x, m[u]);
-            }
+            if (i0 + u >= used) break;
+            M[u * step] = x;
+            const float g = (s.rev ? i0 + u == 0 : i0 + u == used - 1) ? gT : gC;
+            x.x = fmaf(g, x.x, m[u].x);
+            x.y = fmaf(g, x.y, m[u].y);
+            x.z = fmaf(g, x.z, m[u].z);
+            x.w = fmaf(g, x.w, m[u].w);
         }
     }
-    if (s.X_out) s.X_out[chain * D * D + el] = x;
+    if (s.X_out) *reinterpret_cast<float4 *>(s.X_out + chain * D * D + el) = x;
 }
 
 // The output rows of a chunk, from the state at X (element (i, j) at X[i * D + j], or
@@ -406,8 +418,8 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     if ((e = launch_after(scan_local<D>, dim3(grid.x, states), threads<D>(), smem_l, stream, false, all, nch)) !=
         cudaSuccess)
         return e;
-    const dim3 gp((unsigned)(s.n_chains * (D * D / 256)), states);
-    if ((e = launch_after(scan_prefix<D>, gp, 256, 0, stream, true, all, nch)) != cudaSuccess) return e;
+    const dim3 gp((unsigned)(s.n_chains * (D * D / 4 / kPrefix)), states);
+    if ((e = launch_after(scan_prefix<D>, gp, kPrefix, 0, stream, true, all, nch)) != cudaSuccess) return e;
     return launch_after(scan_out<D>, grid, threads<D>(), smem_o, stream, true, all, nch);
 }
 
