@@ -14,9 +14,9 @@
 // scores before it waits for the states, which it reads straight into the MMAs' operands.  Chains
 // of one chunk need no workspace and no order between the parts: one launch does both (scan_one).
 //
-// Measured (one GB300): B4 H8 T1000 d = 64 ragged 34 us, B4 H8 T2048 d = 128 171 us, the three scans of
+// Measured (one GB300): B4 H8 T1000 d = 64 ragged 34 us, B4 H8 T2048 d = 128 165 us, the three scans of
 // a backward pass of B2 H8 T1023 d = 64 44 us.  The short ones are bound by three launches that follow
-// each other, the long ones by the split products: scan_out (107 us of d = 128) issues in 36 % of its
+// each other, the long ones by the split products: scan_out (d = 128) issues in 36 % of its
 // cycles, its tensor pipe is busy for 39 %, and its sixteen warps an SM wait for the states' loads and
 // for each other's MMAs.
 #include "fw_decay_tc.cuh"
@@ -50,7 +50,8 @@ __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
 
 // acc += A B for a warp's 16 MT x 8 NT tile; element (m, k) of A at a[m * am + k * ak], element
 // (k, n) of B at b[k * bk + n * bn].  The MMAs round towards zero: APART sums the two small terms on
-// their own, so that the large sum is cut a third as often.
+// their own, so that the large sum is cut a third as often.  B is fetched a step ahead: the states come
+// from global memory (B4 H8 T2048 d = 128 173 us, then 165 us, with the strides known at compile time).
 template <int MT, int NT, bool APART>
 __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, int am, int ak,
                                      const float *b, int bk, int bn, int K) {
@@ -58,6 +59,14 @@ __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, in
     a += g * am + t * ak;
     b += t * bk + g * bn;
     float low[APART ? MT : 1][APART ? NT : 1][4] = {};
+    float nb[NT][2];
+    auto fetch = [&](int k) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) nb[n][e] = b[(k + 4 * e) * bk + 8 * n * bn];
+    };
+    fetch(0);
 #pragma unroll 2
     for (int k = 0; k < K; k += 8) {
         uint32_t ah[MT][4], al[MT][4];
@@ -70,7 +79,8 @@ __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, in
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) split(b[(k + 4 * e) * bk + 8 * n * bn], bh[n][e], bl[n][e]);
+            for (int e = 0; e < 2; ++e) split(nb[n][e], bh[n][e], bl[n][e]);
+        if (k + 8 < K) fetch(k + 8);
         // the three terms one after the other over all tiles: no MMA waits for the one before it
 #pragma unroll
         for (int term = 0; term < 3; ++term)
@@ -189,7 +199,7 @@ scan_local(const __grid_constant__ Scans all, int64_t nch) {
 constexpr int kPrefix = 128;   // threads of a block
 
 // Four elements of a chain's state a thread, eight chunks read ahead of the recurrence (one element a
-// thread: B4 H8 T2048 d = 128 196 us in all for 171 us, B2 H8 T1023 d = 64 backward 46 us for 44 us).
+// thread: B4 H8 T2048 d = 128 196 us in all, then 171 us, B2 H8 T1023 d = 64 backward 46 us, then 44 us).
 template <int D>
 __global__ void __launch_bounds__(kPrefix)
 scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
@@ -275,8 +285,10 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
 
     const int n0 = wn * 32;
     float acc[2][4][4] = {};
-    if (!zero)
-        gemm<2, 4, true>(acc, sA + m0 * LR, LR, 1, X + n0 * (trans ? D : 1), trans ? 1 : D, trans ? D : 1, D);
+    if (!zero) {
+        if (trans) gemm<2, 4, true>(acc, sA + m0 * LR, LR, 1, X + n0 * D, 1, D, D);
+        else gemm<2, 4, true>(acc, sA + m0 * LR, LR, 1, X + n0, D, 1, D);
+    }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
