@@ -129,6 +129,29 @@ def test_in_place(width):
         assert all(torch.equal(a, c) for a, c in zip((dx, dw, db), ref))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,width", [(150001, 64), (70001, 136), (30001, 520), (9001, 2040), (6001, 4104),
+                                        (3001, 8184)])
+def test_many_rows_a_block(rows, width, dtype):
+    """Blocks that take many rows, some ahead of the others, in place as well; the widths fill the last
+    vectors of a row in part.  The tolerances are those above: a thread adds up a few hundred rows of
+    random signs, whose roundings grow like the sums."""
+    x, dy, w, b = (t.cuda() for t in make(rows, width, dtype, seed=width))
+    y, mean, rstd = fw.layer_norm(x, w, b)
+    dx, dw, db = fw.layer_norm_backward(dy, x, w, mean, rstd)
+    assert R.rel(y, R.layer_norm(x, w, b)[0]) <= TOL[dtype]
+    rdx, rdw, rdb = R.layer_norm_backward(dy, x, w)
+    assert R.rel(dx, rdx) <= TOL[dtype]
+    assert R.rel(dw, rdw) <= TOL[F32] and R.rel(db, rdb) <= TOL[F32]
+    z = x.clone()
+    fw.layer_norm(z, w, b, y=z)
+    assert torch.equal(z, y)
+    g, z = dy.clone(), x.clone()
+    for args, buf in (((g, x), g), ((dy, z), z)):
+        got = fw.layer_norm_backward(*args, w, mean, rstd, dx=buf)
+        assert all(torch.equal(a, c) for a, c in zip(got, (dx, dw, db)))
+
+
 def test_same_bits_on_every_run_and_in_a_graph():
     x, dy, w, b = (t.cuda() for t in make(3000, 640, BF16, seed=4))
     run = lambda: [*fw.layer_norm(x, w, b)] + [*fw.layer_norm_backward(  # noqa: E731
