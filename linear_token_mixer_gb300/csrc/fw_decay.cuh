@@ -116,7 +116,7 @@ struct LayerNormBwdArgs {
     float *ws;
 };
 
-// `n` scans over chains of the same shape (n <= 3) in the same launches.
+// One forward scan, or the three of a backward pass (dq, dv, dk) over chains of the same shape.
 size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype);   // bytes of one scan
 cudaError_t launch_scans(const ScanArgs *s, int n, cudaStream_t stream);
 cudaError_t launch_decay_step(const DecayStepArgs &a, cudaStream_t s);

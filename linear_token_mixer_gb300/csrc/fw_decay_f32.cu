@@ -444,13 +444,7 @@ size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype) {
 
 // bf16 rows run on the fifth-generation tensor cores, fp32 rows here.
 cudaError_t launch_scans(const ScanArgs *s, int n, cudaStream_t stream) {
-    if (s[0].dtype == FW_BF16) {
-        for (int i = 0; i < n; ++i) {
-            const cudaError_t e = launch_scan_tc(s[i], i > 0, stream);
-            if (e != cudaSuccess) return e;
-        }
-        return cudaSuccess;
-    }
+    if (s[0].dtype == FW_BF16) return launch_scans_tc(s, n, stream);
     Scans all{};
     for (int i = 0; i < n; ++i) all.s[i] = s[i];
     return s[0].d == 64 ? launch<64>(all, n, stream) : launch<128>(all, n, stream);

@@ -220,13 +220,25 @@ __device__ __forceinline__ uint64_t below(uint64_t x) {
     return fma2(x & 0xffff0000ffff0000ull, pair(-1.f, -1.f), x);
 }
 
+// The scans of a launch: one forward, or two reverse ones (dv and dk) over the same rows, whose CTAs
+// of a chain are neighbours.  Both read q and do, and the second of them finds the tiles in L2 (B8 H16
+// T2048 d = 128 backward 153 us in launches of their own, 151 us).
+template <int N> struct Jobs {
+    struct {
+        CUtensorMap a, b, c, out;
+        ScanArgs args;
+    } s[N];
+};
+
 // PRE: only the state of a segment, from zero (segment 0: from X0), into the workspace.
 template <int D, bool REV, bool PRE, bool NORM>
 __global__ void __launch_bounds__(NTHREADS, 1)
-scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
-               const __grid_constant__ CUtensorMap tmc, const __grid_constant__ CUtensorMap tmo,
-               const ScanArgs a, const int nseg, const int by_length, const int order) {
+scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, const int by_length, const int order) {
     using L = Lay<D, PRE>;
+    const auto &job = jobs.s[REV ? blockIdx.x & 1 : 0];
+    const int block = REV ? blockIdx.x >> 1 : blockIdx.x;
+    const ScanArgs &a = jobs.s[0].args, &own = job.args;   // own: out, X_out, x0_trans and ws
+    const CUtensorMap &tma = job.a, &tmb = job.b, &tmc = job.c, &tmo = job.out;
     let_next_grid_start();
     if (order & kWaitFirst) wait_previous_grid();
     extern __shared__ uint8_t smem_raw[];
@@ -234,8 +246,8 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grid_seg = PRE ? nseg - 1 : nseg;
-    int64_t chain = blockIdx.x / grid_seg;
-    const int seg = blockIdx.x % grid_seg;
+    int64_t chain = block / grid_seg;
+    const int seg = block % grid_seg;
     if (!PRE && by_length) {                        // the longest batch rows' chains start first
         int *row = reinterpret_cast<int *>(sm + L::MISC + 8);
         const int B = (int)(a.n_chains / a.H);
@@ -252,7 +264,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     const Seg sg = seg_of(n, seg, nseg);
     const int nch = sg.last - sg.first;
     const bool final_seg = !PRE && seg == nseg - 1;
-    if (nch == 0 && !(final_seg && (a.X_out || a.zero_rest)) && !(PRE && seg == 0)) {
+    if (nch == 0 && !(final_seg && (own.X_out || a.zero_rest)) && !(PRE && seg == 0)) {
         if (order & kWaitLast) wait_previous_grid();
         return;
     }
@@ -265,7 +277,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     // is divided by a power of g.
     const bool mild = fabsf(lg) * C <= 24.f;
     const int x_slots = nseg;                       // workspace: nseg - 1 segment states, X0's copy
-    float *const ws = a.ws + chain * x_slots * D * D;
+    float *const ws = own.ws + chain * x_slots * D * D;
 
     volatile int *s_abort = reinterpret_cast<volatile int *>(sm + L::MISC);
     volatile uint32_t *s_tmem = reinterpret_cast<volatile uint32_t *>(sm + L::MISC + 4);
@@ -300,7 +312,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
     // 2^-17 e^-3.5 = 2.3e-7 of the returned state.  (A chunk early rather than late; all of them
     // without decay.)
     int third_from = 0;
-    if (!a.X_out) third_from = INT_MAX;
+    if (!own.X_out) third_from = INT_MAX;
     else if (lg < 0.f) {
         const float left = (float)n - 3.5f / -lg;    // tokens processed when e^-3.5 begins to matter
         third_from = max((int)(fmaxf(left, 0.f) / C) - 2 - sg.first, 0);
@@ -605,7 +617,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
                 const bool whole = w * 32 + 32 <= nv;
                 const int st = i % L::NST;
                 const int64_t row0 = (int64_t)chunk_id(i) * C;
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(own.out) +
                                      (chain * a.T + row0 + row) * D;
                 const uint32_t to = tile(st, XA) + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
                 tmem_stream(tmem + lb + COL_O, 0, D, [&](float (&v)[16], int c) {
@@ -659,7 +671,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             if (lane == 0) bulk_wait0();
             if (!ok && lane == 0) fail_now();
             if (a.zero_rest && final_seg && ok) {    // rows behind the sequence's end
-                uint4 *rest = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (chain * a.T + n) * D);
+                uint4 *rest = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(own.out) + (chain * a.T + n) * D);
                 const int64_t pieces = (a.T - n) * (D / 8);
                 for (int64_t z = tid - 8 * 32; z < pieces; z += 128) rest[z] = make_uint4(0u, 0u, 0u, 0u);
             }
@@ -773,11 +785,11 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
         for (int e = 0; e < XC_; ++e) x[e] = 0.f;
         if (mine) {                                  // the state on entry
             // with S_T = S0 the last segment may finish before another starts: they read a copy
-            const bool copy = nseg > 1 && a.X0 && a.X_out == a.X0;
+            const bool copy = nseg > 1 && a.X0 && own.X_out == a.X0;
             float *const x0_copy = ws + (int64_t)(nseg - 1) * D * D;
             if (seg == 0 && a.X0) {
                 const float *src = !PRE && copy ? x0_copy : a.X0 + chain * D * D;
-                if (a.x0_trans) {
+                if (own.x0_trans) {
 #pragma unroll
                     for (int e = 0; e < XC_; ++e) x[e] = src[(c0 + e) * D + d];
                 } else {
@@ -860,7 +872,7 @@ scan_tc_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ 
             }
         }
         float *dst = PRE ? ws + (int64_t)seg * D * D
-                         : final_seg && a.X_out ? a.X_out + chain * D * D : nullptr;
+                         : final_seg && own.X_out ? own.X_out + chain * D * D : nullptr;
         if (ok && mine && dst)
 #pragma unroll
             for (int e = 0; e < XC_; e += 4)
@@ -903,62 +915,91 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t T, int64_t nc, int d, int
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Segments of each chain, at most what fills the GPU with one CTA an SM: those of the least
-// estimated time, from what was measured at d = 128: 2.8 us a chunk, and where there are segments a
-// launch of 11 us and 2 us a chunk for their states, and 0.7 us to add up each state before the last.
+// Estimated time (us) of chains that take one CTA an SM, each in `s` segments, from what was measured at
+// d = 128: 2.8 us a chunk, and where there are segments a launch of 11 us and 2 us a chunk for their
+// states, and 0.7 us to add up each state before the last.
+double estimate(int64_t chunks, int s) {
+    if (s == 1) return 2.8 * (double)chunks;
+    return 11.0 + 4.8 * (double)((chunks + s - 1) / s) + 0.7 * s;
+}
+
+// Segments of each chain, at most what fills the GPU with one CTA an SM: those of the least estimated
+// time.  (More of them than SMs start one after the other: B1 H32 T32768 in four segments 315 us, in
+// nine 333 us.)
 int segments(int64_t n_chains, int64_t T) {
     const int64_t chunks = (T + C - 1) / C;
     int best = 1;
-    double least = 2.8 * (double)chunks;
-    for (int s = 2; s <= kSMs / n_chains && s <= chunks; ++s) {
-        const double t = 11.0 + 4.8 * (double)((chunks + s - 1) / s) + 0.7 * s;
-        if (t < least) {
-            least = t;
-            best = s;
-        }
-    }
+    for (int s = 2; s <= kSMs / n_chains && s <= chunks; ++s)
+        if (estimate(chunks, s) < estimate(chunks, best)) best = s;
     return best;
 }
 
 // `follows`: behind another scan of the same call.
 template <int D, bool REV>
-cudaError_t launch(const ScanArgs &a, bool follows, cudaStream_t s) {
-    CUtensorMap ta, tb, tc, to;
-    if (!make_map(&ta, a.a, a.T, a.n_chains, D) || !make_map(&tb, a.b, a.T, a.n_chains, D) ||
-        !make_map(&tc, a.c, a.T, a.n_chains, D) || !make_map(&to, a.out, a.T, a.n_chains, D, 32))
-        return cudaErrorInvalidValue;
-    const int nseg = segments(a.n_chains, a.T);
+cudaError_t launch(const ScanArgs *scans, int nseg, bool follows, cudaStream_t s) {
+    constexpr int N = REV ? 2 : 1;
+    Jobs<N> jobs;
+    for (int i = 0; i < N; ++i) {
+        const ScanArgs &a = scans[i];
+        jobs.s[i].args = a;
+        if (!make_map(&jobs.s[i].a, a.a, a.T, a.n_chains, D) || !make_map(&jobs.s[i].b, a.b, a.T, a.n_chains, D) ||
+            !make_map(&jobs.s[i].c, a.c, a.T, a.n_chains, D) || !make_map(&jobs.s[i].out, a.out, a.T, a.n_chains, D, 32))
+            return cudaErrorInvalidValue;
+    }
+    const ScanArgs &a = scans[0];
+    const int64_t ctas = N * a.n_chains;
     cudaError_t e;
     if (nseg > 1) {
         auto k = scan_tc_kernel<D, REV, true, false>;
         constexpr int smem = (int)Lay<D, true>::ALLOC;
         static std::atomic<uint64_t> pre_done{0};
         if ((e = allow_smem(k, smem, pre_done)) != cudaSuccess) return e;
-        if ((e = launch_after(k, dim3((unsigned)(a.n_chains * (nseg - 1))), NTHREADS, smem, s, follows, ta, tb,
-                              tc, to, a, nseg, 0, follows ? kWaitLast : 0)) != cudaSuccess)
+        if ((e = launch_after(k, dim3((unsigned)(ctas * (nseg - 1))), NTHREADS, smem, s, follows, jobs, nseg, 0,
+                              follows ? kWaitLast : 0)) != cudaSuccess)
             return e;
     }
-    auto k = a.norm.on ? scan_tc_kernel<D, REV, false, true> : scan_tc_kernel<D, REV, false, false>;
     constexpr int smem = (int)Lay<D, false>::ALLOC;
+    auto k = scan_tc_kernel<D, REV, false, false>;
+    if constexpr (!REV)                             // (an output norm has no backward pass)
+        if (a.norm.on) k = scan_tc_kernel<D, REV, false, true>;
     static std::atomic<uint64_t> done[2];
     if ((e = allow_smem(k, smem, done[a.norm.on ? 1 : 0])) != cudaSuccess) return e;
     // Padded batches of more chains than SMs: the CTAs of the longest rows start first, so that none
     // of them runs alone in the end.
-    const int by_length = a.lens && a.n_chains > kSMs && a.n_chains / a.H <= kMaxRanked;
-    return launch_after(k, dim3((unsigned)(a.n_chains * nseg)), NTHREADS, smem, s, nseg > 1 || follows, ta, tb, tc,
-                        to, a, nseg, by_length, nseg > 1 ? kWaitFirst : follows ? kWaitLast : 0);
+    const int by_length = a.lens && ctas > kSMs && a.n_chains / a.H <= kMaxRanked;
+    return launch_after(k, dim3((unsigned)(ctas * nseg)), NTHREADS, smem, s, nseg > 1 || follows, jobs, nseg,
+                        by_length, nseg > 1 ? kWaitFirst : follows ? kWaitLast : 0);
+}
+
+// Segments of the forward scan of a backward pass, and of its two reverse ones: a launch after the
+// other, each in as many as it likes, or all three scans at once in one piece (B1 H32 T8192 d = 128
+// one after the other 280 us, at once 181 us; B1 H8 T4096 d = 64, in segments, 64 us).
+void segments_backward(int64_t n_chains, int64_t T, int *fwd, int *rev) {
+    const int64_t chunks = (T + C - 1) / C;
+    *fwd = segments(n_chains, T);
+    *rev = segments(2 * n_chains, T);
+    const double waves = (double)((3 * n_chains + kSMs - 1) / kSMs);
+    if (waves * estimate(chunks, 1) <= estimate(chunks, *fwd) + estimate(chunks, *rev)) *fwd = *rev = 1;
+}
+
+template <int D> cudaError_t launch_scans_of(const ScanArgs *s, int n, cudaStream_t stream) {
+    if (n == 1) return launch<D, false>(s, segments(s->n_chains, s->T), false, stream);
+    int fwd, rev;
+    segments_backward(s->n_chains, s->T, &fwd, &rev);
+    const cudaError_t e = launch<D, false>(s, fwd, false, stream);
+    return e != cudaSuccess ? e : launch<D, true>(s + 1, rev, true, stream);
 }
 
 }  // namespace
 
+// (a pair's segments are no more than one scan's)
 size_t scan_tc_workspace(int64_t n_chains, int64_t T, int d) {
     const int nseg = segments(n_chains, T);
     return nseg > 1 ? (size_t)n_chains * nseg * d * d * sizeof(float) : 0;
 }
 
-cudaError_t launch_scan_tc(const ScanArgs &a, bool follows, cudaStream_t s) {
-    if (a.d == 64) return a.rev ? launch<64, true>(a, follows, s) : launch<64, false>(a, follows, s);
-    return a.rev ? launch<128, true>(a, follows, s) : launch<128, false>(a, follows, s);
+cudaError_t launch_scans_tc(const ScanArgs *s, int n, cudaStream_t stream) {
+    return s->d == 64 ? launch_scans_of<64>(s, n, stream) : launch_scans_of<128>(s, n, stream);
 }
 
 }  // namespace fw
