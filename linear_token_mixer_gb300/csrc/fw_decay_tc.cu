@@ -333,12 +333,23 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         fence_mbar_init();
         *s_abort = 0;
     }
-    for (int i = tid; i <= C; i += NTHREADS) pw[i] = decay_pow(lg, (float)i);
-    if (tid < C) kw[tid] = a.in_scale * decay_pow(lg, (float)(REV ? tid + 1 : C - 1 - tid));
-    if (warp == 3) tmem_alloc(sb + L::MISC + 4, TMEM_COLS);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    // Warp 0 needs none of what follows: it only announces the barriers, and its first tiles are on
+    // their way while the others make the tables and tensor memory ready.
+    if (warp == 0) {
+        __syncwarp();
+        asm volatile("barrier.cta.arrive 1, %0;" ::"n"(NTHREADS) : "memory");
+    } else {
+        const int j = tid - 32;
+        if (j <= C) pw[j] = decay_pow(lg, (float)j);
+        else if (j <= 2 * C) {
+            const int x = j - C - 1;
+            kw[x] = a.in_scale * decay_pow(lg, (float)(REV ? x + 1 : C - 1 - x));
+        }
+        if (warp == 3) tmem_alloc(sb + L::MISC + 4, TMEM_COLS);
+        tc_fence_before();
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(NTHREADS) : "memory");
+        tc_fence_after();
+    }
     const uint32_t tmem = __shfl_sync(~0u, *s_tmem, 0);
 
     // Every MMA of this warp has finished before it leaves.
@@ -668,7 +679,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     mbar_arrive(empty(st, XA));
                 }
             }
-            if (lane == 0) bulk_wait0();
             if (!ok && lane == 0) fail_now();
             if (a.zero_rest && final_seg && ok) {    // rows behind the sequence's end
                 uint4 *rest = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(own.out) + (chain * a.T + n) * D);
