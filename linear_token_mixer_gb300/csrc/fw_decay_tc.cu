@@ -201,6 +201,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -607,22 +612,29 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     // mean and centred sum of squares of 16 values at a time, merged
                     float cnt = 0.f, m2 = 0.f;
                     tmem_stream(tmem + lb + COL_O, 0, D, [&](float (&v)[16], int) {
-                        float t = 0.f, q = 0.f;
+                        uint64_t x[8], y = 0;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            v[e] *= rd;
-                            t += v[e];
+                        for (int e = 0; e < 8; ++e) {
+                            x[e] = mul2(pair(v[2 * e], v[2 * e + 1]), pair(rd, rd));
+                            y = add2(y, x[e]);
                         }
-                        t *= 1.f / 16.f;
+                        float2 f = halves(y);
+                        const float t = (f.x + f.y) * (1.f / 16.f);
+                        y = 0;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) q = fmaf(v[e] - t, v[e] - t, q);
+                        for (int e = 0; e < 8; ++e) {
+                            const uint64_t c = add2(x[e], pair(-t, -t));
+                            y = fma2(c, c, y);
+                        }
+                        f = halves(y);
                         const float r = __fdividef(16.f, cnt + 16.f), dm = t - mean;
                         mean = fmaf(dm, r, mean);
-                        m2 += fmaf(dm * dm, cnt * r, q);
+                        m2 += fmaf(dm * dm, cnt * r, f.x + f.y);
                         cnt += 16.f;
                     });
                     rstd = rsqrtf(m2 / D + a.norm.eps);
                 }
+                const float n1 = rd * rstd, n0 = -mean * rstd;
                 // G and A X have read this chunk's A tile: the rows are staged over it and leave
                 // by a tensor store a warp (whole rows), or one by one at a sequence's end
                 const bool whole = w * 32 + 32 <= nv;
@@ -639,10 +651,14 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                                                             : make_float4(1.f, 1.f, 1.f, 1.f);
                             const float4 bs = a.norm.bias ? __ldg(reinterpret_cast<const float4 *>(a.norm.bias + c + e))
                                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-                            v[e] = fmaf(fmaf(v[e], rd, -mean) * rstd, wt.x, bs.x);
-                            v[e + 1] = fmaf(fmaf(v[e + 1], rd, -mean) * rstd, wt.y, bs.y);
-                            v[e + 2] = fmaf(fmaf(v[e + 2], rd, -mean) * rstd, wt.z, bs.z);
-                            v[e + 3] = fmaf(fmaf(v[e + 3], rd, -mean) * rstd, wt.w, bs.w);
+                            const float2 lo = halves(fma2(fma2(pair(v[e], v[e + 1]), pair(n1, n1), pair(n0, n0)),
+                                                          pair(wt.x, wt.y), pair(bs.x, bs.y)));
+                            const float2 hi = halves(fma2(fma2(pair(v[e + 2], v[e + 3]), pair(n1, n1), pair(n0, n0)),
+                                                          pair(wt.z, wt.w), pair(bs.z, bs.w)));
+                            v[e] = lo.x;
+                            v[e + 1] = lo.y;
+                            v[e + 2] = hi.x;
+                            v[e + 3] = hi.y;
                         }
                     } else {
 #pragma unroll
