@@ -31,8 +31,8 @@
 // Measured (one GB300): B8 H16 T4096 d = 128, 128 chains, 545 MB of rows and states: 103.6 us, 5.3
 // TB/s, 77 % of the measured copy rate; B1 H32 T32768, four segments a chain: 312 us, of which the
 // states of the segments, read again, are a third.  What bounds it is the period of a chunk, 2.8 us,
-// in one CTA: the tensor pipe is busy for 32 % of it, the issue slots for 38 %, DRAM at 56 % (ncu,
-// T2048), and the rest is the roles' round trips through tensor memory and barriers.  A second CTA an
+// in one CTA, and 10 us for its start: at T2048 the tensor pipe is busy for 34 % of the time, the issue
+// slots for 36 %, DRAM at 54 %, and the rest is the roles' round trips through tensor memory and barriers.  A second CTA an
 // SM would fill it but finds no room: the tiles take 192 KB, G, O and the update 384 columns.
 // Tensor memory: G (P over it) 128 columns, O 128, the update 128, the split operand 2 x 48.
 // Every wait is bounded; on expiry the kernel records an error, the other roles stop at their
