@@ -500,7 +500,7 @@ ScanArgs scan_of(const fw_shape *shape, fw_dtype dtype, const float *log_decay,
 extern "C" int64_t fw_decay_workspace(const fw_shape *shape, fw_dtype dtype, int backward) {
     const int st = check_decay(shape, dtype);
     if (st != FW_OK) return st;
-    const size_t one = scan_workspace(shape->B * shape->H, shape->T, shape->d_k, dtype);
+    const size_t one = scan_workspace(shape->B * shape->H, shape->T, shape->d_k, dtype, backward != 0);
     return (int64_t)(backward ? 3 * one : one);
 }
 

@@ -437,8 +437,8 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
 
 }  // namespace
 
-size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype) {
-    if (dtype == FW_BF16) return scan_tc_workspace(n_chains, T, d);
+size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype, bool backward) {
+    if (dtype == FW_BF16) return scan_tc_workspace(n_chains, T, d, backward);
     return (size_t)n_chains * (size_t)((T + C - 1) / C) * d * d * sizeof(float);
 }
 

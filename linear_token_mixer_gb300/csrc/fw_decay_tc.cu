@@ -1018,9 +1018,9 @@ template <int D> cudaError_t launch_scans_of(const ScanArgs *s, int n, cudaStrea
 
 }  // namespace
 
-// (a pair's segments are no more than one scan's)
-size_t scan_tc_workspace(int64_t n_chains, int64_t T, int d) {
-    const int nseg = segments(n_chains, T);
+size_t scan_tc_workspace(int64_t n_chains, int64_t T, int d, bool backward) {
+    int nseg = segments(n_chains, T), rev;
+    if (backward) segments_backward(n_chains, T, &nseg, &rev);   // rev, of twice the chains, is no more
     return nseg > 1 ? (size_t)n_chains * nseg * d * d * sizeof(float) : 0;
 }
 

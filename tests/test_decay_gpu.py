@@ -295,6 +295,25 @@ def test_long_and_many_chains(B, H, T, d, dtype):
     check_state(got[3], ref[3])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,T", [(1, 32, 1300), (2, 13, 900), (3, 1, 5000), (1, 60, 1500)])
+def test_backward_of_few_chains(B, H, T, d):
+    """All three scans at once in one piece, or one after the other in segments, with a workspace of
+    exactly the size that is asked for."""
+    x, g = inputs(B, H, T, d, BF16, seed=T, kind="slow" if H < 10 else "mixed")
+    ln = torch.tensor([T, T - 77, 3][:B], dtype=torch.int32)
+    n = fw.decay_workspace(B, H, T, d, backward=True)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+    for _ in range(2):
+        got = fw.decay_backward(g["q"], g["k"], g["v"], g["ld"], g["do"], g["S0"], g["dS"], scale=0.1,
+                                lens=ln.cuda(), workspace=ws)
+    fw.check()
+    _, _, ref = _reference_on_gpu(g, ln, 0.1)
+    for a, r in zip(got[:3], ref[:3]):
+        check_rows(a, r, BF16)
+    check_state(got[3], ref[3])
+
+
 def _reference_on_gpu(g, ln, scale):
     q, k, v, do = (g[n].double() for n in ("q", "k", "v", "do"))
     B, H, T, d = q.shape
