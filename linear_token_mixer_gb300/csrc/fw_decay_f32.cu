@@ -14,7 +14,7 @@
 // scores before it waits for the states, which it reads straight into the MMAs' operands.  Chains
 // of one chunk need no workspace and no order between the parts: one launch does both (scan_one).
 //
-// Measured (one GB300): B4 H8 T1000 d = 64 ragged 34 us, B4 H8 T2048 d = 128 165 us, the three scans of
+// Measured (one GB300): B4 H8 T1000 d = 64 ragged 34 us, B4 H8 T2048 d = 128 167 us, the three scans of
 // a backward pass of B2 H8 T1023 d = 64 44 us.  The short ones are bound by three launches that follow
 // each other, the long ones by the split products: scan_out (d = 128) issues in 36 % of its
 // cycles, its tensor pipe is busy for 39 %, and its sixteen warps an SM wait for the states' loads and
@@ -48,17 +48,18 @@ __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
-// acc += A B for a warp's 16 MT x 8 NT tile; element (m, k) of A at a[m * am + k * ak], element
-// (k, n) of B at b[k * bk + n * bn].  The MMAs round towards zero: APART sums the two small terms on
-// their own, so that the large sum is cut a third as often.  B is fetched a step ahead: the states come
-// from global memory (B4 H8 T2048 d = 128 173 us, then 165 us, with the strides known at compile time).
-template <int MT, int NT, bool APART>
-__device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, int am, int ak,
+// acc += A B for a warp's 32 x 8 NT tile; element (m, k) of A at a[m * am + k * ak], element (k, n)
+// of B at b[k * bk + n * bn].  The MMAs round towards zero: the two small terms are summed on their
+// own, so that the large sum is cut a third as often (the d = 128 states summed in one: rows 9.6e-7
+// off, apart 7.3e-7, for 2 % of the time).  B is fetched a step ahead: the states come from
+// global memory (B4 H8 T2048 d = 128 173 us, then 165 us, with the strides known at compile time).
+template <int NT>
+__device__ __forceinline__ void gemm(float (&acc)[2][NT][4], const float *a, int am, int ak,
                                      const float *b, int bk, int bn, int K) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     a += g * am + t * ak;
     b += t * bk + g * bn;
-    float low[APART ? MT : 1][APART ? NT : 1][4] = {};
+    float low[2][NT][4] = {};
     float nb[NT][2];
     auto fetch = [&](int k) {
 #pragma unroll
@@ -69,9 +70,9 @@ __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, in
     fetch(0);
 #pragma unroll 2
     for (int k = 0; k < K; k += 8) {
-        uint32_t ah[MT][4], al[MT][4];
+        uint32_t ah[2][4], al[2][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 split(a[(16 * m + 8 * (e & 1)) * am + (k + 4 * (e >> 1)) * ak], ah[m][e], al[m][e]);
@@ -87,17 +88,16 @@ __device__ __forceinline__ void gemm(float (&acc)[MT][NT][4], const float *a, in
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    sm100::mma_tf32_16x8x8(APART && term < 2 ? low[APART ? m : 0][APART ? n : 0] : acc[m][n],
-                                           term == 0 ? al[m] : ah[m], term == 1 ? bl[n] : bh[n]);
+                for (int m = 0; m < 2; ++m)
+                    sm100::mma_tf32_16x8x8(term < 2 ? low[m][n] : acc[m][n], term == 0 ? al[m] : ah[m],
+                                           term == 1 ? bl[n] : bh[n]);
     }
-    if constexpr (APART)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][n][e] += low[m][n][e];
+            for (int e = 0; e < 4; ++e) acc[m][n][e] += low[m][n][e];
 }
 
 // Rows [0, nv) of a chunk's 64 x D tile (rows behind them zero), each times row_w[r].
@@ -160,29 +160,31 @@ __device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, 
     load_tile<D, LD>(sB, static_cast<const float *>(s.b) + base, k.nv, w);
     load_tile<D, LD>(sC, static_cast<const float *>(s.c) + base, k.nv, nullptr);
     __syncthreads();
-    // D x D over 2 x (D / 32) warps: D / 2 rows of X by 32 columns each
+    // D x D over 2 x (D / 32) warps: D / 2 rows of X by 32 columns each, 32 rows at a time
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m0 = (warp & 1) * (D / 2), n0 = (warp >> 1) * 32;
-    constexpr int MT = D / 32;
-    float acc[MT][4][4] = {};
-    gemm<MT, 4, (MT == 2)>(acc, sB + m0, 1, LD, sC + n0, LD, 1, C);
+    const int n0 = (warp >> 1) * 32;
     float *M = ONE ? s.X_out + k.chain * D * D : s.ws + (int64_t)blockIdx.x * D * D;
     const float *X0 = ONE && s.X0 ? s.X0 + k.chain * D * D : nullptr;
     const float gn = decay_pow(lg, (float)k.nv);
+#pragma unroll 1
+    for (int m0 = (warp & 1) * (D / 2), m1 = m0 + D / 2; m0 < m1; m0 += 32) {
+        float acc[2][4][4] = {};
+        gemm<4>(acc, sB + m0, 1, LD, sC + n0, LD, 1, C);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = m0 + 16 * m + (lane >> 2) + 8 * h, c = n0 + 8 * n + 2 * (lane & 3);
-                float2 v = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
-                if (X0) {
-                    v.x = fmaf(gn, s.x0_trans ? X0[c * D + r] : X0[r * D + c], v.x);
-                    v.y = fmaf(gn, s.x0_trans ? X0[(c + 1) * D + r] : X0[r * D + c + 1], v.y);
+                for (int h = 0; h < 2; ++h) {
+                    const int r = m0 + 16 * m + (lane >> 2) + 8 * h, c = n0 + 8 * n + 2 * (lane & 3);
+                    float2 v = make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+                    if (X0) {
+                        v.x = fmaf(gn, s.x0_trans ? X0[c * D + r] : X0[r * D + c], v.x);
+                        v.y = fmaf(gn, s.x0_trans ? X0[(c + 1) * D + r] : X0[r * D + c + 1], v.y);
+                    }
+                    *reinterpret_cast<float2 *>(M + r * D + c) = v;
                 }
-                *reinterpret_cast<float2 *>(M + r * D + c) = v;
-            }
+    }
 }
 
 template <int D>
@@ -265,7 +267,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
         constexpr int NT = C / WN / 8;
         const int n0 = wn * (C / WN);
         float p[2][NT][4] = {};
-        gemm<2, NT, true>(p, sA + m0 * LR, LR, 1, sB + n0 * LR, 1, LR, D);
+        gemm<NT>(p, sA + m0 * LR, LR, 1, sB + n0 * LR, 1, LR, D);
         __syncthreads();                   // B is read
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -286,8 +288,8 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
     const int n0 = wn * 32;
     float acc[2][4][4] = {};
     if (!zero) {
-        if (trans) gemm<2, 4, true>(acc, sA + m0 * LR, LR, 1, X + n0 * D, 1, D, D);
-        else gemm<2, 4, true>(acc, sA + m0 * LR, LR, 1, X + n0, D, 1, D);
+        if (trans) gemm<4>(acc, sA + m0 * LR, LR, 1, X + n0 * D, 1, D, D);
+        else gemm<4>(acc, sA + m0 * LR, LR, 1, X + n0, D, 1, D);
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -301,7 +303,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
                 acc[m][n][2 * h + 1] *= rd;
             }
         }
-    gemm<2, 4, true>(acc, sB + m0 * LP, LP, 1, sC + n0, LC, 1, C);
+    gemm<4>(acc, sB + m0 * LP, LP, 1, sC + n0, LC, 1, C);
 
 #pragma unroll
     for (int m = 0; m < 2; ++m)
