@@ -7,9 +7,12 @@
 //     P = mask . g^|i-j| . G          (bf16)
 //     O = diag(g^(i+1)) (A X) + P C                 128 x d x d, 128 x d x 128
 //     X <- g^n X + (diag(w) B)^T C                  d x d x 128, three times
-// The last product's left operand is split into bf16 terms, so that the fp32 state loses nothing to
-// its operands: three (24 bits of w_j b_j) where the chunk still weighs in the state that is
-// returned, two (16 bits) where e^-3.5 of it or less is left by then, or none is returned.  P and
+// The last product's left operand is split into bf16 terms, each cut towards zero, so that the fp32 state
+// loses nothing to its operands: three (less than 2^-23 of w_j b_j is cut) where a state is returned, two
+// (less than 2^-15 at most, 7e-6 on average, and always towards zero) where it is only read into bf16
+// rows.  (Two terms for chunks of which e^-3.5 or less is left in the returned state, as if every chunk
+// wrote as much, left states whose last tokens write little 1e-5 off; without them B8 H16 T4096 d = 128 takes
+// 105.7 us for 103.1.)  P and
 // the copy of X that A reads are rounded to bf16 once, like the output rows.
 //
 // One CTA per chain, or per segment of a chain where chains are few, warp-specialised:
@@ -39,7 +42,6 @@
 // next wait, copies and MMAs in flight are drained, tensor memory is freed and the kernel exits.
 #include <cudaTypedefs.h>
 
-#include <climits>
 #include <mutex>
 
 #include "fw_decay_tc.cuh"
@@ -313,15 +315,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
     const int tail_tokens = (int)(n - (int64_t)(sg.total - 1) * C);
     const int tail_i = tail_tokens == C ? -1 : (REV ? 0 : sg.total - 1) - sg.first;
     auto tokens = [&](int i) -> int { return i == tail_i ? tail_tokens : C; };
-    // From chunk `third_from` on the update takes the third term: two leave 2^-17 of it, and
-    // 2^-17 e^-3.5 = 2.3e-7 of the returned state.  (A chunk early rather than late; all of them
-    // without decay.)
-    int third_from = 0;
-    if (!own.X_out) third_from = INT_MAX;
-    else if (lg < 0.f) {
-        const float left = (float)n - 3.5f / -lg;    // tokens processed when e^-3.5 begins to matter
-        third_from = max((int)(fmaxf(left, 0.f) / C) - 2 - sg.first, 0);
-    }
+    const bool lo3 = own.X_out != nullptr;          // the update takes its third term
 
     if (tid == 0) {
         for (int i = 0; i < L::NBAR; ++i) {
@@ -453,7 +447,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         const uint64_t dc0 = sdesc_sw128(tile(0, XC), HALF, 1024);
         for (int i = 0; i < nch && ok; ++i, r.next()) {
             const int st = r.st, ub = i % L::UB;
-            const bool lo3 = i >= third_from;
             ok = __all_sync(~0u, wait_bar(full(st, XC), r.ph, limit, s_abort) &&
                                      (i < L::UB || wait_bar(bar(L::UFREE + ub), (uint32_t)(i / L::UB - 1) & 1u, limit, s_abort)));
             const uint64_t dc = dc0 + r.st * ((L::NT * L::TILE) >> 4);
@@ -742,7 +735,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             }
             // ldmatrix x4: matrices (tokens +0, +8) x (rows +0, +8) of X, 16 rows a half-warp
             const uint32_t r8 = (uint32_t)lane & 7u, m = (uint32_t)lane >> 3;
-            const bool lo3 = i >= third_from;
             for (int u = b; u < 4; u += L::KG) {
                 const int use = (4 * i + u) / L::KG;   // of this buffer
                 // thread t: tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3
