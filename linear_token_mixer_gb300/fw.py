@@ -149,7 +149,7 @@ def prefill(q, k, v, beta=None, lam=None, S0=None, *, mode="falcon1", phi="ident
     if S_T is None:
         S_T = torch.empty((B, H, d, d), device=q.device, dtype=torch.float32)
     shp = fw_shape(B, H, T, d, v.shape[-1])
-    _norm(norm, norm_eps, d, q)
+    _norm_ready(norm, norm_eps, q, o, stream, S_T)
     fn = lib().fw_prefill_noalloc if noalloc else lib().fw_prefill_ex
     st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(lam), _ptr(S0), _ptr(k_init), _ptr(o),
             _ptr(S_T), ctypes.byref(shp), DTYPES.get(q.dtype, -1), MODES[mode], PHIS[phi],
@@ -167,7 +167,7 @@ def step(q, k_prev, v, beta, lam, S, *, mode="falcon1", phi="identity", eps=1e-6
     if o is None:
         o = torch.empty_like(q)
     shp = fw_shape(B, H, 1, d, v.shape[-1])
-    _norm(norm, norm_eps, d, q)
+    _norm_ready(norm, norm_eps, q, o, stream, S)
     st = lib().fw_step_ex(_ptr(q), _ptr(k_prev), _ptr(v), _ptr(beta), _ptr(lam), _ptr(S),
                           _ptr(o), ctypes.byref(shp), DTYPES.get(q.dtype, -1), MODES[mode],
                           PHIS[phi], float(eps), _flags(rbw, False), _stream(stream))
@@ -209,7 +209,7 @@ def window_prefill(q, k, v, beta, lam, window, S0=None, *, mode="falcon3", phi="
     if win_out is None:
         win_out = new_window(B, H, d, window, q.device)
     shp = fw_shape(B, H, T, d, v.shape[-1])
-    _norm(norm, norm_eps, d, q)
+    _norm_ready(norm, norm_eps, q, o, stream, S_T, *win_out)
     st = lib().fw_window_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(lam), _ptr(S0),
                                  _ptr(k_init), _window(win_in), _ptr(o), _ptr(S_T),
                                  _window(win_out), ctypes.byref(shp), int(window),
@@ -233,7 +233,7 @@ def window_step(q, k_prev, v, beta, lam, S, window, win_in=None, win_out=None, *
     if win_out is None:
         win_out = new_window(B, H, d, window, q.device)
     shp = fw_shape(B, H, 1, d, v.shape[-1])
-    _norm(norm, norm_eps, d, q)
+    _norm_ready(norm, norm_eps, q, o, stream, S, *win_out)
     st = lib().fw_window_step(_ptr(q), _ptr(k_prev), _ptr(v), _ptr(beta), _ptr(lam), _ptr(S),
                               _window(win_in), _ptr(o), _window(win_out), ctypes.byref(shp),
                               int(window), DTYPES.get(q.dtype, -1), MODES[mode], PHIS[phi],
@@ -322,7 +322,7 @@ def _norm(norm, eps, width, like):
     if norm is None:
         return None
     weight, bias = norm
-    if not 0.0 <= eps < float("inf"):
+    if not 0.0 <= ctypes.c_float(eps).value < float("inf"):
         raise ValueError("fw: norm_eps must be finite and not negative")
     return ctypes.byref(fw_norm(_arg(weight, (width,), torch.float32, "norm weight", like),
                                 _arg(bias, (width,), torch.float32, "norm bias", like), eps))
@@ -487,6 +487,26 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbi
             _arg(dx, shape, dt, "dx", x), _arg(dweight, (width,), f32, "dweight", x),
             _arg(dbias, (width,), f32, "dbias", x), rows, width, DTYPES.get(dt, -1), ws, nws)
     return dx, dweight, dbias
+
+
+def _overlap(a, b):
+    x, y = a.data_ptr(), b.data_ptr()
+    return x < y + b.numel() * b.element_size() and y < x + a.numel() * a.element_size()
+
+
+def _norm_ready(norm, eps, q, o, stream, *written):
+    """Refuse an output norm that _with_norm could not apply to the rows of o (written: what else the
+    call writes).  Called before any state moves, so that a refused call has done nothing."""
+    if norm is None:
+        return
+    _norm(norm, eps, q.shape[-1], q)
+    _arg(o, q.shape, q.dtype, "o", q)
+    _On(q, stream)
+    for t in norm:
+        if t is not None and t.data_ptr() % 16:
+            raise FwError(-4, "fw_layer_norm")
+        if t is not None and any(_overlap(t, z) for z in (o, *written)):
+            raise FwError(-9, "fw_layer_norm")
 
 
 def _with_norm(o, norm, norm_eps, stream):
