@@ -3,6 +3,10 @@
 Argument marshalling only: every step of the recurrence runs in the library's
 CUDA kernels.  There is no CPU path; if libfw.so is missing or fails to load,
 every call raises.  torch supplies device memory and streams.
+
+stream= (of every call; None: the current stream of the tensors' device): the kernels run there.  The
+caller has that stream wait for whatever makes the inputs, and waits for it before the outputs are read
+elsewhere; tensors may be given back at once, since the call marks their memory as in use by the stream.
 """
 from __future__ import annotations
 
@@ -126,6 +130,17 @@ def _stream(stream):
     return s.cuda_stream
 
 
+def _used(stream, *tensors):
+    """Work on `stream` uses these tensors: memory of theirs that the caller gives back, as that of a
+    temporary, is not handed out again before the work is done.  (The current stream, None, needs none
+    of this.)"""
+    if stream is None or stream == torch.cuda.current_stream(stream.device):
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _flags(rbw, same_pair):
     return (FLAG_RBW if rbw else 0) | (FLAG_SAME_PAIR if same_pair else 0)
 
@@ -156,6 +171,7 @@ def prefill(q, k, v, beta=None, lam=None, S0=None, *, mode="falcon1", phi="ident
             float(eps), _flags(rbw, same_pair), ALGOS[algo], _stream(stream))
     if st != FW_OK:
         raise FwError(st, "fw_prefill_noalloc" if noalloc else "fw_prefill")
+    _used(stream, q, k, v, beta, lam, S0, k_init, o, S_T, *(norm or ()))
     return _with_norm(o, norm, norm_eps, stream), S_T
 
 
@@ -173,6 +189,7 @@ def step(q, k_prev, v, beta, lam, S, *, mode="falcon1", phi="identity", eps=1e-6
                           PHIS[phi], float(eps), _flags(rbw, False), _stream(stream))
     if st != FW_OK:
         raise FwError(st, "fw_step")
+    _used(stream, q, k_prev, v, beta, lam, S, o, *(norm or ()))
     return _with_norm(o, norm, norm_eps, stream)
 
 
@@ -217,6 +234,7 @@ def window_prefill(q, k, v, beta, lam, window, S0=None, *, mode="falcon3", phi="
                                  _flags(rbw, same_pair), _stream(stream))
     if st != FW_OK:
         raise FwError(st, "fw_window_prefill")
+    _used(stream, q, k, v, beta, lam, S0, k_init, o, S_T, *(win_in or ()), *win_out, *(norm or ()))
     return _with_norm(o, norm, norm_eps, stream), S_T, win_out
 
 
@@ -240,6 +258,7 @@ def window_step(q, k_prev, v, beta, lam, S, window, win_in=None, win_out=None, *
                               float(eps), _flags(rbw, False), _stream(stream))
     if st != FW_OK:
         raise FwError(st, "fw_window_step")
+    _used(stream, q, k_prev, v, beta, lam, S, o, *(win_in or ()), *win_out, *(norm or ()))
     return _with_norm(o, norm, norm_eps, stream), win_out
 
 
@@ -307,7 +326,7 @@ class _On:
             raise ValueError("fw: the workspace must be contiguous and on %s" % self.like.device)
         return given, given.data_ptr(), given.numel() * given.element_size()
 
-    def call(self, fn, where, *args):
+    def call(self, fn, where, tensors, *args):
         """fn(*args, stream) on the tensors' device."""
         if torch._C._cuda_getDevice() == self.index:
             st = fn(*args, self.handle)
@@ -316,6 +335,8 @@ class _On:
                 st = fn(*args, self.handle)
         if st != FW_OK:
             raise FwError(st, where)
+        if self.stream is not None:
+            _used(self.stream, *tensors)
 
 
 def _norm(norm, eps, width, like):
@@ -385,9 +406,10 @@ def decay_prefill(q, k, v, log_decay, S0=None, *, scale=1.0, lens=None, norm=Non
         S_T = on.new(state, f32)
     code = DTYPES.get(dt, -1)
     _keep, ws, nws = on.workspace(workspace, _decay_need(B, H, T, d, code, 0), "fw_decay_prefill")
-    on.call(lib().fw_decay_prefill, "fw_decay_prefill", *args, _arg(o, shape, dt, "o", q),
-            _arg(S_T, state, f32, "S_T", q), ctypes.byref(fw_shape(B, H, T, d, d)), code, scale,
-            flags, ws, nws)
+    on.call(lib().fw_decay_prefill, "fw_decay_prefill",
+            (q, k, v, log_decay, S0, lens, o, S_T, workspace, *(norm or ())), *args,
+            _arg(o, shape, dt, "o", q), _arg(S_T, state, f32, "S_T", q),
+            ctypes.byref(fw_shape(B, H, T, d, d)), code, scale, flags, ws, nws)
     return o, S_T
 
 
@@ -412,8 +434,9 @@ def decay_backward(q, k, v, log_decay, do, S0=None, dS_T=None, *, scale=1.0, len
         dS0 = on.new(state, f32)
     code = DTYPES.get(dt, -1)
     _keep, ws, nws = on.workspace(workspace, _decay_need(B, H, T, d, code, 1), "fw_decay_backward")
-    on.call(lib().fw_decay_backward, "fw_decay_backward", *args, _arg(dq, shape, dt, "dq", q),
-            _arg(dk, shape, dt, "dk", q), _arg(dv, shape, dt, "dv", q),
+    on.call(lib().fw_decay_backward, "fw_decay_backward",
+            (q, k, v, log_decay, do, S0, dS_T, lens, dq, dk, dv, dS0, workspace), *args,
+            _arg(dq, shape, dt, "dq", q), _arg(dk, shape, dt, "dk", q), _arg(dv, shape, dt, "dv", q),
             _arg(dS0, state, f32, "dS0", q), ctypes.byref(fw_shape(B, H, T, d, d)), code, scale,
             flags, ws, nws)
     return dq, dk, dv, dS0
@@ -430,8 +453,9 @@ def decay_step(q, k, v, log_decay, S, *, scale=1.0, norm=None, norm_eps=1e-5, o=
     on = _On(q, stream)
     if o is None:
         o = on.new(shape, dt)
-    on.call(lib().fw_decay_step, "fw_decay_step", *args, _arg(o, shape, dt, "o", q),
-            ctypes.byref(fw_shape(B, H, 1, d, d)), DTYPES.get(dt, -1), scale)
+    on.call(lib().fw_decay_step, "fw_decay_step", (q, k, v, log_decay, S, o, *(norm or ())), *args,
+            _arg(o, shape, dt, "o", q), ctypes.byref(fw_shape(B, H, 1, d, d)), DTYPES.get(dt, -1),
+            scale)
     return o
 
 
@@ -456,9 +480,9 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, y=None, mean=None, rstd=N
             mean = on.new(lead, f32)
         if rstd is None:
             rstd = on.new(lead, f32)
-    on.call(lib().fw_layer_norm, "fw_layer_norm", *args, _arg(y, shape, dt, "y", x),
-            _arg(mean, lead, f32, "mean", x), _arg(rstd, lead, f32, "rstd", x), lead.numel(), width,
-            DTYPES.get(dt, -1), eps)
+    on.call(lib().fw_layer_norm, "fw_layer_norm", (x, weight, bias, y, mean, rstd), *args,
+            _arg(y, shape, dt, "y", x), _arg(mean, lead, f32, "mean", x), _arg(rstd, lead, f32, "rstd", x),
+            lead.numel(), width, DTYPES.get(dt, -1), eps)
     return y, mean, rstd
 
 
@@ -483,7 +507,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbi
     if dbias is None:
         dbias = on.new((width,), f32)
     _keep, ws, nws = on.workspace(workspace, _layer_norm_need(rows, width), "fw_layer_norm_backward")
-    on.call(lib().fw_layer_norm_backward, "fw_layer_norm_backward", *args,
+    on.call(lib().fw_layer_norm_backward, "fw_layer_norm_backward",
+            (dy, x, weight, mean, rstd, dx, dweight, dbias, workspace), *args,
             _arg(dx, shape, dt, "dx", x), _arg(dweight, (width,), f32, "dweight", x),
             _arg(dbias, (width,), f32, "dbias", x), rows, width, DTYPES.get(dt, -1), ws, nws)
     return dx, dweight, dbias
