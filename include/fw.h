@@ -324,9 +324,10 @@ int fw_window_step(const void *q, const void *k_prev, const void *v, const float
  *               initialised and mean nothing after the call.  Calls that may
  *               overlap (two streams, two captured graphs replayed at once)
  *               need a workspace each.
- *   A NaN or infinity in a row of v (in the backward pass of q, k or d_o) can
- *   reach, besides the rows that depend on it, other rows of the 128 tokens of
- *   its chain that are worked on together.
+ *   A NaN or infinity in a row reaches what depends on it and nothing else; where
+ *   the formulas give an infinity it may arrive as NaN.  A chain of bf16 rows with
+ *   one in v (in the backward pass: in q, k or d_o) is formed token by
+ *   token, about 2 us each, after the usual way.
  *   No output may overlap an input, another output or the workspace, except
  *   S_T = S0.
  */

@@ -14,8 +14,8 @@
 // scores before it waits for the states, which it reads straight into the MMAs' operands.  Chains
 // of one chunk need no workspace and no order between the parts: one launch does both (scan_one).
 //
-// Measured (one GB300): B4 H8 T1000 d = 64 ragged 34 us, B4 H8 T2048 d = 128 167 us, the three scans of
-// a backward pass of B2 H8 T1023 d = 64 44 us.  The short ones are bound by three launches that follow
+// Measured (one GB300): B4 H8 T1000 d = 64 ragged 34 us, B4 H8 T2048 d = 128 171 us (2 % of it the look
+// for rows that are not finite), the three scans of a backward pass of B2 H8 T1023 d = 64 45 us.  The short ones are bound by three launches that follow
 // each other, the long ones by the split products: scan_out (d = 128) issues in 36 % of its
 // cycles, its tensor pipe is busy for 39 %, and its sixteen warps an SM wait for the states' loads and
 // for each other's MMAs.
@@ -253,12 +253,14 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
     constexpr int LR = ld_row<D>(), LC = ld_col<D>(), WN = D / 32, LP = C + 4;
     float *sA = reinterpret_cast<float *>(smem4), *sB = sA + C * LR, *sC = sB + C * LR,
           *pw = sC + C * LC, *red = pw + C + 4;
+    int *const first = reinterpret_cast<int *>(red + C * WN);
     const float lg = s.log_decay[k.chain % s.H];
     for (int i = threadIdx.x; i <= C; i += threads<D>()) pw[i] = decay_pow(lg, (float)i);
     const int64_t base = (k.chain * s.T + k.chunk * C) * D;
     load_tile<D, LR>(sA, static_cast<const float *>(s.a) + base, k.nv, nullptr);
     load_tile<D, LR>(sB, static_cast<const float *>(s.b) + base, k.nv, nullptr);
-    load_tile<D, LC>(sC, static_cast<const float *>(s.c) + base, k.nv, nullptr);
+    const float *const c = static_cast<const float *>(s.c) + base;
+    load_tile<D, LC>(sC, c, k.nv, nullptr);
     __syncthreads();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -311,6 +313,48 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[m][n][e] *= s.out_scale;
+    // P C reads a value of C that the mask keeps from a row as 0 times it, which is NaN of an infinity or
+    // a NaN.  Where a block's rows are not all finite, such values become zero, each column's first in
+    // processing order is noted, and the rows are formed once more; those that see one are NaN.
+    // (Later chunks have it from the state.)
+    float nan = 0.f;                       // 0 while all are finite
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) nan = fmaf(acc[m][n][e], 0.f, nan);
+    if (__syncthreads_or(nan != 0.f)) {
+        for (int i = threadIdx.x; i < D; i += threads<D>()) first[i] = C;
+        __syncthreads();
+        for (int i = threadIdx.x; i < k.nv * D; i += threads<D>())
+            if (!isfinite(c[i])) {
+                atomicMin(first + i % D, s.rev ? C - 1 - i / D : i / D);
+                sC[i / D * LC + i % D] = 0.f;
+            }
+        __syncthreads();
+        const auto each = [&](auto f) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f(acc[m][n][e], m0 + 16 * m + g + 8 * (e >> 1), n0 + 8 * n + 2 * t + (e & 1));
+        };
+        each([&](float &v, int, int) { v = 0.f; });
+        if (!zero)
+#pragma unroll 1
+            for (int i = 0; i < D; ++i)
+                each([&](float &v, int r, int col) { v = fmaf(sA[r * LR + i], trans ? X[col * D + i] : X[i * D + col], v); });
+        each([&](float &v, int r, int) { v *= pw[s.rev ? max(k.nv - 1 - r, 0) : r + 1]; });
+#pragma unroll 1
+        for (int j = 0; j < C; ++j)
+            each([&](float &v, int r, int col) { v = fmaf(sB[r * LP + j], sC[j * LC + col], v); });
+        each([&](float &v, int r, int col) {
+            v = first[col] <= (s.rev ? C - 1 - r : r) ? __int_as_float(0x7fffffff) : v * s.out_scale;
+        });
+    }
     if (s.norm.on) {                       // a row is held by four lanes of each of WN warps
         auto row_sums = [&](float (&z)[2][2]) {
 #pragma unroll
@@ -414,7 +458,7 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     const int64_t nch = (s.T + C - 1) / C;
     const dim3 grid((unsigned)(s.n_chains * nch), n);
     constexpr int smem_l = (2 * C * ld_col<D>() + C) * 4;
-    constexpr int smem_o = (2 * C * ld_row<D>() + C * ld_col<D>() + C + 4 + C * (D / 32)) * 4;
+    constexpr int smem_o = (2 * C * ld_row<D>() + C * ld_col<D>() + C + 4 + C * (D / 32) + D) * 4;
     cudaError_t e;
     bool one = nch == 1;
     for (int i = 0; i < n; ++i) one = one && !(all.s[i].X_out && all.s[i].X_out == all.s[i].X0);

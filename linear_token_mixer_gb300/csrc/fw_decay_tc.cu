@@ -137,6 +137,10 @@ __device__ __forceinline__ int64_t seg_tokens(int64_t n, const Seg &s) {
     return tail ? full - ((int64_t)s.total * C - n) : full;
 }
 
+__device__ __forceinline__ void bar_arrive(int id, int count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // Four 8x8 b16 matrices, transposed: thread t gets rows 2 (t % 4), +1 of column t / 4.
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -237,6 +241,126 @@ template <int N> struct Jobs {
     } s[N];
 };
 
+// The state on entry to segment `seg` of `nseg`, element (r, c) of a chain's: X0 (or its copy, which is never
+// transposed), or the states of the segments before it added up.  `ws`: the chain's workspace.
+template <int D, bool REV>
+__device__ __forceinline__ float entry_state(const ScanArgs &a, const ScanArgs &own, const float *ws, int64_t chain,
+                                             int64_t n, int seg, int nseg, int r, int c) {
+    if (seg == 0) {
+        if (!a.X0) return 0.f;
+        if (nseg > 1 && own.X_out == a.X0) return ws[(int64_t)(nseg - 1) * D * D + r * D + c];
+        const float *X0 = a.X0 + chain * D * D;
+        return own.x0_trans ? X0[c * D + r] : X0[r * D + c];
+    }
+    float x = 0.f;
+#pragma unroll 1
+    for (int s = 0; s < seg; ++s) {
+        const Seg q = seg_of(n, s, nseg);
+        if (q.first >= q.last && s > 0) continue;
+        x = fmaf(decay_pow(a.log_decay[chain % a.H], (float)seg_tokens<REV>(n, q)), x,
+                 ws[(int64_t)s * D * D + r * D + c]);
+    }
+    return x;
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
+    return (bf16x2 & 0x7f80u) == 0x7f80u || (bf16x2 & 0x7f800000u) == 0x7f800000u;
+}
+
+// The rows of a segment's chunks in which C holds an infinity or a NaN once more, token by token: P C
+// reads such a value as 0 times it, which is NaN, also for the rows that the mask keeps from it.  By the 128
+// threads of the O group, with the state in shared memory; a thread holds a column or half of one; about 2 us
+// a token.  Run only where X is not finite in the end, so that the scan itself pays one look at X a
+// CTA, and no time that shows (B8 H16 T4096 d = 128, B16 H16 T4096 d = 64).  Finding such values chunk
+// by chunk and clearing them in the tiles before P C took 7 to 12 us of the former.
+template <int D, bool REV, bool NORM>
+__device__ __forceinline__ void redo_rows(const ScanArgs &a, const ScanArgs &own, const float *ws, float *sm,
+                                          int64_t chain, int64_t n, const Seg &sg, int seg, int nseg) {
+    constexpr int N = 128, PARTS = N / D, ROWS = D / PARTS;
+    const int tid = threadIdx.x & (N - 1), col = tid % D, part = tid / D;
+    const __nv_bfloat16 *const A = static_cast<const __nv_bfloat16 *>(own.a),
+                        *const B = static_cast<const __nv_bfloat16 *>(own.b),
+                        *const Cm = static_cast<const __nv_bfloat16 *>(own.c);
+    if ((tid & 31) == 0) bulk_wait0();                           // this warp's rows are written
+    auto first_token = [&](int i) -> int64_t { return (int64_t)(REV ? sg.total - 1 - i : i) * C; };
+    auto holds = [&](int i) -> bool {                            // by this thread's share of chunk i of C
+        const int64_t t0 = first_token(i);
+        const int pieces = (n - t0 < C ? (int)(n - t0) : C) * (D / 8);
+        const uint4 *const p = reinterpret_cast<const uint4 *>(Cm + (chain * a.T + t0) * D);
+        bool found = false;
+#pragma unroll 1
+        for (int z = tid; z < pieces; z += N) {
+            const uint4 q = p[z];
+            found = found || not_finite(q.x) || not_finite(q.y) || not_finite(q.z) || not_finite(q.w);
+        }
+        return found;
+    };
+    float *const X = sm + part * ROWS * D + col;                // element (r, col) of this part at X[r * D]
+#pragma unroll 1
+    for (int r = 0; r < ROWS; ++r)
+        X[r * D] = entry_state<D, REV>(a, own, ws, chain, n, seg, nseg, part * ROWS + r, col);
+    bar_arrive(5, 384);                                          // the X group may write X_out
+    float *const va = sm + D * D, *const vb = va + D, *const sum = vb + D, *const red = sum + N;
+    int *const shared_last = reinterpret_cast<int *>(red);
+    if (tid == 0) *shared_last = -1;
+    bar_sync(3, N);
+    int last = -1;
+#pragma unroll 1
+    for (int i = sg.first; i < sg.last; ++i)
+        if (holds(i)) last = i;
+    if (last >= 0) atomicMax(shared_last, last);
+    bar_sync(3, N);
+    last = min(*shared_last, sg.last - 1);                       // (of a call given up, tiles may still land there)
+    const float g = decay_pow(a.log_decay[chain % a.H], 1.f);
+    for (int i = sg.first; i <= last; ++i) {
+        const int64_t t0 = first_token(i);
+        const int nv = n - t0 < C ? (int)(n - t0) : C;
+        const bool write = bar_or(3, N, holds(i));
+        for (int j = 0; j < nv; ++j) {
+            const int64_t row = (chain * a.T + t0 + (REV ? nv - 1 - j : j)) * D;
+            bar_sync(3, N);                                    // the token before is done with
+            if (part == 0) {
+                va[col] = to_f32(A[row + col]);
+                vb[col] = to_f32(B[row + col]);
+            }
+            const float c = a.in_scale * to_f32(Cm[row + col]);
+            bar_sync(3, N);
+            float o = 0.f;
+#pragma unroll 2
+            for (int r = 0; r < ROWS; ++r) {
+                const float b = vb[part * ROWS + r], x = REV ? fmaf(b, c, X[r * D]) : fmaf(g, X[r * D], b * c);
+                o = fmaf(va[part * ROWS + r], x, o);
+                X[r * D] = REV ? g * x : x;
+            }
+            if (!write) continue;
+            sum[tid] = o;
+            bar_sync(3, N);
+            o = 0.f;
+            for (int s = 0; s < PARTS; ++s) o += sum[s * D + col];
+            o *= a.out_scale;
+            if (NORM) {
+                // every part holds the row, and its N / D copies add up to as many times the sums
+                float m[2] = {0.f, 0.f};
+#pragma unroll 1
+                for (int z = 0; z < 2; ++z) {
+                    float y = z == 0 ? o : (o - m[0]) * (o - m[0]);
+#pragma unroll 1
+                    for (int s = 16; s; s >>= 1) y += __shfl_xor_sync(~0u, y, s);
+                    if ((tid & 31) == 0) red[z * 4 + (tid >> 5)] = y;
+                    bar_sync(3, N);
+                    m[z] = 0.f;
+                    for (int w = 0; w < 4; ++w) m[z] += red[z * 4 + w];
+                    m[z] *= 1.f / N;
+                }
+                o = (o - m[0]) * rsqrtf(m[1] + a.norm.eps);
+                if (a.norm.weight) o *= a.norm.weight[col];
+                if (a.norm.bias) o += a.norm.bias[col];
+            }
+            if (part == 0) static_cast<__nv_bfloat16 *>(own.out)[row + col] = __float2bfloat16_rn(o);
+        }
+    }
+}
+
 // PRE: only the state of a segment, from zero (segment 0: from X0), into the workspace.
 template <int D, bool REV, bool PRE, bool NORM>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -244,7 +368,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
     using L = Lay<D, PRE>;
     const auto &job = jobs.s[REV ? blockIdx.x & 1 : 0];
     const int block = REV ? blockIdx.x >> 1 : blockIdx.x;
-    const ScanArgs &a = jobs.s[0].args, &own = job.args;   // own: out, X_out, x0_trans and ws
+    const ScanArgs &a = jobs.s[0].args, &own = job.args;   // own: a, b, c, out, X_out, x0_trans and ws
     const CUtensorMap &tma = job.a, &tmb = job.b, &tmc = job.c, &tmo = job.out;
     let_next_grid_start();
     if (order & kWaitFirst) wait_previous_grid();
@@ -291,6 +415,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
     float *const pw = reinterpret_cast<float *>(sm + L::T_PW);   // g^n, n = 0..128
     float *const kw = reinterpret_cast<float *>(sm + L::T_KW);   // w_j of a full chunk
     float *const kt = reinterpret_cast<float *>(sm + L::T_KT);   // w_j of the tail chunk
+    volatile int *const look = reinterpret_cast<volatile int *>(sm + L::MISC + 12);   // X is not finite
     auto bar = [&](int i) -> uint32_t { return sb + L::BAR + 8u * (uint32_t)i; };
     auto full = [&](int st, int x) -> uint32_t { return bar(L::FULL + st * L::NT + x); };
     auto empty = [&](int st, int x) -> uint32_t { return bar(L::EMPTY + st * L::NT + x); };
@@ -331,6 +456,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         }
         fence_mbar_init();
         *s_abort = 0;
+        *look = 0;
     }
     // Warp 0 needs none of what follows: it only announces the barriers, and its first tiles are on
     // their way while the others make the tables and tensor memory ready.
@@ -694,6 +820,8 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                 const int64_t pieces = (a.T - n) * (D / 8);
                 for (int64_t z = tid - 8 * 32; z < pieces; z += 128) rest[z] = make_uint4(0u, 0u, 0u, 0u);
             }
+            bar_sync(4, 384);                        // with the X group
+            if (*look) redo_rows<D, REV, NORM>(a, own, ws, reinterpret_cast<float *>(sm), chain, n, sg, seg, nseg);
         }
     } else if (warp < 16 || warp >= 24) {
         // ---------------------------------------------------------------- (diag(w) B)^T
@@ -888,6 +1016,17 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                 mbar_arrive(bar(L::UFREE + ub));
                 if (more) mbar_arrive(bar(L::XBRDY));
             }
+        }
+        if (!PRE) {
+            // A value of C that is not finite has left its column of X without a finite number, in every
+            // row, and nothing makes one finite again: 0 times it is NaN.
+            uint64_t nan2 = 0;
+#pragma unroll
+            for (int e = 0; e < XC_; e += 2) nan2 = fma2(pair(x[e], x[e + 1]), 0, nan2);
+            const bool bad = bar_or(2, 256, (nan2 & 0x7fffffff7fffffffull) != 0);
+            if (bad) *look = 1;
+            bar_arrive(4, 384);
+            if (bad) bar_sync(5, 384);               // (X_out may be X0, which redone rows begin with)
         }
         float *dst = PRE ? ws + (int64_t)seg * D * D
                          : final_seg && own.X_out ? own.X_out + chain * D * D : nullptr;

@@ -1,0 +1,107 @@
+"""Decayed scans of rows that hold infinities and NaN: the causal mask keeps them from every row that does not
+depend on them.
+
+Tolerances of the rows that they do not reach, element by element relative to the recurrence over
+absolute values: fp32 1e-5 (6.2e-6: a product of split operands leaves out 2^-22 three times over, in two
+products, and the sums take 40 additions of at most 2^-23), bf16 8e-3 (7.83e-3: an operand and the row
+rounded, 2^-8 each); rows behind an output norm relative L2, 8e-3 and 1e-5, as without such values.
+"""
+import pytest
+import torch
+
+from linear_token_mixer_gb300 import fw
+
+import decay_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+TOL = {F32: 1e-5, BF16: 8e-3}
+
+
+def inputs(B, H, T, d, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = {n: torch.randn(B, H, T, d, generator=g).to(dtype) for n in ("q", "k", "v", "do")}
+    x.update(S0=torch.randn(B, H, d, d, generator=g), dS=torch.randn(B, H, d, d, generator=g))
+    return x, {n: t.cuda() for n, t in x.items()}
+
+
+def check_rows(got, ref, size, where, dtype):
+    got = got.cpu().double()[where]
+    assert torch.isfinite(got).all()
+    assert ((got - ref[where]).abs() <= TOL[dtype] * size[where]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ld", [-0.05, -0.5])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,t", [(300, 200), (300, 0), (128, 127), (40, 17), (1300, 700)])
+def test_non_finite_values_reach_no_row_before_them(T, t, value, ld, d, dtype):
+    """A value that is not finite reaches its own column of its own row and of later ones, and of the
+    state, and nothing else, also within the tokens that are worked on together (T = 1300: chains
+    split over the GPU)."""
+    B, H, c = 1, 2, 5
+    x, g = inputs(B, H, T, d, dtype, seed=11)
+    y = {n: z.abs() for n, z in x.items()}
+    l = torch.tensor([ld, ld])
+    at = torch.arange(T)
+    v = g["v"].clone()
+    v[0, 1, t, c] = value
+    o, S = fw.decay_prefill(g["q"], g["k"], v, l.cuda(), g["S0"])
+    in_place = g["S0"].clone()
+    o2, _ = fw.decay_prefill(g["q"], g["k"], v, l.cuda(), in_place, S_T=in_place)
+    _, wS = fw.decay_prefill(g["q"], g["k"], g["v"], l.cuda(), g["S0"])
+    fw.check()
+    hit = torch.zeros(B, H, T, d, dtype=torch.bool)
+    hit[0, 1, t:, c] = True
+    ref, size = (R.forward(z["q"], z["k"], z["v"], l, z["S0"])[0] for z in (x, y))
+    for a in (o, o2):
+        check_rows(a, ref, size, ~hit, dtype)
+        assert not torch.isfinite(a.cpu()[hit]).any()
+    for a in (S, in_place):
+        assert not torch.isfinite(a[0, 1, :, c]).any()
+        a[0, 1, :, c] = wS[0, 1, :, c]
+        assert torch.equal(a, wS)
+    # dv_t and dk_t know the tokens from t on, dq_t those up to t: the same for a row of q, do or k
+    ref, size = (R.backward(z["q"], z["k"], z["v"], l, z["do"], z["S0"], z["dS"]) for z in (x, y))
+    for name in ("k", "q", "do"):
+        bad = {n: (z.clone() if n == name else z) for n, z in g.items()}
+        bad[name][0, 1, t, c] = value
+        got = fw.decay_backward(bad["q"], bad["k"], bad["v"], l.cuda(), bad["do"], bad["S0"], bad["dS"])
+        fw.check()
+        clean = {"k": (at < t, at >= 0, at != t), "q": (at >= 0, at > t, at > t),
+                 "do": (at != t, at > t, at > t)}[name]
+        for a, r, s, rows in zip(got[:3], ref[:3], size[:3], clean):
+            where = torch.ones(B, H, T, d, dtype=torch.bool)
+            where[0, 1] = rows.view(T, 1)
+            check_rows(a, r, s, where, dtype)
+        if name == "do":
+            assert not torch.isfinite(got[0][0, 1, t]).any()
+            assert not torch.isfinite(got[2][0, 1, :t + 1, c]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,t", [(128, 0), (128, 127), (256, 128), (70, 69), (1500, 700)])
+def test_whole_rows_that_are_not_finite(T, t, d, dtype):
+    """A row of v that is all NaN, with and without an output norm, at the borders of a chunk and in a chain
+    that is split over the GPU; a padded batch whose other rows are as they would be."""
+    x, g = inputs(2, 3, T, d, dtype, seed=T + t)
+    l = torch.tensor([-0.01, -0.3, 0.0])
+    ln = torch.tensor([T, max(T - 30, 1)], dtype=torch.int32)
+    gen = torch.Generator().manual_seed(5)
+    w, b = torch.randn(d, generator=gen), torch.randn(d, generator=gen)
+    v = g["v"].clone()
+    v[0, :, t] = float("nan")
+    v[0, 1, T - 1, 3] = float("inf")
+    ro = R.forward(x["q"], x["k"], x["v"], l, x["S0"], 1.0, ln)[0]
+    for norm in (None, (w.cuda(), b.cuda())):
+        o, S = fw.decay_prefill(g["q"], g["k"], v, l.cuda(), g["S0"], norm=norm, lens=ln.cuda())
+        fw.check()
+        r = ro if norm is None else R.layer_norm(ro, w, b)[0]
+        if t > 0:
+            assert R.rel_rows(o[:1, :, :t], r[:1, :, :t], 2) <= TOL[dtype]
+        assert R.rel_rows(o[1:, :, :ln[1]], r[1:, :, :ln[1]], 2) <= TOL[dtype]
+        assert (o[1, :, ln[1]:] == 0).all() and torch.isfinite(S[1]).all()
+        assert not torch.isfinite(o[0, :, t:]).any() and not torch.isfinite(S[0]).any()
