@@ -500,8 +500,7 @@ ScanArgs scan_of(const fw_shape *shape, fw_dtype dtype, const float *log_decay,
 extern "C" int64_t fw_decay_workspace(const fw_shape *shape, fw_dtype dtype, int backward) {
     const int st = check_decay(shape, dtype);
     if (st != FW_OK) return st;
-    const size_t one = scan_workspace(shape->B * shape->H, shape->T, shape->d_k, dtype, backward != 0);
-    return (int64_t)(backward ? 3 * one : one);
+    return (int64_t)scan_workspace(shape->B * shape->H, shape->T, shape->d_k, dtype, backward != 0);
 }
 
 extern "C" int fw_decay_prefill(const void *q, const void *k, const void *v,
@@ -573,7 +572,6 @@ extern "C" int fw_decay_backward(const void *q, const void *k, const void *v,
     ScanArgs s[3];
     for (int i = 0; i < 3; ++i) {
         s[i] = scan_of(shape, dtype, log_decay, lens, err);
-        s[i].ws = static_cast<float *>(workspace) + i * (need / 3 / (int64_t)sizeof(float));
         s[i].rev = i > 0;
         s[i].x0_trans = i != 1;
         s[i].zero_rest = lens && (flags & FW_FLAG_ZERO_REST);
@@ -582,6 +580,7 @@ extern "C" int fw_decay_backward(const void *q, const void *k, const void *v,
     s[1].a = k; s[1].b = q; s[1].c = d_o; s[1].X0 = dS_T; s[1].out = dv; s[1].in_scale = scale;
     s[1].X_out = dS0;
     s[2].a = v; s[2].b = d_o; s[2].c = q; s[2].X0 = dS_T; s[2].out = dk; s[2].in_scale = scale;
+    s[0].ws = static_cast<float *>(workspace);
     const cudaError_t e = launch_scans(s, 3, stream);
     return e == cudaSuccess ? FW_OK : cuda_fail(e);
 }

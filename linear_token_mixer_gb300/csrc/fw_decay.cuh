@@ -117,9 +117,9 @@ struct LayerNormBwdArgs {
 };
 
 // One forward scan, or the three of a backward pass (dq, dv, dk) over chains of the same shape.
-// Bytes of workspace of each scan of a call.
+// Bytes of workspace of a call, and the launch: s[0].ws is the call's workspace, shared out there.
 size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype, bool backward);
-cudaError_t launch_scans(const ScanArgs *s, int n, cudaStream_t stream);
+cudaError_t launch_scans(ScanArgs *s, int n, cudaStream_t stream);
 cudaError_t launch_decay_step(const DecayStepArgs &a, cudaStream_t s);
 cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const LayerNormBwdArgs &a, cudaStream_t s);

@@ -12,7 +12,7 @@
 // B*H*T/64 blocks, which is what short batches need to fill the GPU.  The three launches overlap
 // their starts (programmatic dependent launch): scan_out loads its rows and forms the masked
 // scores before it waits for the states, which it reads straight into the MMAs' operands.  Chains
-// of one chunk need no workspace and no order between the parts: one launch does both (scan_one).
+// of one chunk need no workspace: one launch does both parts (scan_one).
 //
 // Measured (one GB300): B4 H8 T1000 d = 64 ragged 34 us, B4 H8 T2048 d = 128 171 us (2 % of it the look
 // for rows that are not finite), the three scans of a backward pass of B2 H8 T1023 d = 64 45 us.  The short ones are bound by three launches that follow
@@ -437,19 +437,22 @@ scan_out(const __grid_constant__ Scans all, int64_t nch) {
     out_part<D, false>(s, k, ws + (int64_t)blockIdx.x * D * D, trans, smem4);
 }
 
-// Chains of one chunk (X_out apart from X0): final states (z = 0) and rows (z = 1) at once.
+// Chains of one chunk: rows (z = 1) and final states (z = 0) at once, or one after the other (one z)
+// where X_out is X0, which the rows read.
 template <int D>
 __global__ void __launch_bounds__(threads<D>())
 scan_one(const __grid_constant__ Scans all) {
     extern __shared__ float4 smem4[];
     const ScanArgs &s = all.s[blockIdx.y];
     const ChunkOf k = chunk_of(s, 1);
-    if (blockIdx.z == 0) {
-        if (s.X_out) local_part<D, true>(s, k, smem4);
-    } else {
+    const bool both = gridDim.z == 1;
+    if (both || blockIdx.z == 1) {
         if (s.zero_rest) zero_rest<D>(s, k.chain, 0, k.nv);
         if (k.nv > 0) out_part<D, true>(s, k, s.X0 ? s.X0 + k.chain * D * D : nullptr, s.x0_trans, smem4);
     }
+    if (both) __syncthreads();
+    if (both || blockIdx.z == 0)
+        if (s.X_out) local_part<D, true>(s, k, smem4);
 }
 
 template <int D>
@@ -460,13 +463,12 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     constexpr int smem_l = (2 * C * ld_col<D>() + C) * 4;
     constexpr int smem_o = (2 * C * ld_row<D>() + C * ld_col<D>() + C + 4 + C * (D / 32) + D) * 4;
     cudaError_t e;
-    bool one = nch == 1;
-    for (int i = 0; i < n; ++i) one = one && !(all.s[i].X_out && all.s[i].X_out == all.s[i].X0);
-    if (one) {
+    if (nch == 1) {
         constexpr int smem = smem_l > smem_o ? smem_l : smem_o;
         static std::atomic<uint64_t> done{0};
         if ((e = allow_smem(scan_one<D>, smem, done)) != cudaSuccess) return e;
-        scan_one<D><<<dim3((unsigned)s.n_chains, n, 2), threads<D>(), smem, stream>>>(all);
+        const bool in_place = s.X_out && s.X_out == s.X0;
+        scan_one<D><<<dim3((unsigned)s.n_chains, n, in_place ? 1 : 2), threads<D>(), smem, stream>>>(all);
         return cudaGetLastError();
     }
     static std::atomic<uint64_t> local_done{0}, out_done{0};
@@ -483,14 +485,20 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
 
 }  // namespace
 
-size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype, bool backward) {
-    if (dtype == FW_BF16) return scan_tc_workspace(n_chains, T, d, backward);
+// Bytes of the states of every chunk of a scan.
+static size_t state_bytes(int64_t n_chains, int64_t T, int d) {
     return (size_t)n_chains * (size_t)((T + C - 1) / C) * d * d * sizeof(float);
 }
 
+size_t scan_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype, bool backward) {
+    if (dtype == FW_BF16) return scan_tc_workspace(n_chains, T, d, backward);
+    return T <= C ? 0 : (backward ? kSharing : 1) * state_bytes(n_chains, T, d);
+}
+
 // bf16 rows run on the fifth-generation tensor cores, fp32 rows here.
-cudaError_t launch_scans(const ScanArgs *s, int n, cudaStream_t stream) {
+cudaError_t launch_scans(ScanArgs *s, int n, cudaStream_t stream) {
     if (s[0].dtype == FW_BF16) return launch_scans_tc(s, n, stream);
+    if (n > 1 && s[0].ws) s[1].ws = s[0].ws + state_bytes(s->n_chains, s->T, s->d) / sizeof(float);   // (the third: none)
     Scans all{};
     for (int i = 0; i < n; ++i) all.s[i] = s[i];
     return s[0].d == 64 ? launch<64>(all, n, stream) : launch<128>(all, n, stream);

@@ -1139,10 +1139,18 @@ void segments_backward(int64_t n_chains, int64_t T, int *fwd, int *rev) {
     if (waves * estimate(chunks, 1) <= estimate(chunks, *fwd) + estimate(chunks, *rev)) *fwd = *rev = 1;
 }
 
-template <int D> cudaError_t launch_scans_of(const ScanArgs *s, int n, cudaStream_t stream) {
-    if (n == 1) return launch<D, false>(s, segments(s->n_chains, s->T), false, stream);
+// Bytes of a scan's workspace: the states of its segments but the last, and X0's copy.
+size_t segment_bytes(int64_t n_chains, int d, int nseg) {
+    return nseg > 1 ? (size_t)n_chains * nseg * d * d * sizeof(float) : 0;
+}
+
+template <int D> cudaError_t launch_scans_of(ScanArgs *s, int n, cudaStream_t stream) {
+    const int64_t nc = s->n_chains;
+    if (n == 1) return launch<D, false>(s, segments(nc, s->T), false, stream);
     int fwd, rev;
-    segments_backward(s->n_chains, s->T, &fwd, &rev);
+    segments_backward(nc, s->T, &fwd, &rev);
+    s[1].ws = s[0].ws + segment_bytes(nc, D, fwd) / sizeof(float);
+    s[2].ws = s[1].ws + segment_bytes(nc, D, rev) / sizeof(float);
     const cudaError_t e = launch<D, false>(s, fwd, false, stream);
     return e != cudaSuccess ? e : launch<D, true>(s + 1, rev, true, stream);
 }
@@ -1150,12 +1158,13 @@ template <int D> cudaError_t launch_scans_of(const ScanArgs *s, int n, cudaStrea
 }  // namespace
 
 size_t scan_tc_workspace(int64_t n_chains, int64_t T, int d, bool backward) {
-    int nseg = segments(n_chains, T), rev;
-    if (backward) segments_backward(n_chains, T, &nseg, &rev);   // rev, of twice the chains, is no more
-    return nseg > 1 ? (size_t)n_chains * nseg * d * d * sizeof(float) : 0;
+    if (!backward) return segment_bytes(n_chains, d, segments(n_chains, T));
+    int fwd, rev;
+    segments_backward(n_chains, T, &fwd, &rev);
+    return segment_bytes(n_chains, d, fwd) + 2 * segment_bytes(n_chains, d, rev);
 }
 
-cudaError_t launch_scans_tc(const ScanArgs *s, int n, cudaStream_t stream) {
+cudaError_t launch_scans_tc(ScanArgs *s, int n, cudaStream_t stream) {
     return s->d == 64 ? launch_scans_of<64>(s, n, stream) : launch_scans_of<128>(s, n, stream);
 }
 
