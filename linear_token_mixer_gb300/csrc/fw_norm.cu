@@ -632,7 +632,15 @@ cudaError_t add_partials(const LayerNormBwdArgs &a, int64_t n, cudaStream_t s) {
                         (const float *)a.ws, (int)n, a.width, a.dweight, a.dbias);
 }
 
+// Partial rows at most, and those of rows wider than the registers of a block, whose columns are many
+// blocks already.
 int64_t partials(int64_t rows) { return rows < kPartials ? rows : kPartials; }
+int64_t partials_long(int64_t rows, int64_t width) {
+    const int64_t n = kPartials / ((width + kBlock - 1) / kBlock);
+    return n < 1 ? 1 : n < rows ? n : rows;
+}
+// A row wider than this takes the looping kernels in every type.
+constexpr int64_t kWidest = 16384;
 
 template <typename T, int VW, int ROWT, int VPT>
 cudaError_t bwd(const LayerNormBwdArgs &a, cudaStream_t s) {
@@ -691,9 +699,7 @@ cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t s) {
     }
     cudaError_t e;
     if (a.ws) {
-        const int64_t bx = (w + kBlock - 1) / kBlock;
-        int64_t by = kPartials / bx;
-        by = by < 1 ? 1 : by > partials(a.rows) ? partials(a.rows) : by;
+        const int64_t bx = (w + kBlock - 1) / kBlock, by = partials_long(a.rows, w);
         ln_bwd_sums_long<T><<<dim3((unsigned)bx, (unsigned)by), kBlock, 0, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if ((e = add_partials(a, by, s)) != cudaSuccess) return e;
@@ -705,7 +711,8 @@ cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t s) {
 }  // namespace
 
 size_t layer_norm_workspace(int64_t rows, int64_t width) {
-    return (size_t)partials(rows) * 2 * (size_t)width * sizeof(float);
+    const int64_t n = width > kWidest ? partials_long(rows, width) : partials(rows);
+    return (size_t)n * 2 * (size_t)width * sizeof(float);
 }
 
 cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t s) {
