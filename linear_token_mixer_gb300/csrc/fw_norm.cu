@@ -215,8 +215,8 @@ template <typename T, int VW, int ROWT, int VPT> constexpr bool fwd_ahead() {
     return VW * sizeof(T) == 16 && VPT > 1 && ROWT <= 32;
 }
 
-// FAST: every thread holds VPT whole vectors, and weight and bias are given (the checks for the
-// other cases are as many instructions as the work).
+// FAST: every thread holds VPT whole vectors of 16 bytes, and weight and bias are given (the checks for
+// the other cases are as many instructions as the work).
 template <typename T, int VW, int ROWT, int VPT, bool FAST>
 __global__ void __launch_bounds__(block_of<ROWT>(), FAST && ROWT <= 512 ? 512 / block_of<ROWT>() : 1)
 ln_fwd(LayerNormArgs a) {
@@ -571,8 +571,9 @@ template <typename T, int VW, int ROWT, int VPT>
 cudaError_t fwd(const LayerNormArgs &a, cudaStream_t s) {
     constexpr int RPB = block_of<ROWT>() / ROWT;
     int64_t n;
-    const bool fast = VW > 1 && a.width == (int64_t)VW * ROWT * VPT && a.weight && a.bias;
-    auto k = fast ? ln_fwd<T, VW, ROWT, VPT, (VW > 1)> : ln_fwd<T, VW, ROWT, VPT, false>;
+    constexpr bool whole = VW * sizeof(T) == 16;   // (widths that smaller vectors fill take these)
+    const bool fast = whole && a.width == (int64_t)VW * ROWT * VPT && a.weight && a.bias;
+    auto k = fast ? ln_fwd<T, VW, ROWT, VPT, whole> : ln_fwd<T, VW, ROWT, VPT, false>;
     constexpr int smem = fwd_ahead<T, VW, ROWT, VPT>() ? Ahead<block_of<ROWT>(), VPT>::BYTES : 0;
     static std::atomic<uint64_t> done[2];
     cudaError_t e;
@@ -650,8 +651,9 @@ cudaError_t bwd(const LayerNormBwdArgs &a, cudaStream_t s) {
     const int sums = RPB > 1 ? RPB * 2 * (int)a.width * (int)sizeof(float) : 0;   // <= 32 KB
     const int smem = ahead > sums ? ahead : sums;
     int64_t n;
-    const bool fast = VW > 1 && a.width == (int64_t)VW * ROWT * VPT && a.weight;
-    auto k = fast ? ln_bwd<T, VW, ROWT, VPT, (VW > 1)> : ln_bwd<T, VW, ROWT, VPT, false>;
+    constexpr bool whole = VW * sizeof(T) == 16;
+    const bool fast = whole && a.width == (int64_t)VW * ROWT * VPT && a.weight;
+    auto k = fast ? ln_bwd<T, VW, ROWT, VPT, whole> : ln_bwd<T, VW, ROWT, VPT, false>;
     static std::atomic<uint64_t> done[2];
     cudaError_t e;
     if (ahead > 48 * 1024 && (e = allow_smem(k, ahead, done[fast])) != cudaSuccess) return e;
@@ -676,8 +678,10 @@ cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t s) {
         if (nv <= 64) return bwd<T, VW, 32, 2>(a, s);
         if (nv <= 128) return bwd<T, VW, 64, 2>(a, s);
         if (nv <= 256) return bwd<T, VW, 128, 2>(a, s);
-        // sixteen columns a thread: as many as leave its sums in registers (16384 x 2048 fp32: eight 73 us,
-        // sixteen 67 us; 32768 x 2048 bf16: sixteen 81 us, 32, for want of registers, 181 us)
+        // sixteen columns a thread: as many as leave its sums in registers in blocks of up to 512 threads
+        // (16384 x 2048 fp32: eight 73 us, sixteen 67 us; 32768 x 2048 bf16: sixteen 81 us, 32, for want of
+        // registers, 181 us).  Blocks of 1024 have 64 registers a thread, and the widest rows' sums
+        // spill there (bf16 588 bytes): the alternative is the looping kernels, which read the rows twice.
         constexpr int V = VW == 4 ? 4 : 2;
         if (nv <= 512) return bwd<T, VW, 512 / V, V>(a, s);
         if (nv <= 1024) return bwd<T, VW, 1024 / V, V>(a, s);
@@ -691,8 +695,9 @@ cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t s) {
             if (nv <= 512) return bwd<T, V, 128, 4>(a, s);
             if (nv <= 1024) return bwd<T, V, 256, 4>(a, s);
             if (nv <= 2048) return bwd<T, V, 512, 4>(a, s);
-            if (nv <= 4096) return bwd<T, V, 1024, 4>(a, s);
-            return bwd<T, V, 1024, 8>(a, s);
+            if constexpr (V == 1)          // (two elements a load: at most 4096)
+                if (nv > 4096) return bwd<T, V, 1024, 8>(a, s);
+            return bwd<T, V, 1024, 4>(a, s);
         };
         if (w % 2 == 0 && w <= 8192) return by(std::integral_constant<int, 2>{});
         if (w <= 8192) return by(std::integral_constant<int, 1>{});
