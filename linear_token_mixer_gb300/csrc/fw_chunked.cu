@@ -47,12 +47,13 @@
 // Every wait is bounded: on expiry the kernel records an error, the other
 // roles stop at their next wait, copies and MMAs in flight are drained,
 // tensor memory is freed and the kernel exits.
-#include <cudaTypedefs.h>
+#include <cuda.h>
 
 #include <mutex>
 
 #include "fw_internal.cuh"
 #include "fw_sm100.cuh"
+#include "fw_tma.cuh"
 
 namespace fw {
 namespace {
@@ -1426,34 +1427,6 @@ cudaMemPool_t segment_pool(int dev) {
     return pools[dev];
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// [n_chains][T][128] bf16 viewed as a 3-D tensor (d, T, chain); 64 x 64 boxes with
-// the 128-byte swizzle for the tile loads.
-bool make_map(CUtensorMap *m, const void *ptr, int64_t T, int64_t nc) {
-    auto enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)nc};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)T * D * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)C, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box,
-               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 // Falcon-1 and Falcon-1A with phi = elu+1 are declined: phi(k) is close to
@@ -1503,8 +1476,8 @@ size_t chunked_segment_bytes(const PrefillArgs &a, int sms) {
 
 cudaError_t launch_chunked(const PrefillArgs &a, cudaStream_t s) {
     CUtensorMap tq, tk, tv;
-    if (!make_map(&tq, a.q, a.T, a.n_chains) || !make_map(&tk, a.k, a.T, a.n_chains) ||
-        !make_map(&tv, a.v, a.T, a.n_chains))
+    if (!make_map(&tq, a.q, a.T, a.n_chains, D, C) || !make_map(&tk, a.k, a.T, a.n_chains, D, C) ||
+        !make_map(&tv, a.v, a.T, a.n_chains, D, C))
         return cudaErrorInvalidValue;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -51,12 +51,11 @@
 // Every wait is bounded: on expiry the kernel records an error, the other roles
 // stop at their next wait, copies and MMAs in flight are drained, tensor memory
 // is freed and the kernel exits.
-#include <cudaTypedefs.h>
-
-#include <mutex>
+#include <cuda.h>
 
 #include "fw_internal.cuh"
 #include "fw_sm100.cuh"
+#include "fw_tma.cuh"
 
 namespace fw {
 namespace {
@@ -819,34 +818,6 @@ chan_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// [n_chains][T][128] bf16 viewed as (d, T, chain): 64 x 64 boxes with the 128-byte
-// swizzle for the tile loads.
-bool make_map(CUtensorMap *m, const void *ptr, int64_t T, int64_t nc) {
-    auto enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)nc};
-    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)T * D * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)C, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box,
-               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 // Falcon-2 / 2A with bf16 inputs, d = 128, phi = identity (phi = elu+1 would round
@@ -866,8 +837,8 @@ extern "C" int fw_debug_read_chan_trace(unsigned long long *dst, int n) {
 
 cudaError_t launch_chunked_chan(const PrefillArgs &a, cudaStream_t s) {
     CUtensorMap tq, tk, tv;
-    if (!make_map(&tq, a.q, a.T, a.n_chains) || !make_map(&tk, a.k, a.T, a.n_chains) ||
-        !make_map(&tv, a.v, a.T, a.n_chains))
+    if (!make_map(&tq, a.q, a.T, a.n_chains, D, C) || !make_map(&tk, a.k, a.T, a.n_chains, D, C) ||
+        !make_map(&tv, a.v, a.T, a.n_chains, D, C))
         return cudaErrorInvalidValue;
     const bool rbw = (a.flags & FW_FLAG_RBW) != 0;
     auto kern = a.mode == FW_FALCON2A ? (rbw ? chan_kernel<true, true> : chan_kernel<true, false>)

@@ -21,6 +21,8 @@
 
 namespace fw {
 
+constexpr int kSMs = 152;   // of a GB300: the target of a grid (a workspace's size is asked for without a device)
+
 // Let kernel k use `bytes` of dynamic shared memory: one driver call a device, not one a launch.
 // `done` is the kernel's own (a bit for each device).
 template <typename K> cudaError_t allow_smem(K k, int bytes, std::atomic<uint64_t> &done) {
@@ -125,6 +127,32 @@ cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const LayerNormBwdArgs &a, cudaStream_t s);
 size_t layer_norm_workspace(int64_t rows, int64_t width);
 
+// Two fp32 operations in one instruction, on pairs.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // g^n = exp(n log g).  The product n log g is rounded to fp32; what the rounding
 // dropped is recovered by an FMA and multiplied back in, so a large exponent costs no relative
 // accuracy.  g^0 = 1 for every g, g = 0 (log g = -inf) included.

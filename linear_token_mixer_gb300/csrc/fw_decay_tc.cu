@@ -40,12 +40,11 @@
 // Tensor memory: G (P over it) 128 columns, O 128, the update 128, the split operand 2 x 48.
 // Every wait is bounded; on expiry the kernel records an error, the other roles stop at their
 // next wait, copies and MMAs in flight are drained, tensor memory is freed and the kernel exits.
-#include <cudaTypedefs.h>
-
-#include <mutex>
+#include <cuda.h>
 
 #include "fw_decay_tc.cuh"
 #include "fw_sm100.cuh"
+#include "fw_tma.cuh"
 
 namespace fw {
 namespace {
@@ -55,7 +54,6 @@ constexpr int C = 128;
 constexpr int NTHREADS = 896;
 constexpr uint32_t KB = 1024;
 constexpr uint32_t HALF = 16 * KB;           // 128 rows x 128 bytes: 64 columns of a tile
-constexpr int kSMs = 152;                    // the grid's target (a workspace size needs no device)
 // The launches of a call overlap (programmatic dependent launch).  A segment kernel's successor
 // waits for it before it begins; a scan that follows an independent one takes the SMs as they come
 // free and waits for it only before it ends, so that the last grid to end is the last of all.
@@ -191,32 +189,6 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                  : "memory");
 }
 
-// Two fp32 operations in one instruction, on pairs.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 halves(uint64_t x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ void scale2(float &a0, float &a1, uint64_t b) {
     const float2 f = halves(mul2(pair(a0, a1), b));
     a0 = f.x;
@@ -1044,34 +1016,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
     if (order & kWaitLast) wait_previous_grid();
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// [n_chains][T][d] bf16 as a 3-D tensor (d, T, chain), boxes of 64 columns and `rows` rows: rows
-// behind T read as zero.
-bool make_map(CUtensorMap *m, const void *ptr, int64_t T, int64_t nc, int d, int rows = C) {
-    auto enc = encode_fn();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)nc};
-    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)T * d * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box,
-               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Estimated time (us) of chains that take one CTA an SM, each in `s` segments, from what was measured at
 // d = 128: 2.8 us a chunk, and where there are segments a launch of 11 us and 2 us a chunk for their
 // states, and 0.7 us to add up each state before the last.
@@ -1099,8 +1043,8 @@ cudaError_t launch(const ScanArgs *scans, int nseg, bool follows, cudaStream_t s
     for (int i = 0; i < N; ++i) {
         const ScanArgs &a = scans[i];
         jobs.s[i].args = a;
-        if (!make_map(&jobs.s[i].a, a.a, a.T, a.n_chains, D) || !make_map(&jobs.s[i].b, a.b, a.T, a.n_chains, D) ||
-            !make_map(&jobs.s[i].c, a.c, a.T, a.n_chains, D) || !make_map(&jobs.s[i].out, a.out, a.T, a.n_chains, D, 32))
+        if (!make_map(&jobs.s[i].a, a.a, a.T, a.n_chains, D, C) || !make_map(&jobs.s[i].b, a.b, a.T, a.n_chains, D, C) ||
+            !make_map(&jobs.s[i].c, a.c, a.T, a.n_chains, D, C) || !make_map(&jobs.s[i].out, a.out, a.T, a.n_chains, D, 32))
             return cudaErrorInvalidValue;
     }
     const ScanArgs &a = scans[0];

@@ -29,7 +29,7 @@ namespace fw {
 namespace {
 
 constexpr int kBlock = 256;     // block of the part-of-a-warp forms
-constexpr int kPartials = 608;  // most partial rows of dw, db (4 blocks for each of 152 SMs)
+constexpr int kPartials = 4 * kSMs;   // most partial rows of dw, db
 
 template <typename T, int VW> struct Vec;
 template <typename T> struct Vec<T, 1> { T e[1]; };
@@ -39,17 +39,6 @@ template <> struct alignas(8) Vec<float, 2> { float e[2]; };               // ev
 template <> struct alignas(4) Vec<__nv_bfloat16, 2> { __nv_bfloat16 e[2]; };
 
 // fp32 arithmetic on the VW elements of a vector, two in one instruction where there are two.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1,
-                                     float c0, float c1) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a0, a1)), "l"(pack2(b0, b1)), "l"(pack2(c0, c1)));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(r));
-}
 template <int N> struct Row {   // N values
     float e[N];
 };
@@ -58,8 +47,11 @@ template <int N> __device__ __forceinline__ Row<N> fma_n(const Row<N> &a, const 
     Row<N> d;
     if constexpr (N % 2 == 0) {
 #pragma unroll
-        for (int i = 0; i < N; i += 2)
-            fma2(d.e[i], d.e[i + 1], a.e[i], a.e[i + 1], b.e[i], b.e[i + 1], c.e[i], c.e[i + 1]);
+        for (int i = 0; i < N; i += 2) {
+            const float2 f = halves(fma2(pair(a.e[i], a.e[i + 1]), pair(b.e[i], b.e[i + 1]), pair(c.e[i], c.e[i + 1])));
+            d.e[i] = f.x;
+            d.e[i + 1] = f.y;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) d.e[i] = fmaf(a.e[i], b.e[i], c.e[i]);
@@ -558,7 +550,7 @@ template <typename K> cudaError_t resident(K k, int threads, size_t smem, int64_
     int dev = 0, sms = 0, per = 0;
     cudaError_t e;
     *n = blocks;
-    if (blocks <= 148) return cudaSuccess;   // at most one an SM in any case
+    if (blocks <= kSMs) return cudaSuccess;   // at most one an SM in any case
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, threads, smem)) != cudaSuccess) return e;
