@@ -214,6 +214,11 @@ chan_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
         fence_mbar_init();
         *s_abort = 0;
     }
+    // A chain shorter than a chunk leaves beta rows that no copy fills: zero times what the kernel
+    // before left there may be NaN.
+    if (T < C)
+        for (int i = (int)T * D + tid; i < C * D; i += NTHREADS)
+            reinterpret_cast<float *>(sm + OFF_BETA)[i] = 0.f;
     if (warp == 2) tmem_alloc(sb + OFF_MISC + 4, TMEM_COLS);
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmq);
@@ -262,7 +267,8 @@ chan_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                 }
                 if (cb < nch && cb < cx && (cb == 0 || mbar_test(bar(B_BFREE), (uint32_t)(cb - 1) & 1u))) {
                     // the chunk's beta rows: contiguous [t][j] fp32, 512 B per token,
-                    // clipped at the chain's end (rows past T are never read)
+                    // clipped at the chain's end (rows past T are read times a step of zero:
+                    // they hold the chunk before, or the zeros written at the start)
                     const int64_t t0 = (int64_t)cb * C;
                     const int rows = (int)((T - t0) < C ? (T - t0) : C);
                     const uint32_t bytes = (uint32_t)rows * (uint32_t)D * 4u;
