@@ -105,3 +105,52 @@ def test_whole_rows_that_are_not_finite(T, t, d, dtype):
         assert R.rel_rows(o[1:, :, :ln[1]], r[1:, :, :ln[1]], 2) <= TOL[dtype]
         assert (o[1, :, ln[1]:] == 0).all() and torch.isfinite(S[1]).all()
         assert not torch.isfinite(o[0, :, t:]).any() and not torch.isfinite(S[0]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_padded_batch_of_more_chains_than_fit_at_once(d, dtype):
+    """13 x 13 chains of different lengths, the longest first, NaN behind every end and one value inside some
+    chains: rows before it (after it, for dk and dv) are those of the call without it, up to the two calls'
+    roundings (twice the tolerance, relative L2 of a chain's rows), and so is every other chain."""
+    B, H, T, t = 13, 13, 420, 60
+    x, g = inputs(B, H, T, d, dtype, seed=d)
+    ln = torch.tensor([0, 420, 1, 300, 300, 128, 127, 5, 420, 64, 256, 17, 399], dtype=torch.int32)
+    n = ln.view(B, 1, 1, 1)
+    behind = torch.arange(T).view(1, 1, T, 1) >= n
+    nan = torch.full((), float("nan"), dtype=dtype)
+    clean = {k: torch.where(behind, nan, x[k]).cuda() for k in ("q", "k", "v", "do")}
+    l = (-torch.rand(H, generator=torch.Generator().manual_seed(1)) * 0.2).cuda()
+    hit = [(1, 0), (1, 12), (3, 5), (8, 7), (9, 2), (12, 12)]
+
+    def run(bad_name=None):
+        z = {k: (v.clone() if k == bad_name else v) for k, v in clean.items()}
+        if bad_name:
+            for b, h in hit:
+                z[bad_name][b, h, t, 7] = float("inf") if h == 12 else float("nan")
+        o, S = fw.decay_prefill(z["q"], z["k"], z["v"], l, g["S0"], lens=ln.cuda(), norm=None)
+        dq, dk, dv, dS0 = fw.decay_backward(z["q"], z["k"], z["v"], l, z["do"], g["S0"], g["dS"], lens=ln.cuda())
+        fw.check()
+        return o, dq, dk, dv, S, dS0
+
+    want = run()
+    assert all(torch.isfinite(a).all() for a in want)
+    # rows of a hit chain that do not depend on token t: before it (-1), after it (1), all (0)
+    # (o, dq, dk, dv), or that may be anything (None)
+    side = {"v": (-1, -1, None, 0), "k": (-1, -1, 0, None), "do": (0, None, 1, 1), "q": (None, 0, 1, 1)}
+    for name, sides in side.items():
+        got = run(name)
+        for a, r, s in zip(got[:4], want[:4], sides):
+            for b in range(B):
+                for h in range(H):
+                    rows = slice(None)
+                    if (b, h) in hit:
+                        if s is None:
+                            continue
+                        rows = slice(0, t) if s < 0 else slice(t + 1, None) if s > 0 else rows
+                    num, den = (a[b, h, rows] - r[b, h, rows]).double().norm(), r[b, h, rows].double().norm()
+                    assert torch.isfinite(a[b, h, rows]).all() and num <= 2 * TOL[dtype] * den
+        for a, r in zip(got[4:], want[4:]):
+            ok = torch.ones(B, H, dtype=torch.bool)
+            ok[tuple(zip(*hit))] = False
+            assert torch.equal(a[ok.cuda()], r[ok.cuda()])
