@@ -328,6 +328,10 @@ int fw_window_step(const void *q, const void *k_prev, const void *v, const float
  *   the formulas give an infinity it may arrive as NaN.  A chain of bf16 rows with
  *   one in v (in the backward pass: in q, k or d_o) is formed token by
  *   token, about 2 us each, after the usual way.
+ *   bf16 rows: the masked scores, and the state as a row reads it, are rounded to
+ *   bf16 once, like the rows that come out; S_T and dS0 are fp32 throughout.
+ *   Where 128 |log_decay| <= 24, sums within 128 tokens are formed up to e^24 times
+ *   their size: scores or rows beyond about 1e28 may overflow.
  *   No output may overlap an input, another output or the workspace, except
  *   S_T = S0.
  */

@@ -7,8 +7,9 @@
 //     forward   out_i += g^(i+1)   X^T a_i,   X' = g^n X + in_scale sum_j g^(n-1-j) b_j c_j^T
 //     reverse   out_i += g^(n-1-i) X^T a_i,   X' = g^n X + in_scale sum_j g^(j+1)   b_j c_j^T
 // (the reverse scan carries the gradient with respect to the state *before* the token's
-// decay, so its final X is dS0).  Only powers g^m with m >= 0 appear: nothing is divided by
-// a product of decays.
+// decay, so its final X is dS0).  Only powers g^m with m >= 0 appear.  (The bf16 scans divide within a
+// chunk of 128 where 128 |log g| <= 24: the rows' factor g^(i+1) is taken out of the chunk, and
+// the scores by g^-(j+1).)
 //     o  = scan(q, k, v; X0 = S0)                      out_scale = scale
 //     dq = scan(do, v, k; X0 = S0^T)                   out_scale = scale
 //     dv = reverse scan(k, q, do; X0 = dS_T)           in_scale  = scale, final X = dS0

@@ -31,11 +31,11 @@
 // The update of a chunk is summed from zero in tensor memory and added to X by an fp32 FMA: the
 // MMAs round towards zero, and X would carry that bias from chunk to chunk.  It also takes the
 // MMAs of the update off the state's serial chain (update read -> copy -> A X).
-// Measured (one GB300): B8 H16 T4096 d = 128, 128 chains, 545 MB of rows and states: 103.6 us, 5.3
-// TB/s, 77 % of the measured copy rate; B1 H32 T32768, four segments a chain: 312 us, of which the
-// states of the segments, read again, are a third.  What bounds it is the period of a chunk, 2.8 us,
-// in one CTA, and 10 us for its start: at T2048 the tensor pipe is busy for 34 % of the time, the issue
-// slots for 36 %, DRAM at 54 %, and the rest is the roles' round trips through tensor memory and barriers.  A second CTA an
+// Measured (one GB300): B8 H16 T4096 d = 128, 128 chains, 545 MB of rows and states: 105.6 us, 5.2
+// TB/s, 76 % of the measured copy rate; B1 H32 T32768, four segments a chain: 318 us, of which the
+// states of the segments, read again, are a third.  What bounds it is the period of a chunk, 2.8 us (d = 64:
+// 2.05 us), in one CTA, and 10 us for its start: at T2048 the tensor pipe is busy for 38 % of the time, the
+// issue slots for 38 %, DRAM at 55 %, and the rest is the roles' round trips through tensor memory and barriers.  A second CTA an
 // SM would fill it but finds no room: the tiles take 192 KB, G, O and the update 384 columns.
 // Tensor memory: G (P over it) 128 columns, O 128, the update 128, the split operand 2 x 48.
 // Every wait is bounded; on expiry the kernel records an error, the other roles stop at their
@@ -1018,7 +1018,8 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
 
 // Estimated time (us) of chains that take one CTA an SM, each in `s` segments, from what was measured at
 // d = 128: 2.8 us a chunk, and where there are segments a launch of 11 us and 2 us a chunk for their
-// states, and 0.7 us to add up each state before the last.
+// states, and 0.7 us to add up each state before the last.  (d = 64 takes 2.05 us a chunk; its other terms
+// have not been measured, and it takes the same numbers of segments.)
 double estimate(int64_t chunks, int s) {
     if (s == 1) return 2.8 * (double)chunks;
     return 11.0 + 4.8 * (double)((chunks + s - 1) / s) + 0.7 * s;

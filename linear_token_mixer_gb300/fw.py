@@ -157,7 +157,8 @@ def prefill(q, k, v, beta=None, lam=None, S0=None, *, mode="falcon1", phi="ident
     [B,H,d,d] fp32 or None.  noalloc: call fw_prefill_noalloc (the library's
     workspace from its static buffer; pass o and S_T to allocate nothing here
     either).  norm: (weight [d], bias [d]) fp32, either None: layer norm of every
-    row of o, in place."""
+    row of o, in place (bf16 rows are rounded before it and after it; the decayed
+    calls norm the fp32 row)."""
     B, H, T, d = q.shape
     if o is None:
         o = torch.empty_like(q)
