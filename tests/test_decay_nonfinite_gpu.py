@@ -154,3 +154,35 @@ def test_padded_batch_of_more_chains_than_fit_at_once(d, dtype):
             ok = torch.ones(B, H, dtype=torch.bool)
             ok[tuple(zip(*hit))] = False
             assert torch.equal(a[ok.cuda()], r[ok.cuda()])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("t", [3, 1700, 3999])
+def test_backward_of_few_long_chains(t, d):
+    """Chains whose reverse scans are split over the GPU too: rows that do not depend on token t are those of the
+    call without it, up to the two calls' roundings."""
+    B, H, T = 1, 2, 4000
+    _, g = inputs(B, H, T, d, BF16, seed=t)
+    l = torch.tensor([-0.002, -0.1]).cuda()
+    n = fw.decay_workspace(B, H, T, d, BF16, backward=True)
+    assert n > fw.decay_workspace(B, H, T, d, BF16) > 0     # segments in both directions
+
+    def run(name=None):
+        z = {k: (v.clone() if k == name else v) for k, v in g.items()}
+        if name:
+            z[name][0, 1, t, 9] = float("nan")
+        got = fw.decay_backward(z["q"], z["k"], z["v"], l, z["do"], z["S0"], z["dS"])
+        fw.check()
+        return got
+
+    want = run()
+    for name, sides in {"v": (-1, None, 0), "k": (-1, 0, None), "do": (None, 1, 1), "q": (0, 1, 1)}.items():
+        got = run(name)
+        for a, r, s in zip(got[:3], want[:3], sides):
+            assert torch.equal(a[0, 0], r[0, 0])
+            rows = slice(0, t) if s == -1 else slice(t + 1, None) if s == 1 else slice(None)
+            if s is None:
+                rows = torch.arange(T, device="cuda") != t
+            x, y = a[0, 1, rows].double(), r[0, 1, rows].double()
+            assert torch.isfinite(x).all() and (x - y).norm() <= 2 * TOL[BF16] * y.norm()
+        assert torch.equal(got[3][0, 0], want[3][0, 0])
