@@ -97,15 +97,19 @@ typedef struct {
                     written as zeros */
 } fw_window;
 
-/* Flags (bitwise OR) of fw_prefill_ex and fw_step_ex, and (FW_FLAG_ZERO_REST
- * alone) of fw_decay_prefill and fw_decay_backward.
+/* Flags (bitwise OR) of fw_prefill_ex and fw_step_ex, (FW_FLAG_ZERO_REST
+ * alone) of fw_decay_prefill and fw_decay_backward, and those that the fw_conv_*
+ * and fw_select_* calls name.
  * FW_FLAG_RBW: read before the write, o_t = S_{t-1}^T q_t (every mode).
  * FW_FLAG_SAME_PAIR: FW_FALCON1 / FW_FALCON1A pair (phi(k_t), v_t) for every
  *   token, so the first token writes too and k_init is not used (prefill
  *   only; FW_LINATTN always pairs this way, and a step pairs whatever key it
  *   is given).  The pages name these arms without printing formulas; the
  *   readings above are the plainest ones. */
-typedef enum { FW_FLAG_RBW = 1, FW_FLAG_SAME_PAIR = 2, FW_FLAG_ZERO_REST = 4 } fw_flag;
+typedef enum {
+    FW_FLAG_RBW = 1, FW_FLAG_SAME_PAIR = 2, FW_FLAG_ZERO_REST = 4, FW_FLAG_SILU = 8,
+    FW_FLAG_SOFTPLUS = 16
+} fw_flag;
 
 /* Feature map phi.  FW_FALCON1 applies it to the key only (the read uses q as
  * given); FW_LINATTN applies it to both q and k, never to v.
@@ -145,7 +149,8 @@ enum {
     FW_ERR_ARG = -9,         /* eps negative or not finite, or o aliases an input */
     FW_ERR_DEVICE = -10,     /* the current device is not an sm_103 GPU */
     FW_ERR_SCRATCH = -11     /* fw_prefill_noalloc: the call needs more than FW_SCRATCH_BYTES;
-                                fw_decay_*, fw_layer_norm_backward: workspace_bytes too small */
+                                the calls with a workspace of the caller's: workspace_bytes too
+                                small */
 };
 
 /*
@@ -416,6 +421,160 @@ int fw_layer_norm(const void *x, const float *weight, const float *bias, void *y
 int64_t fw_layer_norm_workspace(int64_t rows, int64_t width);
 int fw_layer_norm_backward(const void *dy, const void *x, const float *weight, const float *mean,
                            const float *rstd, void *dx, float *dweight, float *dbias,
+                           int64_t rows, int64_t width, fw_dtype dtype, void *workspace,
+                           int64_t workspace_bytes, cudaStream_t stream);
+
+/* ---- selective scan: decays that depend on the token --------------------------
+ *
+ * The decayed recurrence with a step dt for each token and head (a selective state space, its
+ * state d_k x d_v):
+ *     dt_t = softplus(dt_raw_t + dt_bias[h])   (FW_FLAG_SOFTPLUS; else dt_raw_t + dt_bias[h]),
+ *     S_t  = exp(log_decay[h] dt_t) S_{t-1} + dt_t k_t v_t^T,
+ *     o_t  = scale S_t^T q_t + skip[h] v_t,
+ * over a prompt and for one token.  Heads share queries and keys in `groups` groups of H / groups
+ * neighbours.  As the decayed calls: lens, FW_FLAG_ZERO_REST, the caller's workspace, S_T = S0, and
+ * which overlaps are refused.  log_decay is finite and <= 0 and dt >= 0; where a decay grows instead
+ * (log_decay dt > 0) it is computed as it is, as long as its sums within 128 tokens stay below 80.
+ * A decay below e^-104 is zero: the state starts afresh with the token.
+ *   bf16 rows: the masked scores, and the state as a row reads it, are rounded to bf16 once, like the
+ *   rows that come out; the steps, the decays and S_T are fp32 throughout.  Where the decays of a chunk of
+ *   128 tokens multiply to e^-24 or more, its sums are formed up to e^24 times their size.
+ *   An infinity or NaN in v reaches the rows that depend on it and nothing else, and may arrive as
+ *   NaN; one in k, or in a step, may reach its chunk of 128 tokens and what follows.
+ */
+typedef struct {
+    const void *dt;          /* [B][H][T] (a step: [B][H]) of dt_type */
+    fw_dtype dt_type;        /* FW_F32, or the call's dtype */
+    const float *log_decay;  /* [H] */
+    const float *dt_bias;    /* [H] or NULL (zeros) */
+    const float *skip;       /* [H] or NULL (no such term) */
+    int64_t groups;          /* of queries and keys; H is a multiple of it */
+} fw_gates;
+
+/* Bytes of workspace of fw_select_prefill for this shape and type, or a negative FW_ERR_* code. */
+int64_t fw_select_workspace(const fw_shape *shape, fw_dtype dtype);
+
+/*
+ * fw_select_prefill -- T tokens for B*H independent chains.
+ *   q, k      in   [B][groups][T][d] of `dtype`
+ *   v         in   [B][H][T][d] of `dtype`
+ *   S0        in   float [B][H][d][d] or NULL (zero)
+ *   o         out  [B][H][T][d] of `dtype`
+ *   S_T       out  float [B][H][d][d], the state after the last token; may equal S0
+ *   scale     finite
+ *   flags     0, FW_FLAG_ZERO_REST, FW_FLAG_SOFTPLUS or both (FW_ERR_MODE otherwise)
+ */
+int fw_select_prefill(const void *q, const void *k, const void *v, const fw_gates *gates,
+                      const float *S0, const int32_t *lens, void *o, float *S_T,
+                      const fw_shape *shape, fw_dtype dtype, float scale, unsigned flags,
+                      void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fw_select_step -- one token for B*H states, S updated in place.
+ *   q, k   in      [B][groups][d] of `dtype`
+ *   v      in      [B][H][d] of `dtype`
+ *   S      in/out  float [B][H][d][d]
+ *   o      out     [B][H][d] of `dtype`
+ *   flags  0 or FW_FLAG_SOFTPLUS;  shape: T must be 1
+ */
+int fw_select_step(const void *q, const void *k, const void *v, const fw_gates *gates, float *S,
+                   void *o, const fw_shape *shape, fw_dtype dtype, float scale, unsigned flags,
+                   cudaStream_t stream);
+
+/* ---- short causal convolution ---------------------------------------------------
+ *
+ * Of every channel before a mixer, `width` taps (2 .. FW_CONV_MAX):
+ *     a_t = bias + sum_w weight[w] x_{t-width+1+w},   y_t = a_t, with FW_FLAG_SILU a_t / (1 + exp(-a_t)),
+ * over rows of shape->d_k = d_v = d channels, any d >= 1.  Rows before the first come from `state`, so that
+ * calls continue one another.  lens and FW_FLAG_ZERO_REST as in the decayed calls: rows from lens[b]
+ * on are never used, and the state behind a row of the batch is that behind its last token.
+ *   x, y, dy, dx   [B][H][T][d] of `dtype`
+ *   weight, bias   float [H][d][width], the last tap on the row itself; float [H][d] or NULL (zeros)
+ *   state          [B][H][width-1][d] of `dtype`, oldest row first, or NULL (zeros)
+ *   state_out      the same shape, the last width - 1 rows of the state's and x's; NULL: not wanted; may be state
+ * No other output may overlap an input, another output or the workspace.
+ */
+#define FW_CONV_MAX 8
+int fw_conv_prefill(const void *x, const float *weight, const float *bias, const void *state,
+                    const int32_t *lens, void *y, void *state_out, const fw_shape *shape, int width,
+                    fw_dtype dtype, unsigned flags, cudaStream_t stream);
+
+/* Bytes of workspace of fw_conv_backward, or a negative FW_ERR_* code. */
+int64_t fw_conv_workspace(const fw_shape *shape, int width);
+
+/*
+ * fw_conv_backward -- gradients of fw_conv_prefill, given those of y and of state_out.
+ *   dstate_out       in   [B][H][width-1][d] of `dtype` or NULL (zero)
+ *   dx               out  [B][H][T][d] of `dtype`
+ *   dweight, dbias   out  float [H][d][width], [H][d]; NULL: not wanted.  Sums in fp32, in an order that
+ *                         does not change between runs
+ *   dstate           out  [B][H][width-1][d] of `dtype` or NULL (not wanted)
+ *   workspace        the caller's; may be NULL where neither dweight nor dbias is wanted
+ */
+int fw_conv_backward(const void *dy, const void *x, const float *weight, const float *bias,
+                     const void *state, const int32_t *lens, const void *dstate_out, void *dx,
+                     float *dweight, float *dbias, void *dstate, const fw_shape *shape, int width,
+                     fw_dtype dtype, unsigned flags, void *workspace, int64_t workspace_bytes,
+                     cudaStream_t stream);
+
+/*
+ * fw_conv_step -- one token: x, y [B][H][d]; the state moves on by one row in place.
+ *   flags  0 or FW_FLAG_SILU;  shape: T must be 1
+ */
+int fw_conv_step(const void *x, const float *weight, const float *bias, void *state, void *y,
+                 const fw_shape *shape, int width, fw_dtype dtype, unsigned flags,
+                 cudaStream_t stream);
+
+/* ---- gated norm ----------------------------------------------------------------
+ *
+ * The norm before a block with its scaled residual sum, and the norm behind a mixer with its gate, over
+ * the last axis of x [rows][width], 1 <= width <= FW_GATED_WIDTH:
+ *     u = x + scale residual,   silu(z) = z / (1 + exp(-z)) of z = gate,
+ *     y = norm(u silu(z)) weight + bias,   or (gate_after)   y = (norm(u) weight + bias) silu(z),
+ *     norm(s) = (s - m) r,  m = mean(s), or 0 with rms,  r = 1 / sqrt(mean((s-m)^2) + eps).
+ * u, the statistics and all sums are fp32; `total` is u as it is stored.  Parameters may be those of
+ * each group of rows: row i belongs to group (i / inner) % groups (rows [B][H][T]: groups = H, inner = T).
+ */
+#define FW_GATED_WIDTH 8192
+typedef struct {
+    const void *gate;      /* [rows][width] of `dtype`, or NULL (no gate) */
+    const void *residual;  /* [rows][width] of `dtype`, or NULL (u = x) */
+    const float *scale;    /* [groups][width] or NULL (ones) */
+    const float *weight;   /* [groups][width] or NULL (ones) */
+    const float *bias;     /* [groups][width] or NULL (zeros) */
+    int64_t groups, inner; /* rows = groups * inner * a whole number (1, rows: one group) */
+    float eps;             /* >= 0 */
+    int rms, gate_after;   /* 0 or 1 */
+} fw_gated;
+
+/*
+ * fw_gated_norm.
+ *   y           out  [rows][width] of `dtype`
+ *   total       out  [rows][width] of `dtype`, u; NULL: not wanted
+ *   mean, rstd  out  float [rows]; NULL: not wanted (mean with rms: zeros)
+ * y and total may each be x, gate or residual (other overlaps are refused).
+ */
+int fw_gated_norm(const void *x, const fw_gated *args, void *y, void *total, float *mean, float *rstd,
+                  int64_t rows, int64_t width, fw_dtype dtype, cudaStream_t stream);
+
+/* Bytes of workspace of fw_gated_norm_backward, or a negative FW_ERR_* code. */
+int64_t fw_gated_norm_workspace(int64_t rows, int64_t width, int64_t groups, fw_dtype dtype);
+
+/*
+ * fw_gated_norm_backward -- gradients, given those of y and of total, from the forward pass's inputs
+ * and statistics.
+ *   dtotal                  in   [rows][width] of `dtype` or NULL (zero)
+ *   mean, rstd              in   float [rows] (mean: may be NULL with rms)
+ *   dx, dgate, dresidual    out  [rows][width] of `dtype`; NULL: not wanted (dx is dresidual without scale)
+ *   dweight, dbias, dscale  out  float [groups][width]; NULL: not wanted.  Sums in an order that does not
+ *                                change between runs
+ *   workspace               the caller's; may be NULL where none of the three is wanted
+ * dx, dgate and dresidual may each be dy, dtotal, x, gate or residual (other overlaps are refused).  dgate is
+ * refused without a gate, dresidual and dscale without a residual.
+ */
+int fw_gated_norm_backward(const void *dy, const void *dtotal, const void *x, const fw_gated *args,
+                           const float *mean, const float *rstd, void *dx, void *dgate,
+                           void *dresidual, float *dweight, float *dbias, float *dscale,
                            int64_t rows, int64_t width, fw_dtype dtype, void *workspace,
                            int64_t workspace_bytes, cudaStream_t stream);
 

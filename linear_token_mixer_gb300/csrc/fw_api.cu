@@ -5,8 +5,11 @@
 #include <initializer_list>
 #include <mutex>
 
+#include "fw_conv.cuh"
 #include "fw_decay.cuh"
+#include "fw_gated_norm.cuh"
 #include "fw_internal.cuh"
+#include "fw_select.cuh"
 
 namespace fw {
 namespace {
@@ -676,6 +679,306 @@ extern "C" int fw_layer_norm_backward(const void *dy, const void *x, const float
     LayerNormBwdArgs a{dy, x, weight, mean, rstd, dx, dweight, dbias, rows, width, dtype,
                        sums ? static_cast<float *>(workspace) : nullptr};
     const cudaError_t e = launch_layer_norm_backward(a, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+namespace {
+
+size_t bytes_of(fw_dtype t) { return t == FW_F32 ? 4 : 2; }
+
+// Shape, taps and type of a convolution: any number of channels.
+int check_conv(const fw_shape *shape, int width, fw_dtype dtype) {
+    if (!shape) return FW_ERR_NULL;
+    if (shape->B < 1 || shape->H < 1 || shape->T < 1 || shape->d_k < 1 || shape->d_v != shape->d_k)
+        return FW_ERR_SHAPE;
+    if (width < 2 || width > FW_CONV_MAX) return FW_ERR_SHAPE;
+    if (shape->H > 65535 || shape->B > INT32_MAX / shape->H) return FW_ERR_SHAPE;
+    if (!conv_fits(shape->B, shape->H, shape->T, shape->d_k)) return FW_ERR_SHAPE;
+    if (dtype != FW_F32 && dtype != FW_BF16) return FW_ERR_DTYPE;
+    return FW_OK;
+}
+
+// Sizes of a convolution's buffers in bytes.
+struct ConvSizes {
+    size_t x, state, weight, bias, lens;
+};
+ConvSizes conv_sizes(const fw_shape *s, int width, fw_dtype dtype) {
+    const size_t d = s->d_k, n = (size_t)s->B * s->H * d * bytes_of(dtype), h = (size_t)s->H * d * 4;
+    return {n * s->T, n * (width - 1), h * width, h, (size_t)s->B * 4};
+}
+
+}  // namespace
+
+extern "C" int fw_conv_prefill(const void *x, const float *weight, const float *bias,
+                               const void *state, const int32_t *lens, void *y, void *state_out,
+                               const fw_shape *shape, int width, fw_dtype dtype, unsigned flags,
+                               cudaStream_t stream) {
+    int st = check_conv(shape, width, dtype);
+    if (st != FW_OK) return st;
+    if (flags & ~(unsigned)(FW_FLAG_SILU | FW_FLAG_ZERO_REST)) return FW_ERR_MODE;
+    if (!x || !weight || !y) return FW_ERR_NULL;
+    if (any_misaligned({x, weight, bias, state, lens, y, state_out})) return FW_ERR_ALIGN;
+    const ConvSizes n = conv_sizes(shape, width, dtype);
+    if (outputs_clash({{y, n.x}, {state_out, n.state}},
+                      {{x, n.x}, {weight, n.weight}, {bias, n.bias}, {lens, n.lens},
+                       {state != state_out ? state : nullptr, n.state}}) ||
+        overlaps(y, n.x, state, n.state))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    const ConvArgs a{x, weight, bias, state, lens, y, state_out, shape->B * shape->H, shape->T,
+                     (int)shape->H, shape->d_k, width, dtype, (flags & FW_FLAG_SILU) != 0,
+                     lens && (flags & FW_FLAG_ZERO_REST)};
+    const cudaError_t e = launch_conv(a, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+extern "C" int64_t fw_conv_workspace(const fw_shape *shape, int width) {
+    const int st = check_conv(shape, width, FW_F32);
+    if (st != FW_OK) return st;
+    return (int64_t)conv_workspace(shape->B, (int)shape->H, shape->T, shape->d_k, width);
+}
+
+extern "C" int fw_conv_backward(const void *dy, const void *x, const float *weight,
+                                const float *bias, const void *state, const int32_t *lens,
+                                const void *dstate_out, void *dx, float *dweight, float *dbias,
+                                void *dstate, const fw_shape *shape, int width, fw_dtype dtype,
+                                unsigned flags, void *workspace, int64_t workspace_bytes,
+                                cudaStream_t stream) {
+    int st = check_conv(shape, width, dtype);
+    if (st != FW_OK) return st;
+    if (flags & ~(unsigned)(FW_FLAG_SILU | FW_FLAG_ZERO_REST)) return FW_ERR_MODE;
+    if (!dy || !x || !weight || !dx) return FW_ERR_NULL;
+    if (any_misaligned({dy, x, weight, bias, state, lens, dstate_out, dx, dweight, dbias, dstate, workspace}))
+        return FW_ERR_ALIGN;
+    const bool sums = dweight || dbias;
+    const int64_t need = sums ? fw_conv_workspace(shape, width) : 0;
+    if (sums && !workspace) return FW_ERR_NULL;
+    if (workspace_bytes < need) return FW_ERR_SCRATCH;
+    const ConvSizes n = conv_sizes(shape, width, dtype);
+    if (outputs_clash({{dx, n.x}, {dweight, n.weight}, {dbias, n.bias}, {dstate, n.state}, {workspace, (size_t)need}},
+                      {{dy, n.x}, {x, n.x}, {weight, n.weight}, {bias, n.bias}, {state, n.state}, {lens, n.lens},
+                       {dstate_out, n.state}}))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    const ConvBwdArgs a{dy, x, weight, bias, state, lens, dstate_out, dx, dweight, dbias, dstate,
+                        shape->B, shape->T, (int)shape->H, shape->d_k, width, dtype,
+                        (flags & FW_FLAG_SILU) != 0, lens && (flags & FW_FLAG_ZERO_REST),
+                        sums ? static_cast<float *>(workspace) : nullptr};
+    const cudaError_t e = launch_conv_backward(a, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+extern "C" int fw_conv_step(const void *x, const float *weight, const float *bias, void *state,
+                            void *y, const fw_shape *shape, int width, fw_dtype dtype,
+                            unsigned flags, cudaStream_t stream) {
+    int st = check_conv(shape, width, dtype);
+    if (st != FW_OK) return st;
+    if (shape->T != 1) return FW_ERR_SHAPE;
+    if (flags & ~(unsigned)FW_FLAG_SILU) return FW_ERR_MODE;
+    if (!x || !weight || !state || !y) return FW_ERR_NULL;
+    if (any_misaligned({x, weight, bias, state, y})) return FW_ERR_ALIGN;
+    const ConvSizes n = conv_sizes(shape, width, dtype);
+    if (outputs_clash({{y, n.x}, {state, n.state}}, {{x, n.x}, {weight, n.weight}, {bias, n.bias}}))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    const ConvStepArgs a{x, weight, bias, state, y, shape->B * shape->H, (int)shape->H, shape->d_k,
+                         width, dtype, (flags & FW_FLAG_SILU) != 0};
+    const cudaError_t e = launch_conv_step(a, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+namespace {
+
+// Gates of a selective call, and the head layout they go with.
+int check_gates(const fw_gates *g, const fw_shape *shape, fw_dtype dtype, GateArgs *out) {
+    if (!g || !g->dt || !g->log_decay) return FW_ERR_NULL;
+    if (g->dt_type != FW_F32 && g->dt_type != dtype) return FW_ERR_DTYPE;
+    if (g->groups < 1 || shape->H % g->groups != 0) return FW_ERR_SHAPE;
+    if (any_misaligned({g->dt, g->log_decay, g->dt_bias, g->skip})) return FW_ERR_ALIGN;
+    out->dt = g->dt;
+    out->dt_type = g->dt_type;
+    out->log_decay = g->log_decay;
+    out->dt_bias = g->dt_bias;
+    out->skip = g->skip;
+    out->G = (int)g->groups;
+    return FW_OK;
+}
+
+}  // namespace
+
+extern "C" int64_t fw_select_workspace(const fw_shape *shape, fw_dtype dtype) {
+    const int st = check_decay(shape, dtype);
+    if (st != FW_OK) return st;
+    return (int64_t)select_workspace(shape->B * shape->H, shape->T, shape->d_k, dtype);
+}
+
+extern "C" int fw_select_prefill(const void *q, const void *k, const void *v,
+                                 const fw_gates *gates, const float *S0, const int32_t *lens,
+                                 void *o, float *S_T, const fw_shape *shape, fw_dtype dtype,
+                                 float scale, unsigned flags, void *workspace,
+                                 int64_t workspace_bytes, cudaStream_t stream) {
+    int st = check_decay(shape, dtype);
+    if (st != FW_OK) return st;
+    if (flags & ~(unsigned)(FW_FLAG_ZERO_REST | FW_FLAG_SOFTPLUS)) return FW_ERR_MODE;
+    SelectArgs a{};
+    if ((st = check_gates(gates, shape, dtype, &a.gate)) != FW_OK) return st;
+    if (!q || !k || !v || !o || !S_T) return FW_ERR_NULL;
+    if (any_misaligned({q, k, v, S0, lens, o, S_T, workspace})) return FW_ERR_ALIGN;
+    if (!std::isfinite(scale)) return FW_ERR_ARG;
+    const int64_t nc = shape->B * shape->H;
+    const int d = shape->d_k;
+    const size_t e = bytes_of(dtype), nx = (size_t)nc * shape->T * d * e,
+                 nq = (size_t)shape->B * gates->groups * shape->T * d * e,
+                 ndt = (size_t)nc * shape->T * bytes_of(gates->dt_type), nh = (size_t)shape->H * 4;
+    const size_t ns = (size_t)nc * d * d * sizeof(float);
+    const int64_t need = fw_select_workspace(shape, dtype);
+    if (need > 0 && !workspace) return FW_ERR_NULL;
+    if (workspace_bytes < need) return FW_ERR_SCRATCH;
+    if (outputs_clash({{o, nx}, {S_T, ns}, {workspace, (size_t)need}},
+                      {{q, nq}, {k, nq}, {v, nx}, {gates->dt, ndt}, {gates->log_decay, nh},
+                       {gates->dt_bias, nh}, {gates->skip, nh}, {S0 != S_T ? S0 : nullptr, ns},
+                       {lens, (size_t)shape->B * 4}}))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    a.gate.softplus = (flags & FW_FLAG_SOFTPLUS) != 0;
+    a.scan = scan_of(shape, dtype, gates->log_decay, lens, err);
+    a.scan.a = q; a.scan.b = k; a.scan.c = v; a.scan.X0 = S0; a.scan.X_out = S_T; a.scan.out = o;
+    a.scan.out_scale = scale;
+    a.scan.zero_rest = lens && (flags & FW_FLAG_ZERO_REST);
+    a.scan.ws = static_cast<float *>(workspace);
+    const cudaError_t ce = launch_select(a, stream);
+    return ce == cudaSuccess ? FW_OK : cuda_fail(ce);
+}
+
+extern "C" int fw_select_step(const void *q, const void *k, const void *v, const fw_gates *gates,
+                              float *S, void *o, const fw_shape *shape, fw_dtype dtype, float scale,
+                              unsigned flags, cudaStream_t stream) {
+    int st = check_decay(shape, dtype);
+    if (st != FW_OK) return st;
+    if (shape->T != 1) return FW_ERR_SHAPE;
+    if (flags & ~(unsigned)FW_FLAG_SOFTPLUS) return FW_ERR_MODE;
+    SelectStepArgs a{};
+    if ((st = check_gates(gates, shape, dtype, &a.gate)) != FW_OK) return st;
+    if (!q || !k || !v || !S || !o) return FW_ERR_NULL;
+    if (any_misaligned({q, k, v, S, o})) return FW_ERR_ALIGN;
+    if (!std::isfinite(scale)) return FW_ERR_ARG;
+    const int64_t n = shape->B * shape->H;
+    const int d = shape->d_k;
+    const size_t e = bytes_of(dtype), nx = (size_t)n * d * e, nq = (size_t)shape->B * gates->groups * d * e,
+                 nh = (size_t)shape->H * 4, ns = (size_t)n * d * d * sizeof(float);
+    if (outputs_clash({{o, nx}, {S, ns}},
+                      {{q, nq}, {k, nq}, {v, nx}, {gates->dt, (size_t)n * bytes_of(gates->dt_type)},
+                       {gates->log_decay, nh}, {gates->dt_bias, nh}, {gates->skip, nh}}))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    a.gate.softplus = (flags & FW_FLAG_SOFTPLUS) != 0;
+    a.q = q; a.k = k; a.v = v; a.S = S; a.o = o;
+    a.n_states = n; a.H = (int)shape->H; a.d = d; a.dtype = dtype; a.scale = scale;
+    const cudaError_t ce = launch_select_step(a, stream);
+    return ce == cudaSuccess ? FW_OK : cuda_fail(ce);
+}
+
+namespace {
+
+int check_gated(int64_t rows, int64_t width, int64_t groups, fw_dtype dtype) {
+    if (rows < 1 || rows > (int64_t)INT32_MAX || width < 1 || width > FW_GATED_WIDTH || groups < 1 ||
+        groups > 65535 || rows % groups != 0)
+        return FW_ERR_SHAPE;
+    if (dtype != FW_F32 && dtype != FW_BF16) return FW_ERR_DTYPE;
+    return FW_OK;
+}
+
+// The arguments both passes share.
+int gated_in(const void *x, const fw_gated *g, int64_t rows, int64_t width, fw_dtype dtype, GatedIn *in) {
+    if (!g || !x) return FW_ERR_NULL;
+    const int st = check_gated(rows, width, g->groups, dtype);
+    if (st != FW_OK) return st;
+    if (g->inner < 1 || g->inner > rows / g->groups || rows % (g->groups * g->inner) != 0) return FW_ERR_SHAPE;
+    if (any_misaligned({x, g->gate, g->residual, g->scale, g->weight, g->bias})) return FW_ERR_ALIGN;
+    if (!(std::isfinite(g->eps) && g->eps >= 0.f)) return FW_ERR_ARG;
+    if ((g->rms | g->gate_after) & ~1) return FW_ERR_MODE;
+    *in = GatedIn{x, g->gate, g->residual, g->residual ? g->scale : nullptr, g->weight, g->bias, rows, (int)width,
+                  (int)g->groups, (int)g->inner, dtype, g->eps, g->rms, g->gate_after};
+    return FW_OK;
+}
+
+// Does a row output overlap a row input without being it?
+bool part_of(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins, size_t n) {
+    for (const void *o : outs)
+        for (const void *i : ins)
+            if (o != i && overlaps(o, n, i, n)) return true;
+    return false;
+}
+
+}  // namespace
+
+extern "C" int fw_gated_norm(const void *x, const fw_gated *args, void *y, void *total, float *mean,
+                             float *rstd, int64_t rows, int64_t width, fw_dtype dtype,
+                             cudaStream_t stream) {
+    GatedArgs a{};
+    int st = gated_in(x, args, rows, width, dtype, &a.in);
+    if (st != FW_OK) return st;
+    if (!y) return FW_ERR_NULL;
+    if (any_misaligned({y, total, mean, rstd})) return FW_ERR_ALIGN;
+    const size_t n = (size_t)rows * width * bytes_of(dtype), nr = (size_t)rows * 4,
+                 np = (size_t)args->groups * width * 4;
+    const GatedIn &in = a.in;
+    if (outputs_clash({{y, n}, {total, n}, {mean, nr}, {rstd, nr}},
+                      {{in.weight, np}, {in.bias, np}, {in.scale, np}}) ||
+        outputs_clash({{mean, nr}, {rstd, nr}}, {{x, n}, {in.gate, n}, {in.residual, n}}) ||
+        part_of({y, total}, {x, in.gate, in.residual}, n))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    a.y = y; a.total = total; a.mean = mean; a.rstd = rstd;
+    const cudaError_t e = launch_gated_norm(a, stream);
+    return e == cudaSuccess ? FW_OK : cuda_fail(e);
+}
+
+extern "C" int64_t fw_gated_norm_workspace(int64_t rows, int64_t width, int64_t groups, fw_dtype dtype) {
+    const int st = check_gated(rows, width, groups, dtype);
+    return st != FW_OK ? st : (int64_t)gated_norm_workspace(rows, width, groups, dtype);
+}
+
+extern "C" int fw_gated_norm_backward(const void *dy, const void *dtotal, const void *x,
+                                      const fw_gated *args, const float *mean, const float *rstd,
+                                      void *dx, void *dgate, void *dresidual, float *dweight,
+                                      float *dbias, float *dscale, int64_t rows, int64_t width,
+                                      fw_dtype dtype, void *workspace, int64_t workspace_bytes,
+                                      cudaStream_t stream) {
+    GatedBwdArgs a{};
+    int st = gated_in(x, args, rows, width, dtype, &a.in);
+    if (st != FW_OK) return st;
+    const GatedIn &in = a.in;
+    if (!dy || !rstd || (!mean && !in.rms)) return FW_ERR_NULL;
+    if ((dgate && !in.gate) || ((dresidual || dscale) && !in.residual)) return FW_ERR_ARG;
+    if (any_misaligned({dy, dtotal, mean, rstd, dx, dgate, dresidual, dweight, dbias, dscale, workspace}))
+        return FW_ERR_ALIGN;
+    const bool sums = dweight || dbias || dscale;
+    const int64_t need = sums ? fw_gated_norm_workspace(rows, width, args->groups, dtype) : 0;
+    if (sums && !workspace) return FW_ERR_NULL;
+    if (workspace_bytes < need) return FW_ERR_SCRATCH;
+    const size_t n = (size_t)rows * width * bytes_of(dtype), nr = (size_t)rows * 4,
+                 np = (size_t)args->groups * width * 4;
+    const Span ws{workspace, (size_t)need};
+    if (outputs_clash({{dx, n}, {dgate, n}, {dresidual, n}, {dweight, np}, {dbias, np}, {dscale, np}, ws},
+                      {{in.weight, np}, {in.bias, np}, {in.scale, np}, {mean, nr}, {rstd, nr}}) ||
+        outputs_clash({{dweight, np}, {dbias, np}, {dscale, np}, ws},
+                      {{dy, n}, {dtotal, n}, {x, n}, {in.gate, n}, {in.residual, n}}) ||
+        part_of({dx, dgate, dresidual}, {dy, dtotal, x, in.gate, in.residual}, n))
+        return FW_ERR_ARG;
+    int *err = nullptr;
+    if ((st = device_setup(&err)) != FW_OK) return st;
+    a.dy = dy; a.dtotal = dtotal; a.mean = mean; a.rstd = rstd;
+    a.dx = dx; a.dgate = dgate; a.dresidual = dresidual;
+    a.dweight = dweight; a.dbias = dbias; a.dscale = dscale;
+    a.ws = sums ? static_cast<float *>(workspace) : nullptr;
+    const cudaError_t e = launch_gated_norm_backward(a, stream);
     return e == cudaSuccess ? FW_OK : cuda_fail(e);
 }
 

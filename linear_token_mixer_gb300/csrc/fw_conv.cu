@@ -1,0 +1,470 @@
+// fw_conv.cu -- short causal convolution of every channel, W = 2 .. 8 taps, before a mixer:
+//     a_t = b + sum_w weight[w] x_{t-W+1+w},   y_t = a_t or a_t / (1 + exp(-a_t)),
+// its gradients and its form for one token.  Rows before the first come from a carried state.
+//
+// All three are bound by their rows' bytes.  A thread holds V channels (16 bytes of a row; 8 in the
+// backward pass, which keeps five such rows' worth of registers) and walks a strip of
+// tokens with the last W - 1 rows in registers, so that each row is read once but for the W - 1 rows
+// before a strip.  Rows come kAhead at a time, the next ones in flight while these are worked on.
+// The backward pass forms a_t again, walks W - 1 tokens past its strip, and writes
+//     da_t = dy_t act'(a_t),   dx_{t-W+1} = sum_w weight[w] da_{t-w}
+// as t passes; dweight[w] += da_t x_{t-W+1+w} and dbias += da_t stay in registers over all strips
+// of a thread, are added up in a block, and a second kernel adds the blocks' in a fixed order.
+#include "fw_conv.cuh"
+
+namespace fw {
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kAhead = 4;                     // rows a load turn
+constexpr int kStrip = 64;                    // most tokens of a strip
+constexpr int kStripMin = 8;                  // no fewer: only the first strip reads the state (W - 1 <= 7)
+
+// V channels of a row: as they are stored, and as pairs of fp32.
+template <typename T, int V> struct Raw;
+template <> struct Raw<float, 1> { float v; };
+template <> struct Raw<float, 4> { float4 v; };
+template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 v; };
+template <> struct Raw<__nv_bfloat16, 2> { uint32_t v; };
+template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
+template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
+
+template <int V> struct Chan {
+    static constexpr int N = (V + 1) / 2;
+    uint64_t p[N];                            // (V = 1: the low half)
+};
+
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t x) {
+    return pair(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pair_bf16(uint64_t x) {
+    const float2 f = halves(x);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ Chan<1> widen(const Raw<float, 1> &r) { return {{pair(r.v, 0.f)}}; }
+__device__ __forceinline__ Chan<4> widen(const Raw<float, 4> &r) { return {{pair(r.v.x, r.v.y), pair(r.v.z, r.v.w)}}; }
+__device__ __forceinline__ Chan<1> widen(const Raw<__nv_bfloat16, 1> &r) { return {{pair(__bfloat162float(r.v), 0.f)}}; }
+__device__ __forceinline__ Chan<2> widen(const Raw<__nv_bfloat16, 2> &r) { return {{bf16_pair(r.v)}}; }
+__device__ __forceinline__ Chan<4> widen(const Raw<__nv_bfloat16, 4> &r) { return {{bf16_pair(r.v.x), bf16_pair(r.v.y)}}; }
+__device__ __forceinline__ Chan<8> widen(const Raw<__nv_bfloat16, 8> &r) {
+    return {{bf16_pair(r.v.x), bf16_pair(r.v.y), bf16_pair(r.v.z), bf16_pair(r.v.w)}};
+}
+
+__device__ __forceinline__ void narrow(Raw<float, 1> &r, const Chan<1> &c) { r.v = halves(c.p[0]).x; }
+__device__ __forceinline__ void narrow(Raw<float, 4> &r, const Chan<4> &c) {
+    const float2 a = halves(c.p[0]), b = halves(c.p[1]);
+    r.v = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 1> &r, const Chan<1> &c) { r.v = __float2bfloat16_rn(halves(c.p[0]).x); }
+__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 2> &r, const Chan<2> &c) { r.v = pair_bf16(c.p[0]); }
+__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 4> &r, const Chan<4> &c) {
+    r.v = make_uint2(pair_bf16(c.p[0]), pair_bf16(c.p[1]));
+}
+__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 8> &r, const Chan<8> &c) {
+    r.v = make_uint4(pair_bf16(c.p[0]), pair_bf16(c.p[1]), pair_bf16(c.p[2]), pair_bf16(c.p[3]));
+}
+
+template <typename T, int V> __device__ __forceinline__ Raw<T, V> load(const T *p) {
+    return *reinterpret_cast<const Raw<T, V> *>(p);
+}
+template <typename T, int V> __device__ __forceinline__ void store(T *p, const Chan<V> &c) {
+    Raw<T, V> r;
+    narrow(r, c);
+    *reinterpret_cast<Raw<T, V> *>(p) = r;
+}
+template <int V> __device__ __forceinline__ Chan<V> none() {
+    Chan<V> c;
+#pragma unroll
+    for (int i = 0; i < Chan<V>::N; ++i) c.p[i] = 0;
+    return c;
+}
+template <int V> __device__ __forceinline__ void fma_to(Chan<V> &acc, const Chan<V> &a, const Chan<V> &b) {
+#pragma unroll
+    for (int i = 0; i < Chan<V>::N; ++i) acc.p[i] = fma2(a.p[i], b.p[i], acc.p[i]);
+}
+
+// 1 / (1 + exp(-a)): for bf16 rows by the fast exponential and reciprocal (a few ulp of fp32, a
+// thousandth of the rows' rounding).
+template <typename T> __device__ __forceinline__ float sigmoid(float a) {
+    if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-a));
+    else return __frcp_rn(1.f + __expf(-a));
+}
+template <typename T, int V> __device__ __forceinline__ Chan<V> silu(const Chan<V> &a) {
+    Chan<V> y;
+#pragma unroll
+    for (int i = 0; i < Chan<V>::N; ++i) {
+        const float2 f = halves(a.p[i]);
+        y.p[i] = mul2(a.p[i], pair(sigmoid<T>(f.x), V > 1 ? sigmoid<T>(f.y) : 0.f));
+    }
+    return y;
+}
+// dy silu'(a) = dy s (1 + a (1 - s)), s = sigmoid(a)
+template <typename T, int V> __device__ __forceinline__ Chan<V> silu_grad(const Chan<V> &a, const Chan<V> &dy) {
+    Chan<V> r;
+#pragma unroll
+    for (int i = 0; i < Chan<V>::N; ++i) {
+        const float2 f = halves(a.p[i]);
+        const uint64_t s = pair(sigmoid<T>(f.x), V > 1 ? sigmoid<T>(f.y) : 0.f);
+        const uint64_t one = pair(1.f, 1.f), q = fma2(s, pair(-1.f, -1.f), one);
+        r.p[i] = mul2(mul2(dy.p[i], s), fma2(a.p[i], q, one));
+    }
+    return r;
+}
+
+// The taps of V channels; element (channel, tap) at w[channel * W + tap].
+template <int W, int V> __device__ __forceinline__ void load_taps(Chan<V> (&w)[W], const float *p) {
+    float f[V * W];
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V * W; i += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p + i);
+            f[i] = q.x; f[i + 1] = q.y; f[i + 2] = q.z; f[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; ++i) f[i] = p[i];
+    }
+#pragma unroll
+    for (int t = 0; t < W; ++t)
+#pragma unroll
+        for (int i = 0; i < Chan<V>::N; ++i) w[t].p[i] = pair(f[2 * i * W + t], V > 1 ? f[(2 * i + 1) * W + t] : 0.f);
+}
+template <int V> __device__ __forceinline__ Chan<V> load_bias(const float *p) {
+    Chan<V> b = none<V>();
+    if (p)
+#pragma unroll
+        for (int i = 0; i < Chan<V>::N; ++i) b.p[i] = pair(p[2 * i], V > 1 ? p[2 * i + 1] : 0.f);
+    return b;
+}
+
+// Rows `t` of a chain, or of the state before it (t < 0); zero without a state.
+template <typename T, int V>
+__device__ __forceinline__ Chan<V> row_at(const T *x, const T *state, int64_t t, int W, int d) {
+    if (t >= 0) return widen(load<T, V>(x + t * d));
+    return state ? widen(load<T, V>(state + (t + W - 1) * d)) : none<V>();
+}
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kBlock) conv_kernel(ConvArgs a, uint32_t strip, uint32_t strips, uint32_t cols) {
+    const uint32_t id = blockIdx.x * (uint32_t)kBlock + threadIdx.x;
+    const uint32_t s = id / cols, cv = id % cols, st = s % strips;
+    const int64_t chain = s / strips;
+    if (chain >= a.n_chains) return;
+    const int d = a.d, h = (int)(chain % a.H), c0 = (int)cv * V;
+    const int64_t n = chain_len(a.lens, chain, a.H, a.T);
+    const int64_t t0 = (int64_t)st * strip, t1 = t0 + strip < a.T ? t0 + strip : a.T;
+    const T *const x = static_cast<const T *>(a.x) + chain * a.T * d + c0;
+    const T *const state = a.state ? static_cast<const T *>(a.state) + chain * (W - 1) * d + c0 : nullptr;
+    T *const y = static_cast<T *>(a.y) + chain * a.T * d + c0;
+    const int64_t end = t1 < n ? t1 : n;
+    Chan<V> win[W - 1 + kAhead];
+    if (t0 < end || st == 0) {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) win[i] = row_at<T, V>(x, state, t0 + i - (W - 1), W, d);
+    }
+    if (st == 0 && a.state_out) {             // the last W - 1 of the state's rows and the chain's
+        T *const so = static_cast<T *>(a.state_out) + chain * (W - 1) * d + c0;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {     // (a row of the state is already in win: state_out may be state)
+            const int64_t t = n + i - (W - 1);
+            Chan<V> r = none<V>();
+            if (t >= 0) r = widen(load<T, V>(x + t * d));
+            else
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+                    if (j == t + W - 1) r = win[j];
+            store<T, V>(so + (int64_t)i * d, r);
+        }
+    }
+    if (t0 < end) {
+        Chan<V> w[W];
+        load_taps<W, V>(w, a.weight + ((int64_t)h * d + c0) * W);
+        const Chan<V> bias = load_bias<V>(a.bias ? a.bias + (int64_t)h * d + c0 : nullptr);
+        Raw<T, V> next[kAhead];
+        auto fetch = [&](int64_t t) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (t + u < end) next[u] = load<T, V>(x + (t + u) * d);
+        };
+        fetch(t0);
+#pragma unroll 1
+        for (int64_t t = t0; t < end; t += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) win[W - 1 + u] = widen(next[u]);
+            if (t + kAhead < end) fetch(t + kAhead);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                Chan<V> r = bias;
+#pragma unroll
+                for (int i = 0; i < W; ++i) fma_to(r, w[i], win[u + i]);
+                if (a.silu) r = silu<T, V>(r);
+                if (t + u < end) store<T, V>(y + (t + u) * d, r);
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) win[i] = win[i + kAhead];
+        }
+    }
+    if (a.zero_rest)
+        for (int64_t t = t0 > n ? t0 : n; t < t1; ++t) store<T, V>(y + t * d, none<V>());
+}
+
+// `lanes` (a power of two) of a warp hold the columns of a row, the 32 / lanes parts of it take
+// strips of their own.  blockIdx.y: a head's group of columns; blockIdx.x: a share of the head's strips.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kBlock)
+conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint32_t groups) {
+    constexpr int NW = kBlock / 32;
+    __shared__ float part[NW][32][V * (W + 1)];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cl = lane & (lanes - 1);
+    const int h = (int)(blockIdx.y / groups), d = a.d;
+    const int c0 = ((int)(blockIdx.y % groups) * lanes + cl) * V;
+    const bool mine = c0 < d;
+    Chan<V> w[W], dw[W], db = none<V>();
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = dw[i] = none<V>();
+    Chan<V> bias = none<V>();
+    if (mine) {
+        load_taps<W, V>(w, a.weight + ((int64_t)h * d + c0) * W);
+        bias = load_bias<V>(a.bias ? a.bias + (int64_t)h * d + c0 : nullptr);
+    }
+    const uint32_t parts = 32u / lanes, step = gridDim.x * NW * parts;
+    const uint32_t total = (uint32_t)a.B * strips;
+    for (uint32_t m = (blockIdx.x * NW + warp) * parts + lane / lanes; mine && m < total; m += step) {
+        const uint32_t b = m / strips, st = m % strips;
+        const int64_t chain = (int64_t)b * a.H + h;
+        const int64_t n = chain_len(a.lens, chain, a.H, a.T);
+        const int64_t t0 = (int64_t)st * strip, t1 = t0 + strip < a.T ? t0 + strip : a.T;
+        const int64_t end = t1 < n ? t1 : n;
+        const int64_t at = chain * a.T * d + c0, sat = chain * (W - 1) * d + c0;
+        const T *const x = static_cast<const T *>(a.x) + at, *const dy = static_cast<const T *>(a.dy) + at;
+        const T *const state = a.state ? static_cast<const T *>(a.state) + sat : nullptr;
+        const T *const dso = a.dstate_out ? static_cast<const T *>(a.dstate_out) + sat : nullptr;
+        T *const dx = static_cast<T *>(a.dx) + at, *const ds = a.dstate ? static_cast<T *>(a.dstate) + sat : nullptr;
+        if (a.zero_rest)
+            for (int64_t t = t0 > n ? t0 : n; t < t1; ++t) store<T, V>(dx + t * d, none<V>());
+        if (!(t0 < end || (st == 0 && ds))) continue;
+        Chan<V> win[W - 1 + kAhead], da[W - 1 + kAhead];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            win[i] = row_at<T, V>(x, state, t0 + i - (W - 1), W, d);
+            da[i] = none<V>();
+        }
+        Raw<T, V> nx[kAhead], ny[kAhead];
+        auto fetch = [&](int64_t t) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (t + u < n) {
+                    nx[u] = load<T, V>(x + (t + u) * d);
+                    ny[u] = load<T, V>(dy + (t + u) * d);
+                }
+        };
+        fetch(t0);
+        const int64_t stop = (end > t0 ? end : t0) + W - 1;      // rows up to end - 1 leave at t = end + W - 2
+#pragma unroll 1
+        for (int64_t t = t0; t < stop; t += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const bool on = t + u < n;
+                win[W - 1 + u] = on ? widen(nx[u]) : none<V>();
+                da[W - 1 + u] = on ? widen(ny[u]) : none<V>();
+            }
+            if (t + kAhead < stop) fetch(t + kAhead);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (a.silu) {
+                    Chan<V> r = bias;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) fma_to(r, w[i], win[u + i]);
+                    if (t + u < n) da[W - 1 + u] = silu_grad<T, V>(r, da[W - 1 + u]);
+                }
+                if (t + u < end) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) fma_to(dw[i], da[W - 1 + u], win[u + i]);
+#pragma unroll
+                    for (int i = 0; i < Chan<V>::N; ++i) db.p[i] = add2(db.p[i], da[W - 1 + u].p[i]);
+                }
+                const int64_t s = t + u - (W - 1);               // the row that leaves
+                Chan<V> r = none<V>();
+#pragma unroll
+                for (int i = 0; i < W; ++i) fma_to(r, w[i], da[W - 1 + u - i]);
+                const int64_t q = s - n + W - 1;                 // its place in the state behind the chain
+                if (dso && q >= 0 && q < W - 1 && s < end) {
+                    const Chan<V> e = widen(load<T, V>(dso + q * d));
+#pragma unroll
+                    for (int i = 0; i < Chan<V>::N; ++i) r.p[i] = add2(r.p[i], e.p[i]);
+                }
+                if (s >= t0) {
+                    if (s < end) store<T, V>(dx + s * d, r);
+                } else if (st == 0 && ds && s < 0 && s >= -(W - 1)) {
+                    store<T, V>(ds + (s + W - 1) * d, r);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                win[i] = win[i + kAhead];
+                da[i] = da[i + kAhead];
+            }
+        }
+    }
+    if (!a.ws) return;
+    // the parts of the warp, then the warps of the block
+#pragma unroll
+    for (int i = 0; i <= W; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float2 f = halves(i < W ? dw[i].p[e / 2] : db.p[e / 2]);
+            float z = e & 1 ? f.y : f.x;
+            for (int o = lanes; o < 32; o <<= 1) z += __shfl_xor_sync(~0u, z, o);
+            part[warp][lane][e * (W + 1) + i] = z;
+        }
+    __syncthreads();
+    const int used = lanes * V * (W + 1);
+    for (int i = threadIdx.x; i < used; i += kBlock) {
+        const int l = i / (V * (W + 1)), e = i % (V * (W + 1));
+        float z = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) z += part[k][l][e];
+        const int c = ((int)(blockIdx.y % groups) * lanes + l) * V + e / (W + 1);
+        if (c < d) a.ws[((int64_t)blockIdx.x * a.H + h) * d * (W + 1) + (int64_t)c * (W + 1) + e % (W + 1)] = z;
+    }
+}
+
+// The sums of the blocks, in their order.
+__global__ void __launch_bounds__(kBlock)
+conv_sum_kernel(const float *ws, int slices, int64_t count, int W, float *dweight, float *dbias) {
+    wait_previous_grid();
+    const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    if (i >= count) return;
+    float z = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < slices; ++s) z += ws[s * count + i];
+    const int64_t c = i / (W + 1);
+    const int e = (int)(i % (W + 1));
+    if (e == W) {
+        if (dbias) dbias[c] = z;
+    } else if (dweight) {
+        dweight[c * W + e] = z;
+    }
+}
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kBlock) conv_step_kernel(ConvStepArgs a, uint32_t cols) {
+    const uint32_t id = blockIdx.x * (uint32_t)kBlock + threadIdx.x;
+    const int64_t chain = id / cols;
+    if (chain >= a.n_states) return;
+    const int d = a.d, h = (int)(chain % a.H), c0 = (int)(id % cols) * V;
+    T *const state = static_cast<T *>(a.state) + chain * (W - 1) * d + c0;
+    Raw<T, V> row[W];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) row[i] = load<T, V>(state + (int64_t)i * d);
+    row[W - 1] = load<T, V>(static_cast<const T *>(a.x) + chain * d + c0);
+    Chan<V> w[W];
+    load_taps<W, V>(w, a.weight + ((int64_t)h * d + c0) * W);
+    Chan<V> r = load_bias<V>(a.bias ? a.bias + (int64_t)h * d + c0 : nullptr);
+#pragma unroll
+    for (int i = 0; i < W; ++i) fma_to(r, w[i], widen(row[i]));
+    if (a.silu) r = silu<T, V>(r);
+    store<T, V>(static_cast<T *>(a.y) + chain * d + c0, r);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) *reinterpret_cast<Raw<T, V> *>(state + (int64_t)i * d) = row[i + 1];
+}
+
+// Tokens of a strip: long ones read fewer rows twice, short ones make more threads.  The longest that
+// leaves every SM `threads` of them, within kStripMin .. kStrip.
+uint32_t strip_of(int64_t columns, int64_t T, int64_t threads) {
+    int64_t s = columns * T / (kSMs * threads);
+    s = s < kStripMin ? kStripMin : s > kStrip ? kStrip : s;
+    return (uint32_t)((s + kAhead - 1) / kAhead * kAhead);
+}
+
+// Blocks of the backward pass that share a group of a head's columns: three an SM in all, and no more
+// than there are strips for.
+struct BwdShape {
+    int lanes;
+    uint32_t groups, strip, strips, slices;
+};
+BwdShape bwd_shape(int64_t B, int H, int64_t T, int d, int V) {
+    BwdShape r;
+    const int cols = (d + V - 1) / V;
+    r.lanes = 1;
+    while (r.lanes < 32 && r.lanes < cols) r.lanes *= 2;
+    r.groups = (uint32_t)((cols + r.lanes - 1) / r.lanes);
+    r.strip = strip_of(B * H * cols, T, 512);
+    r.strips = (uint32_t)((T + r.strip - 1) / r.strip);
+    const int64_t y = (int64_t)H * r.groups, per = (kBlock / 32) * (32 / r.lanes);
+    int64_t s = 3 * kSMs / y;
+    const int64_t most = (B * r.strips + per - 1) / per;
+    s = s < 1 ? 1 : s > most ? most : s;
+    r.slices = (uint32_t)s;
+    return r;
+}
+
+int bwd_vector(int d) { return d % 4 == 0 ? 4 : 1; }
+
+template <typename T, int V, int W> cudaError_t run(const ConvArgs &a, cudaStream_t s) {
+    const int64_t cols = a.d / V;
+    const uint32_t strip = strip_of(a.n_chains * cols, a.T, 1024), strips = (uint32_t)((a.T + strip - 1) / strip);
+    const int64_t n = a.n_chains * strips * cols;
+    conv_kernel<T, V, W><<<(unsigned)((n + kBlock - 1) / kBlock), kBlock, 0, s>>>(a, strip, strips, (uint32_t)cols);
+    return cudaGetLastError();
+}
+
+template <typename T, int V, int W> cudaError_t run(const ConvBwdArgs &a, cudaStream_t s) {
+    const BwdShape p = bwd_shape(a.B, a.H, a.T, a.d, V);
+    conv_bwd_kernel<T, V, W><<<dim3(p.slices, a.H * p.groups), kBlock, 0, s>>>(a, p.strip, p.strips, p.lanes, p.groups);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.ws) return e;
+    const int64_t count = (int64_t)a.H * a.d * (W + 1);
+    return launch_after(conv_sum_kernel, dim3((unsigned)((count + kBlock - 1) / kBlock)), kBlock, 0, s, true,
+                        (const float *)a.ws, (int)p.slices, count, W, a.dweight, a.dbias);
+}
+
+template <typename T, int V, int W> cudaError_t run(const ConvStepArgs &a, cudaStream_t s) {
+    const int64_t cols = a.d / V, n = a.n_states * cols;
+    conv_step_kernel<T, V, W><<<(unsigned)((n + kBlock - 1) / kBlock), kBlock, 0, s>>>(a, (uint32_t)cols);
+    return cudaGetLastError();
+}
+
+template <typename T, int V, typename A> cudaError_t by_taps(const A &a, cudaStream_t s) {
+    switch (a.W) {
+    case 2: return run<T, V, 2>(a, s);
+    case 3: return run<T, V, 3>(a, s);
+    case 4: return run<T, V, 4>(a, s);
+    case 5: return run<T, V, 5>(a, s);
+    case 6: return run<T, V, 6>(a, s);
+    case 7: return run<T, V, 7>(a, s);
+    default: return run<T, V, 8>(a, s);
+    }
+}
+
+// 16 bytes of a row a thread where rows are whole multiples of that, else 4 (bf16 of even d), else an element.
+template <typename A> cudaError_t by_type(const A &a, cudaStream_t s) {
+    if (a.dtype == FW_F32) return a.d % 4 == 0 ? by_taps<float, 4>(a, s) : by_taps<float, 1>(a, s);
+    if (a.d % 8 == 0) return by_taps<__nv_bfloat16, 8>(a, s);
+    return a.d % 2 == 0 ? by_taps<__nv_bfloat16, 2>(a, s) : by_taps<__nv_bfloat16, 1>(a, s);
+}
+
+}  // namespace
+
+bool conv_fits(int64_t B, int64_t H, int64_t T, int64_t d) {
+    // threads of a call at the shortest strips and one channel each, and the backward grid's second axis
+    const int64_t strips = (T + kStripMin - 1) / kStripMin;
+    return T <= INT32_MAX && d <= (1 << 24) && H * ((d + 31) / 32) <= 65535 && B * H <= INT32_MAX / d &&
+           B * H * d <= INT32_MAX / strips;
+}
+
+size_t conv_workspace(int64_t B, int H, int64_t T, int d, int W) {
+    return (size_t)bwd_shape(B, H, T, d, bwd_vector(d)).slices * H * d * (W + 1) * sizeof(float);
+}
+
+cudaError_t launch_conv(const ConvArgs &a, cudaStream_t s) { return by_type(a, s); }
+cudaError_t launch_conv_step(const ConvStepArgs &a, cudaStream_t s) { return by_type(a, s); }
+cudaError_t launch_conv_backward(const ConvBwdArgs &a, cudaStream_t s) {
+    const bool four = bwd_vector(a.d) == 4;
+    if (a.dtype == FW_F32) return four ? by_taps<float, 4>(a, s) : by_taps<float, 1>(a, s);
+    return four ? by_taps<__nv_bfloat16, 4>(a, s) : by_taps<__nv_bfloat16, 1>(a, s);
+}
+
+}  // namespace fw

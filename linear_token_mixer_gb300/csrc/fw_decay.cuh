@@ -66,6 +66,18 @@ struct NormArgs {
     float eps;
 };
 
+// Steps and decays of a selective scan (see fw_select.cuh), formed ahead of it for chunks of the scan's own
+// length; n_chunks of them a chain, tokens behind a sequence's end without a step.
+struct SelectTables {
+    const float2 *c;          // [n_chains][n_chunks * C] log decay from the chunk's start to the token, in two terms
+    const float *dt;          // .. the token's step
+    const float *w;           // .. dt times the decay from the token to the chunk's end
+    const float4 *chunk;      // [n_chains][n_chunks] decay of the chunk, its log in two terms, 1 where it is mild
+    const float *skip;        // [H] or NULL
+    int64_t n_chunks;
+    int G;                    // groups of heads that share a and b
+};
+
 struct ScanArgs {
     const void *a, *b, *c;    // [n_chains][T][d]
     const float *log_decay;   // [H], chain % H
@@ -85,6 +97,7 @@ struct ScanArgs {
     int *err;
     long long wait_ns;
     int force_timeout;
+    SelectTables sel;         // selective scans only
 };
 
 struct DecayStepArgs {
@@ -164,6 +177,17 @@ __device__ __forceinline__ float decay_pow(float log_g, float n) {
     const float e = fmaf(n, log_g, -x);
     const float p = expf(x);
     return isfinite(p) ? fmaf(p, e, p) : p;   // overflow and NaN as they are
+}
+
+// e^(hi + lo), lo small.
+__device__ __forceinline__ float exp_two(float hi, float lo) {
+    const float p = expf(hi);
+    return isfinite(p) ? fmaf(p, lo, p) : p;
+}
+
+// The chain of queries and keys of a chain: `G` groups of heads share them.
+__device__ __forceinline__ int64_t group_chain(int64_t chain, int H, int G) {
+    return chain / H * G + chain % H / (H / G);
 }
 
 // Tokens of a chain: T, or the batch row's length clamped to [0, T].

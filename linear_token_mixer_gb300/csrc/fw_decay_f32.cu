@@ -20,6 +20,7 @@
 // cycles, its tensor pipe is busy for 39 %, and its sixteen warps an SM wait for the states' loads and
 // for each other's MMAs.
 #include "fw_decay_tc.cuh"
+#include "fw_select.cuh"
 #include "fw_sm100.cuh"
 
 namespace fw {
@@ -145,19 +146,26 @@ __device__ __forceinline__ ChunkOf chunk_of(const ScanArgs &s, int64_t nch) {
     return r;
 }
 
-// M_c into the workspace; ONE (chains of one chunk): the final state into X_out.
-template <int D, bool ONE>
+// Where a chunk's rows of a and b begin, given where those of c do.
+template <int D, bool SEL> __device__ __forceinline__ int64_t ab_base(const ScanArgs &s, const ChunkOf &k, int64_t base) {
+    return SEL ? (group_chain(k.chain, s.H, s.sel.G) * s.T + k.chunk * C) * D : base;
+}
+
+// M_c into the workspace; ONE (chains of one chunk): the final state into X_out.  SEL here and below: a
+// selective scan, whose weights and decays come from its tables.
+template <int D, bool ONE, bool SEL>
 __device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, float4 *smem4) {
     constexpr int LD = ld_col<D>();
     float *sB = reinterpret_cast<float *>(smem4), *sC = sB + C * LD, *w = sC + C * LD;
-    const float lg = s.log_decay[k.chain % s.H];
+    const float lg = SEL ? 0.f : s.log_decay[k.chain % s.H];
     if (threadIdx.x < C) {
         const int j = threadIdx.x;
-        w[j] = s.in_scale * decay_pow(lg, (float)(s.rev ? j + 1 : max(k.nv - 1 - j, 0)));
+        w[j] = SEL ? s.sel.w[(k.chain * s.sel.n_chunks + k.chunk) * C + j]
+                   : s.in_scale * decay_pow(lg, (float)(s.rev ? j + 1 : max(k.nv - 1 - j, 0)));
     }
     __syncthreads();
     const int64_t base = (k.chain * s.T + k.chunk * C) * D;
-    load_tile<D, LD>(sB, static_cast<const float *>(s.b) + base, k.nv, w);
+    load_tile<D, LD>(sB, static_cast<const float *>(s.b) + ab_base<D, SEL>(s, k, base), k.nv, w);
     load_tile<D, LD>(sC, static_cast<const float *>(s.c) + base, k.nv, nullptr);
     __syncthreads();
     // D x D over 2 x (D / 32) warps: D / 2 rows of X by 32 columns each, 32 rows at a time
@@ -165,7 +173,7 @@ __device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, 
     const int n0 = (warp >> 1) * 32;
     float *M = ONE ? s.X_out + k.chain * D * D : s.ws + (int64_t)blockIdx.x * D * D;
     const float *X0 = ONE && s.X0 ? s.X0 + k.chain * D * D : nullptr;
-    const float gn = decay_pow(lg, (float)k.nv);
+    const float gn = SEL ? s.sel.chunk[k.chain * s.sel.n_chunks + k.chunk].x : decay_pow(lg, (float)k.nv);
 #pragma unroll 1
     for (int m0 = (warp & 1) * (D / 2), m1 = m0 + D / 2; m0 < m1; m0 += 32) {
         float acc[2][4][4] = {};
@@ -187,22 +195,23 @@ __device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, 
     }
 }
 
-template <int D>
+template <int D, bool SEL>
 __global__ void __launch_bounds__(threads<D>())
 scan_local(const __grid_constant__ Scans all, int64_t nch) {
     extern __shared__ float4 smem4[];
+    if (SEL) wait_previous_grid();                   // the tables; no later grid starts before they are there
     let_next_grid_start();
     const ScanArgs &s = all.s[blockIdx.y];
     const ChunkOf k = chunk_of(s, nch);
     if (k.nv == 0 || (k.last && !s.X_out)) return;   // no later chunk and nobody reads the end
-    local_part<D, false>(s, k, smem4);
+    local_part<D, false, SEL>(s, k, smem4);
 }
 
 constexpr int kPrefix = 128;   // threads of a block
 
 // Four elements of a chain's state a thread, eight chunks read ahead of the recurrence (one element a
 // thread: B4 H8 T2048 d = 128 196 us in all, then 171 us, B2 H8 T1023 d = 64 backward 46 us, then 44 us).
-template <int D>
+template <int D, bool SEL>
 __global__ void __launch_bounds__(kPrefix)
 scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
     const ScanArgs &s = all.s[blockIdx.y];
@@ -219,7 +228,7 @@ scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
     }
     const int64_t n = chain_len(s.lens, chain, s.H, s.T);
     const int used = (int)((n + C - 1) / C);
-    const float lg = s.log_decay[chain % s.H];
+    const float lg = SEL ? 0.f : s.log_decay[chain % s.H];
     const float gC = decay_pow(lg, (float)C), gT = decay_pow(lg, (float)(n - (int64_t)(used - 1) * C));
     // in processing order; the end is nobody's entry, and is left out where it is not asked for
     const int read = s.X_out ? used : used - 1;
@@ -235,7 +244,8 @@ scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
         for (int u = 0; u < U; ++u) {
             if (i0 + u >= used) break;
             M[u * step] = x;
-            const float g = (s.rev ? i0 + u == 0 : i0 + u == used - 1) ? gT : gC;
+            const float g = SEL ? s.sel.chunk[chain * nch + i0 + u].x
+                                : (s.rev ? i0 + u == 0 : i0 + u == used - 1) ? gT : gC;
             x.x = fmaf(g, x.x, m[u].x);
             x.y = fmaf(g, x.y, m[u].y);
             x.z = fmaf(g, x.z, m[u].z);
@@ -247,18 +257,35 @@ scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
 
 // The output rows of a chunk, from the state at X (element (i, j) at X[i * D + j], or
 // X[j * D + i] with `trans`); ONE: known before the launch.
-template <int D, bool ONE>
+template <int D, bool ONE, bool SEL>
 __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, const float *X, const bool trans,
                                          float4 *smem4) {
     constexpr int LR = ld_row<D>(), LC = ld_col<D>(), WN = D / 32, LP = C + 4;
     float *sA = reinterpret_cast<float *>(smem4), *sB = sA + C * LR, *sC = sB + C * LR,
           *pw = sC + C * LC, *red = pw + C + 4;
     int *const first = reinterpret_cast<int *>(red + C * WN);
-    const float lg = s.log_decay[k.chain % s.H];
-    for (int i = threadIdx.x; i <= C; i += threads<D>()) pw[i] = decay_pow(lg, (float)i);
-    const int64_t base = (k.chain * s.T + k.chunk * C) * D;
-    load_tile<D, LR>(sA, static_cast<const float *>(s.a) + base, k.nv, nullptr);
-    load_tile<D, LR>(sB, static_cast<const float *>(s.b) + base, k.nv, nullptr);
+    float2 *const lc = reinterpret_cast<float2 *>((reinterpret_cast<uintptr_t>(first + D) + 7) & ~(uintptr_t)7);
+    if (SEL) {                             // pw: the steps; lc: the logs of the decays
+        const int64_t at = (k.chain * s.sel.n_chunks + k.chunk) * C;
+        for (int i = threadIdx.x; i < C; i += threads<D>()) {
+            pw[i] = s.sel.dt[at + i];
+            lc[i] = s.sel.c[at + i];
+        }
+    } else {
+        const float lg = s.log_decay[k.chain % s.H];
+        for (int i = threadIdx.x; i <= C; i += threads<D>()) pw[i] = decay_pow(lg, (float)i);
+    }
+    // the decay from token j, its step among it, to row r >= j; of the state to row r
+    const auto lag_of = [&](int r, int j) -> float {
+        if (SEL) return pw[j] * exp_two(lc[r].x - lc[j].x, lc[r].y - lc[j].y);
+        return pw[s.rev ? j - r : r - j] * s.in_scale;
+    };
+    const auto entry_of = [&](int r) -> float {
+        return SEL ? exp_two(lc[r].x, lc[r].y) : pw[s.rev ? max(k.nv - 1 - r, 0) : r + 1];
+    };
+    const int64_t base = (k.chain * s.T + k.chunk * C) * D, ab = ab_base<D, SEL>(s, k, base);
+    load_tile<D, LR>(sA, static_cast<const float *>(s.a) + ab, k.nv, nullptr);
+    load_tile<D, LR>(sB, static_cast<const float *>(s.b) + ab, k.nv, nullptr);
     const float *const c = static_cast<const float *>(s.c) + base;
     load_tile<D, LC>(sC, c, k.nv, nullptr);
     __syncthreads();
@@ -279,7 +306,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
                 for (int e = 0; e < 4; ++e) {
                     const int r = m0 + 16 * m + g + 8 * (e >> 1), j = n0 + 8 * n + 2 * t + (e & 1);
                     const int lag = s.rev ? j - r : r - j;
-                    sB[r * LP + j] = lag >= 0 && j < k.nv ? p[m][n][e] * (pw[lag] * s.in_scale) : 0.f;
+                    sB[r * LP + j] = lag >= 0 && j < k.nv ? p[m][n][e] * lag_of(r, j) : 0.f;
                 }
     }
     if (!ONE) wait_previous_grid();        // the states
@@ -298,7 +325,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = m0 + 16 * m + g + 8 * h;
-            const float rd = pw[s.rev ? max(k.nv - 1 - r, 0) : r + 1];
+            const float rd = entry_of(r);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 acc[m][n][2 * h] *= rd;
@@ -347,7 +374,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
 #pragma unroll 1
             for (int i = 0; i < D; ++i)
                 each([&](float &v, int r, int col) { v = fmaf(sA[r * LR + i], trans ? X[col * D + i] : X[i * D + col], v); });
-        each([&](float &v, int r, int) { v *= pw[s.rev ? max(k.nv - 1 - r, 0) : r + 1]; });
+        each([&](float &v, int r, int) { v *= entry_of(r); });
 #pragma unroll 1
         for (int j = 0; j < C; ++j)
             each([&](float &v, int r, int col) { v = fmaf(sB[r * LP + j], sC[j * LC + col], v); });
@@ -355,7 +382,23 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
             v = first[col] <= (s.rev ? C - 1 - r : r) ? __int_as_float(0x7fffffff) : v * s.out_scale;
         });
     }
-    if (s.norm.on) {                       // a row is held by four lanes of each of WN warps
+    if (SEL && s.sel.skip) {               // (from memory: sC may have lost values that are not finite)
+        const float skip = s.sel.skip[k.chain % s.H];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = m0 + 16 * m + g + 8 * h;
+                if (r < k.nv)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float2 f = *reinterpret_cast<const float2 *>(c + (int64_t)r * D + n0 + 8 * n + 2 * t);
+                        acc[m][n][2 * h] = fmaf(skip, f.x, acc[m][n][2 * h]);
+                        acc[m][n][2 * h + 1] = fmaf(skip, f.y, acc[m][n][2 * h + 1]);
+                    }
+            }
+    }
+    if (!SEL && s.norm.on) {               // a row is held by four lanes of each of WN warps
         auto row_sums = [&](float (&z)[2][2]) {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
@@ -421,7 +464,7 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
         }
 }
 
-template <int D>
+template <int D, bool SEL>
 __global__ void __launch_bounds__(threads<D>(), 2)
 scan_out(const __grid_constant__ Scans all, int64_t nch) {
     extern __shared__ float4 smem4[];
@@ -434,53 +477,55 @@ scan_out(const __grid_constant__ Scans all, int64_t nch) {
     }
     const bool trans = blockIdx.y == kSharing;
     const float *ws = trans ? all.s[kSharing - 1].ws : s.ws;
-    out_part<D, false>(s, k, ws + (int64_t)blockIdx.x * D * D, trans, smem4);
+    out_part<D, false, SEL>(s, k, ws + (int64_t)blockIdx.x * D * D, trans, smem4);
 }
 
 // Chains of one chunk: rows (z = 1) and final states (z = 0) at once, or one after the other (one z)
 // where X_out is X0, which the rows read.
-template <int D>
+template <int D, bool SEL>
 __global__ void __launch_bounds__(threads<D>())
 scan_one(const __grid_constant__ Scans all) {
     extern __shared__ float4 smem4[];
     const ScanArgs &s = all.s[blockIdx.y];
     const ChunkOf k = chunk_of(s, 1);
+    if (SEL) wait_previous_grid();         // the tables
     const bool both = gridDim.z == 1;
     if (both || blockIdx.z == 1) {
         if (s.zero_rest) zero_rest<D>(s, k.chain, 0, k.nv);
-        if (k.nv > 0) out_part<D, true>(s, k, s.X0 ? s.X0 + k.chain * D * D : nullptr, s.x0_trans, smem4);
+        if (k.nv > 0) out_part<D, true, SEL>(s, k, s.X0 ? s.X0 + k.chain * D * D : nullptr, s.x0_trans, smem4);
     }
     if (both) __syncthreads();
     if (both || blockIdx.z == 0)
-        if (s.X_out) local_part<D, true>(s, k, smem4);
+        if (s.X_out) local_part<D, true, SEL>(s, k, smem4);
 }
 
-template <int D>
+// `SEL`: behind the launch that forms the tables.
+template <int D, bool SEL>
 cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     const ScanArgs &s = all.s[0];
     const int64_t nch = (s.T + C - 1) / C;
     const dim3 grid((unsigned)(s.n_chains * nch), n);
     constexpr int smem_l = (2 * C * ld_col<D>() + C) * 4;
-    constexpr int smem_o = (2 * C * ld_row<D>() + C * ld_col<D>() + C + 4 + C * (D / 32) + D) * 4;
+    constexpr int smem_o = (2 * C * ld_row<D>() + C * ld_col<D>() + C + 4 + C * (D / 32) + D + (SEL ? 2 * C + 2 : 0)) * 4;
     cudaError_t e;
     if (nch == 1) {
         constexpr int smem = smem_l > smem_o ? smem_l : smem_o;
         static std::atomic<uint64_t> done{0};
-        if ((e = allow_smem(scan_one<D>, smem, done)) != cudaSuccess) return e;
+        if ((e = allow_smem(scan_one<D, SEL>, smem, done)) != cudaSuccess) return e;
         const bool in_place = s.X_out && s.X_out == s.X0;
-        scan_one<D><<<dim3((unsigned)s.n_chains, n, in_place ? 1 : 2), threads<D>(), smem, stream>>>(all);
-        return cudaGetLastError();
+        return launch_after(scan_one<D, SEL>, dim3((unsigned)s.n_chains, n, in_place ? 1 : 2), threads<D>(), smem, stream,
+                            SEL, all);
     }
     static std::atomic<uint64_t> local_done{0}, out_done{0};
-    if ((e = allow_smem(scan_local<D>, smem_l, local_done)) != cudaSuccess) return e;
-    if ((e = allow_smem(scan_out<D>, smem_o, out_done)) != cudaSuccess) return e;
+    if ((e = allow_smem(scan_local<D, SEL>, smem_l, local_done)) != cudaSuccess) return e;
+    if ((e = allow_smem(scan_out<D, SEL>, smem_o, out_done)) != cudaSuccess) return e;
     const int states = n < kSharing ? n : kSharing;
-    if ((e = launch_after(scan_local<D>, dim3(grid.x, states), threads<D>(), smem_l, stream, false, all, nch)) !=
+    if ((e = launch_after(scan_local<D, SEL>, dim3(grid.x, states), threads<D>(), smem_l, stream, SEL, all, nch)) !=
         cudaSuccess)
         return e;
     const dim3 gp((unsigned)(s.n_chains * (D * D / 4 / kPrefix)), states);
-    if ((e = launch_after(scan_prefix<D>, gp, kPrefix, 0, stream, true, all, nch)) != cudaSuccess) return e;
-    return launch_after(scan_out<D>, grid, threads<D>(), smem_o, stream, true, all, nch);
+    if ((e = launch_after(scan_prefix<D, SEL>, gp, kPrefix, 0, stream, true, all, nch)) != cudaSuccess) return e;
+    return launch_after(scan_out<D, SEL>, grid, threads<D>(), smem_o, stream, true, all, nch);
 }
 
 }  // namespace
@@ -501,7 +546,16 @@ cudaError_t launch_scans(ScanArgs *s, int n, cudaStream_t stream) {
     if (n > 1 && s[0].ws) s[1].ws = s[0].ws + state_bytes(s->n_chains, s->T, s->d) / sizeof(float);   // (the third: none)
     Scans all{};
     for (int i = 0; i < n; ++i) all.s[i] = s[i];
-    return s[0].d == 64 ? launch<64>(all, n, stream) : launch<128>(all, n, stream);
+    return s[0].d == 64 ? launch<64, false>(all, n, stream) : launch<128, false>(all, n, stream);
+}
+
+// A selective scan; its tables are formed by the launch before it.
+int select_chunk_f32() { return C; }
+size_t select_states_f32(int64_t n_chains, int64_t T, int d) { return T <= C ? 0 : state_bytes(n_chains, T, d); }
+cudaError_t launch_select_f32(const ScanArgs &s, cudaStream_t stream) {
+    Scans all{};
+    all.s[0] = s;
+    return s.d == 64 ? launch<64, true>(all, 1, stream) : launch<128, true>(all, 1, stream);
 }
 
 }  // namespace fw

@@ -1,0 +1,178 @@
+// fw_select.cu -- selective scan: the steps and decays of a prompt, and its form for one token.
+//
+//     dt_t = softplus(dt_raw_t + dt_bias),  g_t = exp(log_decay dt_t),
+//     S_t = g_t S_{t-1} + dt_t k_t v_t^T,   o_t = scale S_t^T q_t + skip v_t
+//
+// A prompt is the chunked scan of fw_decay_tc.cu (bf16) or fw_decay_f32.cu (fp32) with tables in place of
+// powers of one decay: select_tables forms, for every chunk of a chain, the running sum of log g to each
+// token in 64 bits (kept in two fp32 terms: differences of sums of a chunk lose nothing to their size),
+// each token's weight in the chunk's end, and the chunk's decay.  One warp a chunk, 20 bytes a token
+// written for the 4 d (bf16) or 8 d that its rows take; the scan's first tiles load meanwhile.
+//
+// One token: one block a state, the state once through registers, as decay_step_kernel.
+#include "fw_select.cuh"
+
+namespace fw {
+namespace {
+
+constexpr int kTableBlock = 128;
+
+template <int C>
+__global__ void __launch_bounds__(kTableBlock)
+select_tables(GateArgs g, const int32_t *lens, int64_t n_chains, int64_t T, int H, float2 *out_c, float *out_dt,
+              float *out_w, float4 *out_chunk, int64_t n_chunks) {
+    constexpr int PER = C / 32;               // tokens of a lane
+    let_next_grid_start();
+    const int lane = threadIdx.x & 31;
+    const int64_t id = (int64_t)blockIdx.x * (kTableBlock / 32) + (threadIdx.x >> 5);
+    if (id >= n_chains * n_chunks) return;
+    const int64_t chain = id / n_chunks, first = id % n_chunks * C + lane * PER;
+    const int64_t n = chain_len(lens, chain, H, T);
+    const int h = (int)(chain % H);
+    const float rate = g.log_decay[h];
+    float dt[PER];
+    double c[PER];
+    double sum = 0.0, low = 0.0, high = 0.0;  // of the logs, and their least and largest running sum
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const bool on = first + e < n;
+        dt[e] = on ? step_of(g, chain * T + first + e, h) : 0.f;
+        const double x = on ? (double)rate * dt[e] : 0.0;
+        sum += x < -kReset ? -kReset : x;     // (NaN stays)
+        c[e] = sum;
+    }
+    double upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += x;
+    }
+    const double total = __shfl_sync(~0u, upto, 31), before = upto - sum;
+    const int64_t at = id * C + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        c[e] += before;
+        low = fmin(low, c[e]);
+        high = fmax(high, c[e]);
+        const double s = total - c[e];
+        const float hi = (float)c[e], sh = (float)s;
+        out_c[at + e] = make_float2(hi, (float)(c[e] - hi));
+        out_dt[at + e] = dt[e];
+        out_w[at + e] = dt[e] * exp_two(sh, (float)(s - sh));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        low = fmin(low, __shfl_xor_sync(~0u, low, o));
+        high = fmax(high, __shfl_xor_sync(~0u, high, o));
+    }
+    if (lane == 0) {
+        const float hi = (float)total;
+        out_chunk[id] = make_float4(exp_two(hi, (float)(total - hi)), hi, (float)(total - hi),
+                                    low >= -24.0 && high <= 24.0 && isfinite(total) ? 1.f : 0.f);
+    }
+}
+
+constexpr int kThreads = 256;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads)
+select_step_kernel(SelectStepArgs a) {
+    constexpr int TPR = D / 4;             // threads per state row (a float4 each)
+    constexpr int RPP = kThreads / TPR;    // rows per pass
+    constexpr int NP = D / RPP;
+    __shared__ float sq[D], sk[D], sv[D];
+    __shared__ float4 part[RPP][TPR];
+    const int tid = threadIdx.x, cq = tid % TPR, rg = tid / TPR;
+    const int64_t st = blockIdx.x;
+    const int h = (int)(st % a.H);
+    float4 *S = reinterpret_cast<float4 *>(a.S + st * D * D);
+    float4 x[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) x[p] = __ldcs(S + (p * RPP + rg) * TPR + cq);
+    const float dt = step_of(a.gate, st, h), rate = a.gate.log_decay[h], x0 = rate * dt;
+    const float g = x0 < -kReset ? 0.f : exp_two(x0, fmaf(rate, dt, -x0));
+    if (tid < D) {
+        const int64_t qk = group_chain(st, a.H, a.gate.G) * D + tid;
+        sq[tid] = to_f32(static_cast<const T *>(a.q)[qk]) * a.scale;
+        sk[tid] = to_f32(static_cast<const T *>(a.k)[qk]) * dt;
+        sv[tid] = to_f32(static_cast<const T *>(a.v)[st * D + tid]);
+    }
+    __syncthreads();
+    const float4 v = reinterpret_cast<const float4 *>(sv)[cq];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const int i = p * RPP + rg;
+        const float k = sk[i], q = sq[i];
+        x[p].x = fmaf(g, x[p].x, k * v.x);
+        x[p].y = fmaf(g, x[p].y, k * v.y);
+        x[p].z = fmaf(g, x[p].z, k * v.z);
+        x[p].w = fmaf(g, x[p].w, k * v.w);
+        o.x = fmaf(x[p].x, q, o.x);
+        o.y = fmaf(x[p].y, q, o.y);
+        o.z = fmaf(x[p].z, q, o.z);
+        o.w = fmaf(x[p].w, q, o.w);
+        __stcs(S + i * TPR + cq, x[p]);
+    }
+    part[rg][cq] = o;
+    __syncthreads();
+    if (tid < D) {
+        float r = 0.f;
+#pragma unroll
+        for (int g2 = 0; g2 < RPP; ++g2) r += reinterpret_cast<const float *>(part[g2])[tid];
+        if (a.gate.skip) r = fmaf(a.gate.skip[h], sv[tid], r);
+        static_cast<T *>(a.o)[st * D + tid] = from_f32<T>(r);
+    }
+}
+
+// Bytes of the tables, each part a multiple of 16.
+struct TableBytes {
+    size_t c, dt, w, chunk;
+    size_t all() const { return c + dt + w + chunk; }
+};
+TableBytes table_bytes(int64_t n_chains, int64_t T, int C) {
+    const size_t chunks = (size_t)n_chains * (size_t)((T + C - 1) / C), tokens = chunks * C;
+    return {tokens * sizeof(float2), tokens * sizeof(float), tokens * sizeof(float), chunks * sizeof(float4)};
+}
+
+}  // namespace
+
+// [tables][the scan's own]
+size_t select_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype) {
+    if (dtype == FW_BF16) return table_bytes(n_chains, T, select_chunk_tc()).all() + select_states_tc(n_chains, T, d);
+    return table_bytes(n_chains, T, select_chunk_f32()).all() + select_states_f32(n_chains, T, d);
+}
+
+cudaError_t launch_select(const SelectArgs &args, cudaStream_t stream) {
+    ScanArgs s = args.scan;
+    const bool tc = s.dtype == FW_BF16;
+    const int C = tc ? select_chunk_tc() : select_chunk_f32();
+    const TableBytes b = table_bytes(s.n_chains, s.T, C);
+    char *ws = reinterpret_cast<char *>(s.ws);
+    float2 *c = reinterpret_cast<float2 *>(ws);
+    float *dt = reinterpret_cast<float *>(ws + b.c), *w = reinterpret_cast<float *>(ws + b.c + b.dt);
+    float4 *chunk = reinterpret_cast<float4 *>(ws + b.c + b.dt + b.w);
+    s.ws = reinterpret_cast<float *>(ws + b.all());
+    s.sel = SelectTables{c, dt, w, chunk, args.gate.skip, (s.T + C - 1) / C, args.gate.G};
+    const int64_t warps = s.n_chains * s.sel.n_chunks;
+    const unsigned grid = (unsigned)((warps + kTableBlock / 32 - 1) / (kTableBlock / 32));
+    if (C == 128) select_tables<128><<<grid, kTableBlock, 0, stream>>>(args.gate, s.lens, s.n_chains, s.T, s.H, c, dt, w, chunk, s.sel.n_chunks);
+    else select_tables<64><<<grid, kTableBlock, 0, stream>>>(args.gate, s.lens, s.n_chains, s.T, s.H, c, dt, w, chunk, s.sel.n_chunks);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return tc ? launch_select_tc(s, stream) : launch_select_f32(s, stream);
+}
+
+cudaError_t launch_select_step(const SelectStepArgs &a, cudaStream_t s) {
+    const unsigned grid = (unsigned)a.n_states;
+    if (a.dtype == FW_F32) {
+        if (a.d == 64) select_step_kernel<64, float><<<grid, kThreads, 0, s>>>(a);
+        else select_step_kernel<128, float><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        if (a.d == 64) select_step_kernel<64, __nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
+        else select_step_kernel<128, __nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace fw

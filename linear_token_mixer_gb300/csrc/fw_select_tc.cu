@@ -1,0 +1,44 @@
+// fw_select_tc.cu -- launches of the selective scan for bf16 rows (the kernel: fw_scan_tc.cuh).
+#include "fw_scan_tc.cuh"
+#include "fw_select.cuh"
+
+namespace fw {
+namespace {
+
+// As the decayed scan's: chains in segments where they are few.  Behind the launch that forms the tables.
+template <int D> cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
+    const int nseg = segments(a.n_chains, a.T);
+    const int64_t ab = a.n_chains / a.H * a.sel.G;
+    Jobs<1> jobs;
+    jobs.s[0].args = a;
+    if (!make_map(&jobs.s[0].a, a.a, a.T, ab, D, C) || !make_map(&jobs.s[0].b, a.b, a.T, ab, D, C) ||
+        !make_map(&jobs.s[0].c, a.c, a.T, a.n_chains, D, C) || !make_map(&jobs.s[0].out, a.out, a.T, a.n_chains, D, 32))
+        return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (nseg > 1) {
+        auto k = scan_tc_kernel<D, false, true, false, true>;
+        constexpr int smem = (int)Lay<D, true, true>::ALLOC;
+        static std::atomic<uint64_t> pre_done{0};
+        if ((e = allow_smem(k, smem, pre_done)) != cudaSuccess) return e;
+        if ((e = launch_after(k, dim3((unsigned)(a.n_chains * (nseg - 1))), NTHREADS, smem, s, true, jobs, nseg, 0, 0)) !=
+            cudaSuccess)
+            return e;
+    }
+    constexpr int smem = (int)Lay<D, false, true>::ALLOC;
+    auto k = scan_tc_kernel<D, false, false, false, true>;
+    static std::atomic<uint64_t> done{0};
+    if ((e = allow_smem(k, smem, done)) != cudaSuccess) return e;
+    const int by_length = a.lens && a.n_chains > kSMs && a.n_chains / a.H <= kMaxRanked;
+    return launch_after(k, dim3((unsigned)(a.n_chains * nseg)), NTHREADS, smem, s, true, jobs, nseg, by_length,
+                        nseg > 1 ? kWaitFirst : 0);
+}
+
+}  // namespace
+
+int select_chunk_tc() { return C; }
+size_t select_states_tc(int64_t n_chains, int64_t T, int d) { return segment_bytes(n_chains, d, segments(n_chains, T)); }
+cudaError_t launch_select_tc(const ScanArgs &s, cudaStream_t stream) {
+    return s.d == 64 ? launch<64>(s, stream) : launch<128>(s, stream);
+}
+
+}  // namespace fw

@@ -23,7 +23,7 @@ FW_F32, FW_BF16 = 0, 1
 MODES = {"falcon1": 0, "linattn": 1, "falcon1a": 2, "falcon2": 3, "falcon2a": 4,
          "falcon3": 5, "falcon3a": 6}
 WINDOW_MAX = 8
-FLAG_RBW, FLAG_SAME_PAIR, FLAG_ZERO_REST = 1, 2, 4
+FLAG_RBW, FLAG_SAME_PAIR, FLAG_ZERO_REST, FLAG_SILU, FLAG_SOFTPLUS = 1, 2, 4, 8, 16
 PHIS = {"identity": 0, "elu1": 1}
 ALGOS = {"auto": 0, "recurrent": 1, "chunked": 2}
 DTYPES = {torch.float32: FW_F32, torch.bfloat16: FW_BF16}
@@ -56,9 +56,23 @@ class fw_norm(ctypes.Structure):
     _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("eps", ctypes.c_float)]
 
 
+class fw_gates(ctypes.Structure):
+    _fields_ = [("dt", ctypes.c_void_p), ("dt_type", ctypes.c_int), ("log_decay", ctypes.c_void_p),
+                ("dt_bias", ctypes.c_void_p), ("skip", ctypes.c_void_p), ("groups", ctypes.c_int64)]
+
+
+class fw_gated(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int64),
+                ("inner", ctypes.c_int64), ("eps", ctypes.c_float), ("rms", ctypes.c_int),
+                ("gate_after", ctypes.c_int)]
+
+
 EXPORTS = ("fw_prefill", "fw_prefill_ex", "fw_prefill_noalloc", "fw_step", "fw_step_ex", "fw_window_prefill",
            "fw_window_step", "fw_decay_workspace", "fw_decay_prefill", "fw_decay_backward",
-           "fw_decay_step", "fw_layer_norm", "fw_layer_norm_workspace", "fw_layer_norm_backward",
+           "fw_decay_step", "fw_select_workspace", "fw_select_prefill", "fw_select_step", "fw_conv_prefill",
+           "fw_conv_workspace", "fw_conv_backward", "fw_conv_step", "fw_gated_norm", "fw_gated_norm_workspace",
+           "fw_gated_norm_backward", "fw_layer_norm", "fw_layer_norm_workspace", "fw_layer_norm_backward",
            "fw_check",
            "fw_status_string", "fw_version", "fw_last_cuda_error", "fw_set_wait_limit_us",
            "fw_debug_force_timeout", "fw_debug_segment_split")
@@ -94,6 +108,19 @@ def lib():
         L.fw_layer_norm.argtypes = [P, P, P, P, P, P, I64, I64, I, F, P]
         L.fw_layer_norm_workspace.argtypes = [I64, I64]
         L.fw_layer_norm_backward.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I, P, I64, P]
+        G, GN = ctypes.POINTER(fw_gates), ctypes.POINTER(fw_gated)
+        L.fw_select_workspace.argtypes = [SP, I]
+        L.fw_select_prefill.argtypes = [P, P, P, G, P, P, P, P, SP, I, F, U, P, I64, P]
+        L.fw_select_step.argtypes = [P, P, P, G, P, P, SP, I, F, U, P]
+        L.fw_conv_prefill.argtypes = [P, P, P, P, P, P, P, SP, I, I, U, P]
+        L.fw_conv_workspace.argtypes = [SP, I]
+        L.fw_conv_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, SP, I, I, U, P, I64, P]
+        L.fw_conv_step.argtypes = [P, P, P, P, P, SP, I, I, U, P]
+        L.fw_gated_norm.argtypes = [P, GN, P, P, P, P, I64, I64, I, P]
+        L.fw_gated_norm_workspace.argtypes = [I64, I64, I64, I]
+        L.fw_gated_norm_backward.argtypes = [P, P, P, GN, P, P, P, P, P, P, P, P, I64, I64, I, P, I64, P]
+        for f in (L.fw_select_workspace, L.fw_conv_workspace, L.fw_gated_norm_workspace):
+            f.restype = I64
         L.fw_decay_workspace.restype = L.fw_layer_norm_workspace.restype = I64
         L.fw_check.argtypes = [P]
         L.fw_status_string.argtypes = [I]
@@ -109,6 +136,8 @@ def lib():
         for f in (L.fw_prefill, L.fw_prefill_ex, L.fw_prefill_noalloc, L.fw_step, L.fw_step_ex,
                   L.fw_window_prefill,
                   L.fw_window_step, L.fw_decay_prefill, L.fw_decay_backward, L.fw_decay_step,
+                  L.fw_select_prefill, L.fw_select_step, L.fw_conv_prefill, L.fw_conv_backward, L.fw_conv_step,
+                  L.fw_gated_norm, L.fw_gated_norm_backward,
                   L.fw_layer_norm, L.fw_layer_norm_backward, L.fw_check, L.fw_version, L.fw_last_cuda_error):
             f.restype = I
         _lib = L
@@ -458,6 +487,263 @@ def decay_step(q, k, v, log_decay, S, *, scale=1.0, norm=None, norm_eps=1e-5, o=
             _arg(o, shape, dt, "o", q), ctypes.byref(fw_shape(B, H, 1, d, d)), DTYPES.get(dt, -1),
             scale)
     return o
+
+
+@functools.lru_cache(maxsize=4096)
+def _select_need(B, H, T, d, dtype):
+    return lib().fw_select_workspace(ctypes.byref(fw_shape(B, H, T, d, d)), dtype)
+
+
+@functools.lru_cache(maxsize=4096)
+def _conv_need(B, H, T, d, width):
+    return lib().fw_conv_workspace(ctypes.byref(fw_shape(B, H, T, d, d)), width)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_need(rows, width, groups, dtype):
+    return lib().fw_gated_norm_workspace(rows, width, groups, dtype)
+
+
+def _gates(dt, log_decay, dt_bias, skip, shape, groups, like):
+    """fw_gates of a selective call; shape: that of dt."""
+    H, f32 = (shape[1],), torch.float32
+    if dt is None or log_decay is None:
+        raise ValueError("fw: dt and log_decay are required")
+    kind = f32 if dt.dtype is f32 else like.dtype
+    return ctypes.byref(fw_gates(
+        _arg(dt, shape, kind, "dt", like), DTYPES.get(kind, -1), _arg(log_decay, H, f32, "log_decay", like),
+        _arg(dt_bias, H, f32, "dt_bias", like), _arg(skip, H, f32, "skip", like), groups))
+
+
+def select_workspace(B, H, T, d, dtype=torch.bfloat16):
+    """Bytes of workspace of select_prefill for this shape."""
+    n = _select_need(B, H, T, d, DTYPES.get(dtype, -1))
+    if n < 0:
+        raise FwError(int(n), "fw_select_workspace")
+    return n
+
+
+def select_prefill(q, k, v, dt, log_decay, S0=None, *, dt_bias=None, softplus=False, skip=None, scale=1.0,
+                   lens=None, o=None, S_T=None, workspace=None, stream=None):
+    """Selective scan over v [B, H, T, d] with queries and keys q, k [B, G, T, d] (fp32 or bf16), each
+    shared by H / G neighbouring heads: S_t = exp(log_decay[h] dt_t) S_{t-1} + dt_t k_t v_t^T,
+    o_t = scale S_t^T q_t + skip[h] v_t, with the steps dt [B, H, T] (fp32, or q's dtype), dt + dt_bias[h],
+    or softplus(dt + dt_bias[h]).
+
+    log_decay, dt_bias, skip [H] fp32, the last two or None; S0, lens, o, S_T and workspace
+    (of select_workspace() bytes) as in decay_prefill.  Returns (o, S_T)."""
+    shape = B, H, T, d = _axes(v, 4)
+    G = _axes(q, 4)[1]
+    few, state, kind, f32 = (B, G, T, d), (B, H, d, d), q.dtype, torch.float32
+    args = (_arg(q, few, kind, "q", q), _arg(k, few, kind, "k", q), _arg(v, shape, kind, "v", q),
+            _gates(dt, log_decay, dt_bias, skip, (B, H, T), G, q), _arg(S0, state, f32, "S0", q),
+            _arg(lens, (B,), torch.int32, "lens", q))
+    on = _On(q, stream)
+    flags = FLAG_ZERO_REST if o is None and lens is not None else 0
+    if softplus:
+        flags |= FLAG_SOFTPLUS
+    if o is None:
+        o = on.new(shape, kind)
+    if S_T is None:
+        S_T = on.new(state, f32)
+    code = DTYPES.get(kind, -1)
+    _keep, ws, nws = on.workspace(workspace, _select_need(B, H, T, d, code), "fw_select_prefill")
+    on.call(lib().fw_select_prefill, "fw_select_prefill",
+            (q, k, v, dt, log_decay, dt_bias, skip, S0, lens, o, S_T, workspace), *args,
+            _arg(o, shape, kind, "o", q), _arg(S_T, state, f32, "S_T", q),
+            ctypes.byref(fw_shape(B, H, T, d, d)), code, scale, flags, ws, nws)
+    return o, S_T
+
+
+def select_step(q, k, v, dt, log_decay, S, *, dt_bias=None, softplus=False, skip=None, scale=1.0, o=None,
+                stream=None):
+    """One token of select_prefill's recurrence for q, k [B, G, d], v [B, H, d], dt [B, H]; S
+    [B, H, d, d] fp32 is updated in place.  Returns o [B, H, d] in q's dtype."""
+    shape = B, H, d = _axes(v, 3)
+    G = _axes(q, 3)[1]
+    few, kind = (B, G, d), q.dtype
+    args = (_arg(q, few, kind, "q", q), _arg(k, few, kind, "k", q), _arg(v, shape, kind, "v", q),
+            _gates(dt, log_decay, dt_bias, skip, (B, H), G, q), _arg(S, (B, H, d, d), torch.float32, "S", q))
+    on = _On(q, stream)
+    if o is None:
+        o = on.new(shape, kind)
+    on.call(lib().fw_select_step, "fw_select_step", (q, k, v, dt, log_decay, dt_bias, skip, S, o), *args,
+            _arg(o, shape, kind, "o", q), ctypes.byref(fw_shape(B, H, 1, d, d)), DTYPES.get(kind, -1), scale,
+            FLAG_SOFTPLUS if softplus else 0)
+    return o
+
+
+def conv_prefill(x, weight, bias=None, state=None, *, silu=True, lens=None, y=None, state_out=None,
+                 stream=None):
+    """Short causal convolution of every channel of x [B, H, T, d] (fp32 or bf16, any d):
+    y_t = act(bias + sum_w weight[w] x_{t-W+1+w}), act silu or none.
+
+    weight [H, d, W] fp32, W = 2 .. 8, the last tap on the row itself; bias [H, d] fp32 or None;
+    state [B, H, W-1, d] in x's dtype: the rows before the first, oldest first (None: zeros);
+    state_out: a tensor for those behind the last (allocated when None; may be state); lens [B]
+    int32 or None, and rows of y behind them, as in decay_prefill.  Returns (y, state_out)."""
+    shape = B, H, T, d = _axes(x, 4)
+    W, kind, f32 = _taps(weight), x.dtype, torch.float32
+    past = (B, H, W - 1, d)
+    args = (_arg(x, shape, kind, "x", x), _arg(weight, (H, d, W), f32, "weight", x),
+            _arg(bias, (H, d), f32, "bias", x), _arg(state, past, kind, "state", x),
+            _arg(lens, (B,), torch.int32, "lens", x))
+    on = _On(x, stream)
+    flags = (FLAG_SILU if silu else 0) | (FLAG_ZERO_REST if y is None and lens is not None else 0)
+    if y is None:
+        y = on.new(shape, kind)
+    if state_out is None:
+        state_out = on.new(past, kind)
+    on.call(lib().fw_conv_prefill, "fw_conv_prefill", (x, weight, bias, state, lens, y, state_out), *args,
+            _arg(y, shape, kind, "y", x), _arg(state_out, past, kind, "state_out", x),
+            ctypes.byref(fw_shape(B, H, T, d, d)), W, DTYPES.get(kind, -1), flags)
+    return y, state_out
+
+
+def conv_backward(dy, x, weight, bias=None, state=None, dstate_out=None, *, silu=True, lens=None, dx=None,
+                  dweight=None, dbias=None, dstate=None, workspace=None, stream=None):
+    """Gradients of conv_prefill given dy (x's shape and dtype) and dstate_out, that of the returned
+    state, or None.  Returns (dx, dweight, dbias, dstate): dweight, dbias fp32; dstate in x's dtype, None
+    unless state or dstate is given.  Rows of dx behind lens as in decay_backward."""
+    shape = B, H, T, d = _axes(x, 4)
+    W, kind, f32 = _taps(weight), x.dtype, torch.float32
+    past = (B, H, W - 1, d)
+    args = (_arg(dy, shape, kind, "dy", x), _arg(x, shape, kind, "x", x), _arg(weight, (H, d, W), f32, "weight", x),
+            _arg(bias, (H, d), f32, "bias", x), _arg(state, past, kind, "state", x),
+            _arg(lens, (B,), torch.int32, "lens", x), _arg(dstate_out, past, kind, "dstate_out", x))
+    on = _On(x, stream)
+    flags = (FLAG_SILU if silu else 0) | (FLAG_ZERO_REST if dx is None and lens is not None else 0)
+    if dx is None:
+        dx = on.new(shape, kind)
+    if dweight is None:
+        dweight = on.new((H, d, W), f32)
+    if dbias is None:
+        dbias = on.new((H, d), f32)
+    if dstate is None and state is not None:
+        dstate = on.new(past, kind)
+    _keep, ws, nws = on.workspace(workspace, _conv_need(B, H, T, d, W), "fw_conv_backward")
+    on.call(lib().fw_conv_backward, "fw_conv_backward",
+            (dy, x, weight, bias, state, lens, dstate_out, dx, dweight, dbias, dstate, workspace), *args,
+            _arg(dx, shape, kind, "dx", x), _arg(dweight, (H, d, W), f32, "dweight", x),
+            _arg(dbias, (H, d), f32, "dbias", x), _arg(dstate, past, kind, "dstate", x),
+            ctypes.byref(fw_shape(B, H, T, d, d)), W, DTYPES.get(kind, -1), flags, ws, nws)
+    return dx, dweight, dbias, dstate
+
+
+def conv_step(x, weight, bias, state, *, silu=True, y=None, stream=None):
+    """One token of conv_prefill for x [B, H, d]; state [B, H, W-1, d] moves on by one row in place.
+    Returns y [B, H, d]."""
+    shape = B, H, d = _axes(x, 3)
+    W, kind = _taps(weight), x.dtype
+    args = (_arg(x, shape, kind, "x", x), _arg(weight, (H, d, W), torch.float32, "weight", x),
+            _arg(bias, (H, d), torch.float32, "bias", x), _arg(state, (B, H, W - 1, d), kind, "state", x))
+    on = _On(x, stream)
+    if y is None:
+        y = on.new(shape, kind)
+    on.call(lib().fw_conv_step, "fw_conv_step", (x, weight, bias, state, y), *args, _arg(y, shape, kind, "y", x),
+            ctypes.byref(fw_shape(B, H, 1, d, d)), W, DTYPES.get(kind, -1), FLAG_SILU if silu else 0)
+    return y
+
+
+def _taps(weight):
+    if weight.dim() != 3:
+        raise ValueError("fw: weight must be [H, d, W]")
+    return weight.shape[2]
+
+
+def _gated_shape(x, params):
+    """(leading shape, rows, width, groups, inner, shape of a parameter): parameters [width], or
+    [H, width] with x [.., H, T, width]."""
+    if x.dim() < 1:
+        raise ValueError("fw: gated_norm needs at least one axis")
+    shape = x.shape
+    lead, width = shape[:-1], shape[-1]
+    rows = lead.numel()
+    if any(p is not None and p.dim() == 2 for p in params):
+        if x.dim() < 3:
+            raise ValueError("fw: parameters [H, width] go with x [.., H, T, width]")
+        return lead, rows, width, shape[-3], shape[-2], (shape[-3], width)
+    return lead, rows, width, 1, rows, (width,)
+
+
+def gated_norm(x, weight=None, bias=None, *, gate=None, residual=None, scale=None, rms=False, gate_after=False,
+               eps=1e-5, y=None, total=None, mean=None, rstd=None, stats=True, stream=None):
+    """The norm before a block with its scaled residual sum, and the norm behind a mixer with its gate,
+    over the last axis of x (fp32 or bf16, width 1 .. 8192), with u = x + scale residual:
+    y = norm(u silu(gate)) weight + bias, or with gate_after (norm(u) weight + bias) silu(gate).
+    norm: layer norm, or with rms the row over its root mean square.
+
+    gate, residual: x's shape and dtype, or None; scale (with a residual), weight, bias: fp32
+    [width], or all of them [H, width] for x [.., H, T, width], or None.  y and total may each be x, gate or
+    residual.  Returns (y, total, mean, rstd): total is u as stored, None without a residual;
+    the statistics fp32 of x's leading shape (None with stats=False; mean None with rms)."""
+    lead, rows, width, groups, inner, par = _gated_shape(x, (weight, bias, scale))
+    shape, kind, f32 = x.shape, x.dtype, torch.float32
+    x_ = _arg(x, shape, kind, "x", x)
+    _finite_eps(eps)
+    args = fw_gated(_arg(gate, shape, kind, "gate", x), _arg(residual, shape, kind, "residual", x),
+                    _arg(scale, par, f32, "scale", x), _arg(weight, par, f32, "weight", x),
+                    _arg(bias, par, f32, "bias", x), groups, inner, eps, int(rms), int(gate_after))
+    on = _On(x, stream)
+    if y is None:
+        y = on.new(shape, kind)
+    if total is None and residual is not None:
+        total = on.new(shape, kind)
+    if not stats:
+        mean = rstd = None
+    else:
+        mean = None if rms else on.new(lead, f32) if mean is None else mean
+        if rstd is None:
+            rstd = on.new(lead, f32)
+    on.call(lib().fw_gated_norm, "fw_gated_norm", (x, gate, residual, scale, weight, bias, y, total, mean, rstd),
+            x_, ctypes.byref(args), _arg(y, shape, kind, "y", x), _arg(total, shape, kind, "total", x),
+            _arg(mean, lead, f32, "mean", x), _arg(rstd, lead, f32, "rstd", x), rows, width, DTYPES.get(kind, -1))
+    return y, total, mean, rstd
+
+
+def gated_norm_backward(dy, x, weight, bias, mean, rstd, *, gate=None, residual=None, scale=None, rms=False,
+                        gate_after=False, dtotal=None, dx=None, dgate=None, dresidual=None, dweight=None,
+                        dbias=None, dscale=None, workspace=None, stream=None):
+    """Gradients of gated_norm from its inputs and statistics, given dy and dtotal (or None), those of
+    y and total.  Returns (dx, dweight, dbias, dgate, dresidual, dscale): dgate None without a
+    gate, dresidual and dscale None without a residual, dresidual dx itself without a scale.  dx, dgate and dresidual
+    may each be dy, dtotal, x, gate or residual."""
+    lead, rows, width, groups, inner, par = _gated_shape(x, (weight, bias, scale, dweight, dbias, dscale))
+    shape, kind, f32 = x.shape, x.dtype, torch.float32
+    grads = (_arg(dy, shape, kind, "dy", x), _arg(dtotal, shape, kind, "dtotal", x), _arg(x, shape, kind, "x", x))
+    args = fw_gated(_arg(gate, shape, kind, "gate", x), _arg(residual, shape, kind, "residual", x),
+                    _arg(scale, par, f32, "scale", x), _arg(weight, par, f32, "weight", x),
+                    _arg(bias, par, f32, "bias", x), groups, inner, 0.0, int(rms), int(gate_after))
+    stats = (_arg(None if rms else mean, lead, f32, "mean", x), _arg(rstd, lead, f32, "rstd", x))
+    on = _On(x, stream)
+    if dx is None:
+        dx = on.new(shape, kind)
+    if dgate is None and gate is not None:
+        dgate = on.new(shape, kind)
+    if residual is not None and scale is not None:
+        if dresidual is None:
+            dresidual = on.new(shape, kind)
+        if dscale is None:
+            dscale = on.new(par, f32)
+    if dweight is None:
+        dweight = on.new(par, f32)
+    if dbias is None:
+        dbias = on.new(par, f32)
+    _keep, ws, nws = on.workspace(workspace, _gated_need(rows, width, groups, DTYPES.get(kind, -1)),
+                                  "fw_gated_norm_backward")
+    on.call(lib().fw_gated_norm_backward, "fw_gated_norm_backward",
+            (dy, dtotal, x, gate, residual, scale, weight, bias, mean, rstd, dx, dgate, dresidual, dweight, dbias,
+             dscale, workspace),
+            *grads, ctypes.byref(args), *stats, _arg(dx, shape, kind, "dx", x), _arg(dgate, shape, kind, "dgate", x),
+            _arg(dresidual, shape, kind, "dresidual", x), _arg(dweight, par, f32, "dweight", x),
+            _arg(dbias, par, f32, "dbias", x), _arg(dscale, par, f32, "dscale", x), rows, width,
+            DTYPES.get(kind, -1), ws, nws)
+    return dx, dweight, dbias, dgate, dx if residual is not None and dresidual is None else dresidual, dscale
+
+
+def _finite_eps(eps):
+    if not 0.0 <= ctypes.c_float(eps).value < float("inf"):
+        raise ValueError("fw: eps must be finite and not negative")
 
 
 def layer_norm(x, weight=None, bias=None, *, eps=1e-5, y=None, mean=None, rstd=None, stats=True,
