@@ -942,7 +942,7 @@ extern "C" int fw_gated_norm(const void *x, const fw_gated *args, void *y, void 
 
 extern "C" int64_t fw_gated_norm_workspace(int64_t rows, int64_t width, int64_t groups, fw_dtype dtype) {
     const int st = check_gated(rows, width, groups, dtype);
-    return st != FW_OK ? st : (int64_t)gated_norm_workspace(rows, width, groups, dtype);
+    return st != FW_OK ? st : (int64_t)gated_norm_workspace(rows, width, groups);
 }
 
 extern "C" int fw_gated_norm_backward(const void *dy, const void *dtotal, const void *x,

@@ -5,24 +5,25 @@
 // All three are bound by their rows' bytes.  A thread holds V channels (16 bytes of a row; 8 in the
 // backward pass, which keeps five such rows' worth of registers) and walks a strip of
 // tokens with the last W - 1 rows in registers, so that each row is read once but for the W - 1 rows
-// before a strip.  Rows come kAhead at a time, the next ones in flight while these are worked on.
+// before a strip.  Rows come W at a time, the next W in flight while these are worked on.
 // The backward pass forms a_t again, walks W - 1 tokens past its strip, and writes
 //     da_t = dy_t act'(a_t),   dx_{t-W+1} = sum_w weight[w] da_{t-w}
 // as t passes; dweight[w] += da_t x_{t-W+1+w} and dbias += da_t stay in registers over all strips
 // of a thread, are added up in a block, and a second kernel adds the blocks' in a fixed order.
 #include "fw_conv.cuh"
+#include "fw_partial.cuh"
 
 namespace fw {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kAhead = 4;                     // rows a load turn
 constexpr int kStrip = 64;                    // most tokens of a strip
 constexpr int kStripMin = 8;                  // no fewer: only the first strip reads the state (W - 1 <= 7)
 
 // V channels of a row: as they are stored, and as pairs of fp32.
 template <typename T, int V> struct Raw;
 template <> struct Raw<float, 1> { float v; };
+template <> struct Raw<float, 2> { float2 v; };
 template <> struct Raw<float, 4> { float4 v; };
 template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 v; };
 template <> struct Raw<__nv_bfloat16, 2> { uint32_t v; };
@@ -44,6 +45,7 @@ __device__ __forceinline__ uint32_t pair_bf16(uint64_t x) {
 }
 
 __device__ __forceinline__ Chan<1> widen(const Raw<float, 1> &r) { return {{pair(r.v, 0.f)}}; }
+__device__ __forceinline__ Chan<2> widen(const Raw<float, 2> &r) { return {{pair(r.v.x, r.v.y)}}; }
 __device__ __forceinline__ Chan<4> widen(const Raw<float, 4> &r) { return {{pair(r.v.x, r.v.y), pair(r.v.z, r.v.w)}}; }
 __device__ __forceinline__ Chan<1> widen(const Raw<__nv_bfloat16, 1> &r) { return {{pair(__bfloat162float(r.v), 0.f)}}; }
 __device__ __forceinline__ Chan<2> widen(const Raw<__nv_bfloat16, 2> &r) { return {{bf16_pair(r.v)}}; }
@@ -53,6 +55,7 @@ __device__ __forceinline__ Chan<8> widen(const Raw<__nv_bfloat16, 8> &r) {
 }
 
 __device__ __forceinline__ void narrow(Raw<float, 1> &r, const Chan<1> &c) { r.v = halves(c.p[0]).x; }
+__device__ __forceinline__ void narrow(Raw<float, 2> &r, const Chan<2> &c) { r.v = halves(c.p[0]); }
 __device__ __forceinline__ void narrow(Raw<float, 4> &r, const Chan<4> &c) {
     const float2 a = halves(c.p[0]), b = halves(c.p[1]);
     r.v = make_float4(a.x, a.y, b.x, b.y);
@@ -85,12 +88,6 @@ template <int V> __device__ __forceinline__ void fma_to(Chan<V> &acc, const Chan
     for (int i = 0; i < Chan<V>::N; ++i) acc.p[i] = fma2(a.p[i], b.p[i], acc.p[i]);
 }
 
-// 1 / (1 + exp(-a)): for bf16 rows by the fast exponential and reciprocal (a few ulp of fp32, a
-// thousandth of the rows' rounding).
-template <typename T> __device__ __forceinline__ float sigmoid(float a) {
-    if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-a));
-    else return __frcp_rn(1.f + __expf(-a));
-}
 template <typename T, int V> __device__ __forceinline__ Chan<V> silu(const Chan<V> &a) {
     Chan<V> y;
 #pragma unroll
@@ -147,73 +144,76 @@ __device__ __forceinline__ Chan<V> row_at(const T *x, const T *state, int64_t t,
 }
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kBlock) conv_kernel(ConvArgs a, uint32_t strip, uint32_t strips, uint32_t cols) {
+__global__ void __launch_bounds__(kBlock, W * V * sizeof(T) <= 64 ? 2 : 1) conv_kernel(ConvArgs a, uint32_t strip, uint32_t strips, uint32_t cols) {
     const uint32_t id = blockIdx.x * (uint32_t)kBlock + threadIdx.x;
     const uint32_t s = id / cols, cv = id % cols, st = s % strips;
     const int64_t chain = s / strips;
     if (chain >= a.n_chains) return;
     const int d = a.d, h = (int)(chain % a.H), c0 = (int)cv * V;
-    const int64_t n = chain_len(a.lens, chain, a.H, a.T);
-    const int64_t t0 = (int64_t)st * strip, t1 = t0 + strip < a.T ? t0 + strip : a.T;
+    const int n = (int)chain_len(a.lens, chain, a.H, a.T), T_ = (int)a.T;
+    const int t0 = (int)(st * strip), t1 = t0 + (int)strip < T_ ? t0 + (int)strip : T_;
     const T *const x = static_cast<const T *>(a.x) + chain * a.T * d + c0;
     const T *const state = a.state ? static_cast<const T *>(a.state) + chain * (W - 1) * d + c0 : nullptr;
     T *const y = static_cast<T *>(a.y) + chain * a.T * d + c0;
-    const int64_t end = t1 < n ? t1 : n;
-    Chan<V> win[W - 1 + kAhead];
+    const int end = t1 < n ? t1 : n;
+    Chan<V> win[W];                           // the row at t0 + i, and those before it, at i mod W
     if (t0 < end || st == 0) {
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) win[i] = row_at<T, V>(x, state, t0 + i - (W - 1), W, d);
+        for (int i = 1; i < W; ++i) win[i] = row_at<T, V>(x, state, t0 + i - W, W, d);
     }
     if (st == 0 && a.state_out) {             // the last W - 1 of the state's rows and the chain's
         T *const so = static_cast<T *>(a.state_out) + chain * (W - 1) * d + c0;
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) {     // (a row of the state is already in win: state_out may be state)
-            const int64_t t = n + i - (W - 1);
+        for (int i = 1; i < W; ++i) {         // (a row of the state is already in win: state_out may be state)
+            const int t = n + i - W;
             Chan<V> r = none<V>();
-            if (t >= 0) r = widen(load<T, V>(x + t * d));
+            if (t >= 0) r = widen(load<T, V>(x + (int64_t)t * d));
             else
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-                    if (j == t + W - 1) r = win[j];
-            store<T, V>(so + (int64_t)i * d, r);
+                for (int j = 1; j < W; ++j)
+                    if (j == t + W) r = win[j];
+            store<T, V>(so + (int64_t)(i - 1) * d, r);
         }
     }
     if (t0 < end) {
         Chan<V> w[W];
         load_taps<W, V>(w, a.weight + ((int64_t)h * d + c0) * W);
         const Chan<V> bias = load_bias<V>(a.bias ? a.bias + (int64_t)h * d + c0 : nullptr);
-        Raw<T, V> next[kAhead];
-        auto fetch = [&](int64_t t) {
+        Raw<T, V> next[W];
+        const T *from = x + (int64_t)t0 * d;   // of the rows to fetch
+        T *to = y + (int64_t)t0 * d;
+        auto fetch = [&](int t) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (t + u < end) next[u] = load<T, V>(x + (t + u) * d);
+            for (int u = 0; u < W; ++u)
+                if (t + u < end) next[u] = load<T, V>(from + u * d);
+            from += W * d;
         };
         fetch(t0);
 #pragma unroll 1
-        for (int64_t t = t0; t < end; t += kAhead) {
+        for (int t = t0; t < end; t += W, to += W * d) {
+            Raw<T, V> now[W];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) win[W - 1 + u] = widen(next[u]);
-            if (t + kAhead < end) fetch(t + kAhead);
+            for (int u = 0; u < W; ++u) now[u] = next[u];
+            fetch(t + W);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
+            for (int u = 0; u < W; ++u) {
+                win[u] = widen(now[u]);
                 Chan<V> r = bias;
 #pragma unroll
-                for (int i = 0; i < W; ++i) fma_to(r, w[i], win[u + i]);
+                for (int i = 0; i < W; ++i) fma_to(r, w[i], win[(u + 1 + i) % W]);
                 if (a.silu) r = silu<T, V>(r);
-                if (t + u < end) store<T, V>(y + (t + u) * d, r);
+                if (t + u < end) store<T, V>(to + u * d, r);
             }
-#pragma unroll
-            for (int i = 0; i < W - 1; ++i) win[i] = win[i + kAhead];
         }
     }
     if (a.zero_rest)
-        for (int64_t t = t0 > n ? t0 : n; t < t1; ++t) store<T, V>(y + t * d, none<V>());
+        for (int t = t0 > n ? t0 : n; t < t1; ++t) store<T, V>(y + (int64_t)t * d, none<V>());
 }
 
 // `lanes` (a power of two) of a warp hold the columns of a row, the 32 / lanes parts of it take
 // strips of their own.  blockIdx.y: a head's group of columns; blockIdx.x: a share of the head's strips.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kBlock)
+__global__ void __launch_bounds__(kBlock, V == 2 && W > 4 ? 1 : 2)
 conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint32_t groups) {
     constexpr int NW = kBlock / 32;
     __shared__ float part[NW][32][V * (W + 1)];
@@ -234,80 +234,83 @@ conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint3
     for (uint32_t m = (blockIdx.x * NW + warp) * parts + lane / lanes; mine && m < total; m += step) {
         const uint32_t b = m / strips, st = m % strips;
         const int64_t chain = (int64_t)b * a.H + h;
-        const int64_t n = chain_len(a.lens, chain, a.H, a.T);
-        const int64_t t0 = (int64_t)st * strip, t1 = t0 + strip < a.T ? t0 + strip : a.T;
-        const int64_t end = t1 < n ? t1 : n;
+        const int n = (int)chain_len(a.lens, chain, a.H, a.T), T_ = (int)a.T;
+        const int t0 = (int)(st * strip), t1 = t0 + (int)strip < T_ ? t0 + (int)strip : T_;
+        const int end = t1 < n ? t1 : n;
         const int64_t at = chain * a.T * d + c0, sat = chain * (W - 1) * d + c0;
         const T *const x = static_cast<const T *>(a.x) + at, *const dy = static_cast<const T *>(a.dy) + at;
         const T *const state = a.state ? static_cast<const T *>(a.state) + sat : nullptr;
         const T *const dso = a.dstate_out ? static_cast<const T *>(a.dstate_out) + sat : nullptr;
         T *const dx = static_cast<T *>(a.dx) + at, *const ds = a.dstate ? static_cast<T *>(a.dstate) + sat : nullptr;
         if (a.zero_rest)
-            for (int64_t t = t0 > n ? t0 : n; t < t1; ++t) store<T, V>(dx + t * d, none<V>());
+            for (int t = t0 > n ? t0 : n; t < t1; ++t) store<T, V>(dx + (int64_t)t * d, none<V>());
         if (!(t0 < end || (st == 0 && ds))) continue;
-        Chan<V> win[W - 1 + kAhead], da[W - 1 + kAhead];
+        Chan<V> win[W], da[W];                    // the row at t0 + i, and those before it, at i mod W
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) {
-            win[i] = row_at<T, V>(x, state, t0 + i - (W - 1), W, d);
+        for (int i = 1; i < W; ++i) {
+            win[i] = row_at<T, V>(x, state, t0 + i - W, W, d);
             da[i] = none<V>();
         }
-        Raw<T, V> nx[kAhead], ny[kAhead];
-        auto fetch = [&](int64_t t) {
+        Raw<T, V> nx[W], ny[W];
+        const T *fx = x + (int64_t)t0 * d, *fy = dy + (int64_t)t0 * d;   // of the rows to fetch
+        T *to = dx + (int64_t)(t0 - (W - 1)) * d;                        // where the next row leaves to
+        auto fetch = [&](int t) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
+            for (int u = 0; u < W; ++u)
                 if (t + u < n) {
-                    nx[u] = load<T, V>(x + (t + u) * d);
-                    ny[u] = load<T, V>(dy + (t + u) * d);
+                    nx[u] = load<T, V>(fx + u * d);
+                    ny[u] = load<T, V>(fy + u * d);
                 }
+            fx += W * d;
+            fy += W * d;
         };
         fetch(t0);
-        const int64_t stop = (end > t0 ? end : t0) + W - 1;      // rows up to end - 1 leave at t = end + W - 2
+        const int stop = (end > t0 ? end : t0) + W - 1;      // rows up to end - 1 leave at t = end + W - 2
 #pragma unroll 1
-        for (int64_t t = t0; t < stop; t += kAhead) {
+        for (int t = t0; t < stop; t += W, to += W * d) {
+            Raw<T, V> mx[W], my[W];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const bool on = t + u < n;
-                win[W - 1 + u] = on ? widen(nx[u]) : none<V>();
-                da[W - 1 + u] = on ? widen(ny[u]) : none<V>();
+            for (int u = 0; u < W; ++u) {
+                mx[u] = nx[u];
+                my[u] = ny[u];
             }
-            if (t + kAhead < stop) fetch(t + kAhead);
+            if (t + W < stop) fetch(t + W);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
+            for (int u = 0; u < W; ++u) {
+                const bool on = t + u < n;
+                win[u] = on ? widen(mx[u]) : none<V>();
+                da[u] = on ? widen(my[u]) : none<V>();
                 if (a.silu) {
                     Chan<V> r = bias;
 #pragma unroll
-                    for (int i = 0; i < W; ++i) fma_to(r, w[i], win[u + i]);
-                    if (t + u < n) da[W - 1 + u] = silu_grad<T, V>(r, da[W - 1 + u]);
+                    for (int i = 0; i < W; ++i) fma_to(r, w[i], win[(u + 1 + i) % W]);
+                    if (on) da[u] = silu_grad<T, V>(r, da[u]);
                 }
                 if (t + u < end) {
 #pragma unroll
-                    for (int i = 0; i < W; ++i) fma_to(dw[i], da[W - 1 + u], win[u + i]);
+                    for (int i = 0; i < W; ++i) fma_to(dw[i], da[u], win[(u + 1 + i) % W]);
 #pragma unroll
-                    for (int i = 0; i < Chan<V>::N; ++i) db.p[i] = add2(db.p[i], da[W - 1 + u].p[i]);
+                    for (int i = 0; i < Chan<V>::N; ++i) db.p[i] = add2(db.p[i], da[u].p[i]);
                 }
-                const int64_t s = t + u - (W - 1);               // the row that leaves
+                const int s = t + u - (W - 1);               // the row that leaves
                 Chan<V> r = none<V>();
 #pragma unroll
-                for (int i = 0; i < W; ++i) fma_to(r, w[i], da[W - 1 + u - i]);
-                const int64_t q = s - n + W - 1;                 // its place in the state behind the chain
+                for (int i = 0; i < W; ++i) fma_to(r, w[i], da[(u - i + W) % W]);
+                const int q = s - n + W - 1;                 // its place in the state behind the chain
                 if (dso && q >= 0 && q < W - 1 && s < end) {
                     const Chan<V> e = widen(load<T, V>(dso + q * d));
 #pragma unroll
                     for (int i = 0; i < Chan<V>::N; ++i) r.p[i] = add2(r.p[i], e.p[i]);
                 }
                 if (s >= t0) {
-                    if (s < end) store<T, V>(dx + s * d, r);
-                } else if (st == 0 && ds && s < 0 && s >= -(W - 1)) {
+                    if (s < end) store<T, V>(to + u * d, r);
+                } else if (st == 0 && ds && s < 0) {
                     store<T, V>(ds + (s + W - 1) * d, r);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < W - 1; ++i) {
-                win[i] = win[i + kAhead];
-                da[i] = da[i + kAhead];
-            }
         }
     }
+    let_next_grid_start();
     if (!a.ws) return;
     // the parts of the warp, then the warps of the block
 #pragma unroll
@@ -332,21 +335,18 @@ conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint3
 }
 
 // The sums of the blocks, in their order.
-__global__ void __launch_bounds__(kBlock)
+__global__ void __launch_bounds__(kSumCols * kSumShares)
 conv_sum_kernel(const float *ws, int slices, int64_t count, int W, float *dweight, float *dbias) {
     wait_previous_grid();
-    const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-    if (i >= count) return;
-    float z = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < slices; ++s) z += ws[s * count + i];
-    const int64_t c = i / (W + 1);
-    const int e = (int)(i % (W + 1));
-    if (e == W) {
-        if (dbias) dbias[c] = z;
-    } else if (dweight) {
-        dweight[c * W + e] = z;
-    }
+    sum_slices(ws, slices, count, [&](int64_t i, float z) {
+        const int64_t c = i / (W + 1);
+        const int e = (int)(i % (W + 1));
+        if (e == W) {
+            if (dbias) dbias[c] = z;
+        } else if (dweight) {
+            dweight[c * W + e] = z;
+        }
+    });
 }
 
 template <typename T, int V, int W>
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kBlock) conv_step_kernel(ConvStepArgs a, uint3
 uint32_t strip_of(int64_t columns, int64_t T, int64_t threads) {
     int64_t s = columns * T / (kSMs * threads);
     s = s < kStripMin ? kStripMin : s > kStrip ? kStrip : s;
-    return (uint32_t)((s + kAhead - 1) / kAhead * kAhead);
+    return (uint32_t)s;
 }
 
 // Blocks of the backward pass that share a group of a head's columns: three an SM in all, and no more
@@ -401,7 +401,10 @@ BwdShape bwd_shape(int64_t B, int H, int64_t T, int d, int V) {
     return r;
 }
 
-int bwd_vector(int d) { return d % 4 == 0 ? 4 : 1; }
+// Channels a thread of the backward pass: what its registers hold beside the taps and their sums.
+int bwd_vector(int d, int W, fw_dtype dtype) {
+    return dtype == FW_BF16 && W <= 4 && d % 4 == 0 ? 4 : d % 2 == 0 ? 2 : 1;
+}
 
 template <typename T, int V, int W> cudaError_t run(const ConvArgs &a, cudaStream_t s) {
     const int64_t cols = a.d / V;
@@ -417,7 +420,7 @@ template <typename T, int V, int W> cudaError_t run(const ConvBwdArgs &a, cudaSt
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.ws) return e;
     const int64_t count = (int64_t)a.H * a.d * (W + 1);
-    return launch_after(conv_sum_kernel, dim3((unsigned)((count + kBlock - 1) / kBlock)), kBlock, 0, s, true,
+    return launch_after(conv_sum_kernel, sum_grid(count), kSumCols * kSumShares, 0, s, true,
                         (const float *)a.ws, (int)p.slices, count, W, a.dweight, a.dbias);
 }
 
@@ -439,9 +442,9 @@ template <typename T, int V, typename A> cudaError_t by_taps(const A &a, cudaStr
     }
 }
 
-// 16 bytes of a row a thread where rows are whole multiples of that, else 4 (bf16 of even d), else an element.
+// 16 bytes of a row a thread where rows are whole multiples of that, else two elements (even d), else one.
 template <typename A> cudaError_t by_type(const A &a, cudaStream_t s) {
-    if (a.dtype == FW_F32) return a.d % 4 == 0 ? by_taps<float, 4>(a, s) : by_taps<float, 1>(a, s);
+    if (a.dtype == FW_F32) return a.d % 4 == 0 ? by_taps<float, 4>(a, s) : a.d % 2 == 0 ? by_taps<float, 2>(a, s) : by_taps<float, 1>(a, s);
     if (a.d % 8 == 0) return by_taps<__nv_bfloat16, 8>(a, s);
     return a.d % 2 == 0 ? by_taps<__nv_bfloat16, 2>(a, s) : by_taps<__nv_bfloat16, 1>(a, s);
 }
@@ -451,20 +454,24 @@ template <typename A> cudaError_t by_type(const A &a, cudaStream_t s) {
 bool conv_fits(int64_t B, int64_t H, int64_t T, int64_t d) {
     // threads of a call at the shortest strips and one channel each, and the backward grid's second axis
     const int64_t strips = (T + kStripMin - 1) / kStripMin;
-    return T <= INT32_MAX && d <= (1 << 24) && H * ((d + 31) / 32) <= 65535 && B * H <= INT32_MAX / d &&
+    return T <= INT32_MAX - 1024 && d <= (1 << 24) && H * ((d + 31) / 32) <= 65535 && B * H <= INT32_MAX / d &&
            B * H * d <= INT32_MAX / strips;
 }
 
 size_t conv_workspace(int64_t B, int H, int64_t T, int d, int W) {
-    return (size_t)bwd_shape(B, H, T, d, bwd_vector(d)).slices * H * d * (W + 1) * sizeof(float);
+    // (of either type)
+    const uint32_t a = bwd_shape(B, H, T, d, bwd_vector(d, W, FW_F32)).slices, b = bwd_shape(B, H, T, d, bwd_vector(d, W, FW_BF16)).slices;
+    return (size_t)(a > b ? a : b) * H * d * (W + 1) * sizeof(float);
 }
 
 cudaError_t launch_conv(const ConvArgs &a, cudaStream_t s) { return by_type(a, s); }
 cudaError_t launch_conv_step(const ConvStepArgs &a, cudaStream_t s) { return by_type(a, s); }
 cudaError_t launch_conv_backward(const ConvBwdArgs &a, cudaStream_t s) {
-    const bool four = bwd_vector(a.d) == 4;
-    if (a.dtype == FW_F32) return four ? by_taps<float, 4>(a, s) : by_taps<float, 1>(a, s);
-    return four ? by_taps<__nv_bfloat16, 4>(a, s) : by_taps<__nv_bfloat16, 1>(a, s);
+    const int v = bwd_vector(a.d, a.W, a.dtype);
+    if (a.dtype == FW_F32) return v == 2 ? by_taps<float, 2>(a, s) : by_taps<float, 1>(a, s);
+    if (v == 4)
+        return a.W == 4 ? run<__nv_bfloat16, 4, 4>(a, s) : a.W == 3 ? run<__nv_bfloat16, 4, 3>(a, s) : run<__nv_bfloat16, 4, 2>(a, s);
+    return v == 2 ? by_taps<__nv_bfloat16, 2>(a, s) : by_taps<__nv_bfloat16, 1>(a, s);
 }
 
 }  // namespace fw

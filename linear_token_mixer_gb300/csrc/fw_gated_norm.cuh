@@ -5,8 +5,6 @@
 
 namespace fw {
 
-constexpr int kGatedWidth = 8192;   // widest row
-
 // What both passes read: x, gate, residual [rows][width]; scale, weight, bias [groups][width].
 struct GatedIn {
     const void *x, *gate, *residual;          // gate, residual: or NULL
@@ -33,7 +31,7 @@ struct GatedBwdArgs {
     float *ws;                                // of the three sums, or NULL (none wanted)
 };
 
-size_t gated_norm_workspace(int64_t rows, int64_t width, int64_t groups, fw_dtype dtype);
+size_t gated_norm_workspace(int64_t rows, int64_t width, int64_t groups);
 cudaError_t launch_gated_norm(const GatedArgs &a, cudaStream_t s);
 cudaError_t launch_gated_norm_backward(const GatedBwdArgs &a, cudaStream_t s);
 
