@@ -10,105 +10,20 @@
 //     da_t = dy_t act'(a_t),   dx_{t-W+1} = sum_w weight[w] da_{t-w}
 // as t passes; dweight[w] += da_t x_{t-W+1+w} and dbias += da_t stay in registers over all strips
 // of a thread, are added up in a block, and a second kernel adds the blocks' in a fixed order.
+#include <type_traits>
+
 #include "fw_conv.cuh"
 #include "fw_partial.cuh"
+#include "fw_rows.cuh"
 
 namespace fw {
 namespace {
 
+using namespace rows;
+
 constexpr int kBlock = 256;
 constexpr int kStrip = 64;                    // most tokens of a strip
 constexpr int kStripMin = 8;                  // no fewer: only the first strip reads the state (W - 1 <= 7)
-
-// V channels of a row: as they are stored, and as pairs of fp32.
-template <typename T, int V> struct Raw;
-template <> struct Raw<float, 1> { float v; };
-template <> struct Raw<float, 2> { float2 v; };
-template <> struct Raw<float, 4> { float4 v; };
-template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 v; };
-template <> struct Raw<__nv_bfloat16, 2> { uint32_t v; };
-template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
-template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
-
-template <int V> struct Chan {
-    static constexpr int N = (V + 1) / 2;
-    uint64_t p[N];                            // (V = 1: the low half)
-};
-
-__device__ __forceinline__ uint64_t bf16_pair(uint32_t x) {
-    return pair(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t pair_bf16(uint64_t x) {
-    const float2 f = halves(x);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(f.x, f.y);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-__device__ __forceinline__ Chan<1> widen(const Raw<float, 1> &r) { return {{pair(r.v, 0.f)}}; }
-__device__ __forceinline__ Chan<2> widen(const Raw<float, 2> &r) { return {{pair(r.v.x, r.v.y)}}; }
-__device__ __forceinline__ Chan<4> widen(const Raw<float, 4> &r) { return {{pair(r.v.x, r.v.y), pair(r.v.z, r.v.w)}}; }
-__device__ __forceinline__ Chan<1> widen(const Raw<__nv_bfloat16, 1> &r) { return {{pair(__bfloat162float(r.v), 0.f)}}; }
-__device__ __forceinline__ Chan<2> widen(const Raw<__nv_bfloat16, 2> &r) { return {{bf16_pair(r.v)}}; }
-__device__ __forceinline__ Chan<4> widen(const Raw<__nv_bfloat16, 4> &r) { return {{bf16_pair(r.v.x), bf16_pair(r.v.y)}}; }
-__device__ __forceinline__ Chan<8> widen(const Raw<__nv_bfloat16, 8> &r) {
-    return {{bf16_pair(r.v.x), bf16_pair(r.v.y), bf16_pair(r.v.z), bf16_pair(r.v.w)}};
-}
-
-__device__ __forceinline__ void narrow(Raw<float, 1> &r, const Chan<1> &c) { r.v = halves(c.p[0]).x; }
-__device__ __forceinline__ void narrow(Raw<float, 2> &r, const Chan<2> &c) { r.v = halves(c.p[0]); }
-__device__ __forceinline__ void narrow(Raw<float, 4> &r, const Chan<4> &c) {
-    const float2 a = halves(c.p[0]), b = halves(c.p[1]);
-    r.v = make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 1> &r, const Chan<1> &c) { r.v = __float2bfloat16_rn(halves(c.p[0]).x); }
-__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 2> &r, const Chan<2> &c) { r.v = pair_bf16(c.p[0]); }
-__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 4> &r, const Chan<4> &c) {
-    r.v = make_uint2(pair_bf16(c.p[0]), pair_bf16(c.p[1]));
-}
-__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 8> &r, const Chan<8> &c) {
-    r.v = make_uint4(pair_bf16(c.p[0]), pair_bf16(c.p[1]), pair_bf16(c.p[2]), pair_bf16(c.p[3]));
-}
-
-template <typename T, int V> __device__ __forceinline__ Raw<T, V> load(const T *p) {
-    return *reinterpret_cast<const Raw<T, V> *>(p);
-}
-template <typename T, int V> __device__ __forceinline__ void store(T *p, const Chan<V> &c) {
-    Raw<T, V> r;
-    narrow(r, c);
-    *reinterpret_cast<Raw<T, V> *>(p) = r;
-}
-template <int V> __device__ __forceinline__ Chan<V> none() {
-    Chan<V> c;
-#pragma unroll
-    for (int i = 0; i < Chan<V>::N; ++i) c.p[i] = 0;
-    return c;
-}
-template <int V> __device__ __forceinline__ void fma_to(Chan<V> &acc, const Chan<V> &a, const Chan<V> &b) {
-#pragma unroll
-    for (int i = 0; i < Chan<V>::N; ++i) acc.p[i] = fma2(a.p[i], b.p[i], acc.p[i]);
-}
-
-template <typename T, int V> __device__ __forceinline__ Chan<V> silu(const Chan<V> &a) {
-    Chan<V> y;
-#pragma unroll
-    for (int i = 0; i < Chan<V>::N; ++i) {
-        const float2 f = halves(a.p[i]);
-        y.p[i] = mul2(a.p[i], pair(sigmoid<T>(f.x), V > 1 ? sigmoid<T>(f.y) : 0.f));
-    }
-    return y;
-}
-// dy silu'(a) = dy s (1 + a (1 - s)), s = sigmoid(a)
-template <typename T, int V> __device__ __forceinline__ Chan<V> silu_grad(const Chan<V> &a, const Chan<V> &dy) {
-    Chan<V> r;
-#pragma unroll
-    for (int i = 0; i < Chan<V>::N; ++i) {
-        const float2 f = halves(a.p[i]);
-        const uint64_t s = pair(sigmoid<T>(f.x), V > 1 ? sigmoid<T>(f.y) : 0.f);
-        const uint64_t one = pair(1.f, 1.f), q = fma2(s, pair(-1.f, -1.f), one);
-        r.p[i] = mul2(mul2(dy.p[i], s), fma2(a.p[i], q, one));
-    }
-    return r;
-}
 
 // The taps of V channels; element (channel, tap) at w[channel * W + tap].
 template <int W, int V> __device__ __forceinline__ void load_taps(Chan<V> (&w)[W], const float *p) {
@@ -128,14 +43,6 @@ template <int W, int V> __device__ __forceinline__ void load_taps(Chan<V> (&w)[W
 #pragma unroll
         for (int i = 0; i < Chan<V>::N; ++i) w[t].p[i] = pair(f[2 * i * W + t], V > 1 ? f[(2 * i + 1) * W + t] : 0.f);
 }
-template <int V> __device__ __forceinline__ Chan<V> load_bias(const float *p) {
-    Chan<V> b = none<V>();
-    if (p)
-#pragma unroll
-        for (int i = 0; i < Chan<V>::N; ++i) b.p[i] = pair(p[2 * i], V > 1 ? p[2 * i + 1] : 0.f);
-    return b;
-}
-
 // Rows `t` of a chain, or of the state before it (t < 0); zero without a state.
 template <typename T, int V>
 __device__ __forceinline__ Chan<V> row_at(const T *x, const T *state, int64_t t, int W, int d) {
@@ -143,8 +50,39 @@ __device__ __forceinline__ Chan<V> row_at(const T *x, const T *state, int64_t t,
     return state ? widen(load<T, V>(state + (t + W - 1) * d)) : none<V>();
 }
 
+// The next rows of a strip in shared memory: kStages turns of W rows of N arrays, each thread in slots of its
+// own.  (Two bytes are no copy's size: such rows are read from memory when asked for.)
+constexpr int kStages = 3;
+template <typename T, int V, int W, int N> struct Stage {
+    static constexpr int BYTES = V * (int)sizeof(T);
+    static constexpr bool COPY = BYTES >= 4;
+    uint4 *slots;
+    int put = 0, at = 0;
+    static constexpr int bytes() { return COPY ? kStages * N * W * kBlock * BYTES : 0; }
+    __device__ __forceinline__ Raw<T, V> *slot(int s, int a, int u) const {
+        return reinterpret_cast<Raw<T, V> *>(slots) + ((s * N + a) * W + u) * kBlock + threadIdx.x;
+    }
+    // Rows 0 .. left - 1 of those from `p` on into array a of the stage that is put next; the last array moves on.
+    __device__ __forceinline__ void fetch(int a, const T *p, int d, int left) {
+        if constexpr (COPY) {
+#pragma unroll
+            for (int u = 0; u < W; ++u)
+                if (u < left) copy_async<BYTES>(slot(put, a, u), p + u * d);
+            if (a == N - 1 && ++put == kStages) put = 0;
+        }
+    }
+    __device__ __forceinline__ Chan<V> get(int a, int u, const T *p) const {
+        if constexpr (COPY) return widen(*slot(at, a, u));
+        else return widen(load<T, V>(p));
+    }
+    __device__ __forceinline__ void next() {
+        if (++at == kStages) at = 0;
+    }
+};
+
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kBlock, W * V * sizeof(T) <= 64 ? 2 : 1) conv_kernel(ConvArgs a, uint32_t strip, uint32_t strips, uint32_t cols) {
+    extern __shared__ uint4 slots[];
     const uint32_t id = blockIdx.x * (uint32_t)kBlock + threadIdx.x;
     const uint32_t s = id / cols, cv = id % cols, st = s % strips;
     const int64_t chain = s / strips;
@@ -178,33 +116,40 @@ __global__ void __launch_bounds__(kBlock, W * V * sizeof(T) <= 64 ? 2 : 1) conv_
     if (t0 < end) {
         Chan<V> w[W];
         load_taps<W, V>(w, a.weight + ((int64_t)h * d + c0) * W);
-        const Chan<V> bias = load_bias<V>(a.bias ? a.bias + (int64_t)h * d + c0 : nullptr);
-        Raw<T, V> next[W];
-        const T *from = x + (int64_t)t0 * d;   // of the rows to fetch
+        const Chan<V> bias = param<V>(a.bias, (int64_t)h * d + c0, 0.f);
+        Stage<T, V, W, 1> in{slots};
         T *to = y + (int64_t)t0 * d;
-        auto fetch = [&](int t) {
-#pragma unroll
-            for (int u = 0; u < W; ++u)
-                if (t + u < end) next[u] = load<T, V>(from + u * d);
+        int ask = t0;                          // of the rows to fetch
+        const T *from = x + (int64_t)t0 * d;
+        auto fetch = [&]() {
+            in.fetch(0, from, d, end - ask);
+            copies_commit();
             from += W * d;
+            ask += W;
         };
-        fetch(t0);
-#pragma unroll 1
-        for (int t = t0; t < end; t += W, to += W * d) {
-            Raw<T, V> now[W];
-#pragma unroll
-            for (int u = 0; u < W; ++u) now[u] = next[u];
-            fetch(t + W);
+        auto turn = [&](int t, auto whole) {   // W tokens from t on
 #pragma unroll
             for (int u = 0; u < W; ++u) {
-                win[u] = widen(now[u]);
+                if (!whole.value && t + u >= end) break;
+                win[u] = in.get(0, u, x + (int64_t)(t + u) * d);
                 Chan<V> r = bias;
 #pragma unroll
-                for (int i = 0; i < W; ++i) fma_to(r, w[i], win[(u + 1 + i) % W]);
-                if (a.silu) r = silu<T, V>(r);
-                if (t + u < end) store<T, V>(to + u * d, r);
+                for (int i = 0; i < W; ++i) r = fma_n(w[i], win[(u + 1 + i) % W], r);
+                if (a.silu) r = mul_n(r, sigmoid_n<T>(r));
+                store<T, V>(to + u * d, r);
             }
+        };
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) fetch();
+#pragma unroll 1
+        for (int t = t0; t < end; t += W, to += W * d) {
+            copies_wait<kStages - 1>();
+            if (t + W <= end) turn(t, std::true_type{});
+            else turn(t, std::false_type{});
+            fetch();
+            in.next();
         }
+        copies_wait<0>();
     }
     if (a.zero_rest)
         for (int t = t0 > n ? t0 : n; t < t1; ++t) store<T, V>(y + (int64_t)t * d, none<V>());
@@ -216,6 +161,7 @@ template <typename T, int V, int W>
 __global__ void __launch_bounds__(kBlock, V == 2 && W > 4 ? 1 : 2)
 conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint32_t groups) {
     constexpr int NW = kBlock / 32;
+    extern __shared__ uint4 slots[];
     __shared__ float part[NW][32][V * (W + 1)];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cl = lane & (lanes - 1);
     const int h = (int)(blockIdx.y / groups), d = a.d;
@@ -227,7 +173,7 @@ conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint3
     Chan<V> bias = none<V>();
     if (mine) {
         load_taps<W, V>(w, a.weight + ((int64_t)h * d + c0) * W);
-        bias = load_bias<V>(a.bias ? a.bias + (int64_t)h * d + c0 : nullptr);
+        bias = param<V>(a.bias, (int64_t)h * d + c0, 0.f);
     }
     const uint32_t parts = 32u / lanes, step = gridDim.x * NW * parts;
     const uint32_t total = (uint32_t)a.B * strips;
@@ -251,64 +197,70 @@ conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint3
             win[i] = row_at<T, V>(x, state, t0 + i - W, W, d);
             da[i] = none<V>();
         }
-        Raw<T, V> nx[W], ny[W];
+        Stage<T, V, W, 2> in{slots};
         const T *fx = x + (int64_t)t0 * d, *fy = dy + (int64_t)t0 * d;   // of the rows to fetch
         T *to = dx + (int64_t)(t0 - (W - 1)) * d;                        // where the next row leaves to
-        auto fetch = [&](int t) {
-#pragma unroll
-            for (int u = 0; u < W; ++u)
-                if (t + u < n) {
-                    nx[u] = load<T, V>(fx + u * d);
-                    ny[u] = load<T, V>(fy + u * d);
-                }
+        int ask = t0;
+        const int stop = (end > t0 ? end : t0) + W - 1;                  // rows up to end - 1 leave at t = end + W - 2
+        auto fetch = [&]() {
+            const int left = (n < stop ? n : stop) - ask;
+            in.fetch(0, fx, d, left);
+            in.fetch(1, fy, d, left);
+            copies_commit();
             fx += W * d;
             fy += W * d;
+            ask += W;
         };
-        fetch(t0);
-        const int stop = (end > t0 ? end : t0) + W - 1;      // rows up to end - 1 leave at t = end + W - 2
-#pragma unroll 1
-        for (int t = t0; t < stop; t += W, to += W * d) {
-            Raw<T, V> mx[W], my[W];
+        // W tokens from t on; `whole`: all of them are the strip's, and so are the rows that leave, none of which goes
+        // on into the state behind the chain (those leave with t >= n)
+        auto turn = [&](int t, auto whole) {
+            constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
             for (int u = 0; u < W; ++u) {
-                mx[u] = nx[u];
-                my[u] = ny[u];
-            }
-            if (t + W < stop) fetch(t + W);
-#pragma unroll
-            for (int u = 0; u < W; ++u) {
-                const bool on = t + u < n;
-                win[u] = on ? widen(mx[u]) : none<V>();
-                da[u] = on ? widen(my[u]) : none<V>();
+                if (!ALL && t + u >= stop) break;
+                const bool on = ALL || t + u < n;
+                win[u] = on ? in.get(0, u, x + (int64_t)(t + u) * d) : none<V>();
+                da[u] = on ? in.get(1, u, dy + (int64_t)(t + u) * d) : none<V>();
                 if (a.silu) {
                     Chan<V> r = bias;
 #pragma unroll
-                    for (int i = 0; i < W; ++i) fma_to(r, w[i], win[(u + 1 + i) % W]);
-                    if (on) da[u] = silu_grad<T, V>(r, da[u]);
+                    for (int i = 0; i < W; ++i) r = fma_n(w[i], win[(u + 1 + i) % W], r);
+                    const Chan<V> s = sigmoid_n<T>(r), slope = silu_slope(r, s, mul_n(r, s));
+                    if (on) da[u] = mul_n(da[u], slope);
                 }
-                if (t + u < end) {
+                if (ALL || t + u < end) {
 #pragma unroll
-                    for (int i = 0; i < W; ++i) fma_to(dw[i], da[u], win[(u + 1 + i) % W]);
-#pragma unroll
-                    for (int i = 0; i < Chan<V>::N; ++i) db.p[i] = add2(db.p[i], da[u].p[i]);
+                    for (int i = 0; i < W; ++i) dw[i] = fma_n(da[u], win[(u + 1 + i) % W], dw[i]);
+                    db = add_n(db, da[u]);
                 }
-                const int s = t + u - (W - 1);               // the row that leaves
-                Chan<V> r = none<V>();
+                const int s = t + u - (W - 1);                   // the row that leaves
+                Chan<V> r = mul_n(w[0], da[u]);
 #pragma unroll
-                for (int i = 0; i < W; ++i) fma_to(r, w[i], da[(u - i + W) % W]);
-                const int q = s - n + W - 1;                 // its place in the state behind the chain
-                if (dso && q >= 0 && q < W - 1 && s < end) {
-                    const Chan<V> e = widen(load<T, V>(dso + q * d));
-#pragma unroll
-                    for (int i = 0; i < Chan<V>::N; ++i) r.p[i] = add2(r.p[i], e.p[i]);
+                for (int i = 1; i < W; ++i) r = fma_n(w[i], da[(u - i + W) % W], r);
+                if (ALL) {
+                    store<T, V>(to + u * d, r);
+                    continue;
                 }
+                const int q = s - n + W - 1;                     // its place in the state behind the chain
+                if (dso && q >= 0 && q < W - 1 && s < end) r = add_n(r, widen(load<T, V>(dso + q * d)));
                 if (s >= t0) {
                     if (s < end) store<T, V>(to + u * d, r);
                 } else if (st == 0 && ds && s < 0) {
                     store<T, V>(ds + (s + W - 1) * d, r);
                 }
             }
+        };
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) fetch();
+#pragma unroll 1
+        for (int t = t0; t < stop; t += W, to += W * d) {
+            copies_wait<kStages - 1>();
+            if (t >= t0 + W - 1 && t + W <= end) turn(t, std::true_type{});
+            else turn(t, std::false_type{});
+            fetch();
+            in.next();
         }
+        copies_wait<0>();
     }
     let_next_grid_start();
     if (!a.ws) return;
@@ -317,8 +269,7 @@ conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint3
     for (int i = 0; i <= W; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const float2 f = halves(i < W ? dw[i].p[e / 2] : db.p[e / 2]);
-            float z = e & 1 ? f.y : f.x;
+            float z = element(i < W ? dw[i] : db, e);
             for (int o = lanes; o < 32; o <<= 1) z += __shfl_xor_sync(~0u, z, o);
             part[warp][lane][e * (W + 1) + i] = z;
         }
@@ -362,10 +313,10 @@ __global__ void __launch_bounds__(kBlock) conv_step_kernel(ConvStepArgs a, uint3
     row[W - 1] = load<T, V>(static_cast<const T *>(a.x) + chain * d + c0);
     Chan<V> w[W];
     load_taps<W, V>(w, a.weight + ((int64_t)h * d + c0) * W);
-    Chan<V> r = load_bias<V>(a.bias ? a.bias + (int64_t)h * d + c0 : nullptr);
+    Chan<V> r = param<V>(a.bias, (int64_t)h * d + c0, 0.f);
 #pragma unroll
-    for (int i = 0; i < W; ++i) fma_to(r, w[i], widen(row[i]));
-    if (a.silu) r = silu<T, V>(r);
+    for (int i = 0; i < W; ++i) r = fma_n(w[i], widen(row[i]), r);
+    if (a.silu) r = mul_n(r, sigmoid_n<T>(r));
     store<T, V>(static_cast<T *>(a.y) + chain * d + c0, r);
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) *reinterpret_cast<Raw<T, V> *>(state + (int64_t)i * d) = row[i + 1];
@@ -410,15 +361,24 @@ template <typename T, int V, int W> cudaError_t run(const ConvArgs &a, cudaStrea
     const int64_t cols = a.d / V;
     const uint32_t strip = strip_of(a.n_chains * cols, a.T, 1024), strips = (uint32_t)((a.T + strip - 1) / strip);
     const int64_t n = a.n_chains * strips * cols;
-    conv_kernel<T, V, W><<<(unsigned)((n + kBlock - 1) / kBlock), kBlock, 0, s>>>(a, strip, strips, (uint32_t)cols);
+    constexpr int smem = Stage<T, V, W, 1>::bytes();
+    auto k = conv_kernel<T, V, W>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(k, smem, done);
+    if (e != cudaSuccess) return e;
+    k<<<(unsigned)((n + kBlock - 1) / kBlock), kBlock, smem, s>>>(a, strip, strips, (uint32_t)cols);
     return cudaGetLastError();
 }
 
 template <typename T, int V, int W> cudaError_t run(const ConvBwdArgs &a, cudaStream_t s) {
     const BwdShape p = bwd_shape(a.B, a.H, a.T, a.d, V);
-    conv_bwd_kernel<T, V, W><<<dim3(p.slices, a.H * p.groups), kBlock, 0, s>>>(a, p.strip, p.strips, p.lanes, p.groups);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.ws) return e;
+    constexpr int smem = Stage<T, V, W, 2>::bytes();
+    auto k = conv_bwd_kernel<T, V, W>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(k, smem, done);
+    if (e != cudaSuccess) return e;
+    k<<<dim3(p.slices, a.H * p.groups), kBlock, smem, s>>>(a, p.strip, p.strips, p.lanes, p.groups);
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.ws) return e;
     const int64_t count = (int64_t)a.H * a.d * (W + 1);
     return launch_after(conv_sum_kernel, sum_grid(count), kSumCols * kSumShares, 0, s, true,
                         (const float *)a.ws, (int)p.slices, count, W, a.dweight, a.dbias);

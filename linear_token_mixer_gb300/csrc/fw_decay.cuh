@@ -190,21 +190,6 @@ __device__ __forceinline__ int64_t group_chain(int64_t chain, int H, int G) {
     return chain / H * G + chain % H / (H / G);
 }
 
-// 1 / (1 + exp(-a)) for rows of type T: two special-function operations.  bf16 rows take the fast exponential,
-// whose argument's rounding costs |a| 2^-24 relative (a thousandth of the rows' own rounding where it matters); fp32 rows
-// put back what the product -a log2(e) loses to rounding.
-template <typename T> __device__ __forceinline__ float sigmoid(float a) {
-    if constexpr (sizeof(T) == 4) {
-        const float l = -1.44269504f, t = a * l;
-        const float e = exp2f(t);
-        // (an infinity, and what underflows, as they are: 0.693147 (t' - t) with t' = a log2(e) unrounded)
-        const float r = fabsf(t) < 128.f ? fmaf(e, 0.693147181f * fmaf(a, l, -t) - 1.33e-8f * a, e) : e;
-        return __fdividef(1.f, 1.f + r);
-    } else {
-        return __fdividef(1.f, 1.f + __expf(-a));
-    }
-}
-
 // Tokens of a chain: T, or the batch row's length clamped to [0, T].
 __device__ __forceinline__ int64_t chain_len(const int32_t *lens, int64_t chain, int H, int64_t T) {
     if (!lens) return T;

@@ -18,92 +18,25 @@
 // partial row of sums and a second kernel adds them in a fixed order.
 #include "fw_gated_norm.cuh"
 #include "fw_partial.cuh"
+#include "fw_rows.cuh"
 
 namespace fw {
 namespace {
 
-template <typename T, int V> struct Raw;
-template <> struct Raw<float, 1> { float v; };
-template <> struct Raw<float, 2> { float2 v; };
-template <> struct Raw<float, 4> { float4 v; };
-template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 v; };
-template <> struct Raw<__nv_bfloat16, 2> { uint32_t v; };
-template <> struct Raw<__nv_bfloat16, 4> { uint2 v; };
-template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
-
-__device__ __forceinline__ void unpack(uint32_t x, float &a, float &b) {
-    a = __uint_as_float(x << 16);
-    b = __uint_as_float(x & 0xffff0000u);
-}
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ void widen(const Raw<float, 1> &r, float (&x)[1]) { x[0] = r.v; }
-__device__ __forceinline__ void widen(const Raw<float, 2> &r, float (&x)[2]) { x[0] = r.v.x; x[1] = r.v.y; }
-__device__ __forceinline__ void widen(const Raw<float, 4> &r, float (&x)[4]) {
-    x[0] = r.v.x; x[1] = r.v.y; x[2] = r.v.z; x[3] = r.v.w;
-}
-__device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 1> &r, float (&x)[1]) { x[0] = __bfloat162float(r.v); }
-__device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 2> &r, float (&x)[2]) { unpack(r.v, x[0], x[1]); }
-__device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 4> &r, float (&x)[4]) {
-    unpack(r.v.x, x[0], x[1]); unpack(r.v.y, x[2], x[3]);
-}
-__device__ __forceinline__ void widen(const Raw<__nv_bfloat16, 8> &r, float (&x)[8]) {
-    unpack(r.v.x, x[0], x[1]); unpack(r.v.y, x[2], x[3]); unpack(r.v.z, x[4], x[5]); unpack(r.v.w, x[6], x[7]);
-}
-__device__ __forceinline__ void narrow(Raw<float, 1> &r, const float (&x)[1]) { r.v = x[0]; }
-__device__ __forceinline__ void narrow(Raw<float, 2> &r, const float (&x)[2]) { r.v = make_float2(x[0], x[1]); }
-__device__ __forceinline__ void narrow(Raw<float, 4> &r, const float (&x)[4]) { r.v = make_float4(x[0], x[1], x[2], x[3]); }
-__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 1> &r, const float (&x)[1]) { r.v = __float2bfloat16_rn(x[0]); }
-__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 2> &r, const float (&x)[2]) { r.v = pack(x[0], x[1]); }
-__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 4> &r, const float (&x)[4]) {
-    r.v = make_uint2(pack(x[0], x[1]), pack(x[2], x[3]));
-}
-__device__ __forceinline__ void narrow(Raw<__nv_bfloat16, 8> &r, const float (&x)[8]) {
-    r.v = make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
-}
-template <typename T, int V> __device__ __forceinline__ Raw<T, V> load(const void *p, int64_t at) {
-    return *reinterpret_cast<const Raw<T, V> *>(static_cast<const T *>(p) + at);
-}
-template <typename T, int V> __device__ __forceinline__ void store(void *p, int64_t at, const float (&x)[V]) {
-    Raw<T, V> r;
-    narrow(r, x);
-    *reinterpret_cast<Raw<T, V> *>(static_cast<T *>(p) + at) = r;
-}
-// V floats of a parameter; `other` where it is not given.
-template <int V> __device__ __forceinline__ void param(const float *p, int64_t at, float other, float (&x)[V]) {
-    if (!p) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = other;
-    } else if constexpr (V % 4 == 0) {
-#pragma unroll
-        for (int e = 0; e < V; e += 4) {
-            const float4 q = __ldg(reinterpret_cast<const float4 *>(p + at + e));
-            x[e] = q.x; x[e + 1] = q.y; x[e + 2] = q.z; x[e + 3] = q.w;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = __ldg(p + at + e);
-    }
-}
-
+using namespace fw::rows;
 
 constexpr int kEach = 8;                       // elements of a row a thread
 
+// Blocks of an SM, of R threads a row, forward (80 or 64 registers a thread) and backward (128 or 64).
+constexpr int fwd_blocks(int R) { return R < 512 ? 3 : R < 1024 ? 2 : 1; }
+constexpr int bwd_blocks(int R) { return R < 512 ? 2 : 1; }
 template <int R> constexpr int block_of() { return R < 256 ? 256 : R; }
 
-template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src) {
-    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
-    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest `left` groups of copies have landed.
 __device__ __forceinline__ void copies_wait(int left) {
-    if (left == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+    if (left == 0) fw::rows::copies_wait<0>();
+    else if (left == 1) fw::rows::copies_wait<1>();
+    else fw::rows::copies_wait<2>();
 }
 
 // The sums of N values over the R threads that hold a row, in every one of them.  All threads of the block.
@@ -121,24 +54,30 @@ template <int R, int N> __device__ __forceinline__ void row_sums(float (&z)[N], 
 #pragma unroll
             for (int i = 0; i < N; ++i) red[i * ALL + warp] = z[i];
         __syncthreads();
+        if constexpr (NW <= 4) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            z[i] = 0.f;
+            for (int i = 0; i < N; ++i) {
+                z[i] = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) z[i] += red[i * ALL + first + w];
+                for (int w = 0; w < NW; ++w) z[i] += red[i * ALL + first + w];
+            }
+        } else {                               // (a warp reads them once, not each thread all of them)
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = red[i * ALL + first + (threadIdx.x & (NW - 1))];
+#pragma unroll
+            for (int o = NW / 2; o; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < N; ++i) z[i] += __shfl_xor_sync(~0u, z[i], o);
         }
     }
 }
 
-__device__ __forceinline__ int64_t row_of(const GatedIn &in, uint32_t group, uint32_t m) {
-    if (in.groups == 1) return m;
-    return ((int64_t)(m / (uint32_t)in.inner) * in.groups + group) * in.inner + m % (uint32_t)in.inner;
-}
-
-// The rows that a thread works on, up to `stages` of them ahead in its slots of shared memory: `n` arrays, K vectors
-// each.  (Elements of two bytes are no copy's size: those are read from memory when asked for.)
+// The columns of a thread, in K parts of E elements that are worked on at once, and the rows that it works on,
+// up to `stages` of them ahead in its slots of shared memory, N arrays each.  V elements a load; where that is
+// one, the two of a part lie R columns apart and the second may be behind the row's end.  (Elements of two bytes
+// are no copy's size: those are read from memory when asked for.)
 template <typename T, int V, int R, int N> struct Ahead {
-    static constexpr int BYTES = V * (int)sizeof(T), K = kEach / V;
+    static constexpr int E = V > 1 ? V : 2, K = kEach / E, BYTES = V * (int)sizeof(T);
     static constexpr bool COPY = BYTES >= 4;
     const void *src[N];
     Raw<T, V> *slots;
@@ -146,10 +85,13 @@ template <typename T, int V, int R, int N> struct Ahead {
     int64_t at;                                // of the row at hand
     int stage = 0;
 
-    __device__ __forceinline__ Raw<T, V> *slot(int s, int a, int k) const {
-        return slots + ((s * N + a) * K + k) * block_of<R>() + threadIdx.x;
+    __device__ __forceinline__ int column(int k, int e = 0) const {
+        return V > 1 ? (k * R + lane) * V + e : (k * E + e) * R + lane;
     }
-    __device__ __forceinline__ int column(int k) const { return (k * R + lane) * V; }
+    __device__ __forceinline__ bool has(int k, int e = 0) const { return column(k, e) < width; }
+    __device__ __forceinline__ Raw<T, V> *slot(int s, int a, int i) const {
+        return slots + ((s * N + a) * (kEach / V) + i) * block_of<R>() + threadIdx.x;
+    }
     // Copies of a row into a stage, a group of them whether there is a row or not.
     __device__ __forceinline__ void fetch(int s, bool live, int64_t row_at) {
         if constexpr (COPY) {
@@ -158,15 +100,65 @@ template <typename T, int V, int R, int N> struct Ahead {
                 for (int a = 0; a < N; ++a)
                     if (src[a])
 #pragma unroll
-                        for (int k = 0; k < K; ++k)
-                            if (column(k) < width)
-                                copy_async<BYTES>(slot(s, a, k), static_cast<const T *>(src[a]) + row_at + column(k));
+                        for (int i = 0; i < kEach / V; ++i) {
+                            const int c = V > 1 ? column(i) : column(i / E, i % E);
+                            if (c < width) copy_async<BYTES>(slot(s, a, i), static_cast<const T *>(src[a]) + row_at + c);
+                        }
             copies_commit();
         }
     }
-    __device__ __forceinline__ void get(int a, int k, float (&x)[V]) const {
-        if constexpr (COPY) widen(*slot(stage, a, k), x);
-        else widen(load<T, V>(src[a], at + column(k)), x);
+    __device__ __forceinline__ Chan<E> get(int a, int k) const {
+        if constexpr (V > 1) return widen(*slot(stage, a, k));
+        else {
+            float x[2] = {0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (has(k, e)) {
+                    if constexpr (COPY) x[e] = to_f32(slot(stage, a, k * E + e)->v);
+                    else x[e] = to_f32(static_cast<const T *>(src[a])[at + column(k, e)]);
+                }
+            return {{pair(x[0], x[1])}};
+        }
+    }
+    __device__ __forceinline__ void put(void *p, int k, const Chan<E> &x) const {
+        T *const to = static_cast<T *>(p) + at;
+        if constexpr (V > 1) store<T, V>(to + column(k), x);
+        else
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (has(k, e)) to[column(k, e)] = from_f32<T>(element(x, e));
+    }
+    // A parameter's columns; `other` where it is not given.
+    __device__ __forceinline__ Chan<E> of(const float *p, int k, float other) const {
+        if constexpr (V > 1) return param<V>(p, column(k), other);
+        else {
+            float x[2] = {other, other};
+            if (p)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (has(k, e)) x[e] = p[column(k, e)];
+            return {{pair(x[0], x[1])}};
+        }
+    }
+};
+
+// Every step-th row of a group from the m-th on, without a division a row: m = outer inner + i.
+struct Walk {
+    uint32_t m, outer, i, step, step_outer, step_i;
+    __device__ __forceinline__ Walk(const GatedIn &in, uint32_t m_, uint32_t step_)
+        : m(m_), outer(m_ / (uint32_t)in.inner), i(m_ % (uint32_t)in.inner), step(step_),
+          step_outer(step_ / (uint32_t)in.inner), step_i(step_ % (uint32_t)in.inner) {}
+    __device__ __forceinline__ int64_t row(const GatedIn &in) const {
+        return ((int64_t)outer * in.groups + blockIdx.y) * in.inner + i;
+    }
+    __device__ __forceinline__ void next(const GatedIn &in) {
+        m += step;
+        outer += step_outer;
+        i += step_i;
+        if (i >= (uint32_t)in.inner) {
+            i -= (uint32_t)in.inner;
+            ++outer;
+        }
     }
 };
 
@@ -176,251 +168,190 @@ template <typename T, int V, int R, int N, typename F>
 __device__ __forceinline__ void over_rows(Ahead<T, V, R, N> &ahead, const GatedIn &in, uint32_t group_rows, F work) {
     constexpr int RPB = block_of<R>() / R;
     const uint32_t step = gridDim.x * RPB;
-    auto fetch = [&](int s, uint32_t m0) {
-        const uint32_t m = m0 + threadIdx.x / R;
-        const bool live = m0 < group_rows && m < group_rows;
-        ahead.fetch(s, live, live ? row_of(in, blockIdx.y, m) * in.width : 0);
+    uint32_t m0 = blockIdx.x * RPB;
+    Walk at(in, m0 + threadIdx.x / R, step), ask = at;
+    auto fetch = [&](int s) {
+        const bool live = ask.m < group_rows;
+        ahead.fetch(s, live, live ? ask.row(in) * in.width : 0);
+        ask.next(in);
     };
-    uint32_t m0 = blockIdx.x * RPB, ask = m0;
-    for (int s = 0; s < ahead.stages; ++s, ask += step) fetch(s, ask);
-    int64_t row = m0 < group_rows ? row_of(in, blockIdx.y, min(m0 + threadIdx.x / R, group_rows - 1)) : 0;
+    for (int s = 0; s < ahead.stages; ++s) fetch(s);
+    int64_t row = at.m < group_rows ? at.row(in) : 0;
     for (; m0 < group_rows; m0 += step) {
-        const bool live = m0 + threadIdx.x / R < group_rows;
-        const uint32_t m = m0 + step + threadIdx.x / R;
-        const int64_t next = m < group_rows ? row_of(in, blockIdx.y, m) : -1;
+        const bool live = at.m < group_rows;
+        at.next(in);
+        const int64_t next = at.m < group_rows ? at.row(in) : -1;
         ahead.at = row * in.width;
         if (Ahead<T, V, R, N>::COPY) copies_wait(ahead.stages - 1);
         work(live, row, next);
-        fetch(ahead.stage, ask);
+        fetch(ahead.stage);
         row = next < 0 ? row : next;
-        ask += step;
         if (++ahead.stage == ahead.stages) ahead.stage = 0;
     }
     if (Ahead<T, V, R, N>::COPY) copies_wait(0);
 }
 
 template <typename T, int V, int R>
-__global__ void __launch_bounds__(block_of<R>(), 1) gated_kernel(GatedArgs a, uint32_t group_rows, int stages) {
-    constexpr int K = kEach / V, BLOCK = block_of<R>();
+__global__ void __launch_bounds__(block_of<R>(), fwd_blocks(R)) gated_kernel(GatedArgs a, uint32_t group_rows, int stages) {
+    using Rows = Ahead<T, V, R, 3>;
+    constexpr int K = Rows::K, E = Rows::E, BLOCK = block_of<R>();
     extern __shared__ uint4 slots[];
     __shared__ float red[R > 32 ? BLOCK / 32 : 1];
     const GatedIn &in = a.in;
-    Ahead<T, V, R, 3> ahead{{in.x, in.gate, in.residual}, reinterpret_cast<Raw<T, V> *>(slots), stages, in.width,
-                            (int)(threadIdx.x % R), 0};
+    Rows rows{{in.x, in.gate, in.residual}, reinterpret_cast<Raw<T, V> *>(slots), stages, in.width, (int)(threadIdx.x % R), 0};
     const float inv = 1.f / (float)in.width;
     const int64_t pat = (int64_t)blockIdx.y * in.width;
-    float w[K][V], b[K][V], f[K][V];
+    const float *const weight = in.weight ? in.weight + pat : nullptr, *const bias = in.bias ? in.bias + pat : nullptr,
+                *const scale = in.scale ? in.scale + pat : nullptr;
+    Chan<E> w[K], b[K], f[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = ahead.column(k);
-        if (c < in.width) {
-            param<V>(in.weight, pat + c, 1.f, w[k]);
-            param<V>(in.bias, pat + c, 0.f, b[k]);
-            param<V>(in.scale, pat + c, 1.f, f[k]);
+    for (int k = 0; k < K; ++k)
+        if (rows.has(k)) {
+            w[k] = rows.of(weight, k, 1.f);
+            b[k] = rows.of(bias, k, 0.f);
+            f[k] = rows.of(scale, k, 1.f);
         }
-    }
-    over_rows(ahead, in, group_rows, [&](bool live, int64_t row, int64_t) {
-        float s[K][V], sum[1] = {0.f};
+    over_rows(rows, in, group_rows, [&](bool live, int64_t row, int64_t) {
+        Chan<E> s[K], part = none<E>();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = ahead.column(k);
-            if (live && c < in.width) {
-                ahead.get(0, k, s[k]);
-                if (in.residual) {
-                    float r[V];
-                    ahead.get(2, k, r);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) s[k][e] = fmaf(f[k][e], r[e], s[k][e]);
-                }
-                if (a.total) store<T, V>(a.total, ahead.at + c, s[k]);
+            s[k] = none<E>();
+            if (live && rows.has(k)) {
+                s[k] = rows.get(0, k);
+                if (in.residual) s[k] = fma_n(f[k], rows.get(2, k), s[k]);
+                if (a.total) rows.put(a.total, k, s[k]);
                 if (in.gate && !in.gate_after) {
-                    float z[V];
-                    ahead.get(1, k, z);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) s[k][e] *= z[e] * sigmoid<T>(z[e]);
+                    const Chan<E> z = rows.get(1, k);
+                    s[k] = mul_n(s[k], mul_n(z, sigmoid_n<T>(z)));
                 }
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum[0] += s[k][e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) s[k][e] = 0.f;
+                part = add_n(part, s[k]);
             }
         }
-        float mean = 0.f;
+        float sum[1] = {0.f}, mean = 0.f;
         if (!in.rms) {
+            sum[0] = total(part);
             row_sums<R>(sum, red);
             mean = sum[0] * inv;
         }
-        sum[0] = 0.f;
+        part = none<E>();
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (ahead.column(k) < in.width)
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    s[k][e] -= mean;
-                    sum[0] = fmaf(s[k][e], s[k][e], sum[0]);
+            if (rows.has(k)) {
+                if (!in.rms) {
+                    s[k] = add_n(s[k], all<E>(-mean));
+                    if (V == 1 && !rows.has(k, 1)) s[k].p[0] = pair(halves(s[k].p[0]).x, 0.f);
                 }
+                part = fma_n(s[k], s[k], part);
+            }
+        sum[0] = total(part);
         row_sums<R>(sum, red);
         const float rstd = rsqrtf(fmaf(sum[0], inv, in.eps));
         if (!live) return;
-        if (ahead.lane == 0) {
+        if (rows.lane == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = ahead.column(k);
-            if (c >= in.width) continue;
-#pragma unroll
-            for (int e = 0; e < V; ++e) s[k][e] = fmaf(s[k][e] * rstd, w[k][e], b[k][e]);
+            if (!rows.has(k)) continue;
+            s[k] = fma_n(mul_n(s[k], all<E>(rstd)), w[k], b[k]);
             if (in.gate && in.gate_after) {
-                float z[V];
-                ahead.get(1, k, z);
-#pragma unroll
-                for (int e = 0; e < V; ++e) s[k][e] *= z[e] * sigmoid<T>(z[e]);
+                const Chan<E> z = rows.get(1, k);
+                s[k] = mul_n(s[k], mul_n(z, sigmoid_n<T>(z)));
             }
-            store<T, V>(a.y, ahead.at + c, s[k]);
+            rows.put(a.y, k, s[k]);
         }
     });
 }
 
 template <typename T, int V, int R>
-__global__ void __launch_bounds__(block_of<R>(), 1) gated_bwd_kernel(GatedBwdArgs a, uint32_t group_rows, int stages) {
-    constexpr int K = kEach / V, BLOCK = block_of<R>(), RPB = BLOCK / R;
+__global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel(GatedBwdArgs a, uint32_t group_rows, int stages) {
+    using Rows = Ahead<T, V, R, 5>;
+    constexpr int K = Rows::K, E = Rows::E, BLOCK = block_of<R>(), RPB = BLOCK / R;
     extern __shared__ uint4 slots[];
     __shared__ float red[R > 32 ? 2 * BLOCK / 32 : 1];
     const GatedIn &in = a.in;
-    Ahead<T, V, R, 5> ahead{{in.x, a.dy, in.gate, in.residual, a.dtotal}, reinterpret_cast<Raw<T, V> *>(slots), stages,
-                            in.width, (int)(threadIdx.x % R), 0};
+    Rows rows{{in.x, a.dy, in.gate, in.residual, a.dtotal}, reinterpret_cast<Raw<T, V> *>(slots), stages, in.width,
+              (int)(threadIdx.x % R), 0};
     const int width = in.width;
     const float inv = 1.f / (float)width;
     const int64_t pat = (int64_t)blockIdx.y * width;
-    float sums[3][K][V];                       // of dweight, dbias, dscale
+    const float *const weight = in.weight ? in.weight + pat : nullptr, *const bias = in.bias ? in.bias + pat : nullptr,
+                *const scale = in.scale ? in.scale + pat : nullptr;
+    Chan<E> sums[3][K];                        // of dweight, dbias, dscale
 #pragma unroll
     for (int i = 0; i < 3; ++i)
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int e = 0; e < V; ++e) sums[i][k][e] = 0.f;
+        for (int k = 0; k < K; ++k) sums[i][k] = none<E>();
     float next_mean = 0.f, next_rstd = 0.f;    // of the next row
     {
-        const uint32_t m = blockIdx.x * RPB + threadIdx.x / R;
-        if (m < group_rows) {
-            const int64_t row = row_of(in, blockIdx.y, m);
+        const Walk first(in, blockIdx.x * RPB + threadIdx.x / R, 1);
+        if (first.m < group_rows) {
+            const int64_t row = first.row(in);
             if (!in.rms) next_mean = a.mean[row];
             next_rstd = a.rstd[row];
         }
     }
-    over_rows(ahead, in, group_rows, [&](bool live, int64_t row, int64_t next) {
+    Chan<E> w[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (rows.has(k)) w[k] = rows.of(weight, k, 1.f);
+    over_rows(rows, in, group_rows, [&](bool live, int64_t, int64_t next) {
         const float mean = next_mean, rstd = next_rstd;
         if (next >= 0) {
             if (!in.rms) next_mean = a.mean[next];
             next_rstd = a.rstd[next];
         }
-        float sg[K][V];                        // sigmoid of the gate
-        // n = norm(s), g and u of a vector
-        auto form = [&](int k, int c, float (&n)[V], float (&g)[V], float (&u)[V], float (&dy)[V], float (&z)[V]) {
-            ahead.get(0, k, u);
-            if (in.residual) {
-                float f[V], r[V];
-                param<V>(in.scale, pat + c, 1.f, f);
-                ahead.get(3, k, r);
-#pragma unroll
-                for (int e = 0; e < V; ++e) u[e] = fmaf(f[e], r[e], u[e]);
-            }
-            ahead.get(1, k, dy);
-            float w[V];
-            param<V>(in.weight, pat + c, 1.f, w);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                n[e] = u[e];
-                g[e] = dy[e] * w[e];
-            }
-            if (in.gate) {
-                ahead.get(2, k, z);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float act = z[e] * sg[k][e];
-                    if (in.gate_after) g[e] *= act;
-                    else n[e] *= act;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) n[e] = (n[e] - mean) * rstd;
+        auto sum_of = [&](int k) -> Chan<E> {  // u
+            const Chan<E> x = rows.get(0, k);
+            return in.residual ? fma_n(rows.of(scale, k, 1.f), rows.get(3, k), x) : x;
         };
-        float sum[2] = {0.f, 0.f};
+        Chan<E> n[K], g[K], sg[K];             // n = norm(s), g, and the sigmoid of the gate
+        Chan<E> sum_g = none<E>(), sum_gn = none<E>();
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = ahead.column(k);
-            if (live && c < width) {
-                float n[V], g[V], u[V], dy[V], z[V];
+        for (int k = 0; k < K; ++k)
+            if (live && rows.has(k)) {
+                n[k] = sum_of(k);
+                g[k] = mul_n(rows.get(1, k), w[k]);
                 if (in.gate) {
-                    ahead.get(2, k, z);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) sg[k][e] = sigmoid<T>(z[e]);
+                    const Chan<E> z = rows.get(2, k);
+                    sg[k] = sigmoid_n<T>(z);
+                    const Chan<E> act = mul_n(z, sg[k]);
+                    if (in.gate_after) g[k] = mul_n(g[k], act);
+                    else n[k] = mul_n(n[k], act);
                 }
-                form(k, c, n, g, u, dy, z);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    sum[0] += g[e];
-                    sum[1] = fmaf(g[e], n[e], sum[1]);
-                }
+                if (!in.rms) n[k] = add_n(n[k], all<E>(-mean));
+                n[k] = mul_n(n[k], all<E>(rstd));
+                sum_g = add_n(sum_g, g[k]);
+                sum_gn = fma_n(g[k], n[k], sum_gn);
             }
-        }
+        float sum[2] = {total(sum_g), total(sum_gn)};
         row_sums<R>(sum, red);
-        const float mg = in.rms ? 0.f : sum[0] * inv, mgn = sum[1] * inv;
         if (!live) return;
+        const float mg = in.rms ? 0.f : -sum[0] * inv * rstd, mgn = -sum[1] * inv * rstd;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = ahead.column(k);
-            if (c >= width) continue;
-            float n[V], g[V], u[V], dy[V], z[V], d[V];
-            form(k, c, n, g, u, dy, z);
-#pragma unroll
-            for (int e = 0; e < V; ++e) d[e] = rstd * (g[e] - mg - n[e] * mgn);
+            if (!rows.has(k)) continue;
+            // rstd (g - mean(g) - n mean(g n))
+            Chan<E> d = fma_n(n[k], all<E>(mgn), fma_n(g[k], all<E>(rstd), all<E>(mg)));
+            Chan<E> dy = rows.get(1, k);
             if (in.gate) {
-                float dz[V];
-                if (in.gate_after) {
-                    float b[V], w[V];
-                    param<V>(in.weight, pat + c, 1.f, w);
-                    param<V>(in.bias, pat + c, 0.f, b);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) dz[e] = dy[e] * fmaf(n[e], w[e], b[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) dz[e] = d[e] * u[e];
-                }
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float act = z[e] * sg[k][e];
-                    dz[e] *= sg[k][e] * (1.f + z[e] - act);    // silu'
-                    if (in.gate_after) dy[e] *= act;           // of the norm's output
-                    else d[e] *= act;
-                }
-                if (a.dgate) store<T, V>(a.dgate, ahead.at + c, dz);
+                const Chan<E> z = rows.get(2, k), act = mul_n(z, sg[k]);
+                Chan<E> dz;
+                if (in.gate_after) dz = mul_n(dy, fma_n(n[k], w[k], rows.of(bias, k, 0.f)));
+                else dz = mul_n(d, sum_of(k));
+                dz = mul_n(dz, silu_slope(z, sg[k], act));
+                if (in.gate_after) dy = mul_n(dy, act);        // of the norm's output
+                else d = mul_n(d, act);
+                if (a.dgate) rows.put(a.dgate, k, dz);
             }
-            if (a.dtotal) {
-                float t[V];
-                ahead.get(4, k, t);
-#pragma unroll
-                for (int e = 0; e < V; ++e) d[e] += t[e];
-            }
-            if (a.dx) store<T, V>(a.dx, ahead.at + c, d);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                sums[0][k][e] = fmaf(dy[e], n[e], sums[0][k][e]);
-                sums[1][k][e] += dy[e];
-            }
+            if (a.dtotal) d = add_n(d, rows.get(4, k));
+            if (a.dx) rows.put(a.dx, k, d);
+            sums[0][k] = fma_n(dy, n[k], sums[0][k]);
+            sums[1][k] = add_n(sums[1][k], dy);
             if (in.residual) {
-                float f[V], r[V];
-                param<V>(in.scale, pat + c, 1.f, f);
-                ahead.get(3, k, r);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    sums[2][k][e] = fmaf(r[e], d[e], sums[2][k][e]);
-                    f[e] *= d[e];
-                }
-                if (a.dresidual) store<T, V>(a.dresidual, ahead.at + c, f);
+                sums[2][k] = fma_n(rows.get(3, k), d, sums[2][k]);
+                if (a.dresidual) rows.put(a.dresidual, k, mul_n(d, rows.of(scale, k, 1.f)));
             }
         }
     });
@@ -435,15 +366,15 @@ __global__ void __launch_bounds__(block_of<R>(), 1) gated_bwd_kernel(GatedBwdArg
         if constexpr (RPB == 1) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (ahead.column(k) < width)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) out[i * width + ahead.column(k) + e] = sums[i][k][e];
+                for (int e = 0; e < E; ++e)
+                    if (rows.has(k, e)) out[i * width + rows.column(k, e)] = element(sums[i][k], e);
         } else {
             __syncthreads();                   // (the slots are free, or the sums before read)
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int e = 0; e < V; ++e) part[(threadIdx.x / R) * (R * kEach) + ahead.column(k) + e] = sums[i][k][e];
+                for (int e = 0; e < E; ++e) part[(threadIdx.x / R) * (R * kEach) + rows.column(k, e)] = element(sums[i][k], e);
             __syncthreads();
             for (int c = threadIdx.x; c < width; c += BLOCK) {
                 float z = 0.f;
@@ -466,37 +397,34 @@ gated_sum_kernel(const float *ws, int slices, int64_t count, int width, float *d
     });
 }
 
-// Blocks of an SM, of R threads a row.
-constexpr int blocks_an_sm(int R) { return R < 512 ? 3 : R < 1024 ? 2 : 1; }
-
 // Blocks that share the rows of a group: what the SMs hold at once, and no more than there are rows for.
-uint32_t slices_of(int64_t rows, int64_t groups, int R, int turns) {
+uint32_t slices_of(int64_t rows, int64_t groups, int R, int blocks) {
     const int64_t group_rows = rows / groups, each = R < 256 ? 256 / R : 1, most = (group_rows + each - 1) / each;
-    const int64_t s = (int64_t)kSMs * blocks_an_sm(R) * turns / groups;
+    const int64_t s = (int64_t)kSMs * blocks / groups;
     return (uint32_t)(s < 1 ? 1 : s > most ? most : s);
 }
 
 // Rows ahead, of `arrays` a block each, that leave room for the blocks of an SM.
-template <typename T, int R> int stages_of(int arrays) {
-    const int row = arrays * block_of<R>() * kEach * (int)sizeof(T), room = 216 * 1024 / blocks_an_sm(R);
+template <typename T, int R> int stages_of(int arrays, int blocks) {
+    const int row = arrays * block_of<R>() * kEach * (int)sizeof(T), room = 216 * 1024 / blocks;
     return row * 3 <= room ? 3 : row * 2 <= room ? 2 : 1;
 }
 
 template <typename T, int V, int R> cudaError_t run(const GatedArgs &a, cudaStream_t s) {
-    const int stages = stages_of<T, R>(3), smem = stages * 3 * block_of<R>() * kEach * (int)sizeof(T);
+    const int stages = stages_of<T, R>(3, fwd_blocks(R)), smem = stages * 3 * block_of<R>() * kEach * (int)sizeof(T);
     auto k = gated_kernel<T, V, R>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k, smem, done);
     if (e != cudaSuccess) return e;
-    k<<<dim3(slices_of(a.in.rows, a.in.groups, R, 1), a.in.groups), block_of<R>(), smem, s>>>(
+    k<<<dim3(slices_of(a.in.rows, a.in.groups, R, fwd_blocks(R)), a.in.groups), block_of<R>(), smem, s>>>(
         a, (uint32_t)(a.in.rows / a.in.groups), stages);
     return cudaGetLastError();
 }
 
 template <typename T, int V, int R> cudaError_t run(const GatedBwdArgs &a, cudaStream_t s) {
     const GatedIn &in = a.in;
-    const uint32_t slices = slices_of(in.rows, in.groups, R, 1);
-    const int stages = stages_of<T, R>(5), smem = stages * 5 * block_of<R>() * kEach * (int)sizeof(T);
+    const uint32_t slices = slices_of(in.rows, in.groups, R, bwd_blocks(R));
+    const int stages = stages_of<T, R>(5, bwd_blocks(R)), smem = stages * 5 * block_of<R>() * kEach * (int)sizeof(T);
     auto k = gated_bwd_kernel<T, V, R>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(k, smem, done);
@@ -542,7 +470,8 @@ template <typename A> cudaError_t by_type(const A &a, cudaStream_t s) {
 }  // namespace
 
 size_t gated_norm_workspace(int64_t rows, int64_t width, int64_t groups) {
-    return (size_t)slices_of(rows, groups, threads_of((int)width), 1) * groups * 3 * width * sizeof(float);
+    const int R = threads_of((int)width);
+    return (size_t)slices_of(rows, groups, R, bwd_blocks(R)) * groups * 3 * width * sizeof(float);
 }
 
 cudaError_t launch_gated_norm(const GatedArgs &a, cudaStream_t s) { return by_type(a, s); }
