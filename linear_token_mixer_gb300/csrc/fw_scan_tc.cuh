@@ -924,6 +924,18 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         const bool mine = w * 32 < D;
         bool ok = true;
         Ring r;
+        // SEL: the weights of the chunk at hand, those of the next on their way behind the last use of these.
+        // Thread t has tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3, u = b, b + KG, ..
+        constexpr int NU = 4 / L::KG;
+        uint64_t sw[SEL ? NU : 1][4];
+        auto fetch_weights = [&](int i) {
+            const float *from = a.sel.w + (chain * a.sel.n_chunks + chunk_id(i)) * C + 32 * b + 2 * (lane & 3);
+#pragma unroll
+            for (int x = 0; x < NU; ++x)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sw[x][c] = *reinterpret_cast<const uint64_t *>(from + 32 * L::KG * x + 8 * c);
+        };
+        if (SEL && nch > 0) fetch_weights(0);
         for (int i = 0; i < nch; ++i, r.next()) {
             const int st = r.st;
             const uint32_t ph = r.ph;
@@ -931,7 +943,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             const int nv = tokens(i);
             ok = __all_sync(~0u, wait_bar(full(st, XB_), ph, limit, s_abort));
             if (!ok) break;
-            const float *wt = SEL ? a.sel.w + (chain * a.sel.n_chunks + chunk_id(i)) * C : kw;
+            const float *wt = kw;
             if (tail) {
                 // rows behind the end may hold anything: those of B and C become zero before any
                 // product reads them (and the weights too; every warp writes the same values)
@@ -955,13 +967,14 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             }
             // ldmatrix x4: matrices (tokens +0, +8) x (rows +0, +8) of X, 16 rows a half-warp
             const uint32_t r8 = (uint32_t)lane & 7u, m = (uint32_t)lane >> 3;
+#pragma unroll (SEL ? NU : 1)
             for (int u = b; u < 4; u += L::KG) {
                 const int use = (4 * i + u) / L::KG;   // of this buffer
                 // thread t: tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3
                 uint64_t wv[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    wv[c] = *reinterpret_cast<const uint64_t *>(wt + 32 * u + 8 * c + 2 * (lane & 3));
+                    wv[c] = SEL ? sw[u / L::KG][c] : *reinterpret_cast<const uint64_t *>(wt + 32 * u + 8 * c + 2 * (lane & 3));
                 uint32_t hi[8], mid[8], lo[8];
                 auto form = [&](int h) {             // rows w * 32 + 16 h .. +15 of X
 #pragma unroll
@@ -999,6 +1012,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     if (mine) store(h);
                 }
                 if (!ok) break;
+                if (SEL && u + L::KG >= 4 && i + 1 < nch) fetch_weights(i + 1);
                 if (mine) tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();

@@ -5,7 +5,7 @@
 //
 // A prompt is the chunked scan of fw_decay_tc.cu (bf16) or fw_decay_f32.cu (fp32) with tables in place of
 // powers of one decay: select_tables forms, for every chunk of a chain, the running sum of log g to each
-// token in 64 bits (kept in two fp32 terms: differences of sums of a chunk lose nothing to their size),
+// token in two fp32 terms (differences of sums of a chunk lose nothing to their size),
 // each token's weight in the chunk's end, and the chunk's decay.  One warp a chunk, 20 bytes a token
 // written for the 4 d (bf16) or 8 d that its rows take; the scan's first tiles load meanwhile.
 //
@@ -16,6 +16,16 @@ namespace fw {
 namespace {
 
 constexpr int kTableBlock = 128;
+
+// A sum of fp32 values in two terms, hi + lo with |lo| at most half a unit of hi (48 bits; the GPU's 64-bit
+// additions are a sixteenth as fast as these four to eight fp32 ones).
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two add(const Two &a, const Two &b) {
+    const float s = a.hi + b.hi, t = s - a.hi, e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo), hi = s + e;
+    return {hi, e - (hi - s)};
+}
 
 template <int C>
 __global__ void __launch_bounds__(kTableBlock)
@@ -31,45 +41,44 @@ select_tables(GateArgs g, const int32_t *lens, int64_t n_chains, int64_t T, int 
     const int h = (int)(chain % H);
     const float rate = g.log_decay[h];
     float dt[PER];
-    double c[PER];
-    double sum = 0.0, low = 0.0, high = 0.0;  // of the logs, and their least and largest running sum
+    Two c[PER], sum{0.f, 0.f};                // of the logs, to the token
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
         const bool on = first + e < n;
         dt[e] = on ? step_of(g, chain * T + first + e, h) : 0.f;
-        const double x = on ? (double)rate * dt[e] : 0.0;
-        sum += x < -kReset ? -kReset : x;     // (NaN stays)
+        const float x = on ? rate * dt[e] : 0.f;
+        sum = add(sum, x < -kReset ? Two{-kReset, 0.f} : Two{x, on ? fmaf(rate, dt[e], -x) : 0.f});   // (NaN stays)
         c[e] = sum;
     }
-    double upto = sum;
+    Two upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += x;
+        const Two x{__shfl_up_sync(~0u, upto.hi, o), __shfl_up_sync(~0u, upto.lo, o)};
+        if (lane >= o) upto = add(x, upto);
     }
-    const double total = __shfl_sync(~0u, upto, 31), before = upto - sum;
+    const Two total{__shfl_sync(~0u, upto.hi, 31), __shfl_sync(~0u, upto.lo, 31)};
+    Two before{__shfl_up_sync(~0u, upto.hi, 1), __shfl_up_sync(~0u, upto.lo, 1)};
+    if (lane == 0) before = Two{0.f, 0.f};
+    float low = 0.f, high = 0.f;              // the least and the largest sum
     const int64_t at = id * C + lane * PER;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-        c[e] += before;
-        low = fmin(low, c[e]);
-        high = fmax(high, c[e]);
-        const double s = total - c[e];
-        const float hi = (float)c[e], sh = (float)s;
-        out_c[at + e] = make_float2(hi, (float)(c[e] - hi));
+        c[e] = add(before, c[e]);
+        low = fminf(low, c[e].hi);
+        high = fmaxf(high, c[e].hi);
+        const Two s = add(total, Two{-c[e].hi, -c[e].lo});
+        out_c[at + e] = make_float2(c[e].hi, c[e].lo);
         out_dt[at + e] = dt[e];
-        out_w[at + e] = dt[e] * exp_two(sh, (float)(s - sh));
+        out_w[at + e] = dt[e] * exp_two(s.hi, s.lo);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-        low = fmin(low, __shfl_xor_sync(~0u, low, o));
-        high = fmax(high, __shfl_xor_sync(~0u, high, o));
+        low = fminf(low, __shfl_xor_sync(~0u, low, o));
+        high = fmaxf(high, __shfl_xor_sync(~0u, high, o));
     }
-    if (lane == 0) {
-        const float hi = (float)total;
-        out_chunk[id] = make_float4(exp_two(hi, (float)(total - hi)), hi, (float)(total - hi),
-                                    low >= -24.0 && high <= 24.0 && isfinite(total) ? 1.f : 0.f);
-    }
+    if (lane == 0)
+        out_chunk[id] = make_float4(exp_two(total.hi, total.lo), total.hi, total.lo,
+                                    low >= -24.f && high <= 24.f && isfinite(total.hi) ? 1.f : 0.f);
 }
 
 constexpr int kThreads = 256;
