@@ -66,17 +66,28 @@ struct NormArgs {
     float eps;
 };
 
+// Sums of logs of decays up to which a selective scan divides within a chunk: quotients of e^40 = 2.4e17 leave the
+// scores, and their sums, 21 of fp32's and bf16's 38 decimal orders.
+constexpr float kMild = 40.f;
+
 // Steps and decays of a selective scan (see fw_select.cuh), formed ahead of it for chunks of the scan's own
 // length; n_chunks of them a chain, tokens behind a sequence's end without a step.
 struct SelectTables {
-    const float2 *c;          // [n_chains][n_chunks * C] log decay from the chunk's start to the token, in two terms
-    const float *dt;          // .. the token's step
-    const float *w;           // .. dt times the decay from the token to the chunk's end
-    const float4 *chunk;      // [n_chains][n_chunks] decay of the chunk, its log in two terms, 1 where it is mild
+    const float2 *c;          // [n_chains][n_chunks * C] log decay from the chunk's start to the token, in two terms (bf16
+                              // scans: in one, and the token's step)
+    const float *dt;          // .. the token's step (fp32 scans)
+    const float *w;           // .. dt times the decay from the token to the chunk's end (bf16 scans: in the order of
+                              // weight_place)
+    const float4 *chunk;      // [n_chains][n_chunks] decay of the chunk, its log in two terms
+    const float4 *ends;       // .. bf16 scans: c at the ends of its first three blocks of 32 tokens, and 1 where the
+                              // chunk is mild (its sums of logs stay within +-kMild)
     const float *skip;        // [H] or NULL
     int64_t n_chunks;
     int G;                    // groups of heads that share a and b
 };
+// Place of a token's weight within its chunk: the eight that a thread of the bf16 scans needs of 32 tokens, 2 t, + 1
+// of each eight, follow one another.
+__host__ __device__ constexpr int weight_place(int j) { return (j & ~31) + (j & 6) * 4 + (j & 24) / 4 + (j & 1); }
 
 struct ScanArgs {
     const void *a, *b, *c;    // [n_chains][T][d]

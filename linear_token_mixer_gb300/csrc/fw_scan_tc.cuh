@@ -39,9 +39,10 @@
 // issue slots for 38 %, DRAM at 55 %, and the rest is the roles' round trips through tensor memory and barriers.  A second CTA an
 // SM would fill it but finds no room: the tiles take 192 KB, G, O and the update 384 columns.
 // Tensor memory: G (P over it) 128 columns, O 128, the update 128, the split operand 2 x 48.
-// SEL: the decays come from tables in memory (SelectTables), by token and chunk, in place of powers of one:
-// the scores of a steep chunk by products of two decays from a block of 32 columns' end on, each at most 1,
-// and on the diagonal blocks by the decay itself; whether a chunk is mild goes by its own tables.
+// SEL: the decays come from tables in memory (SelectTables), by token and chunk, in place of powers of one.  The
+// scores of a steep chunk take the product of the decays to and from the end of the block of 32 columns before
+// a row's own, each at most 1; those of the diagonal blocks the quotient of the decays from the block's start, or
+// where that is below e^-kMild the decay itself.  Whether a chunk is mild goes by its own tables.
 // Every wait is bounded; on expiry the kernel records an error, the other roles stop at their
 // next wait, copies and MMAs in flight are drained, tensor memory is freed and the kernel exits.
 #pragma once
@@ -185,6 +186,19 @@ template <typename F> __device__ __forceinline__ void tmem_stream(uint32_t taddr
     }
 }
 
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&v)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(taddr)
+                 : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3])::"memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const float (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3])
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
                  "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -255,6 +269,11 @@ __device__ __forceinline__ float entry_state(const ScanArgs &a, const ScanArgs &
                  ws[(int64_t)s * D * D + r * D + c]);
     }
     return x;
+}
+
+// SEL: the log decay to the token before block w of a chunk's four.
+__device__ __forceinline__ float before_block(const float4 &ends, int w) {
+    return w == 0 ? 0.f : w == 1 ? ends.x : w == 2 ? ends.y : ends.z;
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
@@ -331,9 +350,9 @@ __device__ __forceinline__ void redo_rows(const ScanArgs &a, const ScanArgs &own
             float c = a.in_scale * value;
             if (SEL) {
                 const int64_t at = (chain * a.sel.n_chunks + i) * C + j;
-                const float2 z = a.sel.c[at], y = j ? a.sel.c[at - 1] : make_float2(0.f, 0.f);
-                g = exp_two(z.x - y.x, z.y - y.y);
-                c = a.sel.dt[at] * value;
+                const float2 z = a.sel.c[at];
+                g = expf(z.x - (j ? a.sel.c[at - 1].x : 0.f));
+                c = z.y * value;
             }
             bar_sync(3, N);
             float o = 0.f;
@@ -421,8 +440,8 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
     // Otherwise A X is scaled by its rows' decay on its own and the scores by g^(i-j), and nothing
     // is divided by a power of g.
     const bool mild = fabsf(lg) * C <= 24.f;   // (SEL: by the chunk)
-    const float4 *const chunk_info = SEL ? a.sel.chunk + chain * a.sel.n_chunks : nullptr;
-    const bool skips = SEL && !PRE && a.sel.skip;   // O reads C too
+    // SEL: the tables of this segment's chunks, one after the other
+    const int64_t tables = SEL ? chain * a.sel.n_chunks + sg.first : 0;
     const int x_slots = nseg;                       // workspace: nseg - 1 segment states, X0's copy
     float *const ws = own.ws + chain * x_slots * D * D;
 
@@ -464,7 +483,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             const int e = i - L::EMPTY;
             if (e >= 0 && e < L::NST * L::NT)       // B: its readers' warps (and G); C: the
                 c = e % L::NT == XB_ ? 4 * L::KG + (PRE ? 0 : 1)   // update (and P C); A: the O group's warps
-                  : e % L::NT == XC ? (PRE ? 1 : skips ? 6 : 2) : 4;
+                  : e % L::NT == XC ? (PRE ? 1 : 2) : 4;
             if (i == L::PRDY || i == L::OSC || i == L::OFREE || (i >= L::KRDY && i < L::KFREE)) c = 4;
             if (i == L::VZ) c = 4 * L::KG;
             if (i >= L::XBRDY && i < L::KRDY) c = 8;   // XBRDY, UFREE
@@ -548,8 +567,10 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         const uint64_t da0 = sdesc_sw128(tile(0, XA), 16, 1024), db0 = sdesc_sw128(tile(0, XB_), 16, 1024);
         const uint64_t dc0 = sdesc_sw128(tile(0, XC), HALF, 1024);
         uint32_t steep = 0;                          // SEL: steep chunks so far, each a phase of OSC
+        const float4 *info = a.sel.ends + tables;    // SEL: whether a chunk is mild, fetched a chunk ahead
+        float flag = SEL && !PRE && nch > 0 ? info->w : 0.f;
         for (int i = 0; !PRE && i < nch; ++i, r.next()) {
-            const bool one = SEL ? chunk_info[chunk_id(i)].w != 0.f : mild;
+            const bool one = SEL ? flag != 0.f : mild;
             const uint32_t pi = (uint32_t)i & 1u, off_st = r.st * ((L::NT * L::TILE) >> 4);
             const int st = r.st;
             ok = __all_sync(~0u, wait_bar(full(st, XB_), r.ph, limit, s_abort) &&
@@ -570,6 +591,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                 mma_commit(empty(st, XB_));
             }
             __syncwarp();
+            if (SEL && i + 1 < nch) flag = (++info)->w;
             ok = __all_sync(~0u, wait_bar(bar(L::PRDY), pi, limit, s_abort) &&
                                      wait_bar(full(st, XC), r.ph, limit, s_abort) &&
                                      wait_bar(bar(one ? L::QSDONE : L::OSC), SEL && !one ? steep & 1u : pi, limit, s_abort));
@@ -660,27 +682,51 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                         h4 = decay_pow(sg, 4.f), h16 = decay_pow(sg, 16.f);
             float *const sF = reinterpret_cast<float *>(sm + L::T_SF), *const sC = reinterpret_cast<float *>(sm + L::T_SC),
                   *const sD = reinterpret_cast<float *>(sm + L::T_SD);
+            // SEL: of the chunk at hand, fetched a chunk ahead: ends of blocks and whether it is mild, the row's
+            // log and step
+            const float4 *info = a.sel.ends + tables;
+            const float2 *at = a.sel.c + tables * C + row;
+            float4 ends = {};
+            float2 own_row = {};
+            // What a row has of its own value beside the scores: skip v = scale (skip / scale) v goes onto the diagonal,
+            // where it is rounded with the score (2^-9 of it; as a term of its own in the epilogue, 11 us of 131
+            // for B8 H16 T4096 d = 128).  With a scale of zero the scores are.
+            const bool nil = SEL && a.out_scale == 0.f;
+            const float skip = SEL && a.sel.skip ? a.sel.skip[chain % a.H] / (nil ? 1.f : a.out_scale) : 0.f;
+            if (SEL && nch > 0) {
+                ends = *info;
+                own_row = *at;
+            }
             bool ok = true;
             for (int i = 0; i < nch; ++i) {
-                bool one = mild;
-                float mine_c = 0.f, block_c = 0.f;   // SEL: logs to this row, and to the token before its block
+                bool one = mild, even = true;
+                // SEL: logs to this row, from the chunk's start and from its block's; skip over the epilogue's factor
+                float mine_c = 0.f, in_block = 0.f, own_skip = skip;
                 if (SEL) {
-                    const int64_t at = (chain * a.sel.n_chunks + chunk_id(i)) * C;
-                    one = chunk_info[chunk_id(i)].w != 0.f;
-                    mine_c = a.sel.c[at + row].x;
-                    const float dt = a.sel.dt[at + row];
-                    float ends[3];                   // logs to the ends of the blocks before the last
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) ends[b] = a.sel.c[at + 32 * b + 31].x;
+                    one = ends.w != 0.f;
+                    mine_c = own_row.x;
+                    const float dt = own_row.y;
                     bar_sync(6, 128);                // the chunk before is done with (no wait between: it ends)
-                    if (one) sF[row] = dt * __expf(-mine_c);
-                    else {
-#pragma unroll
-                        for (int b = 1; b < 4; ++b)
-                            if (w < b) sF[16 * b * (b - 1) + row] = dt * __expf(ends[b - 1] - mine_c);
+                    if (one) {
+                        const float up = __expf(-mine_c);
+                        sF[row] = dt * up;
+                        own_skip *= up;
+                    } else {
+                        // to the ends of the blocks of 32 before later rows' own, and of the diagonal block, which is this
+                        // warp's own, from its start while its decays are e^-kMild or more, else as they are
+                        if (w < 1) sF[row] = dt * __expf(ends.x - mine_c);
+                        if (w < 2) sF[32 + row] = dt * __expf(ends.y - mine_c);
+                        if (w < 3) sF[96 + row] = dt * __expf(ends.z - mine_c);
+                        in_block = mine_c - before_block(ends, w);
+                        even = __all_sync(~0u, fabsf(in_block) <= kMild);
+                        const float up = even ? __expf(-in_block) : 1.f;
+                        sD[row] = dt * up;
+                        own_skip *= up;
                         sC[row] = mine_c;
-                        sD[row] = dt;
-                        block_c = w == 0 ? 0.f : w == 1 ? ends[0] : w == 2 ? ends[1] : ends[2];
+                    }
+                    if (i + 1 < nch) {
+                        ends = *++info;
+                        own_row = *(at += C);
                     }
                 }
                 ok = __all_sync(~0u, wait_bar(bar(L::GDONE), (uint32_t)i & 1u, limit, s_abort));
@@ -706,22 +752,51 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                 const int nv = tokens(i);
                 const int c0 = REV ? 32 * w : 0, c1 = REV ? C : 32 * w + 32;
                 if constexpr (SEL) {
-                    const float *const F = one ? sF : sF + 16 * w * (w - 1);
-                    const float f = one ? 1.f : __expf(mine_c - block_c);
-                    tmem_stream(tmem + lb + COL_G, c0, c1, [&](float (&v)[16], int c) {
-                        if (one || c < 32 * w) {
+                    // (the rows' own decays are the epilogue's, but for those of a block that is not even)
+                    const float *const left = one ? sF : sF + 16 * w * (w - 1);
+                    float f = 1.f;                   // the rows' decays to their block, if the epilogue has none
+                    if (!even) {
+                        f = __expf(in_block);
+                        // the diagonal block's decays, in place (a rolled loop: this is rare, and code of the usual
+                        // way made longer by it is slower: B16 H16 T4096 d = 64 took 212 us for 191)
+#pragma unroll 1
+                        for (int c = 32 * w; c < 32 * w + 32; c += 4) {
+                            float v[4];
+                            tmem_ld4(tmem + lb + COL_G + c, v);
+                            const float4 z = *reinterpret_cast<const float4 *>(sC + c);
+                            v[0] *= __expf(mine_c - z.x);
+                            v[1] *= __expf(mine_c - z.y);
+                            v[2] *= __expf(mine_c - z.z);
+                            v[3] *= __expf(mine_c - z.w);
+                            tmem_st4(tmem + lb + COL_G + c, v);
+                        }
+                        tmem_st_wait();
+                    }
+                    const float here = nil ? 0.f : 1.f;
+                    if (nil) f = 0.f;
+                    float v[16];
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 16) {
+                        tmem_fetch16(tmem + lb + COL_G + c, v);
+                        const bool before = c < 32 * w;
+                        const float4 *const F = reinterpret_cast<const float4 *>((one || before ? left : sD) + c);
+                        const float r = before ? f : here;
+                        uint64_t t[8];
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4) {
-                                const float4 t = *reinterpret_cast<const float4 *>(F + c + e);
-                                scale2(v[e], v[e + 1], mul2(pair(t.x, t.y), pair(f, f)));
-                                scale2(v[e + 2], v[e + 3], mul2(pair(t.z, t.w), pair(f, f)));
-                            }
-                        } else {
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 q = F[e];
+                            t[2 * e] = mul2(pair(q.x, q.y), pair(r, r));
+                            t[2 * e + 1] = mul2(pair(q.z, q.w), pair(r, r));
+                        }
+                        tmem_landed(v);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] *= sD[c + e] * __expf(mine_c - sC[c + e]);
+                        for (int e = 0; e < 8; ++e) scale2(v[2 * e], v[2 * e + 1], t[e]);
+                        if (!before) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] += c + e == row ? own_skip : 0.f;
                         }
                         put(v, c);
-                    });
+                    }
                 } else if (mild) {
                     // column j times g^-(j+1), reverse g^-(n-1-j)
                     float f = a.in_scale * decay_pow(lg, (float)(REV ? c0 + 1 - nv : -1));
@@ -765,15 +840,34 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             const int w = warp & 3, row = w * 32 + lane;
             const uint32_t lb = (uint32_t)(w * 32) << 16;
             bool ok = true;
-            const float skip = skips ? a.sel.skip[chain % a.H] : 0.f;
+            const float4 *info = a.sel.ends + tables; // SEL: as the P group's
+            const float2 *at = a.sel.c + tables * C + row;
+            float4 ends = {};
+            float row_c = 0.f;
+            if (SEL && nch > 0) {
+                ends = *info;
+                row_c = at->x;
+            }
             for (int i = 0; i < nch; ++i) {
                 const uint32_t pi = (uint32_t)i & 1u;
                 const int nv = tokens(i);
                 bool one = mild;
-                float rd;
+                float rd, last = 1.f;                // the rows' decay of A X, and what of it is P C's too
                 if (SEL) {
-                    one = chunk_info[chunk_id(i)].w != 0.f;
-                    rd = expf(a.sel.c[(chain * a.sel.n_chunks + chunk_id(i)) * C + row].x);
+                    one = ends.w != 0.f;
+                    rd = row_c;
+                    if (!one) {                      // from the block's start on, where that is the P group's too
+                        const float before = before_block(ends, w), in_block = row_c - before;
+                        if (__all_sync(~0u, fabsf(in_block) <= kMild)) {
+                            rd = before;
+                            last = __expf(in_block);
+                        }
+                    }
+                    rd = a.out_scale == 0.f ? 0.f : __expf(rd);
+                    if (i + 1 < nch) {
+                        ends = *++info;
+                        row_c = (at += C)->x;
+                    }
                 } else {
                     rd = pw[REV ? (row < nv ? nv - 1 - row : 0) : row + 1];
                 }
@@ -790,9 +884,9 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(L::OSC));
-                    rd = 1.f;
+                    rd = last;
                 }
-                rd *= a.out_scale;
+                rd *= SEL && a.out_scale == 0.f ? 1.f : a.out_scale;
 
                 ok = __all_sync(~0u, wait_bar(bar(L::PVDONE), pi, limit, s_abort));
                 if (!ok) break;
@@ -833,10 +927,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(own.out) +
                                      (chain * a.T + row0 + row) * D;
                 const uint32_t to = tile(st, XA) + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
-                if (skips) {                         // (landed: P C has read it)
-                    ok = __all_sync(~0u, wait_bar(full(st, XC), (uint32_t)(i / L::NST) & 1u, limit, s_abort));
-                    if (!ok) break;
-                }
                 tmem_stream(tmem + lb + COL_O, 0, D, [&](float (&v)[16], int c) {
                     if (NORM) {
 #pragma unroll
@@ -857,22 +947,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     } else {
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) scale2(v[e], v[e + 1], pair(rd, rd));
-                    }
-                    if (skips) {                     // the row's values, where they lie in their tile
-                        const uint32_t from = tile(st, XC) - tile(st, XA) + to + (uint32_t)(c >> 6) * HALF;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint4 f = ld_shared_v4(from + (((((uint32_t)c & 63u) >> 3) + e ^ ((uint32_t)row & 7u)) << 4));
-                            const uint32_t q[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                float &x0 = v[8 * e + 2 * z], &x1 = v[8 * e + 2 * z + 1];
-                                const float2 s2 = halves(fma2(pair(__uint_as_float(q[z] << 16), __uint_as_float(q[z] & 0xffff0000u)),
-                                                              pair(skip, skip), pair(x0, x1)));
-                                x0 = s2.x;
-                                x1 = s2.y;
-                            }
-                        }
                     }
                     uint32_t pk[8];
 #pragma unroll
@@ -895,7 +969,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar(L::OFREE));
-                    if (skips) mbar_arrive(empty(st, XC));
                     if (whole) {
                         const uint32_t src = tile(st, XA) + (uint32_t)w * 4096u;
                         tma_store_3d(&tmo, src, 0, (int)row0 + w * 32, (int)chain);
@@ -928,14 +1001,19 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         // Thread t has tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3, u = b, b + KG, ..
         constexpr int NU = 4 / L::KG;
         uint64_t sw[SEL ? NU : 1][4];
-        auto fetch_weights = [&](int i) {
-            const float *from = a.sel.w + (chain * a.sel.n_chunks + chunk_id(i)) * C + 32 * b + 2 * (lane & 3);
+        const float *from = a.sel.w + tables * C + 32 * b + 8 * (lane & 3);
+        auto fetch_weights = [&]() {
 #pragma unroll
             for (int x = 0; x < NU; ++x)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sw[x][c] = *reinterpret_cast<const uint64_t *>(from + 32 * L::KG * x + 8 * c);
+                for (int c = 0; c < 4; c += 2) {
+                    const float4 q = *reinterpret_cast<const float4 *>(from + 32 * L::KG * x + 2 * c);
+                    sw[x][c] = pair(q.x, q.y);
+                    sw[x][c + 1] = pair(q.z, q.w);
+                }
+            from += C;
         };
-        if (SEL && nch > 0) fetch_weights(0);
+        if (SEL && nch > 0) fetch_weights();
         for (int i = 0; i < nch; ++i, r.next()) {
             const int st = r.st;
             const uint32_t ph = r.ph;
@@ -1012,7 +1090,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     if (mine) store(h);
                 }
                 if (!ok) break;
-                if (SEL && u + L::KG >= 4 && i + 1 < nch) fetch_weights(i + 1);
+                if (SEL && u + L::KG >= 4 && i + 1 < nch) fetch_weights();
                 if (mine) tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -1094,8 +1172,11 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::XBRDY));
         }
+        const float4 *info = a.sel.chunk + tables;
+        float next_g = SEL && nch > 0 ? info->x : 0.f;   // (fetched a chunk ahead)
         for (int i = 0; i < nch; ++i) {
-            const float g = SEL ? chunk_info[chunk_id(i)].x : pw[tokens(i)];
+            const float g = SEL ? next_g : pw[tokens(i)];
+            if (SEL && i + 1 < nch) next_g = (++info)->x;
             const bool more = !PRE && i + 1 < nch;
             const int ub = i % L::UB;
             ok = __all_sync(~0u, wait_bar(bar(L::UDONE + ub), (uint32_t)(i / L::UB) & 1u, limit, s_abort) &&

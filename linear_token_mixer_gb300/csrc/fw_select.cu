@@ -27,16 +27,25 @@ __device__ __forceinline__ Two add(const Two &a, const Two &b) {
     return {hi, e - (hi - s)};
 }
 
-template <int C>
+// Where the tables are written (see SelectTables).
+struct Tables {
+    float2 *c;
+    float *dt, *w;
+    float4 *chunk, *ends;
+    int64_t n_chunks;
+};
+
+// TC: in the layout of the bf16 scans; mild_too: chunks may be mild (not with a scale of zero, whose epilogue scales
+// A X apart from the rest).
+template <int C, bool TC>
 __global__ void __launch_bounds__(kTableBlock)
-select_tables(GateArgs g, const int32_t *lens, int64_t n_chains, int64_t T, int H, float2 *out_c, float *out_dt,
-              float *out_w, float4 *out_chunk, int64_t n_chunks) {
+select_tables(GateArgs g, const int32_t *lens, int64_t n_chains, int64_t T, int H, int mild_too, Tables out) {
     constexpr int PER = C / 32;               // tokens of a lane
     let_next_grid_start();
     const int lane = threadIdx.x & 31;
     const int64_t id = (int64_t)blockIdx.x * (kTableBlock / 32) + (threadIdx.x >> 5);
-    if (id >= n_chains * n_chunks) return;
-    const int64_t chain = id / n_chunks, first = id % n_chunks * C + lane * PER;
+    if (id >= n_chains * out.n_chunks) return;
+    const int64_t chain = id / out.n_chunks, first = id % out.n_chunks * C + lane * PER;
     const int64_t n = chain_len(lens, chain, H, T);
     const int h = (int)(chain % H);
     const float rate = g.log_decay[h];
@@ -67,18 +76,30 @@ select_tables(GateArgs g, const int32_t *lens, int64_t n_chains, int64_t T, int 
         low = fminf(low, c[e].hi);
         high = fmaxf(high, c[e].hi);
         const Two s = add(total, Two{-c[e].hi, -c[e].lo});
-        out_c[at + e] = make_float2(c[e].hi, c[e].lo);
-        out_dt[at + e] = dt[e];
-        out_w[at + e] = dt[e] * exp_two(s.hi, s.lo);
+        const float w = dt[e] * exp_two(s.hi, s.lo);
+        if (TC) {
+            out.c[at + e] = make_float2(c[e].hi, dt[e]);
+            out.w[id * C + weight_place(lane * PER + e)] = w;
+        } else {
+            out.c[at + e] = make_float2(c[e].hi, c[e].lo);
+            out.dt[at + e] = dt[e];
+            out.w[at + e] = w;
+        }
     }
+    if (TC) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        low = fminf(low, __shfl_xor_sync(~0u, low, o));
-        high = fmaxf(high, __shfl_xor_sync(~0u, high, o));
+        for (int o = 16; o; o >>= 1) {
+            low = fminf(low, __shfl_xor_sync(~0u, low, o));
+            high = fmaxf(high, __shfl_xor_sync(~0u, high, o));
+        }
+        float end[3];
+#pragma unroll
+        for (int b = 0; b < 3; ++b) end[b] = __shfl_sync(~0u, c[PER - 1].hi, 32 / PER * (b + 1) - 1);
+        if (lane == 0)
+            out.ends[id] = make_float4(end[0], end[1], end[2],
+                                       mild_too && low >= -kMild && high <= kMild && isfinite(total.hi) ? 1.f : 0.f);
     }
-    if (lane == 0)
-        out_chunk[id] = make_float4(exp_two(total.hi, total.lo), total.hi, total.lo,
-                                    low >= -24.f && high <= 24.f && isfinite(total.hi) ? 1.f : 0.f);
+    if (lane == 0) out.chunk[id] = make_float4(exp_two(total.hi, total.lo), total.hi, total.lo, 0.f);
 }
 
 constexpr int kThreads = 256;
@@ -134,39 +155,50 @@ select_step_kernel(SelectStepArgs a) {
     }
 }
 
-// Bytes of the tables, each part a multiple of 16.
+// Bytes of the tables' parts, each a multiple of 16.
 struct TableBytes {
-    size_t c, dt, w, chunk;
-    size_t all() const { return c + dt + w + chunk; }
+    size_t c, dt, w, chunk, ends;
+    size_t all() const { return c + dt + w + chunk + ends; }
 };
-TableBytes table_bytes(int64_t n_chains, int64_t T, int C) {
+TableBytes table_bytes(int64_t n_chains, int64_t T, bool tc) {
+    const int C = tc ? select_chunk_tc() : select_chunk_f32();
     const size_t chunks = (size_t)n_chains * (size_t)((T + C - 1) / C), tokens = chunks * C;
-    return {tokens * sizeof(float2), tokens * sizeof(float), tokens * sizeof(float), chunks * sizeof(float4)};
+    return {tokens * sizeof(float2), tc ? 0 : tokens * sizeof(float), tokens * sizeof(float), chunks * sizeof(float4),
+            tc ? chunks * sizeof(float4) : 0};
 }
 
 }  // namespace
 
 // [tables][the scan's own]
 size_t select_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype) {
-    if (dtype == FW_BF16) return table_bytes(n_chains, T, select_chunk_tc()).all() + select_states_tc(n_chains, T, d);
-    return table_bytes(n_chains, T, select_chunk_f32()).all() + select_states_f32(n_chains, T, d);
+    const bool tc = dtype == FW_BF16;
+    return table_bytes(n_chains, T, tc).all() + (tc ? select_states_tc(n_chains, T, d) : select_states_f32(n_chains, T, d));
 }
 
 cudaError_t launch_select(const SelectArgs &args, cudaStream_t stream) {
     ScanArgs s = args.scan;
     const bool tc = s.dtype == FW_BF16;
     const int C = tc ? select_chunk_tc() : select_chunk_f32();
-    const TableBytes b = table_bytes(s.n_chains, s.T, C);
-    char *ws = reinterpret_cast<char *>(s.ws);
-    float2 *c = reinterpret_cast<float2 *>(ws);
-    float *dt = reinterpret_cast<float *>(ws + b.c), *w = reinterpret_cast<float *>(ws + b.c + b.dt);
-    float4 *chunk = reinterpret_cast<float4 *>(ws + b.c + b.dt + b.w);
-    s.ws = reinterpret_cast<float *>(ws + b.all());
-    s.sel = SelectTables{c, dt, w, chunk, args.gate.skip, (s.T + C - 1) / C, args.gate.G};
-    const int64_t warps = s.n_chains * s.sel.n_chunks;
+    const TableBytes b = table_bytes(s.n_chains, s.T, tc);
+    char *p = reinterpret_cast<char *>(s.ws);
+    auto part = [&](size_t n) {
+        char *const at = p;
+        p += n;
+        return at;
+    };
+    Tables t;
+    t.c = reinterpret_cast<float2 *>(part(b.c));
+    t.dt = reinterpret_cast<float *>(part(b.dt));
+    t.w = reinterpret_cast<float *>(part(b.w));
+    t.chunk = reinterpret_cast<float4 *>(part(b.chunk));
+    t.ends = reinterpret_cast<float4 *>(part(b.ends));
+    t.n_chunks = (s.T + C - 1) / C;
+    s.ws = reinterpret_cast<float *>(p);
+    s.sel = SelectTables{t.c, t.dt, t.w, t.chunk, t.ends, args.gate.skip, t.n_chunks, args.gate.G};
+    const int64_t warps = s.n_chains * t.n_chunks;
     const unsigned grid = (unsigned)((warps + kTableBlock / 32 - 1) / (kTableBlock / 32));
-    if (C == 128) select_tables<128><<<grid, kTableBlock, 0, stream>>>(args.gate, s.lens, s.n_chains, s.T, s.H, c, dt, w, chunk, s.sel.n_chunks);
-    else select_tables<64><<<grid, kTableBlock, 0, stream>>>(args.gate, s.lens, s.n_chains, s.T, s.H, c, dt, w, chunk, s.sel.n_chunks);
+    if (tc) select_tables<128, true><<<grid, kTableBlock, 0, stream>>>(args.gate, s.lens, s.n_chains, s.T, s.H, s.out_scale != 0.f, t);
+    else select_tables<64, false><<<grid, kTableBlock, 0, stream>>>(args.gate, s.lens, s.n_chains, s.T, s.H, 1, t);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return tc ? launch_select_tc(s, stream) : launch_select_f32(s, stream);

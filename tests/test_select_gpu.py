@@ -98,6 +98,18 @@ def test_steps_of_either_type_as_they_are(dt_type, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [0.0, -3.0, 1e-6])
+def test_scales(scale, dtype):
+    """A scale of zero leaves skip v alone; a small one makes skip v almost all of a row."""
+    x, g = inputs(1, 3, 1, 300, 64, dtype, seed=7)
+    check(run(g, scale=scale), ref(x, scale=scale), dtype)
+    if scale:
+        check(run(g, scale=scale, skip=False), ref(x, scale=scale, skip=False), dtype)
+    else:
+        assert not run(g, scale=scale, skip=False)[0].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("every", [1, 3, 40, 128])
 def test_states_that_start_afresh(every, dtype):
     """Steps so long that their decay is zero, between mild ones: sequences packed in one row."""
