@@ -22,7 +22,7 @@ namespace {
 using namespace rows;
 
 constexpr int kBlock = 256;
-constexpr int kStrip = 64;                    // most tokens of a strip
+constexpr int kStrip = 256;                   // most tokens of a strip
 constexpr int kStripMin = 8;                  // no fewer: only the first strip reads the state (W - 1 <= 7)
 
 // The taps of V channels; element (channel, tap) at w[channel * W + tap].
@@ -322,16 +322,28 @@ __global__ void __launch_bounds__(kBlock) conv_step_kernel(ConvStepArgs a, uint3
     for (int i = 0; i < W - 1; ++i) *reinterpret_cast<Raw<T, V> *>(state + (int64_t)i * d) = row[i + 1];
 }
 
-// Tokens of a strip: long ones read fewer rows twice, short ones make more threads.  The longest that
-// leaves every SM `threads` of them, within kStripMin .. kStrip.
-uint32_t strip_of(int64_t columns, int64_t T, int64_t threads) {
-    int64_t s = columns * T / (kSMs * threads);
-    s = s < kStripMin ? kStripMin : s > kStrip ? kStrip : s;
-    return (uint32_t)s;
+// Tokens of a strip, of chains that are to be cut in about `parts` each: at least kStripMin, at most kStrip (padded
+// batches), then in whole multiples of the parts.
+uint32_t strip_of(int64_t T, int64_t parts) {
+    if (parts < 1) parts = 1;
+    int64_t s = (T + parts - 1) / parts;
+    if (s > kStrip) {
+        parts *= (s + kStrip - 1) / kStrip;
+        s = (T + parts - 1) / parts;
+    }
+    return (uint32_t)(s < kStripMin ? kStripMin : s);
 }
 
-// Blocks of the backward pass that share a group of a head's columns: three an SM in all, and no more
-// than there are strips for.
+// Parts of a chain whose columns all chains' threads hold: what fills the SMs once, with `threads` each (two waves of
+// blocks and a few more took 29.5 us where one takes 23.3 for B8 H16 T2048 d = 128), or several times where one part
+// each is more than that.
+int64_t parts_of(int64_t columns, int threads) {
+    const int64_t room = (int64_t)kSMs * threads;
+    return columns <= room ? room / columns : columns < 6 * room ? (6 * room + columns - 1) / columns : 1;
+}
+
+// Blocks of the backward pass that share a group of a head's columns: two an SM in all, and no more than there are
+// strips for; each part of their warps takes one strip, or as many as the others.
 struct BwdShape {
     int lanes;
     uint32_t groups, strip, strips, slices;
@@ -342,13 +354,13 @@ BwdShape bwd_shape(int64_t B, int H, int64_t T, int d, int V) {
     r.lanes = 1;
     while (r.lanes < 32 && r.lanes < cols) r.lanes *= 2;
     r.groups = (uint32_t)((cols + r.lanes - 1) / r.lanes);
-    r.strip = strip_of(B * H * cols, T, 512);
+    const int64_t y = (int64_t)H * r.groups, each = (kBlock / 32) * (32 / r.lanes);
+    int64_t s = 2 * kSMs / y;
+    if (s < 1) s = 1;
+    r.strip = strip_of(T, s * each / B);
     r.strips = (uint32_t)((T + r.strip - 1) / r.strip);
-    const int64_t y = (int64_t)H * r.groups, per = (kBlock / 32) * (32 / r.lanes);
-    int64_t s = 3 * kSMs / y;
-    const int64_t most = (B * r.strips + per - 1) / per;
-    s = s < 1 ? 1 : s > most ? most : s;
-    r.slices = (uint32_t)s;
+    const int64_t most = (B * r.strips + each - 1) / each;
+    r.slices = (uint32_t)(s > most ? most : s);
     return r;
 }
 
@@ -359,7 +371,7 @@ int bwd_vector(int d, int W, fw_dtype dtype) {
 
 template <typename T, int V, int W> cudaError_t run(const ConvArgs &a, cudaStream_t s) {
     const int64_t cols = a.d / V;
-    const uint32_t strip = strip_of(a.n_chains * cols, a.T, 1024), strips = (uint32_t)((a.T + strip - 1) / strip);
+    const uint32_t strip = strip_of(a.T, parts_of(a.n_chains * cols, V > 2 ? 512 : 1024)), strips = (uint32_t)((a.T + strip - 1) / strip);
     const int64_t n = a.n_chains * strips * cols;
     constexpr int smem = Stage<T, V, W, 1>::bytes();
     auto k = conv_kernel<T, V, W>;
@@ -414,7 +426,7 @@ template <typename A> cudaError_t by_type(const A &a, cudaStream_t s) {
 bool conv_fits(int64_t B, int64_t H, int64_t T, int64_t d) {
     // threads of a call at the shortest strips and one channel each, and the backward grid's second axis
     const int64_t strips = (T + kStripMin - 1) / kStripMin;
-    return T <= INT32_MAX - 1024 && d <= (1 << 24) && H * ((d + 31) / 32) <= 65535 && B * H <= INT32_MAX / d &&
+    return T <= INT32_MAX - 4096 && d <= (1 << 24) && H * ((d + 31) / 32) <= 65535 && B * H <= INT32_MAX / d &&
            B * H * d <= INT32_MAX / strips;
 }
 

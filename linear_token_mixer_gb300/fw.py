@@ -344,6 +344,10 @@ class _On:
         t.record_stream(self.current)
         return t
 
+    def same(self, t):
+        """A new tensor of t's shape and type."""
+        return torch.empty_like(t) if self.stream is None else self.new(t.shape, t.dtype)
+
     def workspace(self, given, need, where):
         """(tensor to keep alive, address, bytes) of a workspace of `need` bytes."""
         if need < 0:
@@ -543,7 +547,7 @@ def select_prefill(q, k, v, dt, log_decay, S0=None, *, dt_bias=None, softplus=Fa
     if softplus:
         flags |= FLAG_SOFTPLUS
     if o is None:
-        o = on.new(shape, kind)
+        o = on.same(v)
     if S_T is None:
         S_T = on.new(state, f32)
     code = DTYPES.get(kind, -1)
@@ -566,7 +570,7 @@ def select_step(q, k, v, dt, log_decay, S, *, dt_bias=None, softplus=False, skip
             _gates(dt, log_decay, dt_bias, skip, (B, H), G, q), _arg(S, (B, H, d, d), torch.float32, "S", q))
     on = _On(q, stream)
     if o is None:
-        o = on.new(shape, kind)
+        o = on.same(v)
     on.call(lib().fw_select_step, "fw_select_step", (q, k, v, dt, log_decay, dt_bias, skip, S, o), *args,
             _arg(o, shape, kind, "o", q), ctypes.byref(fw_shape(B, H, 1, d, d)), DTYPES.get(kind, -1), scale,
             FLAG_SOFTPLUS if softplus else 0)
@@ -591,7 +595,7 @@ def conv_prefill(x, weight, bias=None, state=None, *, silu=True, lens=None, y=No
     on = _On(x, stream)
     flags = (FLAG_SILU if silu else 0) | (FLAG_ZERO_REST if y is None and lens is not None else 0)
     if y is None:
-        y = on.new(shape, kind)
+        y = on.same(x)
     if state_out is None:
         state_out = on.new(past, kind)
     on.call(lib().fw_conv_prefill, "fw_conv_prefill", (x, weight, bias, state, lens, y, state_out), *args,
@@ -614,7 +618,7 @@ def conv_backward(dy, x, weight, bias=None, state=None, dstate_out=None, *, silu
     on = _On(x, stream)
     flags = (FLAG_SILU if silu else 0) | (FLAG_ZERO_REST if dx is None and lens is not None else 0)
     if dx is None:
-        dx = on.new(shape, kind)
+        dx = on.same(x)
     if dweight is None:
         dweight = on.new((H, d, W), f32)
     if dbias is None:
@@ -639,7 +643,7 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, stream=None):
             _arg(bias, (H, d), torch.float32, "bias", x), _arg(state, (B, H, W - 1, d), kind, "state", x))
     on = _On(x, stream)
     if y is None:
-        y = on.new(shape, kind)
+        y = on.same(x)
     on.call(lib().fw_conv_step, "fw_conv_step", (x, weight, bias, state, y), *args, _arg(y, shape, kind, "y", x),
             ctypes.byref(fw_shape(B, H, 1, d, d)), W, DTYPES.get(kind, -1), FLAG_SILU if silu else 0)
     return y
@@ -659,10 +663,11 @@ def _gated_shape(x, params):
     shape = x.shape
     lead, width = shape[:-1], shape[-1]
     rows = lead.numel()
-    if any(p is not None and p.dim() == 2 for p in params):
-        if x.dim() < 3:
-            raise ValueError("fw: parameters [H, width] go with x [.., H, T, width]")
-        return lead, rows, width, shape[-3], shape[-2], (shape[-3], width)
+    for p in params:
+        if p is not None and p.dim() == 2:
+            if x.dim() < 3:
+                raise ValueError("fw: parameters [H, width] go with x [.., H, T, width]")
+            return lead, rows, width, shape[-3], shape[-2], (shape[-3], width)
     return lead, rows, width, 1, rows, (width,)
 
 
@@ -686,9 +691,9 @@ def gated_norm(x, weight=None, bias=None, *, gate=None, residual=None, scale=Non
                     _arg(bias, par, f32, "bias", x), groups, inner, eps, int(rms), int(gate_after))
     on = _On(x, stream)
     if y is None:
-        y = on.new(shape, kind)
+        y = on.same(x)
     if total is None and residual is not None:
-        total = on.new(shape, kind)
+        total = on.same(x)
     if not stats:
         mean = rstd = None
     else:
@@ -717,12 +722,12 @@ def gated_norm_backward(dy, x, weight, bias, mean, rstd, *, gate=None, residual=
     stats = (_arg(None if rms else mean, lead, f32, "mean", x), _arg(rstd, lead, f32, "rstd", x))
     on = _On(x, stream)
     if dx is None:
-        dx = on.new(shape, kind)
+        dx = on.same(x)
     if dgate is None and gate is not None:
-        dgate = on.new(shape, kind)
+        dgate = on.same(x)
     if residual is not None and scale is not None:
         if dresidual is None:
-            dresidual = on.new(shape, kind)
+            dresidual = on.same(x)
         if dscale is None:
             dscale = on.new(par, f32)
     if dweight is None:
