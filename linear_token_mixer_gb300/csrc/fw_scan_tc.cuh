@@ -997,23 +997,22 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         const bool mine = w * 32 < D;
         bool ok = true;
         Ring r;
-        // SEL: the weights of the chunk at hand, those of the next on their way behind the last use of these.
-        // Thread t has tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3, u = b, b + KG, ..
-        constexpr int NU = 4 / L::KG;
-        uint64_t sw[SEL ? NU : 1][4];
-        const float *from = a.sel.w + tables * C + 32 * b + 8 * (lane & 3);
+        // SEL: the weights of the 32 tokens at hand (thread t has 8 c + 2 (t % 4), +1 for c = 0..3), those of the next
+        // on their way behind the last use of these.  A buffer's turns, 32 KG tokens apart, go on from chunk to chunk.
+        uint64_t wv[4];
+        const float *from = SEL ? a.sel.w + tables * C + 32 * b + 8 * (lane & 3) : nullptr;
+        int turns = nch * (4 / L::KG);
         auto fetch_weights = [&]() {
+            if (turns-- <= 0) return;
 #pragma unroll
-            for (int x = 0; x < NU; ++x)
-#pragma unroll
-                for (int c = 0; c < 4; c += 2) {
-                    const float4 q = *reinterpret_cast<const float4 *>(from + 32 * L::KG * x + 2 * c);
-                    sw[x][c] = pair(q.x, q.y);
-                    sw[x][c + 1] = pair(q.z, q.w);
-                }
-            from += C;
+            for (int c = 0; c < 4; c += 2) {
+                const float4 q = *reinterpret_cast<const float4 *>(from + 2 * c);
+                wv[c] = pair(q.x, q.y);
+                wv[c + 1] = pair(q.z, q.w);
+            }
+            from += 32 * L::KG;
         };
-        if (SEL && nch > 0) fetch_weights();
+        if (SEL) fetch_weights();
         for (int i = 0; i < nch; ++i, r.next()) {
             const int st = r.st;
             const uint32_t ph = r.ph;
@@ -1045,14 +1044,12 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             }
             // ldmatrix x4: matrices (tokens +0, +8) x (rows +0, +8) of X, 16 rows a half-warp
             const uint32_t r8 = (uint32_t)lane & 7u, m = (uint32_t)lane >> 3;
-#pragma unroll (SEL ? NU : 1)
             for (int u = b; u < 4; u += L::KG) {
                 const int use = (4 * i + u) / L::KG;   // of this buffer
                 // thread t: tokens 32 u + 8 c + 2 (t % 4), +1 for c = 0..3
-                uint64_t wv[4];
+                if (!SEL)
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    wv[c] = SEL ? sw[u / L::KG][c] : *reinterpret_cast<const uint64_t *>(wt + 32 * u + 8 * c + 2 * (lane & 3));
+                    for (int c = 0; c < 4; ++c) wv[c] = *reinterpret_cast<const uint64_t *>(wt + 32 * u + 8 * c + 2 * (lane & 3));
                 uint32_t hi[8], mid[8], lo[8];
                 auto form = [&](int h) {             // rows w * 32 + 16 h .. +15 of X
 #pragma unroll
@@ -1090,7 +1087,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     if (mine) store(h);
                 }
                 if (!ok) break;
-                if (SEL && u + L::KG >= 4 && i + 1 < nch) fetch_weights();
+                if (SEL) fetch_weights();
                 if (mine) tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
