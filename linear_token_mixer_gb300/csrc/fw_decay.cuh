@@ -70,20 +70,28 @@ struct NormArgs {
 // scores, and their sums, 21 of fp32's and bf16's 38 decimal orders.
 constexpr float kMild = 40.f;
 
-// Steps and decays of a selective scan (see fw_select.cuh), formed ahead of it for chunks of the scan's own
-// length; n_chunks of them a chain, tokens behind a sequence's end without a step.
-struct SelectTables {
-    const float2 *c;          // [n_chains][n_chunks * C] log decay from the chunk's start to the token, in two terms (bf16
-                              // scans: in one, and the token's step)
-    const float *dt;          // .. the token's step (fp32 scans)
-    const float *w;           // .. dt times the decay from the token to the chunk's end (bf16 scans: in the order of
-                              // weight_place)
-    const float4 *chunk;      // [n_chains][n_chunks] decay of the chunk, its log in two terms
-    const float4 *ends;       // .. bf16 scans: c at the ends of its first three blocks of 32 tokens, and 1 where the
-                              // chunk is mild (its sums of logs stay within +-kMild)
+// The steps of a selective scan (see fw_select.cuh).
+struct GateArgs {
+    const void *dt;           // [n_chains][T] (a step: [n_states])
+    fw_dtype dt_type;
+    const float *log_decay;   // [H]
+    const float *dt_bias;     // [H] or NULL
     const float *skip;        // [H] or NULL
+    int softplus;
+    int G;                    // groups of heads that share a and b: [B][G][T][d]
+};
+
+// What its scans keep of them in the workspace, for chunks of C tokens, n_chunks a chain; tokens behind a
+// sequence's end are without a step.
+struct SelectTables {
+    GateArgs gate;
     int64_t n_chunks;
-    int G;                    // groups of heads that share a and b
+    float4 *chunk;            // [n_chains][n_chunks] decay of the chunk, its log in two terms
+    // bf16 scans:
+    float4 *ends;             // .. log decays from the chunk's start to the ends of its first three blocks of 32
+                              // tokens, and 1 where the chunk is mild (its sums of logs stay within +-kMild)
+    float2 *c;                // [n_chains][n_chunks * C] log decay from the chunk's start to the token, and its step
+    float *w;                 // .. step times the decay from the token to the chunk's end, at weight_place
 };
 // Place of a token's weight within its chunk: the eight that a thread of the bf16 scans needs of 32 tokens, 2 t, + 1
 // of each eight, follow one another.

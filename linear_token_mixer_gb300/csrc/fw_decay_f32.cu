@@ -148,20 +148,30 @@ __device__ __forceinline__ ChunkOf chunk_of(const ScanArgs &s, int64_t nch) {
 
 // Where a chunk's rows of a and b begin, given where those of c do.
 template <int D, bool SEL> __device__ __forceinline__ int64_t ab_base(const ScanArgs &s, const ChunkOf &k, int64_t base) {
-    return SEL ? (group_chain(k.chain, s.H, s.sel.G) * s.T + k.chunk * C) * D : base;
+    return SEL ? (group_chain(k.chain, s.H, s.sel.gate.G) * s.T + k.chunk * C) * D : base;
 }
 
 // M_c into the workspace; ONE (chains of one chunk): the final state into X_out.  SEL here and below: a
-// selective scan, whose weights and decays come from its tables.
+// selective scan, whose weights and decays a warp forms of the chunk's own steps.
 template <int D, bool ONE, bool SEL>
 __device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, float4 *smem4) {
     constexpr int LD = ld_col<D>();
     float *sB = reinterpret_cast<float *>(smem4), *sC = sB + C * LD, *w = sC + C * LD;
     const float lg = SEL ? 0.f : s.log_decay[k.chain % s.H];
-    if (threadIdx.x < C) {
+    float *const chunk_g = w + C;          // SEL: the chunk's decay
+    if (SEL && threadIdx.x < 32) {
+        const ChunkLogs<C> logs = chunk_logs<C>(s.sel.gate, k.chain, s.H, s.T, k.chunk * C + k.nv, k.chunk);
+#pragma unroll
+        for (int e = 0; e < logs.PER; ++e) w[threadIdx.x * logs.PER + e] = logs.weight(e);
+        if (threadIdx.x == 0) {
+            const float4 r = logs.record();
+            *chunk_g = r.x;
+            if (!ONE) s.sel.chunk[k.chain * s.sel.n_chunks + k.chunk] = r;
+        }
+    }
+    if (!SEL && threadIdx.x < C) {
         const int j = threadIdx.x;
-        w[j] = SEL ? s.sel.w[(k.chain * s.sel.n_chunks + k.chunk) * C + j]
-                   : s.in_scale * decay_pow(lg, (float)(s.rev ? j + 1 : max(k.nv - 1 - j, 0)));
+        w[j] = s.in_scale * decay_pow(lg, (float)(s.rev ? j + 1 : max(k.nv - 1 - j, 0)));
     }
     __syncthreads();
     const int64_t base = (k.chain * s.T + k.chunk * C) * D;
@@ -173,7 +183,7 @@ __device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, 
     const int n0 = (warp >> 1) * 32;
     float *M = ONE ? s.X_out + k.chain * D * D : s.ws + (int64_t)blockIdx.x * D * D;
     const float *X0 = ONE && s.X0 ? s.X0 + k.chain * D * D : nullptr;
-    const float gn = SEL ? s.sel.chunk[k.chain * s.sel.n_chunks + k.chunk].x : decay_pow(lg, (float)k.nv);
+    const float gn = SEL ? *chunk_g : decay_pow(lg, (float)k.nv);
 #pragma unroll 1
     for (int m0 = (warp & 1) * (D / 2), m1 = m0 + D / 2; m0 < m1; m0 += 32) {
         float acc[2][4][4] = {};
@@ -199,7 +209,6 @@ template <int D, bool SEL>
 __global__ void __launch_bounds__(threads<D>())
 scan_local(const __grid_constant__ Scans all, int64_t nch) {
     extern __shared__ float4 smem4[];
-    if (SEL) wait_previous_grid();                   // the tables; no later grid starts before they are there
     let_next_grid_start();
     const ScanArgs &s = all.s[blockIdx.y];
     const ChunkOf k = chunk_of(s, nch);
@@ -266,10 +275,13 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
     int *const first = reinterpret_cast<int *>(red + C * WN);
     float2 *const lc = reinterpret_cast<float2 *>((reinterpret_cast<uintptr_t>(first + D) + 7) & ~(uintptr_t)7);
     if (SEL) {                             // pw: the steps; lc: the logs of the decays
-        const int64_t at = (k.chain * s.sel.n_chunks + k.chunk) * C;
-        for (int i = threadIdx.x; i < C; i += threads<D>()) {
-            pw[i] = s.sel.dt[at + i];
-            lc[i] = s.sel.c[at + i];
+        if (threadIdx.x < 32) {
+            const ChunkLogs<C> logs = chunk_logs<C>(s.sel.gate, k.chain, s.H, s.T, k.chunk * C + k.nv, k.chunk);
+#pragma unroll
+            for (int e = 0; e < logs.PER; ++e) {
+                pw[threadIdx.x * logs.PER + e] = logs.dt[e];
+                lc[threadIdx.x * logs.PER + e] = make_float2(logs.c[e].hi, logs.c[e].lo);
+            }
         }
     } else {
         const float lg = s.log_decay[k.chain % s.H];
@@ -382,8 +394,8 @@ __device__ __forceinline__ void out_part(const ScanArgs &s, const ChunkOf &k, co
             v = first[col] <= (s.rev ? C - 1 - r : r) ? __int_as_float(0x7fffffff) : v * s.out_scale;
         });
     }
-    if (SEL && s.sel.skip) {               // (from memory: sC may have lost values that are not finite)
-        const float skip = s.sel.skip[k.chain % s.H];
+    if (SEL && s.sel.gate.skip) {          // (from memory: sC may have lost values that are not finite)
+        const float skip = s.sel.gate.skip[k.chain % s.H];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -488,7 +500,6 @@ scan_one(const __grid_constant__ Scans all) {
     extern __shared__ float4 smem4[];
     const ScanArgs &s = all.s[blockIdx.y];
     const ChunkOf k = chunk_of(s, 1);
-    if (SEL) wait_previous_grid();         // the tables
     const bool both = gridDim.z == 1;
     if (both || blockIdx.z == 1) {
         if (s.zero_rest) zero_rest<D>(s, k.chain, 0, k.nv);
@@ -499,13 +510,12 @@ scan_one(const __grid_constant__ Scans all) {
         if (s.X_out) local_part<D, true, SEL>(s, k, smem4);
 }
 
-// `SEL`: behind the launch that forms the tables.
 template <int D, bool SEL>
 cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
     const ScanArgs &s = all.s[0];
     const int64_t nch = (s.T + C - 1) / C;
     const dim3 grid((unsigned)(s.n_chains * nch), n);
-    constexpr int smem_l = (2 * C * ld_col<D>() + C) * 4;
+    constexpr int smem_l = (2 * C * ld_col<D>() + C + (SEL ? 1 : 0)) * 4;
     constexpr int smem_o = (2 * C * ld_row<D>() + C * ld_col<D>() + C + 4 + C * (D / 32) + D + (SEL ? 2 * C + 2 : 0)) * 4;
     cudaError_t e;
     if (nch == 1) {
@@ -514,13 +524,13 @@ cudaError_t launch(const Scans &all, int n, cudaStream_t stream) {
         if ((e = allow_smem(scan_one<D, SEL>, smem, done)) != cudaSuccess) return e;
         const bool in_place = s.X_out && s.X_out == s.X0;
         return launch_after(scan_one<D, SEL>, dim3((unsigned)s.n_chains, n, in_place ? 1 : 2), threads<D>(), smem, stream,
-                            SEL, all);
+                            false, all);
     }
     static std::atomic<uint64_t> local_done{0}, out_done{0};
     if ((e = allow_smem(scan_local<D, SEL>, smem_l, local_done)) != cudaSuccess) return e;
     if ((e = allow_smem(scan_out<D, SEL>, smem_o, out_done)) != cudaSuccess) return e;
     const int states = n < kSharing ? n : kSharing;
-    if ((e = launch_after(scan_local<D, SEL>, dim3(grid.x, states), threads<D>(), smem_l, stream, SEL, all, nch)) !=
+    if ((e = launch_after(scan_local<D, SEL>, dim3(grid.x, states), threads<D>(), smem_l, stream, false, all, nch)) !=
         cudaSuccess)
         return e;
     const dim3 gp((unsigned)(s.n_chains * (D * D / 4 / kPrefix)), states);
@@ -549,12 +559,16 @@ cudaError_t launch_scans(ScanArgs *s, int n, cudaStream_t stream) {
     return s[0].d == 64 ? launch<64, false>(all, n, stream) : launch<128, false>(all, n, stream);
 }
 
-// A selective scan; its tables are formed by the launch before it.
-int select_chunk_f32() { return C; }
-size_t select_states_f32(int64_t n_chains, int64_t T, int d) { return T <= C ? 0 : state_bytes(n_chains, T, d); }
-cudaError_t launch_select_f32(const ScanArgs &s, cudaStream_t stream) {
+// A selective scan: [states][the chunks' decays], neither where a chain is one chunk.
+static size_t record_bytes(int64_t n_chains, int64_t T) { return (size_t)n_chains * (size_t)((T + C - 1) / C) * sizeof(float4); }
+size_t select_workspace_f32(int64_t n_chains, int64_t T, int d) {
+    return T <= C ? 0 : state_bytes(n_chains, T, d) + record_bytes(n_chains, T);
+}
+cudaError_t launch_select_f32(const ScanArgs &scan, cudaStream_t stream) {
     Scans all{};
-    all.s[0] = s;
+    ScanArgs &s = all.s[0] = scan;
+    s.sel.n_chunks = (s.T + C - 1) / C;
+    if (s.T > C) s.sel.chunk = reinterpret_cast<float4 *>(reinterpret_cast<char *>(s.ws) + state_bytes(s.n_chains, s.T, s.d));
     return s.d == 64 ? launch<64, true>(all, 1, stream) : launch<128, true>(all, 1, stream);
 }
 

@@ -39,7 +39,8 @@
 // issue slots for 38 %, DRAM at 55 %, and the rest is the roles' round trips through tensor memory and barriers.  A second CTA an
 // SM would fill it but finds no room: the tiles take 192 KB, G, O and the update 384 columns.
 // Tensor memory: G (P over it) 128 columns, O 128, the update 128, the split operand 2 x 48.
-// SEL: the decays come from tables in memory (SelectTables), by token and chunk, in place of powers of one.  The
+// SEL: the decays come from tables in memory (SelectTables), by token and chunk, in place of powers of one; a CTA
+// forms those of its chunks before it begins, while the first tiles load.  (A launch of their own: 5 us a call.)  The
 // scores of a steep chunk take the product of the decays to and from the end of the block of 32 columns before
 // a row's own, each at most 1; those of the diagonal blocks the quotient of the decays from the block's start, or
 // where that is below e^-kMild the decay itself.  Whether a chunk is mild goes by its own tables.
@@ -50,6 +51,7 @@
 #include <cuda.h>
 
 #include "fw_decay_tc.cuh"
+#include "fw_select.cuh"
 #include "fw_sm100.cuh"
 #include "fw_tma.cuh"
 
@@ -271,6 +273,70 @@ __device__ __forceinline__ float entry_state(const ScanArgs &a, const ScanArgs &
     return x;
 }
 
+// SEL: the tables of a chunk, four tokens a lane; by a whole warp.  The weights' logs are summed from the chunk's end on,
+// so that those which count are short sums; what is summed from its start on goes into rows of bf16 only.  (With
+// a scale of zero no chunk is mild: the epilogue of a mild one scales A X with the rest.)
+__device__ __forceinline__ void form_tables(const ScanArgs &a, int64_t chain, int64_t n, int64_t chunk) {
+    constexpr int PER = C / 32;
+    const GateArgs &g = a.sel.gate;
+    const int lane = threadIdx.x & 31, h = (int)(chain % a.H);
+    const int64_t first = chunk * C + lane * PER, id = chain * a.sel.n_chunks + chunk;
+    const float rate = g.log_decay[h];
+    float dt[PER], x[PER], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const bool on = first + e < n;
+        dt[e] = on ? step_of(g, chain * a.T + first + e, h) : 0.f;
+        x[e] = on ? rate * dt[e] : 0.f;
+        if (x[e] < -kReset) x[e] = -kReset;   // (NaN stays)
+        sum += x[e];
+    }
+    float upto = sum, from = sum;             // of this lane's tokens and those before, and behind
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float p = __shfl_up_sync(~0u, upto, o), q = __shfl_down_sync(~0u, from, o);
+        if (lane >= o) upto += p;
+        if (lane < 32 - o) from += q;
+    }
+    const float total = __shfl_sync(~0u, from, 0);
+    float before = __shfl_up_sync(~0u, upto, 1), behind = __shfl_down_sync(~0u, from, 1);
+    if (lane == 0) before = 0.f;
+    if (lane == 31) behind = 0.f;
+    float w[PER];
+#pragma unroll
+    for (int e = PER - 1; e >= 0; --e) {
+        w[e] = dt[e] * expf(behind);
+        behind += x[e];
+    }
+    float low = 0.f, high = 0.f;              // the least and the largest sum
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        before += x[e];
+        low = fminf(low, before);
+        high = fmaxf(high, before);
+        x[e] = before;
+    }
+    float4 *const c = reinterpret_cast<float4 *>(a.sel.c + id * C + lane * PER);
+    c[0] = make_float4(x[0], dt[0], x[1], dt[1]);
+    c[1] = make_float4(x[2], dt[2], x[3], dt[3]);
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+        *reinterpret_cast<float2 *>(a.sel.w + id * C + weight_place(lane * PER + e)) = make_float2(w[e], w[e + 1]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        low = fminf(low, __shfl_xor_sync(~0u, low, o));
+        high = fmaxf(high, __shfl_xor_sync(~0u, high, o));
+    }
+    float end[3];
+#pragma unroll
+    for (int b = 0; b < 3; ++b) end[b] = __shfl_sync(~0u, x[PER - 1], 32 / PER * (b + 1) - 1);
+    if (lane == 0) {
+        a.sel.chunk[id] = make_float4(expf(total), total, 0.f, 0.f);
+        a.sel.ends[id] = make_float4(end[0], end[1], end[2],
+                                     a.out_scale != 0.f && low >= -kMild && high <= kMild && isfinite(total) ? 1.f : 0.f);
+    }
+}
+
 // SEL: the log decay to the token before block w of a chunk's four.
 __device__ __forceinline__ float before_block(const float4 &ends, int w) {
     return w == 0 ? 0.f : w == 1 ? ends.x : w == 2 ? ends.y : ends.z;
@@ -334,7 +400,7 @@ __device__ __forceinline__ void redo_rows(const ScanArgs &a, const ScanArgs &own
     bar_sync(3, N);
     last = min(*shared_last, sg.last - 1);                       // (of a call given up, tiles may still land there)
     float g = SEL ? 1.f : decay_pow(a.log_decay[chain % a.H], 1.f);
-    const int64_t ab = SEL ? group_chain(chain, a.H, a.sel.G) : chain;
+    const int64_t ab = SEL ? group_chain(chain, a.H, a.sel.gate.G) : chain;
     for (int i = sg.first; i <= last; ++i) {
         const int64_t t0 = first_token(i);
         const int nv = n - t0 < C ? (int)(n - t0) : C;
@@ -368,7 +434,7 @@ __device__ __forceinline__ void redo_rows(const ScanArgs &a, const ScanArgs &own
             o = 0.f;
             for (int s = 0; s < PARTS; ++s) o += sum[s * D + col];
             o *= a.out_scale;
-            if (SEL && a.sel.skip) o = fmaf(a.sel.skip[chain % a.H], value, o);
+            if (SEL && a.sel.gate.skip) o = fmaf(a.sel.gate.skip[chain % a.H], value, o);
             if (NORM) {
                 // every part holds the row, and its N / D copies add up to as many times the sums
                 float m[2] = {0.f, 0.f};
@@ -428,12 +494,12 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
     const int nch = sg.last - sg.first;
     const bool final_seg = !PRE && seg == nseg - 1;
     if (nch == 0 && !(final_seg && (own.X_out || a.zero_rest)) && !(PRE && seg == 0)) {
-        if (SEL || order & kWaitLast) wait_previous_grid();
+        if (order & kWaitLast) wait_previous_grid();
         return;
     }
     const uint64_t limit = (uint64_t)a.wait_ns;
     const float lg = SEL ? 0.f : a.log_decay[chain % a.H];
-    const int64_t ab_chain = SEL ? group_chain(chain, a.H, a.sel.G) : chain;   // whose rows A and B are
+    const int64_t ab_chain = SEL ? group_chain(chain, a.H, a.sel.gate.G) : chain;   // whose rows A and B are
     // Within a chunk of a mild head every quotient of powers of g is at most e^24 = 2.6e10, which
     // leaves the scores and their sums 28 of fp32's and bf16's 38 decimal orders: the rows' decay
     // of a chunk, g^(i+1) (A X + (mask . g^-(j+1) . G) C), is then one factor in the epilogue.
@@ -500,7 +566,11 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         asm volatile("barrier.cta.arrive 1, %0;" ::"n"(NTHREADS) : "memory");
     } else {
         const int j = tid - 32;
-        if (SEL) {                                  // (tables in memory)
+        if (SEL) {
+            // this segment's tables, unless the launch before has formed them; by all warps that wait for the
+            // first tiles
+            if (PRE || seg == nseg - 1)
+                for (int i = warp - 1; i < nch; i += NTHREADS / 32 - 1) form_tables(a, chain, n, sg.first + i);
         } else if (j <= C) pw[j] = decay_pow(lg, (float)j);
         else if (j <= 2 * C) {
             const int x = j - C - 1;
@@ -510,7 +580,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
         tc_fence_before();
         asm volatile("barrier.cta.sync 1, %0;" ::"n"(NTHREADS) : "memory");
         tc_fence_after();
-        if (SEL) wait_previous_grid();              // the tables (the tiles need not wait for them)
     }
     const uint32_t tmem = __shfl_sync(~0u, *s_tmem, 0);
 
@@ -692,7 +761,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             // where it is rounded with the score (2^-9 of it; as a term of its own in the epilogue, 11 us of 131
             // for B8 H16 T4096 d = 128).  With a scale of zero the scores are.
             const bool nil = SEL && a.out_scale == 0.f;
-            const float skip = SEL && a.sel.skip ? a.sel.skip[chain % a.H] / (nil ? 1.f : a.out_scale) : 0.f;
+            const float skip = SEL && a.sel.gate.skip ? a.sel.gate.skip[chain % a.H] / (nil ? 1.f : a.out_scale) : 0.f;
             if (SEL && nch > 0) {
                 ends = *info;
                 own_row = *at;

@@ -6,16 +6,6 @@
 
 namespace fw {
 
-struct GateArgs {
-    const void *dt;            // [n_chains][T] (a step: [n_states])
-    fw_dtype dt_type;
-    const float *log_decay;    // [H]
-    const float *dt_bias;      // [H] or NULL
-    const float *skip;         // [H] or NULL
-    int softplus;
-    int G;                     // groups of heads that share a and b: [B][G][T][d]
-};
-
 struct SelectArgs {
     ScanArgs scan;             // forward; in_scale 1, no norm
     GateArgs gate;
@@ -36,13 +26,10 @@ size_t select_workspace(int64_t n_chains, int64_t T, int d, fw_dtype dtype);
 cudaError_t launch_select(const SelectArgs &a, cudaStream_t s);
 cudaError_t launch_select_step(const SelectStepArgs &a, cudaStream_t s);
 
-// The scans by type (scan.sel formed by the launch before them): tokens of a chunk, bytes of their own
-// workspace (scan.ws), and the launch.
-int select_chunk_f32();
-size_t select_states_f32(int64_t n_chains, int64_t T, int d);
+// The scans by type: bytes of the workspace from scan.ws on, and the launch.
+size_t select_workspace_f32(int64_t n_chains, int64_t T, int d);
 cudaError_t launch_select_f32(const ScanArgs &scan, cudaStream_t s);
-int select_chunk_tc();
-size_t select_states_tc(int64_t n_chains, int64_t T, int d);
+size_t select_workspace_tc(int64_t n_chains, int64_t T, int d);
 cudaError_t launch_select_tc(const ScanArgs &scan, cudaStream_t s);
 
 // A decay below e^-kReset is zero in fp32: sums of logs are kept finite by it.
@@ -55,6 +42,61 @@ __device__ __forceinline__ float step_of(const GateArgs &g, int64_t at, int h) {
     if (g.dt_bias) x += g.dt_bias[h];
     // log(1 + e^x) = max(x, 0) + log(1 + e^-|x|)
     return g.softplus ? fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))) : x;
+}
+
+// A sum of fp32 values in two terms, hi + lo with |lo| at most half a unit of hi (48 bits; the GPU's 64-bit
+// additions are a sixteenth as fast as these four to eight fp32 ones).
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two add(const Two &a, const Two &b) {
+    const float s = a.hi + b.hi, t = s - a.hi, e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo), hi = s + e;
+    return {hi, e - (hi - s)};
+}
+
+// A chunk's steps and log decays from its start, C / 32 tokens a lane, one after the other; by a whole warp.  The sums
+// are kept in two terms, so that their differences within the chunk lose nothing to their size.
+template <int C> struct ChunkLogs {
+    static constexpr int PER = C / 32;
+    float dt[PER];
+    Two c[PER], total;
+    // a token's step times its decay to the chunk's end
+    __device__ __forceinline__ float weight(int e) const {
+        const Two s = add(total, Two{-c[e].hi, -c[e].lo});
+        return dt[e] * exp_two(s.hi, s.lo);
+    }
+    __device__ __forceinline__ float4 record() const {
+        return make_float4(exp_two(total.hi, total.lo), total.hi, total.lo, 0.f);
+    }
+};
+template <int C>
+__device__ __forceinline__ ChunkLogs<C> chunk_logs(const GateArgs &g, int64_t chain, int H, int64_t T, int64_t n, int64_t chunk) {
+    constexpr int PER = C / 32;
+    ChunkLogs<C> r;
+    const int lane = threadIdx.x & 31, h = (int)(chain % H);
+    const int64_t first = chunk * C + lane * PER;
+    const float rate = g.log_decay[h];
+    Two sum{0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const bool on = first + e < n;
+        r.dt[e] = on ? step_of(g, chain * T + first + e, h) : 0.f;
+        const float x = on ? rate * r.dt[e] : 0.f;
+        sum = add(sum, x < -kReset ? Two{-kReset, 0.f} : Two{x, on ? fmaf(rate, r.dt[e], -x) : 0.f});   // (NaN stays)
+        r.c[e] = sum;
+    }
+    Two upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Two x{__shfl_up_sync(~0u, upto.hi, o), __shfl_up_sync(~0u, upto.lo, o)};
+        if (lane >= o) upto = add(x, upto);
+    }
+    r.total = Two{__shfl_sync(~0u, upto.hi, 31), __shfl_sync(~0u, upto.lo, 31)};
+    Two before{__shfl_up_sync(~0u, upto.hi, 1), __shfl_up_sync(~0u, upto.lo, 1)};
+    if (lane == 0) before = Two{0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < PER; ++e) r.c[e] = add(before, r.c[e]);
+    return r;
 }
 
 }  // namespace fw

@@ -5,10 +5,10 @@
 namespace fw {
 namespace {
 
-// As the decayed scan's: chains in segments where they are few.  Behind the launch that forms the tables.
+// As the decayed scan's: chains in segments where they are few.
 template <int D> cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
     const int nseg = segments(a.n_chains, a.T);
-    const int64_t ab = a.n_chains / a.H * a.sel.G;
+    const int64_t ab = a.n_chains / a.H * a.sel.gate.G;
     Jobs<1> jobs;
     jobs.s[0].args = a;
     if (!make_map(&jobs.s[0].a, a.a, a.T, ab, D, C) || !make_map(&jobs.s[0].b, a.b, a.T, ab, D, C) ||
@@ -20,7 +20,7 @@ template <int D> cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
         constexpr int smem = (int)Lay<D, true, true>::ALLOC;
         static std::atomic<uint64_t> pre_done{0};
         if ((e = allow_smem(k, smem, pre_done)) != cudaSuccess) return e;
-        if ((e = launch_after(k, dim3((unsigned)(a.n_chains * (nseg - 1))), NTHREADS, smem, s, true, jobs, nseg, 0, 0)) !=
+        if ((e = launch_after(k, dim3((unsigned)(a.n_chains * (nseg - 1))), NTHREADS, smem, s, false, jobs, nseg, 0, 0)) !=
             cudaSuccess)
             return e;
     }
@@ -29,15 +29,27 @@ template <int D> cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     if ((e = allow_smem(k, smem, done)) != cudaSuccess) return e;
     const int by_length = a.lens && a.n_chains > kSMs && a.n_chains / a.H <= kMaxRanked;
-    return launch_after(k, dim3((unsigned)(a.n_chains * nseg)), NTHREADS, smem, s, true, jobs, nseg, by_length,
+    return launch_after(k, dim3((unsigned)(a.n_chains * nseg)), NTHREADS, smem, s, nseg > 1, jobs, nseg, by_length,
                         nseg > 1 ? kWaitFirst : 0);
 }
 
 }  // namespace
 
-int select_chunk_tc() { return C; }
-size_t select_states_tc(int64_t n_chains, int64_t T, int d) { return segment_bytes(n_chains, d, segments(n_chains, T)); }
-cudaError_t launch_select_tc(const ScanArgs &s, cudaStream_t stream) {
+// [c][w][chunk][ends][states of segments]: each a multiple of 16 bytes.
+static size_t chunks_of(int64_t n_chains, int64_t T) { return (size_t)n_chains * (size_t)((T + C - 1) / C); }
+size_t select_workspace_tc(int64_t n_chains, int64_t T, int d) {
+    return chunks_of(n_chains, T) * (C * (sizeof(float2) + sizeof(float)) + 2 * sizeof(float4)) +
+           segment_bytes(n_chains, d, segments(n_chains, T));
+}
+cudaError_t launch_select_tc(const ScanArgs &scan, cudaStream_t stream) {
+    ScanArgs s = scan;
+    const size_t n = chunks_of(s.n_chains, s.T);
+    s.sel.n_chunks = (s.T + C - 1) / C;
+    s.sel.c = reinterpret_cast<float2 *>(s.ws);
+    s.sel.w = reinterpret_cast<float *>(s.sel.c + n * C);
+    s.sel.chunk = reinterpret_cast<float4 *>(s.sel.w + n * C);
+    s.sel.ends = s.sel.chunk + n;
+    s.ws = reinterpret_cast<float *>(s.sel.ends + n);
     return s.d == 64 ? launch<64>(s, stream) : launch<128>(s, stream);
 }
 
