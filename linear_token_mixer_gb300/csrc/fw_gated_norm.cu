@@ -142,22 +142,32 @@ template <typename T, int V, int R, int N> struct Ahead {
     }
 };
 
-// Every step-th row of a group from the m-th on, without a division a row: m = outer inner + i.
+// Every step-th row of group blockIdx.y from the m-th on, without a division or a product a row: m = outer inner + i
+// is row (outer groups + group) inner + i.
+struct Steps {                                 // from one to the next, and what a turn of `inner` adds
+    uint32_t m, i, row, turn;
+    int64_t at, turn_at;
+    __device__ __forceinline__ Steps(const GatedIn &in, uint32_t step)
+        : m(step), i(step % (uint32_t)in.inner),
+          row(step / (uint32_t)in.inner * (uint32_t)in.groups * (uint32_t)in.inner + step % (uint32_t)in.inner),
+          turn(((uint32_t)in.groups - 1) * (uint32_t)in.inner), at((int64_t)row * in.width), turn_at((int64_t)turn * in.width) {}
+};
 struct Walk {
-    uint32_t m, outer, i, step, step_outer, step_i;
-    __device__ __forceinline__ Walk(const GatedIn &in, uint32_t m_, uint32_t step_)
-        : m(m_), outer(m_ / (uint32_t)in.inner), i(m_ % (uint32_t)in.inner), step(step_),
-          step_outer(step_ / (uint32_t)in.inner), step_i(step_ % (uint32_t)in.inner) {}
-    __device__ __forceinline__ int64_t row(const GatedIn &in) const {
-        return ((int64_t)outer * in.groups + blockIdx.y) * in.inner + i;
-    }
-    __device__ __forceinline__ void next(const GatedIn &in) {
-        m += step;
-        outer += step_outer;
-        i += step_i;
+    uint32_t m, i, row;
+    int64_t at;                                // of the row's first element
+    __device__ __forceinline__ Walk(const GatedIn &in, uint32_t first)
+        : m(first), i(first % (uint32_t)in.inner),
+          row((first / (uint32_t)in.inner * (uint32_t)in.groups + blockIdx.y) * (uint32_t)in.inner + first % (uint32_t)in.inner),
+          at((int64_t)row * in.width) {}
+    __device__ __forceinline__ void next(const GatedIn &in, const Steps &s) {
+        m += s.m;
+        i += s.i;
+        row += s.row;
+        at += s.at;
         if (i >= (uint32_t)in.inner) {
             i -= (uint32_t)in.inner;
-            ++outer;
+            row += s.turn;
+            at += s.turn_at;
         }
     }
 };
@@ -168,24 +178,21 @@ template <typename T, int V, int R, int N, typename F>
 __device__ __forceinline__ void over_rows(Ahead<T, V, R, N> &ahead, const GatedIn &in, uint32_t group_rows, F work) {
     constexpr int RPB = block_of<R>() / R;
     const uint32_t step = gridDim.x * RPB;
-    uint32_t m0 = blockIdx.x * RPB;
-    Walk at(in, m0 + threadIdx.x / R, step), ask = at;
+    const Steps steps(in, step);
+    Walk at(in, blockIdx.x * RPB + threadIdx.x / R), ask = at;
     auto fetch = [&](int s) {
-        const bool live = ask.m < group_rows;
-        ahead.fetch(s, live, live ? ask.row(in) * in.width : 0);
-        ask.next(in);
+        ahead.fetch(s, ask.m < group_rows, ask.at);
+        ask.next(in, steps);
     };
     for (int s = 0; s < ahead.stages; ++s) fetch(s);
-    int64_t row = at.m < group_rows ? at.row(in) : 0;
-    for (; m0 < group_rows; m0 += step) {
+    for (uint32_t m0 = blockIdx.x * RPB; m0 < group_rows; m0 += step) {
         const bool live = at.m < group_rows;
-        at.next(in);
-        const int64_t next = at.m < group_rows ? at.row(in) : -1;
-        ahead.at = row * in.width;
+        const uint32_t row = at.row;
+        ahead.at = at.at;
+        at.next(in, steps);
         if (Ahead<T, V, R, N>::COPY) copies_wait(ahead.stages - 1);
-        work(live, row, next);
+        work(live, row, at.m < group_rows ? (int64_t)at.row : (int64_t)-1);
         fetch(ahead.stage);
-        row = next < 0 ? row : next;
         if (++ahead.stage == ahead.stages) ahead.stage = 0;
     }
     if (Ahead<T, V, R, N>::COPY) copies_wait(0);
@@ -211,7 +218,7 @@ __global__ void __launch_bounds__(block_of<R>(), fwd_blocks(R)) gated_kernel(Gat
             b[k] = rows.of(bias, k, 0.f);
             f[k] = rows.of(scale, k, 1.f);
         }
-    over_rows(rows, in, group_rows, [&](bool live, int64_t row, int64_t) {
+    over_rows(rows, in, group_rows, [&](bool live, uint32_t row, int64_t) {
         Chan<E> s[K], part = none<E>();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -285,18 +292,17 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
         for (int k = 0; k < K; ++k) sums[i][k] = none<E>();
     float next_mean = 0.f, next_rstd = 0.f;    // of the next row
     {
-        const Walk first(in, blockIdx.x * RPB + threadIdx.x / R, 1);
+        const Walk first(in, blockIdx.x * RPB + threadIdx.x / R);
         if (first.m < group_rows) {
-            const int64_t row = first.row(in);
-            if (!in.rms) next_mean = a.mean[row];
-            next_rstd = a.rstd[row];
+            if (!in.rms) next_mean = a.mean[first.row];
+            next_rstd = a.rstd[first.row];
         }
     }
     Chan<E> w[K];
 #pragma unroll
     for (int k = 0; k < K; ++k)
         if (rows.has(k)) w[k] = rows.of(weight, k, 1.f);
-    over_rows(rows, in, group_rows, [&](bool live, int64_t, int64_t next) {
+    over_rows(rows, in, group_rows, [&](bool live, uint32_t, int64_t next) {
         const float mean = next_mean, rstd = next_rstd;
         if (next >= 0) {
             if (!in.rms) next_mean = a.mean[next];
