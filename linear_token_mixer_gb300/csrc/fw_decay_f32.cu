@@ -19,6 +19,9 @@
 // each other, the long ones by the split products: scan_out (d = 128) issues in 36 % of its
 // cycles, its tensor pipe is busy for 39 %, and its sixteen warps an SM wait for the states' loads and
 // for each other's MMAs.
+//
+// Selective scans (fw_select.cuh) are the same launches; a warp of a block forms the chunk's logs first, in both
+// that need them, which is a launch less than tables of them: B4 H8 T1000 d = 64 37 us, B4 H8 T2048 d = 128 184 us.
 #include "fw_decay_tc.cuh"
 #include "fw_select.cuh"
 #include "fw_sm100.cuh"

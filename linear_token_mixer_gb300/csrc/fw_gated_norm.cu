@@ -16,6 +16,11 @@
 // the squares about it (never E[s^2] - E[s]^2).  Blocks stride over the rows of one group, so that a thread keeps
 // its columns' weights and, in the backward pass, its sums in registers; a block writes one
 // partial row of sums and a second kernel adds them in a fixed order.
+//
+// Measured (one GB300, bf16): 262144 x 128 in 16 groups, rms, gate before: forward 36 us (82 % of the measured copy
+// rate), backward 65 us (76 %); 16384 x 2048 with a gate 39 and 79 us, with a scaled residual 45 and 95 us; 8192 columns
+// backward 213 us (37 %), whose 1024 threads have 64 registers each.  Short rows are bound by instructions, about 28 an
+// element forward (issue slots 76 % busy), wide ones by the two barriers of a row's sums.  64 x 2048: 3.5 us of a call of 20.
 #include "fw_gated_norm.cuh"
 #include "fw_partial.cuh"
 #include "fw_rows.cuh"
@@ -27,7 +32,8 @@ using namespace fw::rows;
 
 constexpr int kEach = 8;                       // elements of a row a thread
 
-// Blocks of an SM, of R threads a row, forward (80 or 64 registers a thread) and backward (128 or 64).
+// Blocks of an SM, of R threads a row, forward (80 or 64 registers a thread) and backward (128 or 64).  (Four forward,
+// without room for the parameters in registers: 262144 x 128 52 us for 47, 16384 x 2048 69 for 55.)
 constexpr int fwd_blocks(int R) { return R < 512 ? 3 : R < 1024 ? 2 : 1; }
 constexpr int bwd_blocks(int R) { return R < 512 ? 2 : 1; }
 template <int R> constexpr int block_of() { return R < 256 ? 256 : R; }

@@ -6,7 +6,8 @@
 // A prompt is the chunked scan of fw_scan_tc.cuh (bf16) or fw_decay_f32.cu (fp32) with each chunk's own logs
 // (chunk_logs) in place of powers of one decay.
 //
-// One token: one block a state, the state once through registers, as decay_step_kernel.
+// One token: one block a state, the state once through registers, as decay_step_kernel.  Bound by the state's bytes:
+// B256 H32 d = 128 bf16 (1.08 GB) 157.9 us, 6.9 TB/s, the measured copy rate.
 #include "fw_select.cuh"
 
 namespace fw {
