@@ -436,9 +436,10 @@ int fw_layer_norm_backward(const void *dy, const void *x, const float *weight, c
  * which overlaps are refused.  log_decay is finite and <= 0 and dt >= 0; where a decay grows instead
  * (log_decay dt > 0) it is computed as it is, as long as its sums within 128 tokens stay below 80.
  * A decay below e^-104 is zero: the state starts afresh with the token.
- *   bf16 rows: the masked scores, and the state as a row reads it, are rounded to bf16 once, like the
- *   rows that come out; the steps, the decays and S_T are fp32 throughout.  Where the decays of a chunk of
- *   128 tokens multiply to e^-24 or more, its sums are formed up to e^24 times their size.
+ *   bf16 rows: the masked scores, with skip / scale on their diagonal, and the state as a row reads it, are
+ *   rounded to bf16 once, like the rows that come out; the steps, the decays and S_T are fp32 throughout.
+ *   Where the decays of a chunk of 128 tokens, or of 32 of them, multiply to e^-40 or more, its sums are formed up
+ *   to e^40 times their size: scores or rows, and skip / scale, beyond about 1e20 may overflow.
  *   An infinity or NaN in v reaches the rows that depend on it and nothing else, and may arrive as
  *   NaN; one in k, or in a step, may reach its chunk of 128 tokens and what follows.
  */
@@ -485,7 +486,7 @@ int fw_select_step(const void *q, const void *k, const void *v, const fw_gates *
  *
  * Of every channel before a mixer, `width` taps (2 .. FW_CONV_MAX):
  *     a_t = bias + sum_w weight[w] x_{t-width+1+w},   y_t = a_t, with FW_FLAG_SILU a_t / (1 + exp(-a_t)),
- * over rows of shape->d_k = d_v = d channels, any d >= 1.  Rows before the first come from `state`, so that
+ * over rows of shape->d_k = d_v = d channels, any d >= 1 (B H T d below 2^34).  Rows before the first come from `state`, so that
  * calls continue one another.  lens and FW_FLAG_ZERO_REST as in the decayed calls: rows from lens[b]
  * on are never used, and the state behind a row of the batch is that behind its last token.
  *   x, y, dy, dx   [B][H][T][d] of `dtype`
@@ -539,7 +540,7 @@ int fw_conv_step(const void *x, const float *weight, const float *bias, void *st
 typedef struct {
     const void *gate;      /* [rows][width] of `dtype`, or NULL (no gate) */
     const void *residual;  /* [rows][width] of `dtype`, or NULL (u = x) */
-    const float *scale;    /* [groups][width] or NULL (ones) */
+    const float *scale;    /* [groups][width] or NULL (ones); refused without a residual */
     const float *weight;   /* [groups][width] or NULL (ones) */
     const float *bias;     /* [groups][width] or NULL (zeros) */
     int64_t groups, inner; /* rows = groups * inner * a whole number (1, rows: one group) */

@@ -902,7 +902,8 @@ int gated_in(const void *x, const fw_gated *g, int64_t rows, int64_t width, fw_d
     if (any_misaligned({x, g->gate, g->residual, g->scale, g->weight, g->bias})) return FW_ERR_ALIGN;
     if (!(std::isfinite(g->eps) && g->eps >= 0.f)) return FW_ERR_ARG;
     if ((g->rms | g->gate_after) & ~1) return FW_ERR_MODE;
-    *in = GatedIn{x, g->gate, g->residual, g->residual ? g->scale : nullptr, g->weight, g->bias, rows, (int)width,
+    if (g->scale && !g->residual) return FW_ERR_ARG;
+    *in = GatedIn{x, g->gate, g->residual, g->scale, g->weight, g->bias, rows, (int)width,
                   (int)g->groups, (int)g->inner, dtype, g->eps, g->rms, g->gate_after};
     return FW_OK;
 }

@@ -231,7 +231,7 @@ conv_bwd_kernel(ConvBwdArgs a, uint32_t strip, uint32_t strips, int lanes, uint3
                     Chan<V> r = bias;
 #pragma unroll
                     for (int i = 0; i < W; ++i) r = fma_n(w[i], win[(u + 1 + i) % W], r);
-                    const Chan<V> s = sigmoid_n<T>(r), slope = silu_slope(r, s, mul_n(r, s));
+                    const Chan<V> slope = silu_slope(r, sigmoid_n<T>(r));
                     if (on) da[u] = mul_n(da[u], slope);
                 }
                 if (ALL || t + u < end) {

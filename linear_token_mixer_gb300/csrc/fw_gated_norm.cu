@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
                 Chan<E> dz;
                 if (in.gate_after) dz = mul_n(dy, fma_n(n[k], w[k], rows.of(bias, k, 0.f)));
                 else dz = mul_n(d, sum_of(k));
-                dz = mul_n(dz, silu_slope(z, sg[k], act));
+                dz = mul_n(dz, silu_slope(z, sg[k]));
                 if (in.gate_after) dy = mul_n(dy, act);        // of the norm's output
                 else d = mul_n(d, act);
                 if (a.dgate) rows.put(a.dgate, k, dz);

@@ -142,10 +142,10 @@ template <typename T, int V> __device__ __forceinline__ Chan<V> sigmoid_n(const 
     }
     return s;
 }
-// silu'(a) = s (1 + a - a s), s = sigmoid(a), given act = a s
-template <int V> __device__ __forceinline__ Chan<V> silu_slope(const Chan<V> &a, const Chan<V> &s, const Chan<V> &act) {
-    const Chan<V> less = fma_n(act, all<V>(-1.f), add_n(a, all<V>(1.f)));
-    return mul_n(s, less);
+// silu'(a) = s (1 + a (1 - s)), s = sigmoid(a)
+template <int V> __device__ __forceinline__ Chan<V> silu_slope(const Chan<V> &a, const Chan<V> &s) {
+    const Chan<V> rest = fma_n(s, all<V>(-1.f), all<V>(1.f));
+    return mul_n(s, fma_n(a, rest, all<V>(1.f)));
 }
 
 // ---- copies into shared memory, each thread waiting for its own ----------------------------------

@@ -82,7 +82,7 @@ def gated(x, weight=None, bias=None, gate=None, residual=None, scale=None, rms=F
     u = x
     if residual is not None:
         u = x + (residual if scale is None else _wide(scale) * residual)
-    act = None if gate is None else gate / (1 + torch.exp(-gate))
+    act = None if gate is None else gate * torch.sigmoid(gate)   # (whose derivative is finite for any gate)
     s = u if act is None or gate_after else u * act
     m = torch.zeros_like(s[..., :1]) if rms else s.mean(-1, keepdim=True)
     r = 1 / torch.sqrt(((s - m) ** 2).mean(-1, keepdim=True) + eps)

@@ -127,6 +127,22 @@ def test_values_that_are_not_finite_reach_their_taps_only(dtype):
     assert torch.isfinite(y).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_slopes_of_large_values(dtype):
+    """silu'(a) is 1 for large a and 0 for large -a, of any size."""
+    a = torch.tensor([60.0, 3e4, 1e7, 2.0 ** 30, 1e30, -60.0, -3e4, -2.0 ** 30, -1e30]).to(dtype)
+    x = a.view(1, 1, 1, -1).cuda()
+    w = torch.zeros(1, 9, 2, device="cuda")
+    w[:, :, 1] = 1.0
+    dx, _, _, _ = fw.conv_backward(torch.ones_like(x), x, w)
+    y, _ = fw.conv_prefill(x, w)
+    r = a.double()
+    sig = 1 / (1 + torch.exp(-r))
+    # (what is below 2^-126 may be zero)
+    for got, want in ((dx, sig * (1 + r * (1 - sig))), (y, r * sig)):
+        assert ((got.cpu().double().view(-1) - want).abs() <= TOL[dtype] * want.abs() + 2.0 ** -126).all()
+
+
 def test_gradients_repeat_to_the_bit():
     x, g = inputs(8, 4, 300, 96, 4, BF16, seed=3)
     first = [t.clone() for t in fw.conv_backward(g["dy"], g["x"], g["w"], g["b"], g["state"])]

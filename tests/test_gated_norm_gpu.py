@@ -178,6 +178,15 @@ def test_in_place(width, dtype):
         assert all(torch.equal(a, b) for a, b in zip(got, grads))
 
 
+@pytest.mark.parametrize("after", [False, True])
+def test_gates_of_any_size(after):
+    """silu(z) is z, and its slope 1, for large z; both 0 for large -z."""
+    x, d = inputs(6, 64, F32, seed=5, residual=False)
+    x["gate"][:, ::4], x["gate"][:, 1::4] = 1e6, -1e6
+    x["gate"][:, 2::4] = 50.0
+    check(x, d, F32, True, after, dtotal=False)
+
+
 def test_values_that_are_not_finite_stay_in_their_row():
     x, d = inputs(20, 300, F32, seed=4)
     g = {n: t.cuda() for n, t in x.items()}

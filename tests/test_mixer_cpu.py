@@ -155,7 +155,8 @@ def test_select_step_refusals(L, kw, code):
 
 @no_gpu
 def test_a_small_workspace_is_refused(L):
-    for T, dt in ((1, 1), (300, 1), (1, 0), (300, 0)):
+    assert fw.select_workspace(1, 4, 64, 64, torch.float32) == 0       # one chunk: none
+    for T, dt in ((1, 1), (300, 1), (65, 0), (300, 0)):
         n = fw.select_workspace(1, 4, T, 64, torch.bfloat16 if dt else torch.float32)
         assert n > 0 and _select(L, shape=(1, 4, T, 64, 64), dtype=dt, dt_type=0, nws=n - 1) == -11
     n = L.fw_conv_workspace(_shape((2, 4, 8, 5, 5)), 3)
@@ -234,7 +235,7 @@ GATED = [(dict(x=None), -1), (dict(args=False), -1), (dict(rows=0), -2), (dict(r
 
 @no_gpu
 @pytest.mark.parametrize("kw,code", GATED + [
-    (dict(y=None), -1), (dict(y=P[0] + 16), -9), (dict(total=P[6]), -9), (dict(total=P[2] + 32), -9),
+    (dict(y=None), -1), (dict(res=None), -9), (dict(y=P[0] + 16), -9), (dict(total=P[6]), -9), (dict(total=P[2] + 32), -9),
     (dict(y=P[4]), -9), (dict(mean=P[0]), -9), (dict(rstd=P[8]), -9), (dict(mean=P[3]), -9), (dict(y=P[6] + 4), -4)])
 def test_gated_refusals(L, kw, code):
     assert _gated(L, **kw) == code

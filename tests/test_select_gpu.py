@@ -163,6 +163,13 @@ def test_chains_in_segments(B, H, G, T, ragged, d, rate):
     check(run(g, lens=lg, S_T=S), want, BF16)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_chains_of_many_chunks(d):
+    """More chunks in one piece than a CTA has warps to form their tables."""
+    x, g = inputs(1, 80, 1, 3700, d, BF16, seed=5, rate=(0.05, 16.0))
+    check(run(g), ref(x), BF16)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_more_chains_than_multiprocessors(dtype):
     B, H, G, T, d = 40, 8, 4, 140, 64
