@@ -763,7 +763,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             float4 ends = {};
             float2 own_row = {};
             // What a row has of its own value beside the scores: skip v = scale (skip / scale) v goes onto the diagonal,
-            // where it is rounded with the score (2^-9 of it; as a term of its own in the epilogue, 11 us of 131
+            // where it is rounded with the score (2^-8 of it at most; as a term of its own in the epilogue, 11 us of 131
             // for B8 H16 T4096 d = 128).  With a scale of zero the scores are.
             const bool nil = SEL && a.out_scale == 0.f;
             const float skip = SEL && a.sel.gate.skip ? a.sel.gate.skip[chain % a.H] / (nil ? 1.f : a.out_scale) : 0.f;
