@@ -30,12 +30,14 @@ namespace {
 
 using namespace fw::rows;
 
-constexpr int kEach = 8;                       // elements of a row a thread
+constexpr int kEach = 8;                       // elements of a row a thread, 16 in the widest rows' backward pass
 
 // Blocks of an SM, of R threads a row, forward (80 or 64 registers a thread) and backward (128 or 64).  (Four forward,
 // without room for the parameters in registers: 262144 x 128 52 us for 47, 16384 x 2048 69 for 55.)
 constexpr int fwd_blocks(int R) { return R < 512 ? 3 : R < 1024 ? 2 : 1; }
 constexpr int bwd_blocks(int R) { return R < 512 ? 2 : 1; }
+// Elements a thread in the backward pass of rows of R threads of eight.
+constexpr int bwd_each(int R, int V) { return R < 1024 || V == 1 ? kEach : 2 * kEach; }
 template <int R> constexpr int block_of() { return R < 256 ? 256 : R; }
 
 // All but the newest `left` groups of copies have landed.
@@ -78,15 +80,25 @@ template <int R, int N> __device__ __forceinline__ void row_sums(float (&z)[N], 
     }
 }
 
-// The columns of a thread, in K parts of E elements that are worked on at once, and the rows that it works on,
-// up to `stages` of them ahead in its slots of shared memory, N arrays each.  V elements a load; where that is
-// one, the two of a part lie R columns apart and the second may be behind the row's end.  (Elements of two bytes
-// are no copy's size: those are read from memory when asked for.)
-template <typename T, int V, int R, int N> struct Ahead {
-    static constexpr int E = V > 1 ? V : 2, K = kEach / E, BYTES = V * (int)sizeof(T);
-    static constexpr bool COPY = BYTES >= 4;
+// All threads of a row (and others) are here, and see what the others have written to shared memory.
+template <int R> __device__ __forceinline__ void row_barrier() {
+    if constexpr (R <= 32) __syncwarp();
+    else __syncthreads();
+}
+
+// The columns of a thread, in K parts of E elements that are worked on at once, and the rows that it works on, up to
+// `stages` of them ahead in shared memory, N arrays each.  V elements a load, in slots of the thread's own; where V is
+// one, the two of a part lie R columns apart and the second may be behind the row's end.  bf16 rows of an odd width begin
+// at any multiple of two bytes, which is no copy's size: the row's threads copy all 16-byte units that the row touches, for
+// one another.  (Outputs may be inputs as well: what a row reads has landed before any of it is written, and of its
+// neighbours' elements in its first and last unit nothing is used.  10000 x 1023 with a gate and a residual, forward
+// and backward: 25 and 71 us; read from memory when asked for, 57 and 217.)
+template <typename T, int V, int R, int N, int C = kEach> struct Ahead {
+    static constexpr int E = V > 1 ? V : 2, K = C / E, BYTES = V * (int)sizeof(T), ROW = R * C * (int)sizeof(T);
+    static constexpr bool SHARED = BYTES < 4;
+    static constexpr int PLACE = block_of<R>() / R * (ROW + (SHARED ? 16 : 0));   // bytes of an array's rows of a block
     const void *src[N];
-    Raw<T, V> *slots;
+    char *slots;
     int stages, width, lane;
     int64_t at;                                // of the row at hand
     int stage = 0;
@@ -95,23 +107,38 @@ template <typename T, int V, int R, int N> struct Ahead {
         return V > 1 ? (k * R + lane) * V + e : (k * E + e) * R + lane;
     }
     __device__ __forceinline__ bool has(int k, int e = 0) const { return column(k, e) < width; }
+    __device__ __forceinline__ char *array_at(int s, int a) const { return slots + (s * N + a) * PLACE; }
     __device__ __forceinline__ Raw<T, V> *slot(int s, int a, int i) const {
-        return slots + ((s * N + a) * (kEach / V) + i) * block_of<R>() + threadIdx.x;
+        return reinterpret_cast<Raw<T, V> *>(array_at(s, a)) + i * block_of<R>() + threadIdx.x;
+    }
+    __device__ __forceinline__ char *row_slot(int s, int a) const {
+        return array_at(s, a) + threadIdx.x / R * (ROW + 16);
     }
     // Copies of a row into a stage, a group of them whether there is a row or not.
     __device__ __forceinline__ void fetch(int s, bool live, int64_t row_at) {
-        if constexpr (COPY) {
-            if (live)
+        if (live)
 #pragma unroll
-                for (int a = 0; a < N; ++a)
-                    if (src[a])
+            for (int a = 0; a < N; ++a) {
+                if (!src[a]) continue;
+                if constexpr (SHARED) {
+                    const int64_t first = row_at * (int)sizeof(T) & ~(int64_t)15;
+                    const int bytes = (int)(row_at * (int)sizeof(T) - first) + width * (int)sizeof(T);
+                    const char *const from = static_cast<const char *>(src[a]) + first;
+                    char *const to = row_slot(s, a);
 #pragma unroll
-                        for (int i = 0; i < kEach / V; ++i) {
-                            const int c = V > 1 ? column(i) : column(i / E, i % E);
-                            if (c < width) copy_async<BYTES>(slot(s, a, i), static_cast<const T *>(src[a]) + row_at + c);
-                        }
-            copies_commit();
-        }
+                    for (int i = 0; i <= ROW / 16 / R; ++i) {
+                        const int c = (i * R + lane) * 16;
+                        if (c < bytes) copy_async_part(to + c, from + c, min(bytes - c, 16));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C / V; ++i) {
+                        const int c = V > 1 ? column(i) : column(i / E, i % E);
+                        if (c < width) copy_async<BYTES>(slot(s, a, i), static_cast<const T *>(src[a]) + row_at + c);
+                    }
+                }
+            }
+        copies_commit();
     }
     __device__ __forceinline__ Chan<E> get(int a, int k) const {
         if constexpr (V > 1) return widen(*slot(stage, a, k));
@@ -120,8 +147,9 @@ template <typename T, int V, int R, int N> struct Ahead {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (has(k, e)) {
-                    if constexpr (COPY) x[e] = to_f32(slot(stage, a, k * E + e)->v);
-                    else x[e] = to_f32(static_cast<const T *>(src[a])[at + column(k, e)]);
+                    if constexpr (SHARED)
+                        x[e] = to_f32(reinterpret_cast<const T *>(row_slot(stage, a))[(at & (16 / (int)sizeof(T) - 1)) + column(k, e)]);
+                    else x[e] = to_f32(slot(stage, a, k * E + e)->v);
                 }
             return {{pair(x[0], x[1])}};
         }
@@ -180,8 +208,8 @@ struct Walk {
 
 // Walks the rows of a block's share of group blockIdx.y: work(live, row, next row or -1) with the row's
 // data in `ahead`.
-template <typename T, int V, int R, int N, typename F>
-__device__ __forceinline__ void over_rows(Ahead<T, V, R, N> &ahead, const GatedIn &in, uint32_t group_rows, F work) {
+template <typename T, int V, int R, int N, int C, typename F>
+__device__ __forceinline__ void over_rows(Ahead<T, V, R, N, C> &ahead, const GatedIn &in, uint32_t group_rows, F work) {
     constexpr int RPB = block_of<R>() / R;
     const uint32_t step = gridDim.x * RPB;
     const Steps steps(in, step);
@@ -190,18 +218,32 @@ __device__ __forceinline__ void over_rows(Ahead<T, V, R, N> &ahead, const GatedI
         ahead.fetch(s, ask.m < group_rows, ask.at);
         ask.next(in, steps);
     };
-    for (int s = 0; s < ahead.stages; ++s) fetch(s);
+    // A stage of the thread's own is filled again as soon as it is read; one that the row's threads share, when all of them
+    // are at the next row (with one stage: when all have read it).
+    constexpr bool SHARED = Ahead<T, V, R, N, C>::SHARED;
+    const int first = ahead.stages - SHARED;
+    for (int s = 0; s < first; ++s) fetch(s);
     for (uint32_t m0 = blockIdx.x * RPB; m0 < group_rows; m0 += step) {
         const bool live = at.m < group_rows;
         const uint32_t row = at.row;
         ahead.at = at.at;
         at.next(in, steps);
-        if (Ahead<T, V, R, N>::COPY) copies_wait(ahead.stages - 1);
+        if constexpr (SHARED) {
+            if (first == 0) {
+                row_barrier<R>();
+                fetch(0);
+            }
+            copies_wait(first == 0 ? 0 : first - 1);
+            row_barrier<R>();
+            if (first > 0) fetch(ahead.stage == 0 ? first : ahead.stage - 1);
+        } else {
+            copies_wait(first - 1);
+        }
         work(live, row, at.m < group_rows ? (int64_t)at.row : (int64_t)-1);
-        fetch(ahead.stage);
+        if constexpr (!SHARED) fetch(ahead.stage);
         if (++ahead.stage == ahead.stages) ahead.stage = 0;
     }
-    if (Ahead<T, V, R, N>::COPY) copies_wait(0);
+    copies_wait(0);
 }
 
 template <typename T, int V, int R>
@@ -211,7 +253,7 @@ __global__ void __launch_bounds__(block_of<R>(), fwd_blocks(R)) gated_kernel(Gat
     extern __shared__ uint4 slots[];
     __shared__ float red[R > 32 ? BLOCK / 32 : 1];
     const GatedIn &in = a.in;
-    Rows rows{{in.x, in.gate, in.residual}, reinterpret_cast<Raw<T, V> *>(slots), stages, in.width, (int)(threadIdx.x % R), 0};
+    Rows rows{{in.x, in.gate, in.residual}, reinterpret_cast<char *>(slots), stages, in.width, (int)(threadIdx.x % R), 0};
     const float inv = 1.f / (float)in.width;
     const int64_t pat = (int64_t)blockIdx.y * in.width;
     const float *const weight = in.weight ? in.weight + pat : nullptr, *const bias = in.bias ? in.bias + pat : nullptr,
@@ -277,14 +319,14 @@ __global__ void __launch_bounds__(block_of<R>(), fwd_blocks(R)) gated_kernel(Gat
     });
 }
 
-template <typename T, int V, int R>
+template <typename T, int V, int R, int C>
 __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel(GatedBwdArgs a, uint32_t group_rows, int stages) {
-    using Rows = Ahead<T, V, R, 5>;
+    using Rows = Ahead<T, V, R, 5, C>;
     constexpr int K = Rows::K, E = Rows::E, BLOCK = block_of<R>(), RPB = BLOCK / R;
     extern __shared__ uint4 slots[];
     __shared__ float red[R > 32 ? 2 * BLOCK / 32 : 1];
     const GatedIn &in = a.in;
-    Rows rows{{in.x, a.dy, in.gate, in.residual, a.dtotal}, reinterpret_cast<Raw<T, V> *>(slots), stages, in.width,
+    Rows rows{{in.x, a.dy, in.gate, in.residual, a.dtotal}, reinterpret_cast<char *>(slots), stages, in.width,
               (int)(threadIdx.x % R), 0};
     const int width = in.width;
     const float inv = 1.f / (float)width;
@@ -304,10 +346,13 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
             next_rstd = a.rstd[first.row];
         }
     }
-    Chan<E> w[K];
+    constexpr bool HOLD = C == kEach;
+    Chan<E> w[HOLD ? K : 1];
+    if constexpr (HOLD)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (rows.has(k)) w[k] = rows.of(weight, k, 1.f);
+        for (int k = 0; k < K; ++k)
+            if (rows.has(k)) w[k] = rows.of(weight, k, 1.f);
+    auto weight_of = [&](int k) { return HOLD ? w[HOLD ? k : 0] : rows.of(weight, k, 1.f); };
     over_rows(rows, in, group_rows, [&](bool live, uint32_t, int64_t next) {
         const float mean = next_mean, rstd = next_rstd;
         if (next >= 0) {
@@ -318,22 +363,26 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
             const Chan<E> x = rows.get(0, k);
             return in.residual ? fma_n(rows.of(scale, k, 1.f), rows.get(3, k), x) : x;
         };
-        Chan<E> n[K], g[K], sg[K];             // n = norm(s), g, and the sigmoid of the gate
+        // n = norm(s), g, and the sigmoid of the gate
+        auto part_of = [&](int k, Chan<E> &n, Chan<E> &g, Chan<E> &sg) {
+            n = sum_of(k);
+            g = mul_n(rows.get(1, k), weight_of(k));
+            if (in.gate) {
+                const Chan<E> z = rows.get(2, k);
+                sg = sigmoid_n<T>(z);
+                const Chan<E> act = mul_n(z, sg);
+                if (in.gate_after) g = mul_n(g, act);
+                else n = mul_n(n, act);
+            }
+            if (!in.rms) n = add_n(n, all<E>(-mean));
+            n = mul_n(n, all<E>(rstd));
+        };
+        Chan<E> n[K], g[K], sg[K];
         Chan<E> sum_g = none<E>(), sum_gn = none<E>();
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (live && rows.has(k)) {
-                n[k] = sum_of(k);
-                g[k] = mul_n(rows.get(1, k), w[k]);
-                if (in.gate) {
-                    const Chan<E> z = rows.get(2, k);
-                    sg[k] = sigmoid_n<T>(z);
-                    const Chan<E> act = mul_n(z, sg[k]);
-                    if (in.gate_after) g[k] = mul_n(g[k], act);
-                    else n[k] = mul_n(n[k], act);
-                }
-                if (!in.rms) n[k] = add_n(n[k], all<E>(-mean));
-                n[k] = mul_n(n[k], all<E>(rstd));
+                part_of(k, n[k], g[k], sg[k]);
                 sum_g = add_n(sum_g, g[k]);
                 sum_gn = fma_n(g[k], n[k], sum_gn);
             }
@@ -344,13 +393,14 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (!rows.has(k)) continue;
+            if constexpr (!HOLD) part_of(k, n[k], g[k], sg[k]);
             // rstd (g - mean(g) - n mean(g n))
             Chan<E> d = fma_n(n[k], all<E>(mgn), fma_n(g[k], all<E>(rstd), all<E>(mg)));
             Chan<E> dy = rows.get(1, k);
             if (in.gate) {
                 const Chan<E> z = rows.get(2, k), act = mul_n(z, sg[k]);
                 Chan<E> dz;
-                if (in.gate_after) dz = mul_n(dy, fma_n(n[k], w[k], rows.of(bias, k, 0.f)));
+                if (in.gate_after) dz = mul_n(dy, fma_n(n[k], weight_of(k), rows.of(bias, k, 0.f)));
                 else dz = mul_n(d, sum_of(k));
                 dz = mul_n(dz, silu_slope(z, sg[k]));
                 if (in.gate_after) dy = mul_n(dy, act);        // of the norm's output
@@ -386,12 +436,12 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int e = 0; e < E; ++e) part[(threadIdx.x / R) * (R * kEach) + rows.column(k, e)] = element(sums[i][k], e);
+                for (int e = 0; e < E; ++e) part[(threadIdx.x / R) * (R * C) + rows.column(k, e)] = element(sums[i][k], e);
             __syncthreads();
             for (int c = threadIdx.x; c < width; c += BLOCK) {
                 float z = 0.f;
 #pragma unroll 4
-                for (int p = 0; p < RPB; ++p) z += part[p * (R * kEach) + c];
+                for (int p = 0; p < RPB; ++p) z += part[p * (R * C) + c];
                 out[i * width + c] = z;
             }
         }
@@ -416,14 +466,15 @@ uint32_t slices_of(int64_t rows, int64_t groups, int R, int blocks) {
     return (uint32_t)(s < 1 ? 1 : s > most ? most : s);
 }
 
-// Rows ahead, of `arrays` a block each, that leave room for the blocks of an SM.
-template <typename T, int R> int stages_of(int arrays, int blocks) {
-    const int row = arrays * block_of<R>() * kEach * (int)sizeof(T), room = 216 * 1024 / blocks;
-    return row * 3 <= room ? 3 : row * 2 <= room ? 2 : 1;
+// Rows ahead, of a block's `bytes` each, that leave room for the blocks of an SM.
+int stages_of(int bytes, int blocks) {
+    const int room = 216 * 1024 / blocks;
+    return bytes * 3 <= room ? 3 : bytes * 2 <= room ? 2 : 1;
 }
 
 template <typename T, int V, int R> cudaError_t run(const GatedArgs &a, cudaStream_t s) {
-    const int stages = stages_of<T, R>(3, fwd_blocks(R)), smem = stages * 3 * block_of<R>() * kEach * (int)sizeof(T);
+    constexpr int ROW = 3 * Ahead<T, V, R, 3>::PLACE;
+    const int stages = stages_of(ROW, fwd_blocks(R)), smem = stages * ROW;
     auto k = gated_kernel<T, V, R>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k, smem, done);
@@ -433,11 +484,13 @@ template <typename T, int V, int R> cudaError_t run(const GatedArgs &a, cudaStre
     return cudaGetLastError();
 }
 
-template <typename T, int V, int R> cudaError_t run(const GatedBwdArgs &a, cudaStream_t s) {
+template <typename T, int V, int R0> cudaError_t run(const GatedBwdArgs &a, cudaStream_t s) {
+    constexpr int C = bwd_each(R0, V), R = R0 * kEach / C;
     const GatedIn &in = a.in;
     const uint32_t slices = slices_of(in.rows, in.groups, R, bwd_blocks(R));
-    const int stages = stages_of<T, R>(5, bwd_blocks(R)), smem = stages * 5 * block_of<R>() * kEach * (int)sizeof(T);
-    auto k = gated_bwd_kernel<T, V, R>;
+    constexpr int ROW = 5 * Ahead<T, V, R, 5, C>::PLACE;
+    const int stages = stages_of(ROW, bwd_blocks(R)), smem = stages * ROW;
+    auto k = gated_bwd_kernel<T, V, R, C>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(k, smem, done);
     if (e != cudaSuccess) return e;

@@ -157,11 +157,13 @@ def test_a_mean_far_from_zero_and_rows_that_are_equal(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("width", [96, 1024, 5000])
-def test_in_place(width, dtype):
-    x, d = inputs(23, width, dtype, seed=2)
+@pytest.mark.parametrize("width", [7, 33, 96, 130, 1023, 1024, 4097, 5000])
+@pytest.mark.parametrize("after", [False, True])
+@pytest.mark.parametrize("rows", [23, 1300])
+def test_in_place(rows, after, width, dtype):
+    x, d = inputs(rows, width, dtype, seed=2)
     g = {n: t.cuda() for n, t in {**x, **d}.items()}
-    kind = dict(scale=g["scale"], rms=True)
+    kind = dict(scale=g["scale"], rms=True, gate_after=after)
     y, total, _, rstd = fw.gated_norm(g["x"], g["weight"], g["bias"], gate=g["gate"], residual=g["residual"], **kind)
     for a, b in (("x", "residual"), ("gate", "x"), ("residual", "gate")):
         z = {n: t.clone() for n, t in g.items()}
