@@ -14,14 +14,17 @@
 // thread into slots of its own, so that nothing but the copies has to be waited for), and the backward
 // pass reads a row from there twice, which costs fewer registers than keeping it.  The mean is taken first and
 // the squares about it (never E[s^2] - E[s]^2).  Blocks stride over the rows of one group, so that a thread keeps
-// its columns' weights and, in the backward pass, its sums in registers; a block writes one
+// its columns' parameters and, in the backward pass, its sums in registers; a block writes one
 // partial row of sums and a second kernel adds them in a fixed order.
 //
 // Measured (one GB300, bf16): 262144 x 128 in 16 groups, rms, gate before: forward 36 us (82 % of the measured copy
-// rate), backward 65 us (76 %); 16384 x 2048 with a gate 39 and 79 us, with a scaled residual 45 and 95 us; 8192 columns
-// backward 213 us (37 %), whose 1024 threads have 64 registers each.  Short rows are bound by instructions, about 28 an
-// element forward (issue slots 76 % busy), wide ones by the two barriers of a row's sums.  64 x 2048: 3.5 us of a call of 20.
+// rate), backward 65 us (76 %); 16384 x 2048 with a gate 39 and 79 us, with a scaled residual 45 and 81 us; 4096 x 8192 with a
+// gate 47 and 128 us (39 %).  Short rows are bound by instructions, about 28 an element forward (issue slots 76 % busy),
+// wide ones by the two barriers of a row's sums.  64 x 2048: 3.5 us of a call of 20.
 #include "fw_gated_norm.cuh"
+
+#include <type_traits>
+
 #include "fw_partial.cuh"
 #include "fw_rows.cuh"
 
@@ -30,13 +33,15 @@ namespace {
 
 using namespace fw::rows;
 
-constexpr int kEach = 8;                       // elements of a row a thread, 16 in the widest rows' backward pass
+constexpr int kEach = 8;                       // elements of a row a thread
 
 // Blocks of an SM, of R threads a row, forward (80 or 64 registers a thread) and backward (128 or 64).  (Four forward,
 // without room for the parameters in registers: 262144 x 128 52 us for 47, 16384 x 2048 69 for 55.)
 constexpr int fwd_blocks(int R) { return R < 512 ? 3 : R < 1024 ? 2 : 1; }
 constexpr int bwd_blocks(int R) { return R < 512 ? 2 : 1; }
-// Elements a thread in the backward pass of rows of R threads of eight.
+// Elements a thread in the backward pass: where 1024 threads with eight each would have 64 registers, 512 with sixteen, which
+// form a row's values again behind its sums instead of holding them (4096 x 8192 with a gate 145 -> 128 us, with a
+// scaled residual 178 -> 156).  Single elements are better off with the 1024 (4096 x 8191: 221 us for 291).
 constexpr int bwd_each(int R, int V) { return R < 1024 || V == 1 ? kEach : 2 * kEach; }
 template <int R> constexpr int block_of() { return R < 256 ? 256 : R; }
 
@@ -92,10 +97,10 @@ template <int R> __device__ __forceinline__ void row_barrier() {
 // at any multiple of two bytes, which is no copy's size: the row's threads copy all 16-byte units that the row touches, for
 // one another.  (Outputs may be inputs as well: what a row reads has landed before any of it is written, and of its
 // neighbours' elements in its first and last unit nothing is used.  10000 x 1023 with a gate and a residual, forward
-// and backward: 25 and 71 us; read from memory when asked for, 57 and 217.)
+// and backward: 25 and 55 us; read from memory when asked for, 57 and 217.)
 template <typename T, int V, int R, int N, int C = kEach> struct Ahead {
     static constexpr int E = V > 1 ? V : 2, K = C / E, BYTES = V * (int)sizeof(T), ROW = R * C * (int)sizeof(T);
-    static constexpr bool SHARED = BYTES < 4;
+    static constexpr bool SHARED = BYTES == 2;
     static constexpr int PLACE = block_of<R>() / R * (ROW + (SHARED ? 16 : 0));   // bytes of an array's rows of a block
     const void *src[N];
     char *slots;
@@ -147,8 +152,7 @@ template <typename T, int V, int R, int N, int C = kEach> struct Ahead {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (has(k, e)) {
-                    if constexpr (SHARED)
-                        x[e] = to_f32(reinterpret_cast<const T *>(row_slot(stage, a))[(at & (16 / (int)sizeof(T) - 1)) + column(k, e)]);
+                    if constexpr (SHARED) x[e] = to_f32(reinterpret_cast<const T *>(row_slot(stage, a))[(at & 7) + column(k, e)]);
                     else x[e] = to_f32(slot(stage, a, k * E + e)->v);
                 }
             return {{pair(x[0], x[1])}};
@@ -346,13 +350,23 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
             next_rstd = a.rstd[first.row];
         }
     }
-    constexpr bool HOLD = C == kEach;
-    Chan<E> w[HOLD ? K : 1];
-    if constexpr (HOLD)
+    // The columns' weights stay in registers, and their scales too but for eight elements a load, for which there is no room.
+    constexpr bool HOLD = C == kEach, HOLD_SCALE = HOLD && R < 1024 && V < 8;
+    Chan<E> w[K], f[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (rows.has(k)) w[k] = rows.of(weight, k, 1.f);
-    auto weight_of = [&](int k) { return HOLD ? w[HOLD ? k : 0] : rows.of(weight, k, 1.f); };
+    for (int k = 0; k < K; ++k)
+        if (rows.has(k)) {
+            if constexpr (HOLD) w[k] = rows.of(weight, k, 1.f);
+            if constexpr (HOLD_SCALE) f[k] = rows.of(scale, k, 1.f);
+        }
+    auto weight_of = [&](int k) {
+        if constexpr (HOLD) return w[k];
+        else return rows.of(weight, k, 1.f);
+    };
+    auto scale_of = [&](int k) {
+        if constexpr (HOLD_SCALE) return f[k];
+        else return rows.of(scale, k, 1.f);
+    };
     over_rows(rows, in, group_rows, [&](bool live, uint32_t, int64_t next) {
         const float mean = next_mean, rstd = next_rstd;
         if (next >= 0) {
@@ -361,7 +375,7 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
         }
         auto sum_of = [&](int k) -> Chan<E> {  // u
             const Chan<E> x = rows.get(0, k);
-            return in.residual ? fma_n(rows.of(scale, k, 1.f), rows.get(3, k), x) : x;
+            return in.residual ? fma_n(scale_of(k), rows.get(3, k), x) : x;
         };
         // n = norm(s), g, and the sigmoid of the gate
         auto part_of = [&](int k, Chan<E> &n, Chan<E> &g, Chan<E> &sg) {
@@ -413,7 +427,7 @@ __global__ void __launch_bounds__(block_of<R>(), bwd_blocks(R)) gated_bwd_kernel
             sums[1][k] = add_n(sums[1][k], dy);
             if (in.residual) {
                 sums[2][k] = fma_n(rows.get(3, k), d, sums[2][k]);
-                if (a.dresidual) rows.put(a.dresidual, k, mul_n(d, rows.of(scale, k, 1.f)));
+                if (a.dresidual) rows.put(a.dresidual, k, mul_n(d, scale_of(k)));
             }
         }
     });
@@ -518,7 +532,7 @@ template <typename T, int V, typename A> cudaError_t by_width(const A &a, cudaSt
     case 256: return run<T, V, 256>(a, s);
     case 512: return run<T, V, 512>(a, s);
     default:
-        // (1024 threads have 64 registers each: a vector of eight at a time is more than they hold)
+        // (1024 threads have 64 registers each, and 512 with sixteen elements 128: eight at a time are more than they hold)
         return run<T, V == 8 ? 4 : V, 1024>(a, s);
     }
 }
@@ -528,8 +542,12 @@ template <typename A> cudaError_t by_type(const A &a, cudaStream_t s) {
     const int w = a.in.width;
     if (a.in.dtype == FW_F32)
         return w % 4 == 0 ? by_width<float, 4>(a, s) : w % 2 == 0 ? by_width<float, 2>(a, s) : by_width<float, 1>(a, s);
-    return w % 8 == 0 ? by_width<__nv_bfloat16, 8>(a, s)
-                      : w % 2 == 0 ? by_width<__nv_bfloat16, 2>(a, s) : by_width<__nv_bfloat16, 1>(a, s);
+    // (Backwards with a residual eight bytes, which leaves room for the scales in registers: 16384 x 2048 81 us for
+    // 95, 8192 x 4096 88 for 104; without one 81 for 66 of 262144 x 128, 101 for 89 of 8192 x 4096.)
+    if (w % 8 == 0)
+        return std::is_same_v<A, GatedBwdArgs> && a.in.residual ? by_width<__nv_bfloat16, 4>(a, s)
+                                                               : by_width<__nv_bfloat16, 8>(a, s);
+    return w % 2 == 0 ? by_width<__nv_bfloat16, 2>(a, s) : by_width<__nv_bfloat16, 1>(a, s);
 }
 
 }  // namespace
