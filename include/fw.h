@@ -436,10 +436,11 @@ int fw_layer_norm_backward(const void *dy, const void *x, const float *weight, c
  * which overlaps are refused.  log_decay is finite and <= 0 and dt >= 0; where a decay grows instead
  * (log_decay dt > 0) it is computed as it is, as long as its sums within 128 tokens stay below 80.
  * A decay below e^-104 is zero: the state starts afresh with the token.
- *   bf16 rows: the masked scores, with skip / scale on their diagonal, and the state as a row reads it, are
- *   rounded to bf16 once, like the rows that come out; the steps, the decays and S_T are fp32 throughout.
+ *   bf16 rows: the masked scores and the state as a row reads it are rounded to bf16 once, like the rows that come
+ *   out; the steps, the decays, skip v and S_T are fp32 throughout.
  *   Where the decays of a chunk of 128 tokens, or of 32 of them, multiply to e^-40 or more, its sums are formed up
- *   to e^40 times their size: scores or rows, and skip / scale, beyond about 1e20 may overflow.
+ *   to e^40 times their size: scores or rows beyond about 1e20 may overflow, and of a scale below 1e-20 the scan's share of
+ *   a row may come out as zero.
  *   An infinity or NaN in v reaches the rows that depend on it and nothing else, and may arrive as
  *   NaN; one in k, or in a step, may reach its chunk of 128 tokens and what follows.
  */

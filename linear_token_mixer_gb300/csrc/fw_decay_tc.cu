@@ -21,7 +21,7 @@ cudaError_t launch(const ScanArgs *scans, int nseg, bool follows, cudaStream_t s
     const int64_t ctas = N * a.n_chains;
     cudaError_t e;
     if (nseg > 1) {
-        auto k = scan_tc_kernel<D, REV, true, false, false>;
+        auto k = scan_tc_kernel<D, REV, true, false, false, false>;
         constexpr int smem = (int)Lay<D, true, false>::ALLOC;
         static std::atomic<uint64_t> pre_done{0};
         if ((e = allow_smem(k, smem, pre_done)) != cudaSuccess) return e;
@@ -30,9 +30,9 @@ cudaError_t launch(const ScanArgs *scans, int nseg, bool follows, cudaStream_t s
             return e;
     }
     constexpr int smem = (int)Lay<D, false, false>::ALLOC;
-    auto k = scan_tc_kernel<D, REV, false, false, false>;
+    auto k = scan_tc_kernel<D, REV, false, false, false, false>;
     if constexpr (!REV)                             // (an output norm has no backward pass)
-        if (a.norm.on) k = scan_tc_kernel<D, REV, false, true, false>;
+        if (a.norm.on) k = scan_tc_kernel<D, REV, false, true, false, false>;
     static std::atomic<uint64_t> done[2];
     if ((e = allow_smem(k, smem, done[a.norm.on ? 1 : 0])) != cudaSuccess) return e;
     // Padded batches of more chains than SMs: the CTAs of the longest rows start first, so that none

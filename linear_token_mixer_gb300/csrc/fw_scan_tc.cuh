@@ -43,9 +43,12 @@
 // forms those of its chunks before it begins, while the first tiles load.  (A launch of their own: 5 us a call.)  The
 // scores of a steep chunk take the product of the decays to and from the end of the block of 32 columns before
 // a row's own, each at most 1; those of the diagonal blocks the quotient of the decays from the block's start, or
-// where that is below e^-kMild the decay itself.  Whether a chunk is mild goes by its own tables.  Measured: B8 H16
-// T4096 d = 128, keys and queries for each head, 126 us (mild chunks 125, steep ones 129; without SEL 101 and 113), with
-// those of two groups 120 us: not its bytes (80 and 47 us at the measured copy rate) but the period of a chunk, 3.4 us.
+// where that is below e^-kMild the decay itself.  Whether a chunk is mild goes by its own tables.  skip v is added to a row in
+// the epilogue, in fp32, from the tile of C that P C has read (a tile leaves with the row's own rounding only; on the
+// scores' diagonal it would be rounded with them, and skip / scale times the factors there could overflow); calls without it
+// are a kernel of their own.  Measured: B8 H16 T4096 d = 128, keys and queries for each head, 127 us (mild chunks 123, steep
+// ones 128; 125, 121 and 125 without skip; without SEL 101 and 113), with those of one group 125 us; B16 d = 64 198 us, 187
+// without skip: not its bytes (80 and 43 us at the measured copy rate) but the period of a chunk, 3.4 us.
 // What that goes by is all roles' instructions rather than one chain: without the third term of the update it
 // takes 111 us, without P 103, without X 112, without a branch that no chunk takes 10 us less, and one warp of eight
 // stalls for instructions (tensor pipe 41 % busy, issue slots 49 %, DRAM 43 % at T2048).  B1 H32 T32768 402 us.
@@ -279,8 +282,7 @@ __device__ __forceinline__ float entry_state(const ScanArgs &a, const ScanArgs &
 }
 
 // SEL: the tables of a chunk, four tokens a lane; by a whole warp.  The weights' logs are summed from the chunk's end on,
-// so that those which count are short sums; what is summed from its start on goes into rows of bf16 only.  (With
-// a scale of zero no chunk is mild: the epilogue of a mild one scales A X with the rest.)
+// so that those which count are short sums; what is summed from its start on goes into rows of bf16 only.
 __device__ __forceinline__ void form_tables(const ScanArgs &a, int64_t chain, int64_t n, int64_t chunk) {
     constexpr int PER = C / 32;
     const GateArgs &g = a.sel.gate;
@@ -338,7 +340,7 @@ __device__ __forceinline__ void form_tables(const ScanArgs &a, int64_t chain, in
     if (lane == 0) {
         a.sel.chunk[id] = make_float4(expf(total), total, 0.f, 0.f);
         a.sel.ends[id] = make_float4(end[0], end[1], end[2],
-                                     a.out_scale != 0.f && low >= -kMild && high <= kMild && isfinite(total) ? 1.f : 0.f);
+                                     low >= -kMild && high <= kMild && isfinite(total) ? 1.f : 0.f);
     }
 }
 
@@ -463,12 +465,14 @@ __device__ __forceinline__ void redo_rows(const ScanArgs &a, const ScanArgs &own
     }
 }
 
-// PRE: only the state of a segment, from zero (segment 0: from X0), into the workspace.
-template <int D, bool REV, bool PRE, bool NORM, bool SEL>
+// PRE: only the state of a segment, from zero (segment 0: from X0), into the workspace.  SKIP (with SEL): rows have skip v
+// added, in fp32 behind the scan, before they are rounded.
+template <int D, bool REV, bool PRE, bool NORM, bool SEL, bool SKIP>
 __global__ void __launch_bounds__(NTHREADS, 1)
 scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, const int by_length, const int order) {
     using L = Lay<D, PRE, SEL>;
     static_assert(!SEL || !REV, "selective scans run forward");
+    static_assert(!SKIP || (SEL && !PRE && !NORM), "skip v is a selective scan's");
     const auto &job = jobs.s[REV ? blockIdx.x & 1 : 0];
     const int block = REV ? blockIdx.x >> 1 : blockIdx.x;
     const ScanArgs &a = jobs.s[0].args, &own = job.args;   // own: a, b, c, out, X_out, x0_trans and ws
@@ -553,8 +557,8 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             uint32_t c = 1;
             const int e = i - L::EMPTY;
             if (e >= 0 && e < L::NST * L::NT)       // B: its readers' warps (and G); C: the
-                c = e % L::NT == XB_ ? 4 * L::KG + (PRE ? 0 : 1)   // update (and P C); A: the O group's warps
-                  : e % L::NT == XC ? (PRE ? 1 : 2) : 4;
+                c = e % L::NT == XB_ ? 4 * L::KG + (PRE ? 0 : 1)   // update (and P C; SKIP: the O group's warps); A: those
+                  : e % L::NT == XC ? (PRE ? 1 : SKIP ? 6 : 2) : 4;
             if (i == L::PRDY || i == L::OSC || i == L::OFREE || (i >= L::KRDY && i < L::KFREE)) c = 4;
             if (i == L::VZ) c = 4 * L::KG;
             if (i >= L::XBRDY && i < L::KRDY) c = 8;   // XBRDY, UFREE
@@ -762,11 +766,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             const float2 *at = a.sel.c + tables * C + row;
             float4 ends = {};
             float2 own_row = {};
-            // What a row has of its own value beside the scores: skip v = scale (skip / scale) v goes onto the diagonal,
-            // where it is rounded with the score (2^-8 of it at most; as a term of its own in the epilogue, 11 us of 131
-            // for B8 H16 T4096 d = 128).  With a scale of zero the scores are.
-            const bool nil = SEL && a.out_scale == 0.f;
-            const float skip = SEL && a.sel.gate.skip ? a.sel.gate.skip[chain % a.H] / (nil ? 1.f : a.out_scale) : 0.f;
             if (SEL && nch > 0) {
                 ends = *info;
                 own_row = *at;
@@ -774,17 +773,15 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             bool ok = true;
             for (int i = 0; i < nch; ++i) {
                 bool one = mild, even = true;
-                // SEL: logs to this row, from the chunk's start and from its block's; skip over the epilogue's factor
-                float mine_c = 0.f, in_block = 0.f, own_skip = skip;
+                // SEL: logs to this row, from the chunk's start and from its block's
+                float mine_c = 0.f, in_block = 0.f;
                 if (SEL) {
                     one = ends.w != 0.f;
                     mine_c = own_row.x;
                     const float dt = own_row.y;
                     bar_sync(6, 128);                // the chunk before is done with (no wait between: it ends)
                     if (one) {
-                        const float up = __expf(-mine_c);
-                        sF[row] = dt * up;
-                        own_skip *= up;
+                        sF[row] = dt * __expf(-mine_c);
                     } else {
                         // to the ends of the blocks of 32 before later rows' own, and of the diagonal block, which is this
                         // warp's own, from its start while its decays are e^-kMild or more, else as they are
@@ -793,9 +790,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                         if (w < 3) sF[96 + row] = dt * __expf(ends.z - mine_c);
                         in_block = mine_c - before_block(ends, w);
                         even = __all_sync(~0u, fabsf(in_block) <= kMild);
-                        const float up = even ? __expf(-in_block) : 1.f;
-                        sD[row] = dt * up;
-                        own_skip *= up;
+                        sD[row] = even ? dt * __expf(-in_block) : dt;
                         sC[row] = mine_c;
                     }
                     if (i + 1 < nch) {
@@ -846,15 +841,13 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                         }
                         tmem_st_wait();
                     }
-                    const float here = nil ? 0.f : 1.f;
-                    if (nil) f = 0.f;
                     float v[16];
 #pragma unroll 1
                     for (int c = c0; c < c1; c += 16) {
                         tmem_fetch16(tmem + lb + COL_G + c, v);
                         const bool before = c < 32 * w;
                         const float4 *const F = reinterpret_cast<const float4 *>((one || before ? left : sD) + c);
-                        const float r = before ? f : here;
+                        const float r = before ? f : 1.f;
                         uint64_t t[8];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -865,10 +858,6 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                         tmem_landed(v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) scale2(v[2 * e], v[2 * e + 1], t[e]);
-                        if (!before) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] += c + e == row ? own_skip : 0.f;
-                        }
                         put(v, c);
                     }
                 } else if (mild) {
@@ -918,6 +907,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             const float2 *at = a.sel.c + tables * C + row;
             float4 ends = {};
             float row_c = 0.f;
+            const float skip = SKIP ? a.sel.gate.skip[chain % a.H] : 0.f;
             if (SEL && nch > 0) {
                 ends = *info;
                 row_c = at->x;
@@ -937,7 +927,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                             last = __expf(in_block);
                         }
                     }
-                    rd = a.out_scale == 0.f ? 0.f : __expf(rd);
+                    rd = __expf(rd);
                     if (i + 1 < nch) {
                         ends = *++info;
                         row_c = (at += C)->x;
@@ -960,9 +950,10 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     if (lane == 0) mbar_arrive(bar(L::OSC));
                     rd = last;
                 }
-                rd *= SEL && a.out_scale == 0.f ? 1.f : a.out_scale;
+                rd *= a.out_scale;
 
-                ok = __all_sync(~0u, wait_bar(bar(L::PVDONE), pi, limit, s_abort));
+                ok = __all_sync(~0u, wait_bar(bar(L::PVDONE), pi, limit, s_abort) &&
+                                         (!SKIP || wait_bar(full(i % L::NST, XC), (uint32_t)(i / L::NST) & 1u, limit, s_abort)));
                 if (!ok) break;
                 tc_fence_after();
                 float mean = 0.f, rstd = 1.f;
@@ -1001,6 +992,10 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(own.out) +
                                      (chain * a.T + row0 + row) * D;
                 const uint32_t to = tile(st, XA) + (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u;
+                // eight columns c + 8 e of the row's place in a tile (SKIP: v is there in C's)
+                auto piece = [&](int c, int e) -> uint32_t {
+                    return (uint32_t)(c >> 6) * HALF + (((((uint32_t)c & 63u) >> 3) + e ^ ((uint32_t)row & 7u)) << 4);
+                };
                 tmem_stream(tmem + lb + COL_O, 0, D, [&](float (&v)[16], int c) {
                     if (NORM) {
 #pragma unroll
@@ -1018,6 +1013,20 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                             v[e + 2] = hi.x;
                             v[e + 3] = hi.y;
                         }
+                    } else if (SKIP) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8) {
+                            const uint4 q = ld_shared_v4(to + (tile(st, XC) - tile(st, XA)) + piece(c, e / 8));
+                            const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const uint64_t own_v = mul2(pair(__uint_as_float(x[z] << 16), __uint_as_float(x[z] & 0xffff0000u)),
+                                                            pair(skip, skip));
+                                const float2 f = halves(fma2(pair(v[e + 2 * z], v[e + 2 * z + 1]), pair(rd, rd), own_v));
+                                v[e + 2 * z] = f.x;
+                                v[e + 2 * z + 1] = f.y;
+                            }
+                        }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) scale2(v[e], v[e + 1], pair(rd, rd));
@@ -1028,9 +1037,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     if (whole) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            st_shared_v4(to + (uint32_t)(c >> 6) * HALF +
-                                             (((((uint32_t)c & 63u) >> 3) + e ^ ((uint32_t)row & 7u)) << 4),
-                                         pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+                            st_shared_v4(to + piece(c, e), pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                     } else if (row < nv) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
@@ -1043,6 +1050,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar(L::OFREE));
+                    if (SKIP) mbar_arrive(empty(st, XC));
                     if (whole) {
                         const uint32_t src = tile(st, XA) + (uint32_t)w * 4096u;
                         tma_store_3d(&tmo, src, 0, (int)row0 + w * 32, (int)chain);

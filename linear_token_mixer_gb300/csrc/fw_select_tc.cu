@@ -16,7 +16,7 @@ template <int D> cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     cudaError_t e;
     if (nseg > 1) {
-        auto k = scan_tc_kernel<D, false, true, false, true>;
+        auto k = scan_tc_kernel<D, false, true, false, true, false>;
         constexpr int smem = (int)Lay<D, true, true>::ALLOC;
         static std::atomic<uint64_t> pre_done{0};
         if ((e = allow_smem(k, smem, pre_done)) != cudaSuccess) return e;
@@ -25,9 +25,10 @@ template <int D> cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
             return e;
     }
     constexpr int smem = (int)Lay<D, false, true>::ALLOC;
-    auto k = scan_tc_kernel<D, false, false, false, true>;
-    static std::atomic<uint64_t> done{0};
-    if ((e = allow_smem(k, smem, done)) != cudaSuccess) return e;
+    const bool skip = a.sel.gate.skip != nullptr;
+    auto k = skip ? scan_tc_kernel<D, false, false, false, true, true> : scan_tc_kernel<D, false, false, false, true, false>;
+    static std::atomic<uint64_t> done[2];
+    if ((e = allow_smem(k, smem, done[skip ? 1 : 0])) != cudaSuccess) return e;
     const int by_length = a.lens && a.n_chains > kSMs && a.n_chains / a.H <= kMaxRanked;
     return launch_after(k, dim3((unsigned)(a.n_chains * nseg)), NTHREADS, smem, s, nseg > 1, jobs, nseg, by_length,
                         nseg > 1 ? kWaitFirst : 0);
