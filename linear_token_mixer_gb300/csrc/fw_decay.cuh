@@ -89,9 +89,10 @@ struct SelectTables {
     int64_t n_chunks;
     float4 *chunk;            // [n_chains][n_chunks] decay of the chunk, its log in two terms
     // bf16 scans:
-    float4 *ends;             // .. log decays from the chunk's start to the ends of its first three blocks of 32
-                              // tokens, and 1 where the chunk is mild (its sums of logs stay within +-kMild)
-    float2 *c;                // [n_chains][n_chunks * C] log decay from the chunk's start to the token, and its step
+    float4 *ends;             // .. log decays of its first three blocks of 32 tokens, and 1 where the chunk is
+                              // mild (its sums of logs stay within +-kMild)
+    float2 *c;                // [n_chains][n_chunks * C] log decay to the token from the chunk's start, or from its
+                              // block's where the chunk is not mild, and its step
     float *w;                 // .. step times the decay from the token to the chunk's end, at weight_place
 };
 // Place of a token's weight within its chunk: the eight that a thread of the bf16 scans needs of 32 tokens, 2 t, + 1

@@ -44,11 +44,11 @@
 // scores of a steep chunk take the product of the decays to and from the end of the block of 32 columns before
 // a row's own, each at most 1; those of the diagonal blocks the quotient of the decays from the block's start, or
 // where that is below e^-kMild the decay itself.  Whether a chunk is mild goes by its own tables.  skip v is added to a row in
-// the epilogue, in fp32, from the tile of C that P C has read (a tile leaves with the row's own rounding only; on the
-// scores' diagonal it would be rounded with them, and skip / scale times the factors there could overflow); calls without it
-// are a kernel of their own.  Measured: B8 H16 T4096 d = 128, keys and queries for each head, 127 us (mild chunks 123, steep
-// ones 128; 125, 121 and 125 without skip; without SEL 101 and 113), with those of one group 125 us; B16 d = 64 198 us, 187
-// without skip: not its bytes (80 and 43 us at the measured copy rate) but the period of a chunk, 3.4 us.
+// the epilogue, in fp32, from the tile of C that P C has read, so that it is rounded with the row and never before (on the
+// scores' diagonal it was, and skip / scale times the factors there could overflow); calls without it are a kernel of
+// their own.  Measured: B8 H16 T4096 d = 128, keys and queries for each head, 128 us (mild chunks 124, steep ones 129;
+// 124, 120 and 124 without skip; without SEL 101 and 113), with those of one group 128 us; B16 d = 64 198 us, 190 without
+// skip: not its bytes (80 and 43 us at the measured copy rate) but the period of a chunk, 3.4 us.
 // What that goes by is all roles' instructions rather than one chain: without the third term of the update it
 // takes 111 us, without P 103, without X 112, without a branch that no chunk takes 10 us less, and one warp of eight
 // stalls for instructions (tensor pipe 41 % busy, issue slots 49 %, DRAM 43 % at T2048).  B1 H32 T32768 402 us.
@@ -97,7 +97,7 @@ template <int D, bool PRE, bool SEL> struct Lay {
     static constexpr uint32_t TAB = XB + (uint32_t)D * D * 2;
     static constexpr uint32_t T_PW = TAB, T_KW = T_PW + 132 * 4, T_KT = T_KW + 128 * 4;
     // SEL, of the P group: a steep chunk's decays to the ends of blocks (a mild one's from the
-    // chunk's start), sums of logs, steps
+    // chunk's start), logs, steps
     static constexpr uint32_t T_SF = TAB, T_SC = T_SF + 192 * 4, T_SD = T_SC + 128 * 4;
     static constexpr uint32_t BAR = !SEL ? T_KT + 128 * 4 : PRE ? TAB : T_SD + 128 * 4;
     // barriers
@@ -281,12 +281,15 @@ __device__ __forceinline__ float entry_state(const ScanArgs &a, const ScanArgs &
     return x;
 }
 
-// SEL: the tables of a chunk, four tokens a lane; by a whole warp.  The weights' logs are summed from the chunk's end on,
-// so that those which count are short sums; what is summed from its start on goes into rows of bf16 only.
+// SEL: the tables of a chunk, four tokens a lane; by a whole warp.  Logs are summed within blocks of 32 tokens and over
+// the blocks, for the weights from the chunk's end: what counts are short sums, which lose nothing to tokens far off that keep
+// nothing (logs of 104 each, 1e4 in a chunk).  Of a chunk that is not mild the sums of a block go on in two terms and are
+// rounded once, so that a difference of two is off by a unit of the larger: 1.5e-5 for logs of 200 in a block, 2.4e-4 at
+// most (32 tokens that keep nothing).
 __device__ __forceinline__ void form_tables(const ScanArgs &a, int64_t chain, int64_t n, int64_t chunk) {
-    constexpr int PER = C / 32;
+    constexpr int PER = C / 32, LANES = 32 / PER;   // of a block
     const GateArgs &g = a.sel.gate;
-    const int lane = threadIdx.x & 31, h = (int)(chain % a.H);
+    const int lane = threadIdx.x & 31, h = (int)(chain % a.H), place = lane % LANES, block = lane / LANES;
     const int64_t first = chunk * C + lane * PER, id = chain * a.sel.n_chunks + chunk;
     const float rate = g.log_decay[h];
     float dt[PER], x[PER], sum = 0.f;
@@ -298,55 +301,73 @@ __device__ __forceinline__ void form_tables(const ScanArgs &a, int64_t chain, in
         if (x[e] < -kReset) x[e] = -kReset;   // (NaN stays)
         sum += x[e];
     }
-    float upto = sum, from = sum;             // of this lane's tokens and those before, and behind
+    float upto = sum, from = sum;             // of this lane's tokens and those before, and behind, in the block
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const float p = __shfl_up_sync(~0u, upto, o), q = __shfl_down_sync(~0u, from, o);
-        if (lane >= o) upto += p;
-        if (lane < 32 - o) from += q;
+    for (int o = 1; o < LANES; o <<= 1) {
+        const float p = __shfl_up_sync(~0u, upto, o, LANES), q = __shfl_down_sync(~0u, from, o, LANES);
+        if (place >= o) upto += p;
+        if (place < LANES - o) from += q;
     }
-    const float total = __shfl_sync(~0u, from, 0);
-    float before = __shfl_up_sync(~0u, upto, 1), behind = __shfl_down_sync(~0u, from, 1);
-    if (lane == 0) before = 0.f;
-    if (lane == 31) behind = 0.f;
+    float all[4];                             // of the blocks
+#pragma unroll
+    for (int b = 0; b < 4; ++b) all[b] = __shfl_sync(~0u, from, LANES * b);
+    const float total = all[0] + all[1] + all[2] + all[3];
+    float start = 0.f, rest = 0.f;            // of the blocks before, and behind
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+        if (block > b) start += all[b];
+        if (block < 3 - b) rest += all[3 - b];
+    }
+    float before = __shfl_up_sync(~0u, upto, 1, LANES), behind = __shfl_down_sync(~0u, from, 1, LANES);
+    if (place == 0) before = 0.f;
+    if (place == LANES - 1) behind = 0.f;
     float w[PER];
 #pragma unroll
     for (int e = PER - 1; e >= 0; --e) {
-        w[e] = dt[e] * expf(behind);
+        w[e] = dt[e] * expf(behind + rest);
         behind += x[e];
     }
-    float low = 0.f, high = 0.f;              // the least and the largest sum
+    float low = 0.f, high = 0.f, sums[PER];   // from the chunk's start: the least and the largest, and each token's
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
         before += x[e];
-        low = fminf(low, before);
-        high = fmaxf(high, before);
-        x[e] = before;
+        sums[e] = start + before;
+        low = fminf(low, sums[e]);
+        high = fmaxf(high, sums[e]);
     }
-    float4 *const c = reinterpret_cast<float4 *>(a.sel.c + id * C + lane * PER);
-    c[0] = make_float4(x[0], dt[0], x[1], dt[1]);
-    c[1] = make_float4(x[2], dt[2], x[3], dt[3]);
-#pragma unroll
-    for (int e = 0; e < PER; e += 2)
-        *reinterpret_cast<float2 *>(a.sel.w + id * C + weight_place(lane * PER + e)) = make_float2(w[e], w[e + 1]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         low = fminf(low, __shfl_xor_sync(~0u, low, o));
         high = fmaxf(high, __shfl_xor_sync(~0u, high, o));
     }
-    float end[3];
+    const bool one = low >= -kMild && high <= kMild && isfinite(total);
+    if (!one) {                               // (the whole warp)
+        Two s[PER], all_before{0.f, 0.f};
 #pragma unroll
-    for (int b = 0; b < 3; ++b) end[b] = __shfl_sync(~0u, x[PER - 1], 32 / PER * (b + 1) - 1);
+        for (int e = 0; e < PER; ++e) s[e] = add(e ? s[e - 1] : all_before, Two{x[e], 0.f});
+        Two t = s[PER - 1];
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) {
+            const Two p{__shfl_up_sync(~0u, t.hi, o, LANES), __shfl_up_sync(~0u, t.lo, o, LANES)};
+            if (place >= o) t = add(p, t);
+        }
+        const Two p{__shfl_up_sync(~0u, t.hi, 1, LANES), __shfl_up_sync(~0u, t.lo, 1, LANES)};
+        if (place > 0) all_before = p;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) sums[e] = add(all_before, s[e]).hi;
+#pragma unroll
+        for (int b = 0; b < 3; ++b) all[b] = __shfl_sync(~0u, sums[PER - 1], LANES * b + LANES - 1);
+    }
+    float4 *const c = reinterpret_cast<float4 *>(a.sel.c + id * C + lane * PER);
+    c[0] = make_float4(sums[0], dt[0], sums[1], dt[1]);
+    c[1] = make_float4(sums[2], dt[2], sums[3], dt[3]);
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+        *reinterpret_cast<float2 *>(a.sel.w + id * C + weight_place(lane * PER + e)) = make_float2(w[e], w[e + 1]);
     if (lane == 0) {
         a.sel.chunk[id] = make_float4(expf(total), total, 0.f, 0.f);
-        a.sel.ends[id] = make_float4(end[0], end[1], end[2],
-                                     low >= -kMild && high <= kMild && isfinite(total) ? 1.f : 0.f);
+        a.sel.ends[id] = make_float4(all[0], all[1], all[2], one ? 1.f : 0.f);
     }
-}
-
-// SEL: the log decay to the token before block w of a chunk's four.
-__device__ __forceinline__ float before_block(const float4 &ends, int w) {
-    return w == 0 ? 0.f : w == 1 ? ends.x : w == 2 ? ends.y : ends.z;
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t bf16x2) {
@@ -423,9 +444,9 @@ __device__ __forceinline__ void redo_rows(const ScanArgs &a, const ScanArgs &own
             float c = a.in_scale * value;
             if (SEL) {
                 const int64_t at = (chain * a.sel.n_chunks + i) * C + j;
-                const float2 z = a.sel.c[at];
-                g = expf(z.x - (j ? a.sel.c[at - 1].x : 0.f));
-                c = z.y * value;
+                const float dt = a.sel.c[at].y;
+                g = expf(a.sel.gate.log_decay[chain % a.H] * dt);
+                c = dt * value;
             }
             bar_sync(3, N);
             float o = 0.f;
@@ -760,7 +781,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                         h4 = decay_pow(sg, 4.f), h16 = decay_pow(sg, 16.f);
             float *const sF = reinterpret_cast<float *>(sm + L::T_SF), *const sC = reinterpret_cast<float *>(sm + L::T_SC),
                   *const sD = reinterpret_cast<float *>(sm + L::T_SD);
-            // SEL: of the chunk at hand, fetched a chunk ahead: ends of blocks and whether it is mild, the row's
+            // SEL: of the chunk at hand, fetched a chunk ahead: logs of blocks and whether it is mild, the row's
             // log and step
             const float4 *info = a.sel.ends + tables;
             const float2 *at = a.sel.c + tables * C + row;
@@ -773,25 +794,30 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             bool ok = true;
             for (int i = 0; i < nch; ++i) {
                 bool one = mild, even = true;
-                // SEL: logs to this row, from the chunk's start and from its block's
-                float mine_c = 0.f, in_block = 0.f;
+                float in_block = 0.f;                // SEL: log to this row, from its block's start
                 if (SEL) {
                     one = ends.w != 0.f;
-                    mine_c = own_row.x;
                     const float dt = own_row.y;
                     bar_sync(6, 128);                // the chunk before is done with (no wait between: it ends)
                     if (one) {
-                        sF[row] = dt * __expf(-mine_c);
+                        sF[row] = dt * __expf(-own_row.x);
                     } else {
                         // to the ends of the blocks of 32 before later rows' own, and of the diagonal block, which is this
                         // warp's own, from its start while its decays are e^-kMild or more, else as they are
-                        if (w < 1) sF[row] = dt * __expf(ends.x - mine_c);
-                        if (w < 2) sF[32 + row] = dt * __expf(ends.y - mine_c);
-                        if (w < 3) sF[96 + row] = dt * __expf(ends.z - mine_c);
-                        in_block = mine_c - before_block(ends, w);
+                        in_block = own_row.x;
                         even = __all_sync(~0u, fabsf(in_block) <= kMild);
+                        float z = (w == 0 ? ends.x : w == 1 ? ends.y : ends.z) - in_block;   // to the block's end
+                        if (w < 1) {
+                            sF[row] = dt * __expf(z);
+                            z += ends.y;
+                        }
+                        if (w < 2) {
+                            sF[32 + row] = dt * __expf(z);
+                            z += ends.z;
+                        }
+                        if (w < 3) sF[96 + row] = dt * __expf(z);
                         sD[row] = even ? dt * __expf(-in_block) : dt;
-                        sC[row] = mine_c;
+                        sC[row] = in_block;
                     }
                     if (i + 1 < nch) {
                         ends = *++info;
@@ -833,10 +859,10 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                             float v[4];
                             tmem_ld4(tmem + lb + COL_G + c, v);
                             const float4 z = *reinterpret_cast<const float4 *>(sC + c);
-                            v[0] *= __expf(mine_c - z.x);
-                            v[1] *= __expf(mine_c - z.y);
-                            v[2] *= __expf(mine_c - z.z);
-                            v[3] *= __expf(mine_c - z.w);
+                            v[0] *= __expf(in_block - z.x);
+                            v[1] *= __expf(in_block - z.y);
+                            v[2] *= __expf(in_block - z.z);
+                            v[3] *= __expf(in_block - z.w);
                             tmem_st4(tmem + lb + COL_G + c, v);
                         }
                         tmem_st_wait();
@@ -921,10 +947,14 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
                     one = ends.w != 0.f;
                     rd = row_c;
                     if (!one) {                      // from the block's start on, where that is the P group's too
-                        const float before = before_block(ends, w), in_block = row_c - before;
-                        if (__all_sync(~0u, fabsf(in_block) <= kMild)) {
+                        float before = 0.f;
+                        if (w > 0) before += ends.x;
+                        if (w > 1) before += ends.y;
+                        if (w > 2) before += ends.z;
+                        rd = before + row_c;
+                        if (__all_sync(~0u, fabsf(row_c) <= kMild)) {
                             rd = before;
-                            last = __expf(in_block);
+                            last = __expf(row_c);
                         }
                     }
                     rd = __expf(rd);

@@ -66,3 +66,27 @@ def test_skip_beside_a_scale_of_any_size(scale, rate, d, dtype):
     assert torch.isfinite(o).all()
     assert ((o.double() - want).abs() <= (half + 2.0 ** -23) * want.abs() + inner * part + 2.0 ** -126).all()
     assert R.rel_rows(S, rS, 2) <= 1e-5
+
+
+@pytest.mark.parametrize("first,written,tol", [(96, False, 3.3e-4), (96, True, 1.1e-3), (112, False, 4.6e-4)])
+def test_decays_behind_tokens_that_keep_nothing(first, written, tol):
+    """The first 96 or 112 tokens of a chunk keep nothing (their logs are 104 or more each); those behind them keep almost all of
+    it, and their decays are as exact as in a chunk of their own, or, where 16 of their block of 32 keep nothing, off by a unit of
+    a sum of 1664, 1.3e-4.  The factor by which all chains' rows of a token are off is the
+    decays' common error and the mean of roundings of random sign: those of P (2^-8 at most, 1.6e-3 in the mean square of a value)
+    and of the rows (64 x 64 of them, 2.5e-5).  Where the first tokens write nothing, a row is a sum of eight terms or more in 64
+    chains, sum_j P_ij v_j: 1.6e-3 / sqrt(8 x 64) = 7e-5, with sums that vary from chain to chain 1.1e-4, and three times that
+    3.3e-4.  Where they write, with steps of 400 beside 0.0003, a row is one term, the last such token's, in 64 chains, 2.1e-4,
+    and the largest of 24 rows five times that."""
+    B, H, T, d = 8, 8, 128, 64
+    x, _ = inputs(B, H, H, T, d, BF16, (1.0, 1.0), seed=9)
+    x["q"], x["k"] = x["q"].float().abs().bfloat16(), x["k"].float().abs().bfloat16()
+    x["dt"][:] = 0.0003
+    x["dt"][:, :, :first] = 400.0
+    if not written:
+        x["k"][:, :, :first] = 0.0
+    x["skip"].zero_()
+    o, _ = run({n: t.cuda() for n, t in x.items()}, scale=100.0)
+    want, _ = R.select(x["q"], x["k"], x["v"], x["dt"], x["ld"], x["S0"], scale=100.0)
+    o, want = (t.double()[:, :, first + 8:] for t in (o, want))
+    assert ((o * want).sum((0, 1, 3)) / (want * want).sum((0, 1, 3)) - 1).abs().max().item() <= tol
