@@ -439,7 +439,7 @@ int fw_layer_norm_backward(const void *dy, const void *x, const float *weight, c
  *   bf16 rows: the masked scores and the state as a row reads it are rounded to bf16 once, like the rows that come
  *   out; the steps, the decays, skip v and S_T are fp32 throughout.  Within a chunk of 128 tokens the scores' decays
  *   are exponentials of differences of logs that are summed over 32 tokens: off by 2.4e-4 of themselves where most of
- *   32 tokens keep nothing, by 1e-5 or less where their logs sum to -100 or more.
+ *   32 tokens keep nothing, by 3e-5 or less where their logs sum to -100 or more.
  *   Where the decays of a chunk of 128 tokens, or of 32 of them, multiply to e^-40 or more, its sums are formed up
  *   to e^40 times their size: scores or rows beyond about 1e20 may overflow, and of a scale below 1e-20 the scan's share of
  *   a row may come out as zero.
@@ -489,8 +489,8 @@ int fw_select_step(const void *q, const void *k, const void *v, const fw_gates *
  *
  * Of every channel before a mixer, `width` taps (2 .. FW_CONV_MAX):
  *     a_t = bias + sum_w weight[w] x_{t-width+1+w},   y_t = a_t, with FW_FLAG_SILU a_t / (1 + exp(-a_t)),
- * over rows of shape->d_k = d_v = d channels, any d >= 1 (B H T d below 2^34).  Rows before the first come from `state`, so that
- * calls continue one another.  lens and FW_FLAG_ZERO_REST as in the decayed calls: rows from lens[b]
+ * over rows of shape->d_k = d_v = d channels, 1 <= d <= 2^24 (H <= 65535, B H d ceil(T / 8) < 2^31; the gradients also
+ * H ceil(d / 32) <= 65535).  Rows before the first come from `state`, so that calls continue one another.  lens and FW_FLAG_ZERO_REST as in the decayed calls: rows from lens[b]
  * on are never used, and the state behind a row of the batch is that behind its last token.
  *   x, y, dy, dx   [B][H][T][d] of `dtype`
  *   weight, bias   float [H][d][width], the last tap on the row itself; float [H][d] or NULL (zeros)
@@ -503,7 +503,7 @@ int fw_conv_prefill(const void *x, const float *weight, const float *bias, const
                     const int32_t *lens, void *y, void *state_out, const fw_shape *shape, int width,
                     fw_dtype dtype, unsigned flags, cudaStream_t stream);
 
-/* Bytes of workspace of fw_conv_backward, or a negative FW_ERR_* code. */
+/* Bytes of workspace of fw_conv_backward, or a negative FW_ERR_* code (of shapes that it refuses, too). */
 int64_t fw_conv_workspace(const fw_shape *shape, int width);
 
 /*

@@ -736,6 +736,7 @@ extern "C" int fw_conv_prefill(const void *x, const float *weight, const float *
 extern "C" int64_t fw_conv_workspace(const fw_shape *shape, int width) {
     const int st = check_conv(shape, width, FW_F32);
     if (st != FW_OK) return st;
+    if (!conv_backward_fits(shape->H, shape->d_k)) return FW_ERR_SHAPE;
     return (int64_t)conv_workspace(shape->B, (int)shape->H, shape->T, shape->d_k, width);
 }
 
@@ -747,6 +748,7 @@ extern "C" int fw_conv_backward(const void *dy, const void *x, const float *weig
                                 cudaStream_t stream) {
     int st = check_conv(shape, width, dtype);
     if (st != FW_OK) return st;
+    if (!conv_backward_fits(shape->H, shape->d_k)) return FW_ERR_SHAPE;
     if (flags & ~(unsigned)(FW_FLAG_SILU | FW_FLAG_ZERO_REST)) return FW_ERR_MODE;
     if (!dy || !x || !weight || !dx) return FW_ERR_NULL;
     if (any_misaligned({dy, x, weight, bias, state, lens, dstate_out, dx, dweight, dbias, dstate, workspace}))

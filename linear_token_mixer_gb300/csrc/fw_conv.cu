@@ -430,11 +430,11 @@ template <typename A> cudaError_t by_type(const A &a, cudaStream_t s) {
 }  // namespace
 
 bool conv_fits(int64_t B, int64_t H, int64_t T, int64_t d) {
-    // threads of a call at the shortest strips and one channel each, and the backward grid's second axis
+    // threads of a call at the shortest strips and one channel each
     const int64_t strips = (T + kStripMin - 1) / kStripMin;
-    return T <= INT32_MAX - 4096 && d <= (1 << 24) && H * ((d + 31) / 32) <= 65535 && B * H <= INT32_MAX / d &&
-           B * H * d <= INT32_MAX / strips;
+    return T <= INT32_MAX - 4096 && d <= (1 << 24) && B * H <= INT32_MAX / d && B * H * d <= INT32_MAX / strips;
 }
+bool conv_backward_fits(int64_t H, int64_t d) { return H * ((d + 31) / 32) <= 65535; }   // (the grid's second axis)
 
 size_t conv_workspace(int64_t B, int H, int64_t T, int d, int W) {
     // (of either type)

@@ -46,8 +46,9 @@ struct ConvStepArgs {
     int silu;
 };
 
-// Whether the kernels' 32-bit counts hold B H T rows of d channels.
+// Whether the kernels' 32-bit counts hold B H T rows of d channels, and the backward pass's grid a head's groups of them.
 bool conv_fits(int64_t B, int64_t H, int64_t T, int64_t d);
+bool conv_backward_fits(int64_t H, int64_t d);
 size_t conv_workspace(int64_t B, int H, int64_t T, int d, int W);
 cudaError_t launch_conv(const ConvArgs &a, cudaStream_t s);
 cudaError_t launch_conv_backward(const ConvBwdArgs &a, cudaStream_t s);

@@ -579,7 +579,7 @@ def select_step(q, k, v, dt, log_decay, S, *, dt_bias=None, softplus=False, skip
 
 def conv_prefill(x, weight, bias=None, state=None, *, silu=True, lens=None, y=None, state_out=None,
                  stream=None):
-    """Short causal convolution of every channel of x [B, H, T, d] (fp32 or bf16, any d):
+    """Short causal convolution of every channel of x [B, H, T, d] (fp32 or bf16, d up to 2^24):
     y_t = act(bias + sum_w weight[w] x_{t-W+1+w}), act silu or none.
 
     weight [H, d, W] fp32, W = 2 .. 8, the last tap on the row itself; bias [H, d] fp32 or None;
@@ -608,7 +608,7 @@ def conv_backward(dy, x, weight, bias=None, state=None, dstate_out=None, *, silu
                   dweight=None, dbias=None, dstate=None, workspace=None, stream=None):
     """Gradients of conv_prefill given dy (x's shape and dtype) and dstate_out, that of the returned
     state, or None.  Returns (dx, dweight, dbias, dstate): dweight, dbias fp32; dstate in x's dtype, None
-    unless state or dstate is given.  Rows of dx behind lens as in decay_backward."""
+    unless state or dstate is given.  Rows of dx behind lens as in decay_backward.  H ceil(d / 32) up to 65535."""
     shape = B, H, T, d = _axes(x, 4)
     W, kind, f32 = _taps(weight), x.dtype, torch.float32
     past = (B, H, W - 1, d)
