@@ -82,13 +82,17 @@ struct GateArgs {
     int G;                    // groups of heads that share a and b: [B][G][T][d]
 };
 
+constexpr int kDecayStride = 4;
 // What its scans keep of them in the workspace, for chunks of C tokens, n_chunks a chain; tokens behind a
 // sequence's end are without a step.
 struct SelectTables {
     GateArgs gate;
     int64_t n_chunks;
-    float4 *chunk;            // [n_chains][n_chunks] decay of the chunk, its log in two terms
+    // fp32 scans: [n_chains][n_chunks] decay of the chunk, kDecayStride apart, since a block writes one (side by side in a
+    // sector, B4 H8 T2048 d = 128 188 us for 184)
+    float *decay;
     // bf16 scans:
+    float2 *chunk;            // [n_chains][n_chunks] decay of the chunk, and its log
     float4 *ends;             // .. log decays of its first three blocks of 32 tokens, and 1 where the chunk is
                               // mild (its sums of logs stay within +-kMild)
     float2 *c;                // [n_chains][n_chunks * C] log decay to the token from the chunk's start, or from its

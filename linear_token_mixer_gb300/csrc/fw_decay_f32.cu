@@ -167,9 +167,9 @@ __device__ __forceinline__ void local_part(const ScanArgs &s, const ChunkOf &k, 
 #pragma unroll
         for (int e = 0; e < logs.PER; ++e) w[threadIdx.x * logs.PER + e] = logs.weight(e);
         if (threadIdx.x == 0) {
-            const float4 r = logs.record();
-            *chunk_g = r.x;
-            if (!ONE) s.sel.chunk[k.chain * s.sel.n_chunks + k.chunk] = r;
+            const float r = logs.decay();
+            *chunk_g = r;
+            if (!ONE) s.sel.decay[(k.chain * s.sel.n_chunks + k.chunk) * kDecayStride] = r;
         }
     }
     if (!SEL && threadIdx.x < C) {
@@ -256,7 +256,7 @@ scan_prefix(const __grid_constant__ Scans all, int64_t nch) {
         for (int u = 0; u < U; ++u) {
             if (i0 + u >= used) break;
             M[u * step] = x;
-            const float g = SEL ? s.sel.chunk[chain * nch + i0 + u].x
+            const float g = SEL ? s.sel.decay[(chain * nch + i0 + u) * kDecayStride]
                                 : (s.rev ? i0 + u == 0 : i0 + u == used - 1) ? gT : gC;
             x.x = fmaf(g, x.x, m[u].x);
             x.y = fmaf(g, x.y, m[u].y);
@@ -563,15 +563,17 @@ cudaError_t launch_scans(ScanArgs *s, int n, cudaStream_t stream) {
 }
 
 // A selective scan: [states][the chunks' decays], neither where a chain is one chunk.
-static size_t record_bytes(int64_t n_chains, int64_t T) { return (size_t)n_chains * (size_t)((T + C - 1) / C) * sizeof(float4); }
+static size_t decay_bytes(int64_t n_chains, int64_t T) {
+    return (size_t)n_chains * (size_t)((T + C - 1) / C) * kDecayStride * sizeof(float);
+}
 size_t select_workspace_f32(int64_t n_chains, int64_t T, int d) {
-    return T <= C ? 0 : state_bytes(n_chains, T, d) + record_bytes(n_chains, T);
+    return T <= C ? 0 : state_bytes(n_chains, T, d) + decay_bytes(n_chains, T);
 }
 cudaError_t launch_select_f32(const ScanArgs &scan, cudaStream_t stream) {
     Scans all{};
     ScanArgs &s = all.s[0] = scan;
     s.sel.n_chunks = (s.T + C - 1) / C;
-    if (s.T > C) s.sel.chunk = reinterpret_cast<float4 *>(reinterpret_cast<char *>(s.ws) + state_bytes(s.n_chains, s.T, s.d));
+    if (s.T > C) s.sel.decay = s.ws + state_bytes(s.n_chains, s.T, s.d) / sizeof(float);
     return s.d == 64 ? launch<64, true>(all, 1, stream) : launch<128, true>(all, 1, stream);
 }
 

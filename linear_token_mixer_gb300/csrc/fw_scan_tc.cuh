@@ -46,8 +46,8 @@
 // where that is below e^-kMild the decay itself.  Whether a chunk is mild goes by its own tables.  skip v is added to a row in
 // the epilogue, in fp32, from the tile of C that P C has read, so that it is rounded with the row and never before (on the
 // scores' diagonal it was, and skip / scale times the factors there could overflow); calls without it are a kernel of
-// their own.  Measured: B8 H16 T4096 d = 128, keys and queries for each head, 128 us (mild chunks 124, steep ones 129;
-// 124, 120 and 124 without skip; without SEL 101 and 113), with those of one group 128 us; B16 d = 64 198 us, 190 without
+// their own.  Measured: B8 H16 T4096 d = 128, keys and queries for each head, 128 us (mild chunks 125, steep ones 131;
+// 125, 121 and 125 without skip; without SEL 101 and 113), with those of one group 128 us; B16 d = 64 193 us, 187 without
 // skip: not its bytes (80 and 43 us at the measured copy rate) but the period of a chunk, 3.4 us.
 // What that goes by is all roles' instructions rather than one chain: without the third term of the update it
 // takes 111 us, without P 103, without X 112, without a branch that no chunk takes 10 us less, and one warp of eight
@@ -250,8 +250,7 @@ template <int N> struct Jobs {
 __device__ __forceinline__ float chunks_decay(const SelectTables &t, int64_t chain, int first, int last) {
     double x = 0.0;
     for (int c = first + (int)(threadIdx.x & 31); c < last; c += 32) {
-        const float4 q = t.chunk[chain * t.n_chunks + c];
-        x += (double)q.y + q.z;
+        x += t.chunk[chain * t.n_chunks + c].y;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
@@ -365,7 +364,7 @@ __device__ __forceinline__ void form_tables(const ScanArgs &a, int64_t chain, in
     for (int e = 0; e < PER; e += 2)
         *reinterpret_cast<float2 *>(a.sel.w + id * C + weight_place(lane * PER + e)) = make_float2(w[e], w[e + 1]);
     if (lane == 0) {
-        a.sel.chunk[id] = make_float4(expf(total), total, 0.f, 0.f);
+        a.sel.chunk[id] = make_float2(expf(total), total);
         a.sel.ends[id] = make_float4(all[0], all[1], all[2], one ? 1.f : 0.f);
     }
 }
@@ -1281,7 +1280,7 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::XBRDY));
         }
-        const float4 *info = a.sel.chunk + tables;
+        const float2 *info = a.sel.chunk + tables;
         float next_g = SEL && nch > 0 ? info->x : 0.f;   // (fetched a chunk ahead)
         for (int i = 0; i < nch; ++i) {
             const float g = SEL ? next_g : pw[tokens(i)];

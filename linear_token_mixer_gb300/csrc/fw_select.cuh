@@ -65,9 +65,7 @@ template <int C> struct ChunkLogs {
         const Two s = add(total, Two{-c[e].hi, -c[e].lo});
         return dt[e] * exp_two(s.hi, s.lo);
     }
-    __device__ __forceinline__ float4 record() const {
-        return make_float4(exp_two(total.hi, total.lo), total.hi, total.lo, 0.f);
-    }
+    __device__ __forceinline__ float decay() const { return exp_two(total.hi, total.lo); }
 };
 template <int C>
 __device__ __forceinline__ ChunkLogs<C> chunk_logs(const GateArgs &g, int64_t chain, int H, int64_t T, int64_t n, int64_t chunk) {

@@ -36,10 +36,12 @@ template <int D> cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-// [c][w][chunk][ends][states of segments]: each a multiple of 16 bytes.
+// [c][w][ends][chunk][states of segments]: each a multiple of 16 bytes.
 static size_t chunks_of(int64_t n_chains, int64_t T) { return (size_t)n_chains * (size_t)((T + C - 1) / C); }
+static size_t even(size_t n) { return n + (n & 1); }
 size_t select_workspace_tc(int64_t n_chains, int64_t T, int d) {
-    return chunks_of(n_chains, T) * (C * (sizeof(float2) + sizeof(float)) + 2 * sizeof(float4)) +
+    const size_t n = chunks_of(n_chains, T);
+    return n * (C * (sizeof(float2) + sizeof(float)) + sizeof(float4)) + even(n) * sizeof(float2) +
            segment_bytes(n_chains, d, segments(n_chains, T));
 }
 cudaError_t launch_select_tc(const ScanArgs &scan, cudaStream_t stream) {
@@ -48,9 +50,9 @@ cudaError_t launch_select_tc(const ScanArgs &scan, cudaStream_t stream) {
     s.sel.n_chunks = (s.T + C - 1) / C;
     s.sel.c = reinterpret_cast<float2 *>(s.ws);
     s.sel.w = reinterpret_cast<float *>(s.sel.c + n * C);
-    s.sel.chunk = reinterpret_cast<float4 *>(s.sel.w + n * C);
-    s.sel.ends = s.sel.chunk + n;
-    s.ws = reinterpret_cast<float *>(s.sel.ends + n);
+    s.sel.ends = reinterpret_cast<float4 *>(s.sel.w + n * C);
+    s.sel.chunk = reinterpret_cast<float2 *>(s.sel.ends + n);
+    s.ws = reinterpret_cast<float *>(s.sel.chunk + even(n));
     return s.d == 64 ? launch<64>(s, stream) : launch<128>(s, stream);
 }
 
