@@ -47,15 +47,15 @@ cudaError_t launch(const ScanArgs *scans, int nseg, bool follows, cudaStream_t s
 // one after the other 280 us, at once 181 us; B1 H8 T4096 d = 64, in segments, 64 us).
 void segments_backward(int64_t n_chains, int64_t T, int *fwd, int *rev) {
     const int64_t chunks = (T + C - 1) / C;
-    *fwd = segments(n_chains, T);
-    *rev = segments(2 * n_chains, T);
+    *fwd = segments(kDecayTimes, n_chains, T);
+    *rev = segments(kDecayTimes, 2 * n_chains, T);
     const double waves = (double)((3 * n_chains + kSMs - 1) / kSMs);
-    if (waves * estimate(chunks, 1) <= estimate(chunks, *fwd) + estimate(chunks, *rev)) *fwd = *rev = 1;
+    if (waves * estimate(kDecayTimes, chunks, 1) <= estimate(kDecayTimes, chunks, *fwd) + estimate(kDecayTimes, chunks, *rev)) *fwd = *rev = 1;
 }
 
 template <int D> cudaError_t launch_scans_of(ScanArgs *s, int n, cudaStream_t stream) {
     const int64_t nc = s->n_chains;
-    if (n == 1) return launch<D, false>(s, segments(nc, s->T), false, stream);
+    if (n == 1) return launch<D, false>(s, segments(kDecayTimes, nc, s->T), false, stream);
     int fwd, rev;
     segments_backward(nc, s->T, &fwd, &rev);
     s[1].ws = s[0].ws + segment_bytes(nc, D, fwd) / sizeof(float);
@@ -67,7 +67,7 @@ template <int D> cudaError_t launch_scans_of(ScanArgs *s, int n, cudaStream_t st
 }  // namespace
 
 size_t scan_tc_workspace(int64_t n_chains, int64_t T, int d, bool backward) {
-    if (!backward) return segment_bytes(n_chains, d, segments(n_chains, T));
+    if (!backward) return segment_bytes(n_chains, d, segments(kDecayTimes, n_chains, T));
     int fwd, rev;
     segments_backward(n_chains, T, &fwd, &rev);
     return segment_bytes(n_chains, d, fwd) + 2 * segment_bytes(n_chains, d, rev);

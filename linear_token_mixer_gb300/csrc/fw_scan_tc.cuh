@@ -1340,23 +1340,28 @@ scan_tc_kernel(const __grid_constant__ Jobs<REV ? 2 : 1> jobs, const int nseg, c
     if (order & kWaitLast) wait_previous_grid();
 }
 
-// Estimated time (us) of chains that take one CTA an SM, each in `s` segments, from what was measured at
-// d = 128: 2.8 us a chunk, and where there are segments a launch of 11 us and 2 us a chunk for their
-// states, and 0.7 us to add up each state before the last.  (d = 64 takes 2.05 us a chunk; its other terms
-// have not been measured, and it takes the same numbers of segments.)
-double estimate(int64_t chunks, int s) {
-    if (s == 1) return 2.8 * (double)chunks;
-    return 11.0 + 4.8 * (double)((chunks + s - 1) / s) + 0.7 * s;
+// Times (us) of chains that take one CTA an SM: in one piece a start and so much a chunk; in segments a start with a launch
+// more, so much a chunk for states and rows, and what it takes to add up each state before the last.
+struct Times {
+    double start, chunk, seg_start, seg_chunk, join;
+};
+// As measured of the decayed scan at d = 128.  (d = 64 takes 2.05 us a chunk; its other terms have not been measured,
+// and it takes the same numbers of segments.)
+constexpr Times kDecayTimes{0.0, 2.8, 11.0, 4.8, 0.7};
+
+double estimate(const Times &t, int64_t chunks, int s) {
+    if (s == 1) return t.start + t.chunk * (double)chunks;
+    return t.seg_start + t.seg_chunk * (double)((chunks + s - 1) / s) + t.join * s;
 }
 
 // Segments of each chain, at most what fills the GPU with one CTA an SM: those of the least estimated
 // time.  (More of them than SMs start one after the other: B1 H32 T32768 in four segments 315 us, in
 // nine 333 us.)
-int segments(int64_t n_chains, int64_t T) {
+int segments(const Times &t, int64_t n_chains, int64_t T) {
     const int64_t chunks = (T + C - 1) / C;
     int best = 1;
     for (int s = 2; s <= kSMs / n_chains && s <= chunks; ++s)
-        if (estimate(chunks, s) < estimate(chunks, best)) best = s;
+        if (estimate(t, chunks, s) < estimate(t, chunks, best)) best = s;
     return best;
 }
 

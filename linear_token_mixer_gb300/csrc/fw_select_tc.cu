@@ -5,9 +5,16 @@
 namespace fw {
 namespace {
 
+// Measured of this scan (a segment's decay is summed over its chunks' logs for each 16 columns of a state, which is most of
+// what joining takes).  Best of all numbers of segments, with that of the decayed scan's times in brackets: d = 128
+// H8 T4096 4, 71 us (16, 111); H8 T16384 10, 139 us (19, 164); H16 T2048 4, 55 us (8, 70; in one piece 66); H32
+// T32768 4, 395 us (4); d = 64 H8 T4096 8, 43 us (16, 55), H16 T2048 4, 35 us (8, 39).
+constexpr Times kTimes128{9.0, 3.4, 11.3, 5.4, 5.7}, kTimes64{5.0, 2.4, 9.0, 3.9, 2.15};
+int pieces(int64_t n_chains, int64_t T, int d) { return segments(d == 64 ? kTimes64 : kTimes128, n_chains, T); }
+
 // As the decayed scan's: chains in segments where they are few.
 template <int D> cudaError_t launch(const ScanArgs &a, cudaStream_t s) {
-    const int nseg = segments(a.n_chains, a.T);
+    const int nseg = pieces(a.n_chains, a.T, D);
     const int64_t ab = a.n_chains / a.H * a.sel.gate.G;
     Jobs<1> jobs;
     jobs.s[0].args = a;
@@ -42,7 +49,7 @@ static size_t even(size_t n) { return n + (n & 1); }
 size_t select_workspace_tc(int64_t n_chains, int64_t T, int d) {
     const size_t n = chunks_of(n_chains, T);
     return n * (C * (sizeof(float2) + sizeof(float)) + sizeof(float4)) + even(n) * sizeof(float2) +
-           segment_bytes(n_chains, d, segments(n_chains, T));
+           segment_bytes(n_chains, d, pieces(n_chains, T, d));
 }
 cudaError_t launch_select_tc(const ScanArgs &scan, cudaStream_t stream) {
     ScanArgs s = scan;

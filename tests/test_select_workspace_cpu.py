@@ -15,3 +15,14 @@ def test_bytes_of_a_workspace(B, H, T, d):
     # pairs of chunks), its blocks' logs
     n = B * H * -(-T // 128)
     assert fw.select_workspace(B, H, T, d) == n * (128 * 12 + 16) + (n + n % 2) * 8
+
+
+@pytest.mark.parametrize("B,H,T,d,pieces", [(1, 8, 4096, 128, 4), (1, 8, 16384, 128, 10), (1, 16, 2048, 128, 4), (1, 32, 32768, 128, 4),
+                                            (2, 32, 4096, 128, 2), (1, 16, 640, 128, 1), (2, 64, 32768, 128, 1),
+                                            (1, 8, 4096, 64, 8), (1, 16, 2048, 64, 4), (2, 32, 8192, 64, 2)])
+def test_pieces_of_a_chain(B, H, T, d, pieces):
+    """Few chains go in as many pieces at once as was measured best for this scan; a state of each is in the workspace."""
+    B_.build()
+    n = B * H * -(-T // 128)
+    states = fw.select_workspace(B, H, T, d) - n * (128 * 12 + 16) - (n + n % 2) * 8
+    assert states == (B * H * pieces * d * d * 4 if pieces > 1 else 0)
