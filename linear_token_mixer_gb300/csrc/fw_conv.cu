@@ -13,9 +13,10 @@
 // of a thread, are added up in a block, and a second kernel adds the blocks' in a fixed order.
 //
 // Measured (one GB300, W = 4 with silu): B8 H16 T2048 d = 128 bf16 forward 23.3 us, 85 % of the measured copy rate;
-// backward 45.2 us, 66 %: 23 instructions an element (the taps three times over, silu and its slope) issue in half the
-// cycles, with 16 warps an SM whose registers hold taps, sums and windows.  fp32 d = 65 B4 H8 T1023 W = 3: 4.9 and
-// 10.3 us, of which launches are most.  One token of B256 H32 d = 128: 6 us behind a call of 13.
+// backward 44 us, 67 %, with neither the issue slots (54 % busy) nor DRAM (51 %) full: 23 instructions an element (the
+// taps three times over, silu and its slope) in 16 warps an SM, whose registers hold taps, sums and windows, and which wait
+// for their own results.  fp32: B8 H8 T2048 d = 128 20 and 37 us (99 and 80 %); B4 H8 T1023 d = 65 W = 3 5.5 and 10 us, of
+// which launches are most.  One token of B256 H32 d = 128: 6 us behind a call of 13.
 #include <type_traits>
 
 #include "fw_conv.cuh"

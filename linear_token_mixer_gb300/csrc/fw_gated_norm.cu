@@ -542,8 +542,9 @@ template <typename A> cudaError_t by_type(const A &a, cudaStream_t s) {
     const int w = a.in.width;
     if (a.in.dtype == FW_F32)
         return w % 4 == 0 ? by_width<float, 4>(a, s) : w % 2 == 0 ? by_width<float, 2>(a, s) : by_width<float, 1>(a, s);
-    // (Backwards with a residual eight bytes, which leaves room for the scales in registers: 16384 x 2048 81 us for
-    // 95, 8192 x 4096 88 for 104; without one 81 for 66 of 262144 x 128, 101 for 89 of 8192 x 4096.)
+    // (Backwards with a residual eight bytes, which leaves room for the scales in registers: 262144 x 128 70 us for 73,
+    // 65536 x 512 77 for 95, 16384 x 2048 80 for 98, 8192 x 4096 87 for 103; with a gate too 113 for 123 of 16384 x 2048, but
+    // 100 for 98 of 262144 x 128.  Without a residual 81 for 66 of 262144 x 128, 101 for 89 of 8192 x 4096.)
     if (w % 8 == 0)
         return std::is_same_v<A, GatedBwdArgs> && a.in.residual ? by_width<__nv_bfloat16, 4>(a, s)
                                                                : by_width<__nv_bfloat16, 8>(a, s);

@@ -49,9 +49,9 @@
 // their own.  Measured: B8 H16 T4096 d = 128, keys and queries for each head, 128 us (mild chunks 125, steep ones 131;
 // 125, 121 and 125 without skip; without SEL 101 and 113), with those of one group 128 us; B16 d = 64 193 us, 187 without
 // skip: not its bytes (80 and 43 us at the measured copy rate) but the period of a chunk, 3.4 us.
-// What that goes by is all roles' instructions rather than one chain: without the third term of the update it
-// takes 111 us, without P 103, without X 112, without a branch that no chunk takes 10 us less, and one warp of eight
-// stalls for instructions (tensor pipe 41 % busy, issue slots 49 %, DRAM 43 % at T2048).  B1 H32 T32768 402 us.
+// What that goes by is all roles' instructions rather than one chain: of 126 us (with skip v on the diagonal) the third term
+// of the update was 15, P 23, X 14, a branch that no chunk takes 10, and one warp of nine stalls for instructions (tensor
+// pipe 39 % busy, issue slots 47 %, DRAM 44 % at T2048).  B1 H32 T32768 397 us.
 // Every wait is bounded; on expiry the kernel records an error, the other roles stop at their
 // next wait, copies and MMAs in flight are drained, tensor memory is freed and the kernel exits.
 #pragma once
