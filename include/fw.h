@@ -438,7 +438,7 @@ int fw_layer_norm_backward(const void *dy, const void *x, const float *weight, c
  * A decay below e^-104 is zero: the state starts afresh with the token.
  *   bf16 rows: the masked scores and the state as a row reads it are rounded to bf16 once, like the rows that come
  *   out; the steps, the decays, skip v and S_T are fp32 throughout.  Within a chunk of 128 tokens the scores' decays
- *   are exponentials of differences of logs that are summed over 32 tokens: off by 2.4e-4 of themselves where most of
+ *   are exponentials of differences of logs that are summed over 32 tokens: off by 2.5e-4 of themselves where most of
  *   32 tokens keep nothing, by 3e-5 or less where their logs sum to -100 or more.
  *   Where the decays of a chunk of 128 tokens, or of 32 of them, multiply to e^-40 or more, its sums are formed up
  *   to e^40 times their size: scores or rows beyond about 1e20 may overflow, and of a scale below 1e-20 the scan's share of

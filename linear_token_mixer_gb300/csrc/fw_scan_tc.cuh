@@ -283,7 +283,7 @@ __device__ __forceinline__ float entry_state(const ScanArgs &a, const ScanArgs &
 // SEL: the tables of a chunk, four tokens a lane; by a whole warp.  Logs are summed within blocks of 32 tokens and over
 // the blocks, for the weights from the chunk's end: what counts are short sums, which lose nothing to tokens far off that keep
 // nothing (logs of 104 each, 1e4 in a chunk).  Of a chunk that is not mild the sums of a block go on in two terms and are
-// rounded once, so that a difference of two is off by a unit of the larger: 1.5e-5 for logs of 200 in a block, 2.4e-4 at
+// rounded once, so that a difference of two is off by a unit of the larger: 1.5e-5 for logs of 200 in a block, 2.5e-4 at
 // most (32 tokens that keep nothing).
 __device__ __forceinline__ void form_tables(const ScanArgs &a, int64_t chain, int64_t n, int64_t chunk) {
     constexpr int PER = C / 32, LANES = 32 / PER;   // of a block
